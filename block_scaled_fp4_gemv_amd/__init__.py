@@ -8,6 +8,16 @@ the stream; tensors are passed as raw device pointers.
     nvfp4_gemv_scaled(..., sf_layout, alpha, workspace=None, stream=None)
     nvfp4_scales_to_blocked(plain, blocked, rows, K, L, stream=None)
 
+FP4 linear layers and routed experts (last part of the header):
+
+    nvfp4_global_scale(x, scale, rows, K, L, workspace)
+    nvfp4_quantize(x, codes, scales, rows, K, L, sf_layout, global_scale=None)
+    nvfp4_dequantize(codes, scales, out, rows, K, L, sf_layout, global_scale=None)
+    nvfp4_gemm(a, b, sfa, sfb, c, M, N, K, L, sf_layout, workspace=None)
+    nvfp4_moe_route(logits, ids, weights, offsets, order, T, E, k, workspace=...)
+    nvfp4_gemm_experts(a, b, sfa, sfb, c, M, K, E, rows, slots_per_row, sf_layout, offsets, order)
+    nvfp4_moe_combine(y, ids, weights, out, T, k, M)
+
     a   uint8 [L, M, K/2]   packed E2M1, low nibble = even k
     b   uint8 [L, K/2]
     sfa uint8 plain [L, M, K/16] or blocked [L, ceil(M/128)*ceil(K/64)*512]
@@ -35,6 +45,13 @@ NVFP4_ERR_WORKSPACE = 5
 NVFP4_ERR_HIP = 6
 NVFP4_ERR_INVALID_SCALE = 7
 NVFP4_ERR_INVALID_STRIDE = 8
+NVFP4_ERR_INVALID_TYPE = 9
+NVFP4_ERR_INVALID_ROUTING = 10
+NVFP4_F16 = 0
+NVFP4_BF16 = 1
+NVFP4_F32 = 2
+NVFP4_SCORE_SOFTMAX = 0
+NVFP4_SCORE_SIGMOID = 1
 
 EXPORTED_SYMBOLS = (
     "nvfp4_gemv",
@@ -51,6 +68,18 @@ EXPORTED_SYMBOLS = (
     "nvfp4_gemm_small_n_plan",
     "nvfp4_scales_to_blocked",
     "nvfp4_blocked_scales_bytes",
+    "nvfp4_global_scale",
+    "nvfp4_global_scale_workspace_bytes",
+    "nvfp4_quantize",
+    "nvfp4_dequantize",
+    "nvfp4_gemm",
+    "nvfp4_gemm_workspace_bytes",
+    "nvfp4_gemm_plan",
+    "nvfp4_moe_route",
+    "nvfp4_moe_route_workspace_bytes",
+    "nvfp4_gemm_experts",
+    "nvfp4_gemm_experts_workspace_bytes",
+    "nvfp4_moe_combine",
     "nvfp4_status_string",
     "nvfp4_last_hip_error",
 )
@@ -88,6 +117,22 @@ class Plan(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class GemmPlan(ctypes.Structure):
+    """nvfp4_gemm_plan_t."""
+    _fields_ = [("tile_m", ctypes.c_int32), ("tile_n", ctypes.c_int32),
+                ("k_splits", ctypes.c_int32), ("k_per_split", ctypes.c_int32),
+                ("workgroups", ctypes.c_int64)]
+
+    def as_dict(self) -> dict:
+        return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class Routing(ctypes.Structure):
+    """nvfp4_routing_t."""
+    _fields_ = [("score", ctypes.c_int32), ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scaling", ctypes.c_float)]
 
 
 _lib = None
@@ -134,6 +179,32 @@ def lib():
     L.nvfp4_scales_to_blocked.argtypes = [vp, vp, i64, i64, i64, vp]
     L.nvfp4_blocked_scales_bytes.restype = ctypes.c_size_t
     L.nvfp4_blocked_scales_bytes.argtypes = [i64, i64, i64]
+    f32, size = ctypes.c_float, ctypes.c_size_t
+    L.nvfp4_global_scale.restype = i32
+    L.nvfp4_global_scale.argtypes = [vp, i32, vp, i64, i64, i64, i64, i64, vp, size, vp]
+    L.nvfp4_global_scale_workspace_bytes.restype = size
+    L.nvfp4_global_scale_workspace_bytes.argtypes = []
+    L.nvfp4_quantize.restype = i32
+    L.nvfp4_quantize.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, i64, i64, i32, vp]
+    L.nvfp4_dequantize.restype = i32
+    L.nvfp4_dequantize.argtypes = [vp, vp, vp, vp, i32, i64, i64, i64, i32, vp]
+    L.nvfp4_gemm.restype = i32
+    L.nvfp4_gemm.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, i64, i32, f32, vp, vp, vp, size, vp]
+    L.nvfp4_gemm_workspace_bytes.restype = size
+    L.nvfp4_gemm_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    L.nvfp4_gemm_plan.restype = i32
+    L.nvfp4_gemm_plan.argtypes = [i64, i64, i64, i64, ctypes.POINTER(GemmPlan)]
+    L.nvfp4_moe_route.restype = i32
+    L.nvfp4_moe_route.argtypes = [vp, i32, vp, vp, vp, vp, vp, i64, i64, i64, ctypes.POINTER(Routing), vp, size, vp]
+    L.nvfp4_moe_route_workspace_bytes.restype = size
+    L.nvfp4_moe_route_workspace_bytes.argtypes = [i64, i64, i64]
+    L.nvfp4_gemm_experts.restype = i32
+    L.nvfp4_gemm_experts.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, i64, i64, i32, vp, vp, f32, vp, vp, vp,
+                                     size, vp]
+    L.nvfp4_gemm_experts_workspace_bytes.restype = size
+    L.nvfp4_gemm_experts_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    L.nvfp4_moe_combine.restype = i32
+    L.nvfp4_moe_combine.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, vp]
     L.nvfp4_status_string.restype = ctypes.c_char_p
     L.nvfp4_status_string.argtypes = [i32]
     L.nvfp4_last_hip_error.restype = i32
@@ -362,6 +433,204 @@ def nvfp4_scales_to_blocked(plain, blocked, rows: int, K: int, L: int, stream=No
     st = lib().nvfp4_scales_to_blocked(pp, pb, rows, K, L, _stream_handle(stream))
     if st != NVFP4_OK:
         raise Nvfp4Error(st, "nvfp4_scales_to_blocked")
+
+
+# ---------------------------------------------------------------- FP4 linear layers, routed experts
+
+_DTYPES = {"torch.float16": (NVFP4_F16, 2), "torch.bfloat16": (NVFP4_BF16, 2), "torch.float32": (NVFP4_F32, 4)}
+
+
+def _dtype_id(x, dtype):
+    """nvfp4_dtype_t of a tensor (or of ``dtype``, needed for raw pointers)."""
+    if dtype is None:
+        if x is None or isinstance(x, int):
+            raise ValueError("raw pointers need dtype=")
+        dtype = x.dtype
+    if isinstance(dtype, int):
+        return dtype                        # passed through; the library rejects unknown values
+    known = _DTYPES.get(str(dtype))
+    if known is None:
+        raise ValueError(f"{dtype} is none of float16, bfloat16, float32")
+    return known[0]
+
+
+def _need(**ops) -> None:
+    """name=((pointer, bytes held or None), bytes needed): raises where a tensor is too small."""
+    for name, ((_, held), need) in ops.items():
+        if held is not None and held < need:
+            raise ValueError(f"{name} holds {held} bytes, the shape needs {need}")
+
+
+def _typed(x, name, *dtypes):
+    """(pointer, bytes) of a tensor whose type has to be one of ``dtypes``."""
+    if x is not None and not isinstance(x, int) and str(x.dtype) not in dtypes:
+        raise ValueError(f"{name} is {x.dtype}, not {' or '.join(d.replace('torch.', '') for d in dtypes)}")
+    return _ptr_and_bytes(x)
+
+
+def _strided(x, name, rows, K, L, row_stride, batch_stride):
+    """Pointer of an [L][rows][K] tensor and its strides in elements, checked
+    against what the tensor's memory holds behind its first element."""
+    if row_stride is None:
+        row_stride = K
+    if batch_stride is None:
+        batch_stride = rows * row_stride
+    if x is None or isinstance(x, int):
+        return x, row_stride, batch_stride
+    if not x.is_cuda:
+        raise ValueError("operands must be device tensors")
+    if min(rows, K, L) >= 1 and min(row_stride, batch_stride) >= 0:
+        held = x.untyped_storage().nbytes() // x.element_size() - x.storage_offset()
+        need = (L - 1) * batch_stride + (rows - 1) * row_stride + K
+        if held < need:
+            raise ValueError(f"{name} holds {held} elements, the shape needs {need}")
+    return x.data_ptr(), row_stride, batch_stride
+
+
+def _scale_bytes(rows, K, L, lay):
+    return L * (cdiv(rows, 128) * cdiv(K, 64) * 512 if lay == NVFP4_SF_BLOCKED else rows * (K // 16))
+
+
+def _done(status, where) -> None:
+    if status != NVFP4_OK:
+        raise Nvfp4Error(status, where)
+
+
+def nvfp4_global_scale_workspace_bytes() -> int:
+    return int(lib().nvfp4_global_scale_workspace_bytes())
+
+
+def nvfp4_global_scale(x, scale, rows: int, K: int, L: int, workspace, workspace_bytes: int | None = None,
+                       row_stride: int | None = None, batch_stride: int | None = None, dtype=None,
+                       stream=None) -> None:
+    """Enqueue scale[0] = max finite |x| * (1 / 2688) (strides in elements; dense by default)."""
+    px, rs, bs = _strided(x, "x", rows, K, L, row_stride, batch_stride)
+    sc, (pw, nw) = _typed(scale, "scale", "torch.float32"), _ptr_and_bytes(workspace)
+    _need(scale=(sc, 4))
+    _done(lib().nvfp4_global_scale(px, _dtype_id(x, dtype), sc[0], rows, K, L, rs, bs, pw,
+                                   (nw or 0) if workspace_bytes is None else workspace_bytes,
+                                   _stream_handle(stream)), "nvfp4_global_scale")
+
+
+def nvfp4_quantize(x, codes, scales, rows: int, K: int, L: int, sf_layout, global_scale=None,
+                   row_stride: int | None = None, batch_stride: int | None = None, dtype=None,
+                   stream=None) -> None:
+    """Enqueue the quantisation of x [L][rows][K] (strides in elements; dense by
+    default) to NVFP4 codes and scales; global_scale: float32 on the device."""
+    px, rs, bs = _strided(x, "x", rows, K, L, row_stride, batch_stride)
+    lay = layout_id(sf_layout)
+    co, sc = _ptr_and_bytes(codes), _ptr_and_bytes(scales)
+    gs = _typed(global_scale, "global_scale", "torch.float32")
+    if min(rows, K, L) >= 1:
+        _need(codes=(co, L * rows * K // 2), scales=(sc, _scale_bytes(rows, K, L, lay)), global_scale=(gs, 4))
+    _done(lib().nvfp4_quantize(px, _dtype_id(x, dtype), gs[0], co[0], sc[0], rows, K, L, rs, bs, lay,
+                               _stream_handle(stream)), "nvfp4_quantize")
+
+
+def nvfp4_dequantize(codes, scales, out, rows: int, K: int, L: int, sf_layout, global_scale=None, dtype=None,
+                     stream=None) -> None:
+    """Enqueue out [L][rows][K] = the values that codes and scales stand for."""
+    lay, dt = layout_id(sf_layout), _dtype_id(out, dtype)
+    co, sc, ou = _ptr_and_bytes(codes), _ptr_and_bytes(scales), _ptr_and_bytes(out)
+    gs = _typed(global_scale, "global_scale", "torch.float32")
+    if min(rows, K, L) >= 1:
+        _need(codes=(co, L * rows * K // 2), scales=(sc, _scale_bytes(rows, K, L, lay)),
+              out=(ou, L * rows * K * (4 if dt == NVFP4_F32 else 2)), global_scale=(gs, 4))
+    _done(lib().nvfp4_dequantize(co[0], sc[0], gs[0], ou[0], dt, rows, K, L, lay, _stream_handle(stream)),
+          "nvfp4_dequantize")
+
+
+def nvfp4_gemm_workspace_bytes(M: int, N: int, K: int, L: int) -> int:
+    return int(lib().nvfp4_gemm_workspace_bytes(M, N, K, L))
+
+
+def nvfp4_gemm_plan(M: int, N: int, K: int, L: int) -> dict:
+    plan = GemmPlan()
+    _done(lib().nvfp4_gemm_plan(M, N, K, L, ctypes.byref(plan)), "nvfp4_gemm_plan")
+    return plan.as_dict()
+
+
+def nvfp4_gemm(a, b, sfa, sfb, c, M: int, N: int, K: int, L: int, sf_layout, alpha: float = 1.0, scale_a=None,
+               scale_b=None, workspace=None, workspace_bytes: int | None = None, dtype=None, stream=None) -> None:
+    """Enqueue c[l][n][m] = alpha * ga * gb * sum_k A*SFA*B_n*SFB_n for any N; c
+    float16, bfloat16 or float32; scale_a, scale_b: float32 on the device; a
+    (zero-initialised) workspace of nvfp4_gemm_workspace_bytes."""
+    lay, dt = layout_id(sf_layout), _dtype_id(c, dtype)
+    oa, ob, osa, osb, oc = map(_ptr_and_bytes, (a, b, sfa, sfb, c))
+    ga, gb = _typed(scale_a, "scale_a", "torch.float32"), _typed(scale_b, "scale_b", "torch.float32")
+    pw, nw = _ptr_and_bytes(workspace)
+    if min(M, N, K, L) >= 1:
+        _need(a=(oa, L * M * K // 2), b=(ob, L * N * K // 2), sfa=(osa, _scale_bytes(M, K, L, lay)),
+              sfb=(osb, _scale_bytes(N, K, L, lay)), c=(oc, L * N * M * (4 if dt == NVFP4_F32 else 2)),
+              scale_a=(ga, 4), scale_b=(gb, 4))
+    _done(lib().nvfp4_gemm(oa[0], ob[0], osa[0], osb[0], oc[0], dt, M, N, K, L, lay, float(alpha), ga[0], gb[0], pw,
+                           (nw or 0) if workspace_bytes is None else workspace_bytes, _stream_handle(stream)),
+          "nvfp4_gemm")
+
+
+def nvfp4_moe_route_workspace_bytes(T: int, E: int, k: int) -> int:
+    return int(lib().nvfp4_moe_route_workspace_bytes(T, E, k))
+
+
+_SCORES = {"softmax": NVFP4_SCORE_SOFTMAX, "sigmoid": NVFP4_SCORE_SIGMOID}
+
+
+def nvfp4_moe_route(logits, ids, weights, offsets, order, T: int, E: int, k: int, score="softmax", bias=None,
+                    n_group: int = 1, topk_group: int = 1, group_top: int = 1, renormalize: bool = True,
+                    scaling: float = 1.0, workspace=None, workspace_bytes: int | None = None, dtype=None,
+                    stream=None) -> None:
+    """Enqueue the routing of T tokens to k of E experts: ids and weights [T][k],
+    and the experts' lists (offsets [E + 1], order [T * k])."""
+    dt = _dtype_id(logits, dtype)
+    lo, (pw, nw) = _ptr_and_bytes(logits), _ptr_and_bytes(workspace)
+    bi, we = _typed(bias, "bias", "torch.float32"), _typed(weights, "weights", "torch.float32")
+    idt, off, orr = (_typed(x, n, "torch.int32") for x, n in ((ids, "ids"), (offsets, "offsets"), (order, "order")))
+    if min(T, E, k) >= 1:
+        _need(logits=(lo, T * E * (4 if dt == NVFP4_F32 else 2)), bias=(bi, 4 * E), ids=(idt, 4 * T * k),
+              weights=(we, 4 * T * k), offsets=(off, 4 * (E + 1)), order=(orr, 4 * T * k))
+    opts = Routing(_SCORES.get(score, score), n_group, topk_group, group_top, int(renormalize), float(scaling))
+    _done(lib().nvfp4_moe_route(lo[0], dt, bi[0], idt[0], we[0], off[0], orr[0], T, E, k, ctypes.byref(opts), pw,
+                                (nw or 0) if workspace_bytes is None else workspace_bytes, _stream_handle(stream)),
+          "nvfp4_moe_route")
+
+
+def nvfp4_gemm_experts_workspace_bytes(M: int, K: int, E: int, S: int) -> int:
+    return int(lib().nvfp4_gemm_experts_workspace_bytes(M, K, E, S))
+
+
+def nvfp4_gemm_experts(a, b, sfa, sfb, c, M: int, K: int, E: int, rows: int, slots_per_row: int, sf_layout, offsets,
+                       order, alpha: float = 1.0, scale_a=None, scale_b=None, workspace=None,
+                       workspace_bytes: int | None = None, dtype=None, stream=None) -> None:
+    """Enqueue c[s][m] for every slot s of the experts' lists: the row
+    s // slots_per_row of b times the weights a[e] of the slot's expert e."""
+    lay, dt = layout_id(sf_layout), _dtype_id(c, dtype)
+    oa, ob, osa, osb, oc = map(_ptr_and_bytes, (a, b, sfa, sfb, c))
+    ga, gb = _typed(scale_a, "scale_a", "torch.float32"), _typed(scale_b, "scale_b", "torch.float32")
+    off, orr = _typed(offsets, "offsets", "torch.int32"), _typed(order, "order", "torch.int32")
+    pw, nw = _ptr_and_bytes(workspace)
+    if min(M, K, E, rows, slots_per_row) >= 1:
+        S = rows * slots_per_row
+        _need(a=(oa, E * M * K // 2), b=(ob, rows * K // 2), sfa=(osa, _scale_bytes(M, K, E, lay)),
+              sfb=(osb, _scale_bytes(rows, K, 1, lay)), c=(oc, S * M * (4 if dt == NVFP4_F32 else 2)),
+              offsets=(off, 4 * (E + 1)), order=(orr, 4 * S), scale_a=(ga, 4 * E), scale_b=(gb, 4))
+    _done(lib().nvfp4_gemm_experts(oa[0], ob[0], osa[0], osb[0], oc[0], dt, M, K, E, rows, slots_per_row, lay, off[0],
+                                   orr[0], float(alpha), ga[0], gb[0], pw,
+                                   (nw or 0) if workspace_bytes is None else workspace_bytes, _stream_handle(stream)),
+          "nvfp4_gemm_experts")
+
+
+def nvfp4_moe_combine(y, ids, weights, out, T: int, k: int, M: int, dtype=None, stream=None) -> None:
+    """Enqueue out[t] = sum_j weights[t][j] * y[t * k + j] over ids[t][j] >= 0."""
+    dt = _dtype_id(y, dtype)
+    if dt != _dtype_id(out, dtype):
+        raise ValueError("y and out have different types")
+    size = 4 if dt == NVFP4_F32 else 2
+    oy, oo = _ptr_and_bytes(y), _ptr_and_bytes(out)
+    idt, we = _typed(ids, "ids", "torch.int32"), _typed(weights, "weights", "torch.float32")
+    if min(T, k, M) >= 1:
+        _need(y=(oy, T * k * M * size), ids=(idt, 4 * T * k), weights=(we, 4 * T * k), out=(oo, T * M * size))
+    _done(lib().nvfp4_moe_combine(oy[0], dt, idt[0], we[0], oo[0], T, k, M, _stream_handle(stream)),
+          "nvfp4_moe_combine")
 
 
 def nvfp4_status_string(status: int) -> str:

@@ -58,6 +58,12 @@ __device__ __attribute__((always_inline)) inline uint16_t f16_bits(float v)
     return __builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
+// float32 -> bfloat16 bits, round to nearest even, NaN kept
+__device__ __attribute__((always_inline)) inline uint32_t bf16_bits(float v)
+{
+    return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
 // Sum over aligned groups of RED lanes (RED = 1..64, a power of two) with DPP.
 // The group's sum ends in its last lane: row_shr accumulates a window of RED
 // lanes inside each 16-lane row, row_bcast15 / row_bcast31 carry the row sums

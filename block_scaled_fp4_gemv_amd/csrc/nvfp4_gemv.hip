@@ -1711,6 +1711,8 @@ const char *nvfp4_status_string(int status)
     case NVFP4_ERR_HIP: return "HIP runtime error";
     case NVFP4_ERR_INVALID_SCALE: return "global scale alpha is not finite";
     case NVFP4_ERR_INVALID_STRIDE: return "operand stride out of range or misaligned";
+    case NVFP4_ERR_INVALID_TYPE: return "unknown element type";
+    case NVFP4_ERR_INVALID_ROUTING: return "router option out of range";
     default: return "unknown status";
     }
 }

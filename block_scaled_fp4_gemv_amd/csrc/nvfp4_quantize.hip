@@ -1,0 +1,480 @@
+// Quantisation of activations to NVFP4 on MI355X (gfx950): the global scale,
+// codes and block scales, and the way back to values.
+//
+//   g    = max finite |x| * (1 / 2688)
+//   s[b] = E4M3 nearest to max_b |x| / (6 g),   q[k] = E2M1 nearest to x[k] / (s[b] g)
+//
+// Exactness. Both roundings are those of the exact quotients. A code is decided
+// by comparing |x| with a midpoint of two codes times s and g: midpoint * s
+// has at most 7 significant bits (an exact float32), and the sign of
+// fma(midpoint * s, -g, |x|) is the sign of the exact difference, since the
+// fused multiply-add rounds once and to the nearest, and a nonzero difference
+// of these operands stays nonzero (g >= 2^-100, so the midpoints are at least
+// 2^-111 and a difference at least 2^-142). The same test with 6 * (midpoint
+// of two E4M3 values), at most 7 bits, decides the scale. No division's
+// rounding enters.
+//
+// What bounds it: HBM. Each kernel reads and writes every byte once.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <type_traits>
+
+#include "nvfp4_device.h"
+#include "nvfp4_gemv.h"
+#include "nvfp4_internal.h"
+
+namespace {
+
+constexpr int kQThreads = 256;
+constexpr int kAmaxThreads = 256;
+constexpr int kAmaxMaxGrid = 1024;
+constexpr float kMinScale = 7.8886091e-31f;     // 2^-100
+constexpr int64_t kMaxGrid = 0xFFFFFF;           // workgroups of 256 threads in 2^32 work items
+
+// ------------------------------------------------------------------ loads
+
+// 16 consecutive elements as float32 (exact for every type). The address has
+// the type's own alignment only: gfx950 takes 16-byte global loads at any.
+template <int DT>
+__device__ __attribute__((always_inline)) inline void load16(const uint8_t *p, float (&v)[16])
+{
+    if constexpr (DT == NVFP4_F32) {
+        __builtin_memcpy(v, p, 64);
+    } else {
+        uint32_t w[8];
+        __builtin_memcpy(w, p, 32);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (DT == NVFP4_BF16) {
+                v[2 * i] = __builtin_bit_cast(float, w[i] << 16);
+                v[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xFFFF0000u);
+            } else {
+                const half2_t h = as_h2(w[i]);
+                v[2 * i] = (float)h.x;
+                v[2 * i + 1] = (float)h.y;
+            }
+        }
+    }
+}
+
+template <int DT>
+__device__ __attribute__((always_inline)) inline uint32_t load_bits(const uint8_t *p)
+{
+    if constexpr (DT == NVFP4_F32) {
+        uint32_t w;
+        __builtin_memcpy(&w, p, 4);
+        return w;
+    } else {
+        uint16_t h;
+        __builtin_memcpy(&h, p, 2);
+        if constexpr (DT == NVFP4_BF16)
+            return (uint32_t)h << 16;
+        return __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(_Float16, h));
+    }
+}
+
+template <int DT>
+constexpr int kSize = DT == NVFP4_F32 ? 4 : 2;
+
+// ------------------------------------------------------------------ global scale
+
+// |x| as an ordered integer, 0 for NaN and infinities
+__device__ __attribute__((always_inline)) inline uint32_t finite_size(uint32_t bits)
+{
+    const uint32_t a = bits & 0x7FFFFFFFu;
+    return a < 0x7F800000u ? a : 0u;
+}
+
+// Grid-stride over pieces of 16 elements of every row; maxima are joined with
+// an atomic maximum (any order gives the same result), the last workgroup (by
+// ticket) writes the scale and clears the two counters.
+template <int DT>
+__global__ __launch_bounds__(kAmaxThreads) void nvfp4_global_scale_kernel(
+    const uint8_t *__restrict__ x, float *__restrict__ scale, uint32_t *__restrict__ ws, int64_t pieces, int64_t K,
+    int64_t rows, int64_t row_bytes, int64_t batch_bytes, int32_t per_row)
+{
+    uint32_t top = 0;
+    const int64_t step = (int64_t)gridDim.x * kAmaxThreads;
+    for (int64_t i = (int64_t)blockIdx.x * kAmaxThreads + threadIdx.x; i < pieces; i += step) {
+        const int64_t r = i / per_row, k = (i - r * per_row) * 16;
+        const int64_t l = r / rows;
+        const uint8_t *p = x + l * batch_bytes + (r - l * rows) * row_bytes + k * kSize<DT>;
+        if (k + 16 <= K) {
+            float v[16];
+            load16<DT>(p, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                top = max(top, finite_size(__builtin_bit_cast(uint32_t, v[j])));
+        } else {
+            for (int64_t j = k; j < K; ++j)
+                top = max(top, finite_size(load_bits<DT>(p + (j - k) * kSize<DT>)));
+        }
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1)
+        top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    __shared__ uint32_t wave_top[kAmaxThreads / 64];
+    if (threadIdx.x % 64 == 0)
+        wave_top[threadIdx.x / 64] = top;
+    __syncthreads();
+    if (threadIdx.x != 0)
+        return;
+#pragma unroll
+    for (int w = 1; w < kAmaxThreads / 64; ++w)
+        top = max(top, wave_top[w]);
+    if (gridDim.x > 1) {
+        // the maximum has to be in place before the ticket is taken: the
+        // returned value is waited for
+        const uint32_t was = __hip_atomic_fetch_max(&ws[0], top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" : : "v"(was) : "memory");
+        const uint32_t before = __hip_atomic_fetch_add(&ws[1], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (before != gridDim.x - 1)
+            return;
+        top = __hip_atomic_exchange(&ws[0], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(&ws[1], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    // the product with the float32 nearest to 1/2688: within one step of the
+    // quotient, and any g near it serves (the codes are exact for the g written)
+    *scale = top ? fmaxf(__builtin_bit_cast(float, top) * (1.0f / 2688.0f), kMinScale) : 1.0f;
+}
+
+// ------------------------------------------------------------------ quantise
+
+__device__ __attribute__((always_inline)) inline float e4m3_value(uint32_t code)
+{
+    return __builtin_amdgcn_cvt_f32_fp8((int)code, 0);
+}
+
+// E4M3 code of the exact quotient amax / (6 g), amax finite or infinite, >= 0.
+// The float32 quotient is within a few units of its last place, so its code is
+// the right one or a neighbour; the two midpoints around it decide.
+__device__ __attribute__((always_inline)) inline uint32_t scale_code(float amax, float g)
+{
+    const float v = fminf((amax / g) * (1.0f / 6.0f), 448.0f);
+    uint32_t c = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xFFu;
+    const float here = e4m3_value(c);
+    const float above = e4m3_value(c < 126u ? c + 1 : c), below = e4m3_value(c > 0u ? c - 1 : c);
+    const float up = fmaf(3.0f * (here + above), -g, amax);     // 6 * midpoint
+    const float down = fmaf(3.0f * (here + below), -g, amax);
+    const bool odd = c & 1u;
+    if (c < 126u && (up > 0.0f || (up == 0.0f && odd)))
+        return c + 1;
+    if (c > 0u && (down < 0.0f || (down == 0.0f && odd)))
+        return c - 1;
+    return c;
+}
+
+// E2M1 code (sign included) of the exact quotient x / (s g), s > 0.
+__device__ __attribute__((always_inline)) inline uint32_t value_code(float x, float s, float g)
+{
+    const float a = fabsf(x);
+    // one count per midpoint passed; at a tie the even neighbour's side
+    uint32_t n = 0;
+    n += fmaf(0.25f * s, -g, a) > 0.0f;
+    n += fmaf(0.75f * s, -g, a) >= 0.0f;
+    n += fmaf(1.25f * s, -g, a) > 0.0f;
+    n += fmaf(1.75f * s, -g, a) >= 0.0f;
+    n += fmaf(2.5f * s, -g, a) > 0.0f;
+    n += fmaf(3.5f * s, -g, a) >= 0.0f;
+    n += fmaf(5.0f * s, -g, a) > 0.0f;
+    return n | ((__builtin_bit_cast(uint32_t, x) >> 31) << 3);
+}
+
+// One block of 16 values -> 8 bytes of codes and the scale code.
+__device__ __attribute__((always_inline)) inline uint2_t quantize_block(const float (&v)[16], float g, bool g_good,
+                                                                        uint32_t &scale)
+{
+    float amax = 0.0f;
+    bool nan = !g_good;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        amax = fmaxf(amax, fabsf(v[i]));
+        nan |= v[i] != v[i];
+    }
+    if (nan) {
+        scale = 0x7Fu;
+        return (uint2_t){0u, 0u};
+    }
+    scale = scale_code(amax, g);
+    if (scale == 0u)
+        return (uint2_t){0u, 0u};
+    const float s = e4m3_value(scale);
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        w[i / 8] |= value_code(v[i], s, g) << (4 * (i % 8));
+    return (uint2_t){w[0], w[1]};
+}
+
+struct QParams {
+    int64_t rows, row_bytes, batch_bytes;
+    int32_t nkb;                     // 16-element blocks per row
+    int32_t wg_per_band;             // workgroups per band of rows (blocked) or batch (plain)
+    int32_t bands;                   // bands of rows per batch (blocked)
+};
+
+__device__ __attribute__((always_inline)) inline bool good_scale(float g)
+{
+    return g >= kMinScale && g < __builtin_inff();
+}
+
+// Plain scales: one thread per block, blocks of a batch in order.
+template <int DT>
+__global__ __launch_bounds__(kQThreads) void nvfp4_quantize_plain_kernel(
+    const uint8_t *__restrict__ x, const float *__restrict__ gp, uint8_t *__restrict__ codes,
+    uint8_t *__restrict__ scales, QParams p)
+{
+    const float g = gp ? *gp : 1.0f;
+    const int64_t l = blockIdx.x / (uint32_t)p.wg_per_band;
+    const int64_t i = (int64_t)(blockIdx.x % (uint32_t)p.wg_per_band) * kQThreads + threadIdx.x;
+    if (i >= p.rows * p.nkb)
+        return;
+    const int64_t r = i / p.nkb;
+    const int32_t kb = (int32_t)(i - r * p.nkb);
+    float v[16];
+    load16<DT>(x + l * p.batch_bytes + r * p.row_bytes + (int64_t)kb * 16 * kSize<DT>, v);
+    uint32_t s;
+    const uint2_t q = quantize_block(v, g, good_scale(g), s);
+    const int64_t o = l * p.rows * p.nkb + i;
+    *(uint2_t *)(codes + o * 8) = q;
+    scales[o] = (uint8_t)s;
+}
+
+// Blocked scales: a workgroup takes 16 rows, r32 .. r32+3 of each 32-row
+// quarter of a 128-row block, and 16 columns of blocks. Four neighbouring
+// threads hold the four scales of a row and 4-column group; one of them
+// stores the word. Rows and columns past the matrix write zero scales.
+template <int DT>
+__global__ __launch_bounds__(kQThreads) void nvfp4_quantize_blocked_kernel(
+    const uint8_t *__restrict__ x, const float *__restrict__ gp, uint8_t *__restrict__ codes,
+    uint8_t *__restrict__ scales, QParams p)
+{
+    const float g = gp ? *gp : 1.0f;
+    const int32_t t = threadIdx.x;
+    const uint32_t band = blockIdx.x / (uint32_t)p.wg_per_band;            // batch * bands + 16-row band
+    const int32_t kb = (int32_t)(blockIdx.x % (uint32_t)p.wg_per_band) * 16 + t % 16;
+    const int64_t l = band / (uint32_t)p.bands;
+    const int32_t b = (int32_t)(band % (uint32_t)p.bands);
+    const int64_t rb = b / 8;
+    const int32_t r32 = (b % 8) * 4 + t / 64, quarter = (t / 16) % 4;
+    const int64_t r = rb * 128 + quarter * 32 + r32;
+    const int32_t ncb = (p.nkb + 3) / 4;
+    uint32_t s = 0u;
+    if (r < p.rows && kb < p.nkb) {
+        float v[16];
+        load16<DT>(x + l * p.batch_bytes + r * p.row_bytes + (int64_t)kb * 16 * kSize<DT>, v);
+        const uint2_t q = quantize_block(v, g, good_scale(g), s);
+        *(uint2_t *)(codes + ((l * p.rows + r) * p.nkb + kb) * 8) = q;
+    }
+    // four lanes' scales in one word, lane 0 of the four stores it
+    s <<= 8 * (t % 4);
+    s |= (uint32_t)__shfl_xor((int)s, 1);
+    s |= (uint32_t)__shfl_xor((int)s, 2);
+    if (t % 4 == 0 && kb / 4 < ncb) {
+        const int64_t nrb = (p.rows + 127) / 128;
+        *(uint32_t *)(scales + ((l * nrb + rb) * ncb + kb / 4) * 512 + r32 * 16 + quarter * 4) = s;
+    }
+}
+
+// ------------------------------------------------------------------ dequantise
+
+template <int DT>
+__device__ __attribute__((always_inline)) inline void store16(uint8_t *p, const float (&v)[16])
+{
+    if constexpr (DT == NVFP4_F32) {
+        __builtin_memcpy(p, v, 64);
+    } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (DT == NVFP4_F16)
+                w[i] = (uint32_t)f16_bits(v[2 * i]) | ((uint32_t)f16_bits(v[2 * i + 1]) << 16);
+            else
+                w[i] = bf16_bits(v[2 * i]) | (bf16_bits(v[2 * i + 1]) << 16);
+        }
+        __builtin_memcpy(p, w, 32);
+    }
+}
+
+template <int DT, int LAYOUT>
+__global__ __launch_bounds__(kQThreads) void nvfp4_dequantize_kernel(
+    const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, const float *__restrict__ gp,
+    uint8_t *__restrict__ out, int64_t rows, int64_t blocks, int32_t nkb)
+{
+    const int64_t i = (int64_t)blockIdx.x * kQThreads + threadIdx.x;
+    if (i >= blocks)
+        return;
+    const float g = gp ? *gp : 1.0f;
+    const int64_t lr = i / nkb;
+    const int32_t kb = (int32_t)(i - lr * nkb);
+    int64_t at = i;
+    if constexpr (LAYOUT == NVFP4_SF_BLOCKED) {
+        const int64_t l = lr / rows, r = lr - l * rows;
+        const int64_t nrb = (rows + 127) / 128, ncb = (nkb + 3) / 4;
+        at = ((l * nrb + r / 128) * ncb + kb / 4) * 512 + (r % 32) * 16 + ((r % 128) / 32) * 4 + kb % 4;
+    }
+    const uint2_t q = *(const uint2_t *)(codes + i * 8);
+    const float s = e4m3_value(scales[at]);
+    float v[16];
+    const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+        const half2_t h[4] = {fp4x2<0>(w[d]), fp4x2<1>(w[d]), fp4x2<2>(w[d]), fp4x2<3>(w[d])};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[8 * d + 2 * j] = (float)h[j].x * s * g;
+            v[8 * d + 2 * j + 1] = (float)h[j].y * s * g;
+        }
+    }
+    store16<DT>(out + i * 16 * kSize<DT>, v);
+}
+
+// ------------------------------------------------------------------ host
+
+constexpr int64_t kMaxRows = INT64_C(1) << 40, kMaxStride = INT64_C(1) << 40;
+
+bool known_type(int dtype) { return dtype == NVFP4_F16 || dtype == NVFP4_BF16 || dtype == NVFP4_F32; }
+int64_t type_size(int dtype) { return dtype == NVFP4_F32 ? 4 : 2; }
+bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+bool good_strides(int64_t rows, int64_t K, int64_t row_stride, int64_t batch_stride)
+{
+    return row_stride >= (rows > 1 ? K : 0) && row_stride < kMaxStride && batch_stride >= 0 &&
+           batch_stride < kMaxStride;
+}
+
+nvfp4_status_t finish()
+{
+    const hipError_t e = hipGetLastError();
+    if (e == hipSuccess)
+        return NVFP4_OK;
+    nvfp4_record_hip_error((int)e);
+    return NVFP4_ERR_HIP;
+}
+
+template <typename F>
+void by_type(int dtype, F f)
+{
+    if (dtype == NVFP4_F16)
+        f(std::integral_constant<int, NVFP4_F16>{});
+    else if (dtype == NVFP4_BF16)
+        f(std::integral_constant<int, NVFP4_BF16>{});
+    else
+        f(std::integral_constant<int, NVFP4_F32>{});
+}
+
+} // namespace
+
+extern "C" {
+
+size_t nvfp4_global_scale_workspace_bytes(void) { return 256; }
+
+nvfp4_status_t nvfp4_global_scale(const void *x, int dtype, float *scale, int64_t rows, int64_t K, int64_t L,
+                                  int64_t row_stride, int64_t batch_stride, void *workspace,
+                                  size_t workspace_bytes, void *stream)
+{
+    if (!x || !scale)
+        return NVFP4_ERR_NULL_POINTER;
+    if (!known_type(dtype))
+        return NVFP4_ERR_INVALID_TYPE;
+    if (rows < 1 || K < 1 || L < 1 || rows > kMaxRows || L > kMaxRows || K > INT32_MAX / 2 || rows > kMaxRows / L ||
+        rows * L > (INT64_C(1) << 62) / K)
+        return NVFP4_ERR_INVALID_SHAPE;
+    if (!good_strides(rows, K, row_stride, batch_stride))
+        return NVFP4_ERR_INVALID_STRIDE;
+    const int64_t size = type_size(dtype);
+    if (!aligned(x, size) || !aligned(scale, 4))
+        return NVFP4_ERR_MISALIGNED;
+    if (!workspace || workspace_bytes < nvfp4_global_scale_workspace_bytes() || !aligned(workspace, 256))
+        return NVFP4_ERR_WORKSPACE;
+    const int64_t per_row = (K + 15) / 16, pieces = rows * L * per_row;
+    const int64_t grid = std::min<int64_t>(kAmaxMaxGrid, (pieces + kAmaxThreads - 1) / kAmaxThreads);
+    by_type(dtype, [&](auto dt) {
+        hipLaunchKernelGGL((nvfp4_global_scale_kernel<dt()>), dim3((uint32_t)grid), dim3(kAmaxThreads), 0,
+                           (hipStream_t)stream, (const uint8_t *)x, scale, (uint32_t *)workspace, pieces, K, rows,
+                           row_stride * size, batch_stride * size, (int32_t)per_row);
+    });
+    return finish();
+}
+
+nvfp4_status_t nvfp4_quantize(const void *x, int dtype, const float *global_scale, void *codes, void *scales,
+                              int64_t rows, int64_t K, int64_t L, int64_t row_stride, int64_t batch_stride,
+                              int sf_layout, void *stream)
+{
+    if (!x || !codes || !scales)
+        return NVFP4_ERR_NULL_POINTER;
+    if (!known_type(dtype))
+        return NVFP4_ERR_INVALID_TYPE;
+    if (nvfp4_blocked_scales_bytes(rows, K, L) == 0 || rows * L > (INT64_C(1) << 62) / K)
+        return NVFP4_ERR_INVALID_SHAPE;
+    if (sf_layout != NVFP4_SF_PLAIN && sf_layout != NVFP4_SF_BLOCKED)
+        return NVFP4_ERR_INVALID_LAYOUT;
+    if (!good_strides(rows, K, row_stride, batch_stride))
+        return NVFP4_ERR_INVALID_STRIDE;
+    const int64_t size = type_size(dtype);
+    const bool blocked = sf_layout == NVFP4_SF_BLOCKED;
+    if (!aligned(x, size) || !aligned(codes, 8) || (blocked && !aligned(scales, 4)) ||
+        (global_scale && !aligned(global_scale, 4)))
+        return NVFP4_ERR_MISALIGNED;
+    QParams p{};
+    p.rows = rows;
+    p.row_bytes = row_stride * size;
+    p.batch_bytes = batch_stride * size;
+    p.nkb = (int32_t)(K / 16);
+    int64_t grid;
+    if (blocked) {
+        const int64_t bands = (rows + 127) / 128 * 8, per = (p.nkb + 15) / 16;
+        if (bands > INT32_MAX || bands > kMaxGrid / per / L)
+            return NVFP4_ERR_INVALID_SHAPE;
+        p.bands = (int32_t)bands;
+        p.wg_per_band = (int32_t)per;
+        grid = L * bands * per;
+    } else {
+        const int64_t per = (rows * p.nkb + kQThreads - 1) / kQThreads;
+        if (per > kMaxGrid / L)
+            return NVFP4_ERR_INVALID_SHAPE;
+        p.wg_per_band = (int32_t)per;
+        grid = L * per;
+    }
+    by_type(dtype, [&](auto dt) {
+        auto go = [&](auto kern) {
+            hipLaunchKernelGGL(kern, dim3((uint32_t)grid), dim3(kQThreads), 0, (hipStream_t)stream,
+                               (const uint8_t *)x, global_scale, (uint8_t *)codes, (uint8_t *)scales, p);
+        };
+        blocked ? go(nvfp4_quantize_blocked_kernel<dt()>) : go(nvfp4_quantize_plain_kernel<dt()>);
+    });
+    return finish();
+}
+
+nvfp4_status_t nvfp4_dequantize(const void *codes, const void *scales, const float *global_scale, void *out,
+                                int dtype, int64_t rows, int64_t K, int64_t L, int sf_layout, void *stream)
+{
+    if (!codes || !scales || !out)
+        return NVFP4_ERR_NULL_POINTER;
+    if (!known_type(dtype))
+        return NVFP4_ERR_INVALID_TYPE;
+    if (nvfp4_blocked_scales_bytes(rows, K, L) == 0 || rows * L > (INT64_C(1) << 62) / K)
+        return NVFP4_ERR_INVALID_SHAPE;
+    if (sf_layout != NVFP4_SF_PLAIN && sf_layout != NVFP4_SF_BLOCKED)
+        return NVFP4_ERR_INVALID_LAYOUT;
+    if (!aligned(codes, 8) || !aligned(out, type_size(dtype)) || (global_scale && !aligned(global_scale, 4)))
+        return NVFP4_ERR_MISALIGNED;
+    const int64_t nkb = K / 16, blocks = L * rows * nkb;
+    const int64_t grid = (blocks + kQThreads - 1) / kQThreads;
+    if (grid > kMaxGrid)
+        return NVFP4_ERR_INVALID_SHAPE;
+    by_type(dtype, [&](auto dt) {
+        auto go = [&](auto kern) {
+            hipLaunchKernelGGL(kern, dim3((uint32_t)grid), dim3(kQThreads), 0, (hipStream_t)stream,
+                               (const uint8_t *)codes, (const uint8_t *)scales, global_scale, (uint8_t *)out, rows,
+                               blocks, (int32_t)nkb);
+        };
+        sf_layout == NVFP4_SF_BLOCKED ? go(nvfp4_dequantize_kernel<dt(), NVFP4_SF_BLOCKED>)
+                                      : go(nvfp4_dequantize_kernel<dt(), NVFP4_SF_PLAIN>);
+    });
+    return finish();
+}
+
+} // extern "C"

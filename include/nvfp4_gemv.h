@@ -1,5 +1,6 @@
 /*
- * nvfp4_gemv.h -- C ABI of the MI355X (gfx950) NVFP4 block-scaled batched GEMV.
+ * nvfp4_gemv.h -- C ABI of the MI355X (gfx950) NVFP4 block-scaled batched GEMV,
+ * and of the FP4 linear layers and routed experts around it (last part).
  *
  * Operation (kernelbot NVFP4 GEMV, submission 103289, `cute_kernel`: each k
  * contributes a * sfa * b * sfb, the contributions of one output row are
@@ -69,8 +70,17 @@ typedef enum {
     NVFP4_ERR_WORKSPACE = 5,        /* workspace missing, misaligned or too small  */
     NVFP4_ERR_HIP = 6,              /* a HIP call failed; see nvfp4_last_hip_error */
     NVFP4_ERR_INVALID_SCALE = 7,    /* the global scale alpha is NaN or infinite   */
-    NVFP4_ERR_INVALID_STRIDE = 8    /* an operand stride is out of range or misaligned */
+    NVFP4_ERR_INVALID_STRIDE = 8,   /* an operand stride is out of range or misaligned */
+    NVFP4_ERR_INVALID_TYPE = 9,     /* not an nvfp4_dtype_t                       */
+    NVFP4_ERR_INVALID_ROUTING = 10  /* a router option is out of range            */
 } nvfp4_status_t;
+
+/* Element types of activations, results and logits. */
+typedef enum {
+    NVFP4_F16 = 0,
+    NVFP4_BF16 = 1,
+    NVFP4_F32 = 2
+} nvfp4_dtype_t;
 
 /*
  * Batched GEMV as defined above. If the problem is split along K (small M*L),
@@ -293,6 +303,202 @@ nvfp4_status_t nvfp4_scales_to_blocked(const void *plain, void *blocked, int64_t
 
 /* Bytes of the blocked layout for (rows, K, L); 0 for an invalid shape. */
 size_t nvfp4_blocked_scales_bytes(int64_t rows, int64_t K, int64_t L);
+
+/*
+ * ---------------------------------------------------------------------------
+ * FP4 linear layers: activations to NVFP4, products with any number of rows,
+ * routed experts. Conventions as above (device pointers, nothing synchronised,
+ * nothing allocated, every argument validated before any HIP call). No call
+ * of this part keeps state between calls, so all may be captured into HIP
+ * graphs and run on several streams at once; a workspace belongs to one call
+ * at a time. Global scales are float32 values on the DEVICE, so that a layer
+ * runs from activations to result without the host.
+ *
+ * Workspaces of this part: device memory of at least the bytes that the
+ * matching _workspace_bytes function gives, 256-byte aligned, zero-filled
+ * before its first use. Every completed call leaves its counters zero, so one
+ * workspace serves any later call of this part without clearing, on one stream.
+ * A size of 0 means none is needed (NULL is then accepted).
+ */
+
+/*
+ * Global scale of a tensor for nvfp4_quantize: the largest block of x then
+ * gets the largest scale, E4M3's 448, and its largest value the largest code, 6:
+ *
+ *   *scale = max over finite x of |x|, times the float32 nearest to 1 / 2688
+ *            (one rounding to float32), at least 2^-100; 1 if every finite x is zero
+ *
+ *   x       dtype (nvfp4_dtype_t) [L][rows][K], strides in elements: row_stride
+ *           between rows (>= K, or anything >= 0 if rows == 1), batch_stride
+ *           between batches (>= 0); a value contiguous in k; aligned to its type
+ *   scale   float32, written
+ * NaN and infinite values are passed over. Requirements: rows, L >= 1; K >= 1.
+ */
+size_t nvfp4_global_scale_workspace_bytes(void);
+nvfp4_status_t nvfp4_global_scale(const void *x, int dtype, float *scale, int64_t rows, int64_t K,
+                                  int64_t L, int64_t row_stride, int64_t batch_stride,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Quantisation to NVFP4. Per row and block b of 16 consecutive k, with the
+ * global scale g = *global_scale (NULL: g = 1):
+ *
+ *   s[b]  = E4M3 nearest to  max_{k in b} |x[k]| / (6 g)   (at most 448)
+ *   q[k]  = E2M1 nearest to  x[k] / (s[b] g)               (at most 6 in size)
+ *
+ * Ties go to the even code. Both roundings are those of the exact quotients:
+ * no intermediate rounding decides a code. The sign of x[k] is kept (a value
+ * that rounds to zero keeps it too). s[b] = 0 gives codes of 0. A block with
+ * a NaN gets the scale code 0x7F (NaN), so that products with it are NaN; an
+ * infinite x[k] saturates to code 6 of its block, whose scale is then 448. A g
+ * that is not finite or below 2^-100 makes every scale 0x7F.
+ *
+ *   x       as for nvfp4_global_scale
+ *   codes   uint8 [L][rows][K/2], written (8-byte aligned)
+ *   scales  uint8, written in sf_layout: plain [L][rows][K/16]; blocked: the
+ *           128x4 layout, nvfp4_blocked_scales_bytes(rows, K, L) bytes, padding
+ *           written as 0 (4-byte aligned)
+ * The outputs are operands of nvfp4_gemv (rows = 1 or M), nvfp4_gemm_small_n
+ * and nvfp4_gemm: those want 16-byte aligned codes. Requirements: rows, L >= 1;
+ * K % 32 == 0; codes and scales do not overlap x.
+ */
+nvfp4_status_t nvfp4_quantize(const void *x, int dtype, const float *global_scale, void *codes,
+                              void *scales, int64_t rows, int64_t K, int64_t L, int64_t row_stride,
+                              int64_t batch_stride, int sf_layout, void *stream);
+
+/*
+ * The values that codes and scales stand for: out[l][r][k] = q * s * g, out
+ * of type dtype, dense [L][rows][K]. q * s is exact; the product with g is
+ * rounded to float32 and then to dtype (so at most half a step and 2^-24 off).
+ */
+nvfp4_status_t nvfp4_dequantize(const void *codes, const void *scales, const float *global_scale,
+                                void *out, int dtype, int64_t rows, int64_t K, int64_t L,
+                                int sf_layout, void *stream);
+
+/*
+ * Product of NVFP4 matrices with any number of rows N (prompts and batches;
+ * nvfp4_gemm_small_n's operation without its limit on N):
+ *
+ *   c[l][n][m] = alpha * ga * gb * sum_{k<K} e2m1(A[l][m][k]) * e4m3(SFA[l][m][k/16])
+ *                                          * e2m1(B[l][n][k]) * e4m3(SFB[l][n][k/16])
+ *
+ *   a, b, sfa, sfb, sf_layout  as for nvfp4_gemm_small_n, N >= 1
+ *   scale_a, scale_b           float32 on the device, ga and gb (NULL: 1)
+ *   c      dtype [L][N][M], written; aligned to its type
+ * Accumulation is float32 (the products are exact), one rounding of the scaled
+ * sum to float32 and one to dtype; float16 overflows to +-inf. The order of
+ * summation is fixed for a shape, so equal calls give equal bits.
+ * Requirements: M, N, L >= 1; K % 32 == 0; M, N <= 2^30; K <= 2^22; a, b, sfa
+ * and sfb 16-byte aligned; alpha finite.
+ */
+size_t nvfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t L);
+nvfp4_status_t nvfp4_gemm(const void *a, const void *b, const void *sfa, const void *sfb, void *c,
+                          int dtype, int64_t M, int64_t N, int64_t K, int64_t L, int sf_layout,
+                          float alpha, const float *scale_a, const float *scale_b, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* What nvfp4_gemm launches for a shape (for tests and reports): rows of A and
+ * of B per workgroup, slices of K, K-elements per slice, workgroups. */
+typedef struct {
+    int32_t tile_m, tile_n;
+    int32_t k_splits, k_per_split;
+    int64_t workgroups;
+} nvfp4_gemm_plan_t;
+
+nvfp4_status_t nvfp4_gemm_plan(int64_t M, int64_t N, int64_t K, int64_t L, nvfp4_gemm_plan_t *plan);
+
+/*
+ * Router of a mixture of experts: the k experts of each of T tokens, their
+ * weights, and the experts' lists that nvfp4_gemm_experts takes.
+ *
+ *   score[t][e]  softmax over e of logits[t] (NVFP4_SCORE_SOFTMAX) or
+ *                1 / (1 + exp(-logits[t][e])) (NVFP4_SCORE_SIGMOID)
+ *   pick[t][e]   score + bias[e] (bias NULL: score)
+ *   groups       the E experts form n_group runs of E / n_group; a group's
+ *                value is the sum of its group_top largest picks (of those not
+ *                masked); only experts of the topk_group groups of largest
+ *                value are left
+ *   ids[t][j]    the k left experts of largest pick, largest first
+ *   weights[t][j] score (without bias) of expert ids[t][j]; if renormalize,
+ *                divided by the token's sum of them; times scaling
+ *
+ * Scores and picks are compared in float64 (ties, also between groups, go to
+ * the lower index), weights are rounded once more to float32 at the end and are
+ * within a few float32 steps.
+ * A logit of -inf or NaN masks its expert: score 0, never picked; so does a
+ * bias of -inf or NaN, which leaves the scores as they are. Where fewer
+ * than k experts are left, the rest of ids is -1 with weight 0; a token whose
+ * mask leaves none gets only those. Logits of +inf share a softmax equally.
+ * If the sum of a token's scores is 0, renormalised weights are 0.
+ *
+ * The experts' lists hold the slots t * k + j with ids[t][j] >= 0, sorted by
+ * expert and then by slot:
+ *   offsets int32 [E + 1]   expert e's slots are order[offsets[e] .. offsets[e+1])
+ *   order   int32 [T * k]   entries from offsets[E] on are not written
+ *
+ *   logits dtype [T][E] dense, bias float32 [E], ids int32 [T][k], weights
+ *   float32 [T][k]; all aligned to their types.
+ * Requirements: T >= 1, T * k <= 2^30; 1 <= E <= 1024; 1 <= k <= min(E, 64);
+ * n_group divides E and is at most 64; 1 <= topk_group <= n_group; 1 <= group_top
+ * <= E / n_group, at most 2; scaling finite.
+ */
+typedef enum {
+    NVFP4_SCORE_SOFTMAX = 0,
+    NVFP4_SCORE_SIGMOID = 1
+} nvfp4_score_t;
+
+typedef struct {
+    int32_t score;          /* nvfp4_score_t */
+    int32_t n_group, topk_group, group_top;
+    int32_t renormalize;    /* 0 or 1 */
+    float scaling;
+} nvfp4_routing_t;
+
+size_t nvfp4_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t k);
+nvfp4_status_t nvfp4_moe_route(const void *logits, int dtype, const float *bias, int32_t *ids,
+                               float *weights, int32_t *offsets, int32_t *order, int64_t T,
+                               int64_t E, int64_t k, const nvfp4_routing_t *routing,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Products of routed rows with their experts' NVFP4 weights. Slot s has row
+ * s / slots_per_row of B (slots_per_row = k: the tokens' rows, each taken for
+ * k slots; 1: a row for each slot) and the expert e whose list holds s:
+ *
+ *   c[s][m] = alpha * ga[e] * gb * sum_{k<K} e2m1(A[e][m][k]) * e4m3(SFA[e][m][k/16])
+ *                * e2m1(B[s / slots_per_row][k]) * e4m3(SFB[s / slots_per_row][k/16])
+ *
+ *   a, sfa   the experts' weights: as nvfp4_gemm's with E batches
+ *   b, sfb   rows x K, one batch
+ *   offsets, order   as nvfp4_moe_route writes them (on the device): offsets
+ *            rise from 0 to at most S = rows * slots_per_row, and order's
+ *            entries are slots in [0, S), each once. Entries outside [0, S)
+ *            are passed over, offsets are clamped to 0..S: nothing is read or
+ *            written out of bounds whatever they hold.
+ *   scale_a  float32 [E] on the device (NULL: 1), scale_b float32 (NULL: 1)
+ *   c        dtype [S][M]; rows of slots in no list are not written
+ * Rounding, order of summation and requirements as for nvfp4_gemm; E <= 1024,
+ * rows, slots_per_row >= 1, S <= 2^30.
+ */
+size_t nvfp4_gemm_experts_workspace_bytes(int64_t M, int64_t K, int64_t E, int64_t S);
+nvfp4_status_t nvfp4_gemm_experts(const void *a, const void *b, const void *sfa, const void *sfb,
+                                  void *c, int dtype, int64_t M, int64_t K, int64_t E, int64_t rows,
+                                  int64_t slots_per_row, int sf_layout, const int32_t *offsets,
+                                  const int32_t *order, float alpha, const float *scale_a,
+                                  const float *scale_b, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
+/*
+ * Weighted sum of each token's slots:
+ *   out[t][m] = sum_j weights[t][j] * y[t * k + j][m]   over j with ids[t][j] >= 0
+ * in float32, j = 0, 1, .., rounded once to dtype; 0 for a token with no such
+ * j. Slots with a negative id are not read (their rows may hold anything).
+ *   y dtype [T * k][M], out dtype [T][M], ids int32 and weights float32 [T][k];
+ * all aligned to their types. Requirements: T, k, M >= 1; k <= 64; T * k <= 2^30;
+ * M <= 2^30.
+ */
+nvfp4_status_t nvfp4_moe_combine(const void *y, int dtype, const int32_t *ids, const float *weights,
+                                 void *out, int64_t T, int64_t k, int64_t M, void *stream);
 
 /* Static description of a status code (never NULL). */
 const char *nvfp4_status_string(int status);

@@ -1,0 +1,182 @@
+"""CPU checks of the FP4 linear layers' C ABI: every refusal comes before any HIP
+call, the binding checks types and sizes, plans and workspaces are consistent."""
+import ctypes
+
+import pytest
+
+import block_scaled_fp4_gemv_amd as g
+
+P = 0x100000        # fake, aligned device addresses (never dereferenced: every call here is refused)
+INF, NAN = float("inf"), float("nan")
+
+
+def quantize(x=P, dtype=1, gs=P, codes=P, scales=P, rows=4, K=64, L=1, rs=64, bs=256, lay=1):
+    return g.lib().nvfp4_quantize(x, dtype, gs, codes, scales, rows, K, L, rs, bs, lay, None)
+
+
+def global_scale(x=P, dtype=1, scale=P, rows=4, K=64, L=1, rs=64, bs=256, ws=P, n=256):
+    return g.lib().nvfp4_global_scale(x, dtype, scale, rows, K, L, rs, bs, ws, n, None)
+
+
+def dequantize(codes=P, scales=P, gs=P, out=P, dtype=1, rows=4, K=64, L=1, lay=1):
+    return g.lib().nvfp4_dequantize(codes, scales, gs, out, dtype, rows, K, L, lay, None)
+
+
+def gemm(a=P, b=P, sfa=P, sfb=P, c=P, dtype=1, M=64, N=64, K=64, L=1, lay=1, alpha=1.0, ga=P, gb=P, ws=None, n=0):
+    return g.lib().nvfp4_gemm(a, b, sfa, sfb, c, dtype, M, N, K, L, lay, alpha, ga, gb, ws, n, None)
+
+
+def experts(a=P, b=P, sfa=P, sfb=P, c=P, dtype=1, M=64, K=64, E=4, rows=8, per=2, lay=1, off=P, order=P, alpha=1.0,
+            ga=P, gb=P, ws=None, n=0):
+    return g.lib().nvfp4_gemm_experts(a, b, sfa, sfb, c, dtype, M, K, E, rows, per, lay, off, order, alpha, ga, gb, ws,
+                                      n, None)
+
+
+def route(logits=P, dtype=1, bias=P, ids=P, weights=P, off=P, order=P, T=4, E=8, k=2, score=0, n_group=1, topk_group=1,
+          group_top=1, renorm=1, scaling=1.0, ws=P, n=1 << 20, opts=True):
+    o = g.Routing(score, n_group, topk_group, group_top, renorm, scaling)
+    return g.lib().nvfp4_moe_route(logits, dtype, bias, ids, weights, off, order, T, E, k,
+                                   ctypes.byref(o) if opts else None, ws, n, None)
+
+
+def combine(y=P, dtype=1, ids=P, weights=P, out=P, T=4, k=2, M=64):
+    return g.lib().nvfp4_moe_combine(y, dtype, ids, weights, out, T, k, M, None)
+
+
+NULL, SHAPE, ALIGN, LAYOUT = (g.NVFP4_ERR_NULL_POINTER, g.NVFP4_ERR_INVALID_SHAPE, g.NVFP4_ERR_MISALIGNED,
+                              g.NVFP4_ERR_INVALID_LAYOUT)
+WORK, SCALE, STRIDE, TYPE, ROUTING = (g.NVFP4_ERR_WORKSPACE, g.NVFP4_ERR_INVALID_SCALE, g.NVFP4_ERR_INVALID_STRIDE,
+                                      g.NVFP4_ERR_INVALID_TYPE, g.NVFP4_ERR_INVALID_ROUTING)
+
+
+@pytest.mark.parametrize("call,bad,status", [
+    (quantize, dict(x=None), NULL), (quantize, dict(codes=None), NULL), (quantize, dict(scales=None), NULL),
+    (quantize, dict(dtype=3), TYPE), (quantize, dict(rows=0), SHAPE), (quantize, dict(K=48), SHAPE),
+    (quantize, dict(L=0), SHAPE), (quantize, dict(rows=-1), SHAPE), (quantize, dict(rows=2 ** 31), SHAPE),
+    (quantize, dict(lay=2), LAYOUT), (quantize, dict(rs=63), STRIDE), (quantize, dict(bs=-1), STRIDE),
+    (quantize, dict(rs=2 ** 40), STRIDE), (quantize, dict(x=P + 1), ALIGN), (quantize, dict(dtype=2, x=P + 2), ALIGN),
+    (quantize, dict(codes=P + 4), ALIGN), (quantize, dict(scales=P + 2), ALIGN), (quantize, dict(gs=P + 2), ALIGN),
+    (quantize, dict(rows=2 ** 29, K=2 ** 20, rs=2 ** 20), SHAPE),
+    (global_scale, dict(x=None), NULL), (global_scale, dict(scale=None), NULL), (global_scale, dict(ws=None), WORK),
+    (global_scale, dict(n=255), WORK), (global_scale, dict(ws=P + 8), WORK), (global_scale, dict(dtype=-1), TYPE),
+    (global_scale, dict(rows=0), SHAPE), (global_scale, dict(rows=2 ** 39, L=2 ** 39), SHAPE),
+    (global_scale, dict(rs=10), STRIDE), (global_scale, dict(scale=P + 2), ALIGN),
+    (dequantize, dict(codes=None), NULL), (dequantize, dict(out=None), NULL), (dequantize, dict(dtype=7), TYPE),
+    (dequantize, dict(K=16), SHAPE), (dequantize, dict(lay=-1), LAYOUT), (dequantize, dict(codes=P + 1), ALIGN),
+    (dequantize, dict(out=P + 1), ALIGN), (dequantize, dict(dtype=2, out=P + 2), ALIGN),
+    (gemm, dict(a=None), NULL), (gemm, dict(b=None), NULL), (gemm, dict(sfa=None), NULL), (gemm, dict(sfb=None), NULL),
+    (gemm, dict(c=None), NULL), (gemm, dict(dtype=9), TYPE), (gemm, dict(M=0), SHAPE), (gemm, dict(N=0), SHAPE),
+    (gemm, dict(K=33), SHAPE), (gemm, dict(K=2 ** 23), SHAPE), (gemm, dict(L=0), SHAPE), (gemm, dict(N=2 ** 31), SHAPE),
+    (gemm, dict(M=2 ** 30, N=2 ** 30), SHAPE), (gemm, dict(lay=5), LAYOUT), (gemm, dict(a=P + 8), ALIGN),
+    (gemm, dict(b=P + 8), ALIGN), (gemm, dict(sfa=P + 4), ALIGN), (gemm, dict(sfb=P + 4), ALIGN),
+    (gemm, dict(c=P + 1), ALIGN), (gemm, dict(dtype=2, c=P + 2), ALIGN), (gemm, dict(ga=P + 1), ALIGN),
+    (gemm, dict(alpha=NAN), SCALE), (gemm, dict(alpha=INF), SCALE),
+    (experts, dict(off=None), NULL), (experts, dict(order=None), NULL),
+    (experts, dict(a=None), NULL), (experts, dict(dtype=3), TYPE), (experts, dict(E=0), SHAPE),
+    (experts, dict(E=1025), SHAPE), (experts, dict(rows=0), SHAPE), (experts, dict(per=0), SHAPE),
+    (experts, dict(per=2 ** 31), SHAPE), (experts, dict(K=0), SHAPE), (experts, dict(off=P + 2), ALIGN),
+    (experts, dict(order=P + 1), ALIGN), (experts, dict(alpha=-INF), SCALE), (experts, dict(lay=3), LAYOUT),
+    (route, dict(logits=None), NULL), (route, dict(ids=None), NULL), (route, dict(opts=False), NULL),
+    (route, dict(dtype=3), TYPE), (route, dict(T=0), SHAPE), (route, dict(E=0), SHAPE), (route, dict(k=0), SHAPE),
+    (route, dict(k=9), SHAPE), (route, dict(E=1025), SHAPE), (route, dict(E=128, k=65), SHAPE),
+    (route, dict(T=2 ** 30), SHAPE), (route, dict(score=2), ROUTING), (route, dict(n_group=3), ROUTING),
+    (route, dict(n_group=0), ROUTING), (route, dict(n_group=4, topk_group=5), ROUTING),
+    (route, dict(topk_group=0), ROUTING), (route, dict(group_top=0), ROUTING), (route, dict(group_top=3), ROUTING),
+    (route, dict(n_group=8, topk_group=4, group_top=2), ROUTING), (route, dict(E=128, n_group=128), ROUTING),
+    (route, dict(renorm=2), ROUTING), (route, dict(scaling=NAN), SCALE), (route, dict(ids=P + 2), ALIGN),
+    (route, dict(logits=P + 1), ALIGN), (route, dict(bias=P + 2), ALIGN), (route, dict(ws=None), WORK),
+    (route, dict(n=8), WORK), (route, dict(ws=P + 16), WORK),
+    (combine, dict(y=None), NULL), (combine, dict(ids=None), NULL), (combine, dict(out=None), NULL),
+    (combine, dict(dtype=4), TYPE), (combine, dict(T=0), SHAPE), (combine, dict(k=0), SHAPE), (combine, dict(k=65), SHAPE),
+    (combine, dict(M=0), SHAPE), (combine, dict(T=2 ** 30), SHAPE), (combine, dict(M=2 ** 31), SHAPE),
+    (combine, dict(y=P + 1), ALIGN), (combine, dict(out=P + 1), ALIGN), (combine, dict(weights=P + 2), ALIGN),
+], ids=lambda v: v.__name__ if callable(v) else "-".join(map(str, v)) if isinstance(v, dict) else str(v))
+def test_refused(call, bad, status):
+    assert call(**bad) == status
+
+
+def test_products_that_split_k_want_a_workspace():
+    M, N, K = 128, 16, 16384
+    need = g.nvfp4_gemm_workspace_bytes(M, N, K, 1)
+    assert need > 0 and need % 256 == 0 and g.nvfp4_gemm_plan(M, N, K, 1)["k_splits"] > 1
+    assert gemm(M=M, N=N, K=K, ws=None, n=need) == WORK
+    assert gemm(M=M, N=N, K=K, ws=P, n=need - 1) == WORK
+    assert gemm(M=M, N=N, K=K, ws=P + 16, n=need) == WORK
+    need = g.nvfp4_gemm_experts_workspace_bytes(M, K, 4, 16)
+    assert need > 0
+    assert experts(M=M, K=K, rows=8, per=2, ws=None, n=need) == WORK
+    assert experts(M=M, K=K, rows=8, per=2, ws=P, n=need - 256) == WORK
+
+
+SHAPES = [(1, 1, 32, 1), (7168, 1, 16384, 1), (128, 16, 2048, 1), (7168, 16, 2048, 1), (1000, 33, 4096, 3),
+          (4096, 64, 7168, 8), (4096, 333, 7168, 1), (7168, 4096, 16384, 1), (127, 1000, 64, 1), (513, 129, 160, 2),
+          (8192, 4096, 16352, 2), (1, 4096, 16384, 1), (20000, 1, 32, 1), (64, 64, 1 << 22, 1), (1 << 20, 64, 64, 1)]
+
+
+@pytest.mark.parametrize("M,N,K,L", SHAPES)
+def test_plans_cover_the_shape(M, N, K, L):
+    p = g.nvfp4_gemm_plan(M, N, K, L)
+    tiles = g.cdiv(M, p["tile_m"]) * g.cdiv(N, p["tile_n"]) * L
+    assert p["workgroups"] == tiles * p["k_splits"]
+    assert p["k_per_split"] % 128 == 0 and 1 <= p["k_splits"] <= 16
+    assert (p["k_splits"] - 1) * p["k_per_split"] < K <= p["k_splits"] * p["k_per_split"]
+    need = g.nvfp4_gemm_workspace_bytes(M, N, K, L)
+    assert (need > 0) == (p["k_splits"] > 1)
+    if need:
+        assert tiles <= 16384 and 65536 + p["k_splits"] * L * N * M * 4 <= need <= 65536 + (64 << 20) + 256
+
+
+def test_workspace_bytes_of_bad_shapes_are_zero():
+    assert g.nvfp4_gemm_workspace_bytes(0, 16, 2048, 1) == 0
+    assert g.nvfp4_gemm_workspace_bytes(128, 16, 2047, 1) == 0
+    assert g.nvfp4_gemm_experts_workspace_bytes(128, 64, 2000, 16) == 0
+    assert g.nvfp4_moe_route_workspace_bytes(4, 8, 9) == 0
+    with pytest.raises(g.Nvfp4Error):
+        g.nvfp4_gemm_plan(128, 0, 64, 1)
+
+
+class Fake:
+    """A device tensor's face: dtype, size, contiguity."""
+    is_cuda = True
+
+    def __init__(self, n, dtype="torch.uint8", size=1):
+        self.n, self.dtype, self.size = n, dtype, size
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return P
+
+    def numel(self):
+        return self.n
+
+    def element_size(self):
+        return self.size
+
+
+def test_binding_checks_types_and_sizes():
+    u8, f32, i32 = Fake(1 << 20), Fake(1 << 20, "torch.float32", 4), Fake(1 << 20, "torch.int32", 4)
+    bf = Fake(1 << 20, "torch.bfloat16", 2)
+    with pytest.raises(ValueError, match="c holds"):
+        g.nvfp4_gemm(u8, u8, u8, u8, Fake(63 * 64, "torch.bfloat16", 2), 64, 64, 64, 1, "plain")
+    with pytest.raises(ValueError, match="sfb holds"):
+        g.nvfp4_gemm(u8, u8, u8, Fake(255), bf, 64, 64, 64, 1, "plain")
+    with pytest.raises(ValueError, match="none of float16"):
+        g.nvfp4_gemm(u8, u8, u8, u8, Fake(1 << 20, "torch.float64", 8), 64, 64, 64, 1, "plain")
+    with pytest.raises(ValueError, match="scale_a is"):
+        g.nvfp4_gemm(u8, u8, u8, u8, bf, 64, 64, 64, 1, "plain", scale_a=bf)
+    with pytest.raises(ValueError, match="need dtype"):
+        g.nvfp4_gemm(u8, u8, u8, u8, P, 64, 64, 64, 1, "plain")
+    with pytest.raises(ValueError, match="offsets holds"):
+        g.nvfp4_gemm_experts(u8, u8, u8, u8, bf, 64, 64, 4, 8, 2, "plain", Fake(4, "torch.int32", 4), i32)
+    with pytest.raises(ValueError, match="order is"):
+        g.nvfp4_gemm_experts(u8, u8, u8, u8, bf, 64, 64, 4, 8, 2, "plain", i32, f32)
+    with pytest.raises(ValueError, match="ids is"):
+        g.nvfp4_moe_combine(bf, f32, f32, bf, 4, 2, 64)
+    with pytest.raises(ValueError, match="different types"):
+        g.nvfp4_moe_combine(bf, i32, f32, f32, 4, 2, 64)
+    with pytest.raises(ValueError, match="weights holds"):
+        g.nvfp4_moe_route(f32, i32, Fake(7, "torch.float32", 4), i32, i32, 4, 8, 2, workspace=u8)
+    with pytest.raises(ValueError, match="codes holds"):
+        g.nvfp4_dequantize(Fake(10), u8, bf, 4, 64, 1, "plain")

@@ -254,10 +254,21 @@ def _ptr_and_bytes(x):
     return x.data_ptr(), x.numel() * x.element_size()
 
 
+_raw_stream = None
+
+
 def _stream_handle(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without a Stream object (2.8 us on the machine's CPU, this 0.2)
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            get, dev = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+            if get is None or dev is None:
+                return torch.cuda.current_stream().cuda_stream
+            torch.cuda.current_stream()                     # initialises torch's device state
+            _raw_stream = lambda: get(dev())  # noqa: E731
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -454,18 +465,31 @@ def _dtype_id(x, dtype):
     return known[0]
 
 
-def _need(**ops) -> None:
-    """name=((pointer, bytes held or None), bytes needed): raises where a tensor is too small."""
-    for name, ((_, held), need) in ops.items():
-        if held is not None and held < need:
-            raise ValueError(f"{name} holds {held} bytes, the shape needs {need}")
+def _op(x, need, name, dtype=None):
+    """Device pointer of a dense tensor that holds at least ``need`` bytes and,
+    where ``dtype`` is given, has that type; raw pointers and None pass."""
+    if x is None or isinstance(x, int):
+        return x
+    if not x.is_cuda:
+        raise ValueError("operands must be device tensors")
+    if not x.is_contiguous():
+        raise ValueError("operands must be contiguous")
+    if dtype is not None and str(x.dtype) != dtype:
+        raise ValueError(f"{name} is {x.dtype}, not {dtype.replace('torch.', '')}")
+    held = x.numel() * x.element_size()
+    if held < need:
+        raise ValueError(f"{name} holds {held} bytes, the shape needs {need}")
+    return x.data_ptr()
 
 
-def _typed(x, name, *dtypes):
-    """(pointer, bytes) of a tensor whose type has to be one of ``dtypes``."""
-    if x is not None and not isinstance(x, int) and str(x.dtype) not in dtypes:
-        raise ValueError(f"{name} is {x.dtype}, not {' or '.join(d.replace('torch.', '') for d in dtypes)}")
-    return _ptr_and_bytes(x)
+_F32, _I32 = "torch.float32", "torch.int32"
+
+
+def _workspace(x, nbytes):
+    """(pointer, bytes) of a workspace, its own size by default."""
+    if nbytes is None:
+        nbytes = 0 if x is None or isinstance(x, int) else x.numel() * x.element_size()
+    return _op(x, 0, "workspace"), nbytes
 
 
 def _strided(x, name, rows, K, L, row_stride, batch_stride):
@@ -505,10 +529,8 @@ def nvfp4_global_scale(x, scale, rows: int, K: int, L: int, workspace, workspace
                        stream=None) -> None:
     """Enqueue scale[0] = max finite |x| * (1 / 2688) (strides in elements; dense by default)."""
     px, rs, bs = _strided(x, "x", rows, K, L, row_stride, batch_stride)
-    sc, (pw, nw) = _typed(scale, "scale", "torch.float32"), _ptr_and_bytes(workspace)
-    _need(scale=(sc, 4))
-    _done(lib().nvfp4_global_scale(px, _dtype_id(x, dtype), sc[0], rows, K, L, rs, bs, pw,
-                                   (nw or 0) if workspace_bytes is None else workspace_bytes,
+    pw, nw = _workspace(workspace, workspace_bytes)
+    _done(lib().nvfp4_global_scale(px, _dtype_id(x, dtype), _op(scale, 4, "scale", _F32), rows, K, L, rs, bs, pw, nw,
                                    _stream_handle(stream)), "nvfp4_global_scale")
 
 
@@ -519,11 +541,10 @@ def nvfp4_quantize(x, codes, scales, rows: int, K: int, L: int, sf_layout, globa
     default) to NVFP4 codes and scales; global_scale: float32 on the device."""
     px, rs, bs = _strided(x, "x", rows, K, L, row_stride, batch_stride)
     lay = layout_id(sf_layout)
-    co, sc = _ptr_and_bytes(codes), _ptr_and_bytes(scales)
-    gs = _typed(global_scale, "global_scale", "torch.float32")
-    if min(rows, K, L) >= 1:
-        _need(codes=(co, L * rows * K // 2), scales=(sc, _scale_bytes(rows, K, L, lay)), global_scale=(gs, 4))
-    _done(lib().nvfp4_quantize(px, _dtype_id(x, dtype), gs[0], co[0], sc[0], rows, K, L, rs, bs, lay,
+    on = 1 if min(rows, K, L) >= 1 else 0                   # the library reports shape errors itself
+    _done(lib().nvfp4_quantize(px, _dtype_id(x, dtype), _op(global_scale, 4, "global_scale", _F32),
+                               _op(codes, on * L * rows * K // 2, "codes"),
+                               _op(scales, on * _scale_bytes(rows, K, L, lay), "scales"), rows, K, L, rs, bs, lay,
                                _stream_handle(stream)), "nvfp4_quantize")
 
 
@@ -531,13 +552,12 @@ def nvfp4_dequantize(codes, scales, out, rows: int, K: int, L: int, sf_layout, g
                      stream=None) -> None:
     """Enqueue out [L][rows][K] = the values that codes and scales stand for."""
     lay, dt = layout_id(sf_layout), _dtype_id(out, dtype)
-    co, sc, ou = _ptr_and_bytes(codes), _ptr_and_bytes(scales), _ptr_and_bytes(out)
-    gs = _typed(global_scale, "global_scale", "torch.float32")
-    if min(rows, K, L) >= 1:
-        _need(codes=(co, L * rows * K // 2), scales=(sc, _scale_bytes(rows, K, L, lay)),
-              out=(ou, L * rows * K * (4 if dt == NVFP4_F32 else 2)), global_scale=(gs, 4))
-    _done(lib().nvfp4_dequantize(co[0], sc[0], gs[0], ou[0], dt, rows, K, L, lay, _stream_handle(stream)),
-          "nvfp4_dequantize")
+    n = L * rows * K if min(rows, K, L) >= 1 else 0
+    _done(lib().nvfp4_dequantize(_op(codes, n // 2, "codes"),
+                                 _op(scales, _scale_bytes(rows, K, L, lay) if n else 0, "scales"),
+                                 _op(global_scale, 4, "global_scale", _F32),
+                                 _op(out, n * (4 if dt == NVFP4_F32 else 2), "out"), dt, rows, K, L, lay,
+                                 _stream_handle(stream)), "nvfp4_dequantize")
 
 
 def nvfp4_gemm_workspace_bytes(M: int, N: int, K: int, L: int) -> int:
@@ -556,16 +576,14 @@ def nvfp4_gemm(a, b, sfa, sfb, c, M: int, N: int, K: int, L: int, sf_layout, alp
     float16, bfloat16 or float32; scale_a, scale_b: float32 on the device; a
     (zero-initialised) workspace of nvfp4_gemm_workspace_bytes."""
     lay, dt = layout_id(sf_layout), _dtype_id(c, dtype)
-    oa, ob, osa, osb, oc = map(_ptr_and_bytes, (a, b, sfa, sfb, c))
-    ga, gb = _typed(scale_a, "scale_a", "torch.float32"), _typed(scale_b, "scale_b", "torch.float32")
-    pw, nw = _ptr_and_bytes(workspace)
-    if min(M, N, K, L) >= 1:
-        _need(a=(oa, L * M * K // 2), b=(ob, L * N * K // 2), sfa=(osa, _scale_bytes(M, K, L, lay)),
-              sfb=(osb, _scale_bytes(N, K, L, lay)), c=(oc, L * N * M * (4 if dt == NVFP4_F32 else 2)),
-              scale_a=(ga, 4), scale_b=(gb, 4))
-    _done(lib().nvfp4_gemm(oa[0], ob[0], osa[0], osb[0], oc[0], dt, M, N, K, L, lay, float(alpha), ga[0], gb[0], pw,
-                           (nw or 0) if workspace_bytes is None else workspace_bytes, _stream_handle(stream)),
-          "nvfp4_gemm")
+    pw, nw = _workspace(workspace, workspace_bytes)
+    on = 1 if min(M, N, K, L) >= 1 else 0
+    _done(lib().nvfp4_gemm(_op(a, on * L * M * K // 2, "a"), _op(b, on * L * N * K // 2, "b"),
+                           _op(sfa, on * _scale_bytes(M, K, L, lay), "sfa"),
+                           _op(sfb, on * _scale_bytes(N, K, L, lay), "sfb"),
+                           _op(c, on * L * N * M * (4 if dt == NVFP4_F32 else 2), "c"), dt, M, N, K, L, lay,
+                           alpha, _op(scale_a, 4, "scale_a", _F32), _op(scale_b, 4, "scale_b", _F32), pw, nw,
+                           _stream_handle(stream)), "nvfp4_gemm")
 
 
 def nvfp4_moe_route_workspace_bytes(T: int, E: int, k: int) -> int:
@@ -582,16 +600,15 @@ def nvfp4_moe_route(logits, ids, weights, offsets, order, T: int, E: int, k: int
     """Enqueue the routing of T tokens to k of E experts: ids and weights [T][k],
     and the experts' lists (offsets [E + 1], order [T * k])."""
     dt = _dtype_id(logits, dtype)
-    lo, (pw, nw) = _ptr_and_bytes(logits), _ptr_and_bytes(workspace)
-    bi, we = _typed(bias, "bias", "torch.float32"), _typed(weights, "weights", "torch.float32")
-    idt, off, orr = (_typed(x, n, "torch.int32") for x, n in ((ids, "ids"), (offsets, "offsets"), (order, "order")))
-    if min(T, E, k) >= 1:
-        _need(logits=(lo, T * E * (4 if dt == NVFP4_F32 else 2)), bias=(bi, 4 * E), ids=(idt, 4 * T * k),
-              weights=(we, 4 * T * k), offsets=(off, 4 * (E + 1)), order=(orr, 4 * T * k))
-    opts = Routing(_SCORES.get(score, score), n_group, topk_group, group_top, int(renormalize), float(scaling))
-    _done(lib().nvfp4_moe_route(lo[0], dt, bi[0], idt[0], we[0], off[0], orr[0], T, E, k, ctypes.byref(opts), pw,
-                                (nw or 0) if workspace_bytes is None else workspace_bytes, _stream_handle(stream)),
-          "nvfp4_moe_route")
+    pw, nw = _workspace(workspace, workspace_bytes)
+    on = 1 if min(T, E, k) >= 1 else 0
+    slots = on * 4 * T * k
+    opts = Routing(_SCORES.get(score, score), n_group, topk_group, group_top, int(renormalize), scaling)
+    _done(lib().nvfp4_moe_route(_op(logits, on * T * E * (4 if dt == NVFP4_F32 else 2), "logits"), dt,
+                                _op(bias, on * 4 * E, "bias", _F32), _op(ids, slots, "ids", _I32),
+                                _op(weights, slots, "weights", _F32), _op(offsets, on * 4 * (E + 1), "offsets", _I32),
+                                _op(order, slots, "order", _I32), T, E, k, ctypes.byref(opts), pw, nw,
+                                _stream_handle(stream)), "nvfp4_moe_route")
 
 
 def nvfp4_gemm_experts_workspace_bytes(M: int, K: int, E: int, S: int) -> int:
@@ -604,18 +621,16 @@ def nvfp4_gemm_experts(a, b, sfa, sfb, c, M: int, K: int, E: int, rows: int, slo
     """Enqueue c[s][m] for every slot s of the experts' lists: the row
     s // slots_per_row of b times the weights a[e] of the slot's expert e."""
     lay, dt = layout_id(sf_layout), _dtype_id(c, dtype)
-    oa, ob, osa, osb, oc = map(_ptr_and_bytes, (a, b, sfa, sfb, c))
-    ga, gb = _typed(scale_a, "scale_a", "torch.float32"), _typed(scale_b, "scale_b", "torch.float32")
-    off, orr = _typed(offsets, "offsets", "torch.int32"), _typed(order, "order", "torch.int32")
-    pw, nw = _ptr_and_bytes(workspace)
-    if min(M, K, E, rows, slots_per_row) >= 1:
-        S = rows * slots_per_row
-        _need(a=(oa, E * M * K // 2), b=(ob, rows * K // 2), sfa=(osa, _scale_bytes(M, K, E, lay)),
-              sfb=(osb, _scale_bytes(rows, K, 1, lay)), c=(oc, S * M * (4 if dt == NVFP4_F32 else 2)),
-              offsets=(off, 4 * (E + 1)), order=(orr, 4 * S), scale_a=(ga, 4 * E), scale_b=(gb, 4))
-    _done(lib().nvfp4_gemm_experts(oa[0], ob[0], osa[0], osb[0], oc[0], dt, M, K, E, rows, slots_per_row, lay, off[0],
-                                   orr[0], float(alpha), ga[0], gb[0], pw,
-                                   (nw or 0) if workspace_bytes is None else workspace_bytes, _stream_handle(stream)),
+    pw, nw = _workspace(workspace, workspace_bytes)
+    on = 1 if min(M, K, E, rows, slots_per_row) >= 1 else 0
+    S = on * rows * slots_per_row
+    _done(lib().nvfp4_gemm_experts(_op(a, on * E * M * K // 2, "a"), _op(b, on * rows * K // 2, "b"),
+                                   _op(sfa, on * _scale_bytes(M, K, E, lay), "sfa"),
+                                   _op(sfb, on * _scale_bytes(rows, K, 1, lay), "sfb"),
+                                   _op(c, S * M * (4 if dt == NVFP4_F32 else 2), "c"), dt, M, K, E, rows,
+                                   slots_per_row, lay, _op(offsets, on * 4 * (E + 1), "offsets", _I32),
+                                   _op(order, 4 * S, "order", _I32), alpha, _op(scale_a, on * 4 * E, "scale_a", _F32),
+                                   _op(scale_b, 4, "scale_b", _F32), pw, nw, _stream_handle(stream)),
           "nvfp4_gemm_experts")
 
 
@@ -624,13 +639,11 @@ def nvfp4_moe_combine(y, ids, weights, out, T: int, k: int, M: int, dtype=None, 
     dt = _dtype_id(y, dtype)
     if dt != _dtype_id(out, dtype):
         raise ValueError("y and out have different types")
-    size = 4 if dt == NVFP4_F32 else 2
-    oy, oo = _ptr_and_bytes(y), _ptr_and_bytes(out)
-    idt, we = _typed(ids, "ids", "torch.int32"), _typed(weights, "weights", "torch.float32")
-    if min(T, k, M) >= 1:
-        _need(y=(oy, T * k * M * size), ids=(idt, 4 * T * k), weights=(we, 4 * T * k), out=(oo, T * M * size))
-    _done(lib().nvfp4_moe_combine(oy[0], dt, idt[0], we[0], oo[0], T, k, M, _stream_handle(stream)),
-          "nvfp4_moe_combine")
+    n = T * M * (4 if dt == NVFP4_F32 else 2) if min(T, k, M) >= 1 else 0
+    slots = 4 * T * k if n else 0
+    _done(lib().nvfp4_moe_combine(_op(y, k * n, "y"), dt, _op(ids, slots, "ids", _I32),
+                                  _op(weights, slots, "weights", _F32), _op(out, n, "out"), T, k, M,
+                                  _stream_handle(stream)), "nvfp4_moe_combine")
 
 
 def nvfp4_status_string(status: int) -> str:

@@ -9,25 +9,29 @@
 // The FP4 matrix instruction cannot apply an E4M3 scale per 16: its block
 // scales are powers of two per 32.
 //
-// Kernel. A workgroup of 4 waves owns a tile of BM rows of A by BN rows of B
-// and walks K in stages of 128. A stage's packed codes and scale words go
-// straight from global memory into LDS (copies that need no register), in a
-// ring of NS stages; each wave reads the packed codes from LDS and decodes its
-// own fragments (one conversion and one packed multiply per two values), so LDS
-// holds and moves 4 bits per value, not 16.
+// Common to both kernels. Packed codes and scale words (4 scales: 64 k of one
+// row) go straight from global memory into a ring of LDS stages, by copies that
+// need no register; a stage is 128 k. Waves read the packed codes and decode
+// their own fragments (one conversion and one packed multiply per two values),
+// so LDS holds and moves 4 bits per value, not 16.
+//   MFMA 32x32x16: lane i holds row i % 32; lanes 0..31 take a stage's first 64
+// k, lanes 32..63 the other 64 (the order of k inside a stage is free as long
+// as A and B agree). Rows of B are the instruction's rows, rows of A its
+// columns, so a lane's results are neighbours in m of its neighbours'.
 //   LDS rows are 64 bytes (128 codes). 16-byte piece c of row r lies at piece
 // c ^ ((r / 4) % 4): any 16 consecutive rows' pieces c fall on all banks.
-//   Scale words (4 scales: 64 k of one row) lie as in the 128x4 blocked layout,
-// word (r, half) at half * tile + (r % 32) * 16 + (r / 32) * 4, so one read
-// gives a lane the words of its row in up to four 32-row fragments. Blocked or
-// plain, rows in order or gathered: the address of each word is computed once
-// per workgroup and steps by a constant.
-//   MFMA 32x32x16: lane i holds row i % 32; lanes 0..31 take the stage's first
-// 64 k, lanes 32..63 the other 64 (the order of k inside a stage is free as
-// long as A and B agree). Rows of B are the instruction's rows, rows of A its
-// columns, so that a lane's results are neighbours in m of its neighbours'.
+//   Scale words lie as in the 128x4 blocked layout, word (r, half) at half * tile
+// + (r % 32) * 16 + (r / 32) * 4, so one read gives a lane the words of its row
+// in up to four 32-row fragments. Blocked or plain, rows in order or gathered:
+// the address of each word is computed once and steps by a constant. Plain
+// rows of K % 64 = 32 are 2-byte aligned: their words are copied in halves.
 //   K can be split over workgroups: float32 partial sums in the workspace, the
 // last workgroup of a tile (by ticket) adds them in the order of the slices.
+//
+// Wide kernel (many rows of B): 4 waves share a tile's stages, one barrier per
+// stage. Wave kernel (few rows of B: bound by the weights' bytes): each wave
+// has a ring of its own and takes every KW-th stage, no barrier in the loop; the
+// waves' sums are added in LDS in the order of the waves.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -44,8 +48,10 @@ namespace {
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float16_t __attribute__((ext_vector_type(16)));
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;                   // wide kernel
 constexpr int kWaves = 4;
+constexpr int kLdsBytes = 160 * 1024;           // LDS of a CU
+constexpr int kStaticLds = 2048;                // slot table and ticket, at most
 constexpr int kStageK = 128;                    // k per stage
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTickets = 16384;              // tiles of a split product
@@ -54,22 +60,25 @@ constexpr int64_t kMaxPartialBytes = INT64_C(64) << 20;
 constexpr int kMaxSplits = 16;
 constexpr int64_t kMaxGrid = 0xFFFFFF;          // workgroups of 256 threads in 2^32 work items
 
-// what copies of k past the end read instead
-__device__ const uint4_t g_zeros[4] = {};
-
 // ------------------------------------------------------------------ copies to LDS
 
-// 16 or 4 bytes per lane from global memory into LDS at dst + lane * 16 (lane
-// * 4). The compiler does not count them: the kernel waits for them itself.
+// 16, 4 or 2 bytes per lane from base + off into LDS at dst + lane * 16 (lane *
+// 4; 2 bytes land in the low half of a dword). The base is uniform and steps
+// along K in scalar registers, the lane's offset stays. The compiler does not
+// count the copies: the kernels wait for them themselves.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-__device__ __attribute__((always_inline)) inline void copy16(const void *src, uint32_t dst)
+__device__ __attribute__((always_inline)) inline void copy16(const uint8_t *base, uint32_t off, uint32_t dst)
 {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "s"(dst) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "s"(dst) : "memory", "m0");
 }
-__device__ __attribute__((always_inline)) inline void copy4(const void *src, uint32_t dst)
+__device__ __attribute__((always_inline)) inline void copy4(const uint8_t *base, uint32_t off, uint32_t dst)
 {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" : : "v"(src), "s"(dst) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(base), "s"(dst) : "memory", "m0");
+}
+__device__ __attribute__((always_inline)) inline void copy2(const uint8_t *base, uint32_t off, uint32_t dst)
+{
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_ushort %0, %1" : : "v"(off), "s"(base), "s"(dst) : "memory", "m0");
 }
 #pragma clang diagnostic pop
 
@@ -147,53 +156,70 @@ __device__ __attribute__((always_inline)) inline void read_words(const uint8_t *
     }
 }
 
-// ------------------------------------------------------------------ the kernel
+// words of FM fragments from LDS: whole, or in halves `hi` bytes apart
+template <int FM, bool ODD>
+__device__ __attribute__((always_inline)) inline void load_words(const uint8_t *p, uint32_t hi, uint32_t (&w)[FM])
+{
+    read_words<FM>(p, w);
+    if constexpr (ODD) {
+        uint32_t h[FM];
+        read_words<FM>(p + hi, h);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            w[i] = (w[i] & 0xFFFFu) | (h[i] << 16);
+    }
+}
 
-// FM x FN fragments of 32 x 32 per wave, WM x WN waves, NS stages in the ring.
-template <int FM, int FN, int WM, int WN, int NS>
-struct Tile {
-    static_assert(WM * WN == kWaves);
-    static constexpr int kFM = FM, kFN = FN, kWM = WM, kWN = WN, kNS = NS;
-    static constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
-    // words per line of a scale tile: 32-row groups that share a line
-    static constexpr int LA = BM >= 128 ? 4 : BM / 32, LB = BN >= 128 ? 4 : BN / 32;
-    static constexpr int kCodesA = BM * 64, kCodesB = BN * 64;
-    static constexpr int kStage = kCodesA + kCodesB + BM * 8 + BN * 8;
-    static constexpr int kOffB = kCodesA, kOffSA = kCodesA + kCodesB, kOffSB = kOffSA + BM * 8;
-    // wave copies per stage: codes in 1 KiB, scale words in 256 bytes
-    static constexpr int TA = kCodesA / 1024, TB = kCodesB / 1024, TSA = BM * 8 / 256, TSB = BN * 8 / 256;
-    static constexpr int kLds = NS * kStage;
-    static_assert(TA % kWaves == 0 && TSA % kWaves == 0);
-    static_assert(TB % kWaves == 0 || TB < kWaves);
-    static_assert(TSB % kWaves == 0 || TSB < kWaves);
-    // copies that every wave makes, and those of some waves: B's codes by the
-    // first TB waves, B's words by the last TSB
-    static constexpr int kBase = TA / kWaves + TB / kWaves + TSA / kWaves + TSB / kWaves;
-    static_assert((TB % kWaves) + (TSB % kWaves) <= kWaves, "at most one more copy per wave");
+// The word's scales that lie before K's end; `left`: k from the word's first to the end.
+__device__ __attribute__((always_inline)) inline uint32_t word_mask(int left)
+{
+    return left >= 64 ? ~0u : left == 32 ? 0xFFFFu : 0u;
+}
+
+// Copies one 64-lane group of scale words. A word past K's end is replaced by
+// the stage's first of the same row (`back` bytes before), its upper half by its
+// lower: nothing past a row is read, and the reader masks what it gets.
+template <bool ODD>
+__device__ __attribute__((always_inline)) inline void copy_words(const uint8_t *base, uint32_t off, int left,
+                                                                 uint32_t back, uint32_t dst, uint32_t hi)
+{
+    off -= left <= 0 ? back : 0u;
+    if constexpr (ODD) {
+        copy2(base, off, dst);
+        copy2(base, off + (left == 32 || left == -32 ? 0u : 2u), dst + hi);
+    } else {
+        copy4(base, off, dst);
+    }
+}
+
+// A row range's part of an operand: codes and scale words from its first row on.
+struct Source {
+    const uint8_t *codes, *words;
 };
 
-template <class T, bool EXPERTS, bool REGS>
-__global__ __launch_bounds__(kThreads, 1) void nvfp4_gemm_kernel(GemmParams p)
-{
-    constexpr int FM = T::kFM, FN = T::kFN, NS = T::kNS, BM = T::BM, BN = T::BN;
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    __shared__ int32_t s_slot[EXPERTS ? BN : 1];
-    __shared__ uint32_t s_ticket;
-    const int lane = threadIdx.x % 64;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int nkb = p.K / 16;
+// ------------------------------------------------------------------ which tile
 
-    // --- which tile
+struct Where {
+    int l, m0, n0, count;                       // batch or expert (-1: none), first rows, rows of B
+    uint32_t tile;
+    int split;
+};
+
+template <bool EXPERTS, int BM, int BN, int THREADS>
+__device__ __attribute__((always_inline)) inline Where locate(const GemmParams &p, int32_t *s_slot)
+{
+    const int lane = threadIdx.x % 64;
+    Where w;
     uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
-    const int split = (int)(id % (uint32_t)p.splits);
+    w.split = (int)(id % (uint32_t)p.splits);
     id /= (uint32_t)p.splits;
-    const uint32_t tile = id;
-    int l = 0, m0, n0, count;                   // batch or expert, first rows, rows of B in the tile
+    w.tile = id;
     if constexpr (EXPERTS) {
-        m0 = (int)(id % (uint32_t)p.tiles_m) * BM;
+        w.m0 = (int)(id % (uint32_t)p.tiles_m) * BM;
         int want = (int)(id / (uint32_t)p.tiles_m);
         // the expert whose list holds tile `want` of all lists' tiles: 64 experts at a time
         int found = -1;
+        w.n0 = w.count = 0;
         for (int e0 = 0; e0 < p.L; e0 += 64) {
             const int e = e0 + lane;
             int from = 0, n = 0;
@@ -213,152 +239,259 @@ __global__ __launch_bounds__(kThreads, 1) void nvfp4_gemm_kernel(GemmParams p)
                 const int src = __ffsll((unsigned long long)past) - 1;
                 const int in_list = want - (__shfl(upto, src) - __shfl(tiles, src));
                 found = e0 + src;
-                n0 = __shfl(from, src) + in_list * BN;
-                count = min(BN, __shfl(n, src) - in_list * BN);
+                w.n0 = __shfl(from, src) + in_list * BN;
+                w.count = min(BN, __shfl(n, src) - in_list * BN);
                 break;
             }
             want -= __shfl(upto, 63);
         }
-        if (found < 0)
-            return;                             // past the last tile (the whole workgroup)
-        l = __builtin_amdgcn_readfirstlane(found);
-        n0 = __builtin_amdgcn_readfirstlane(n0);
-        count = __builtin_amdgcn_readfirstlane(count);
-        for (int i = threadIdx.x; i < BN; i += kThreads) {
-            const int s = i < count ? p.order[n0 + i] : -1;
+        w.l = __builtin_amdgcn_readfirstlane(found);
+        w.n0 = __builtin_amdgcn_readfirstlane(w.n0);
+        w.count = __builtin_amdgcn_readfirstlane(w.count);
+        if (w.l < 0)
+            return w;                           // past the last tile (the whole workgroup)
+        for (int i = threadIdx.x; i < BN; i += THREADS) {
+            const int s = i < w.count ? p.order[w.n0 + i] : -1;
             s_slot[i] = s >= 0 && s < p.N ? s : -1;
         }
         __syncthreads();
     } else {
         // bands of 8 tiles along n, so that one XCD's tiles share rows of both
         const uint32_t per = (uint32_t)p.tiles_m * (uint32_t)p.tiles_n;
-        l = (int)(id / per);
+        w.l = (int)(id / per);
         id %= per;
         const uint32_t band = id / ((uint32_t)p.tiles_m * 8u);
         id -= band * (uint32_t)p.tiles_m * 8u;
         const uint32_t wide = min(8u, (uint32_t)p.tiles_n - band * 8u);
-        m0 = (int)(id / wide) * BM;
-        n0 = (int)(band * 8u + id % wide) * BN;
-        count = min(BN, p.N - n0);
+        w.m0 = (int)(id / wide) * BM;
+        w.n0 = (int)(band * 8u + id % wide) * BN;
+        w.count = min(BN, p.N - w.n0);
     }
-    const uint8_t *A = p.a + (int64_t)l * p.M * (p.K / 2), *SA = p.sfa + l * p.sfa_batch;
-    const uint8_t *B = p.b, *SB = p.sfb;
-    if constexpr (!EXPERTS) {
-        B += (int64_t)l * p.N * (p.K / 2);
-        SB += l * p.sfb_batch;
-    }
-    auto row_b = [&](int i) -> int {            // row of B of the tile's row i (a valid one for any i)
-        if constexpr (EXPERTS)
-            return max(s_slot[i], 0) / p.slots_per_row;
-        else
-            return min(n0 + i, p.N - 1);
-    };
+    return w;
+}
 
-    // --- this wave's copies: source addresses of the first stage
-    const int first = split * p.stages_per_split;
+// Operand A from the tile's first 128-row block on (rows of codes from m0 on).
+__device__ __attribute__((always_inline)) inline Source source_a(const GemmParams &p, const Where &w)
+{
+    const int64_t words = p.blocked ? (int64_t)(w.m0 / 128) * ((p.K / 16 + 3) / 4) * 512 : (int64_t)w.m0 * (p.K / 16);
+    return {p.a + ((int64_t)w.l * p.M + w.m0) * (p.K / 2), p.sfa + w.l * p.sfa_batch + words};
+}
+// Offsets of the tile's row i (any i below BM; rows past M are row M - 1) in source_a.
+__device__ __attribute__((always_inline)) inline uint32_t codes_at_a(const GemmParams &p, const Where &w, int i)
+{
+    return (uint32_t)min(i, p.M - 1 - w.m0) * (uint32_t)(p.K / 2);
+}
+__device__ __attribute__((always_inline)) inline uint32_t words_at_a(const GemmParams &p, const Where &w, int i, int half)
+{
+    const int r = min(i, p.M - 1 - w.m0) + (p.blocked ? w.m0 % 128 : 0);
+    return (uint32_t)scale_word_at(p.blocked, r, half, p.K / 16);
+}
+
+// Operand B: dense from the tile's first row on; experts' rows are gathered
+// from all of it (at most 2^32 bytes, the entry point checks).
+template <bool EXPERTS>
+__device__ __attribute__((always_inline)) inline Source source_b(const GemmParams &p, const Where &w)
+{
+    if constexpr (EXPERTS)
+        return {p.b, p.sfb};
+    const int64_t words = p.blocked ? (int64_t)(w.n0 / 128) * ((p.K / 16 + 3) / 4) * 512 : (int64_t)w.n0 * (p.K / 16);
+    return {p.b + ((int64_t)w.l * p.N + w.n0) * (p.K / 2), p.sfb + w.l * p.sfb_batch + words};
+}
+template <bool EXPERTS>
+__device__ __attribute__((always_inline)) inline uint32_t codes_at_b(const GemmParams &p, const Where &w,
+                                                                     const int32_t *s_slot, int i)
+{
+    if constexpr (EXPERTS)
+        return (uint32_t)(max(s_slot[i], 0) / p.slots_per_row) * (uint32_t)(p.K / 2);
+    return (uint32_t)min(i, w.count - 1) * (uint32_t)(p.K / 2);
+}
+template <bool EXPERTS>
+__device__ __attribute__((always_inline)) inline uint32_t words_at_b(const GemmParams &p, const Where &w,
+                                                                     const int32_t *s_slot, int i, int half)
+{
+    if constexpr (EXPERTS)
+        return (uint32_t)scale_word_at(p.blocked, max(s_slot[i], 0) / p.slots_per_row, half, p.K / 16);
+    return (uint32_t)scale_word_at(p.blocked, min(i, w.count - 1) + (p.blocked ? w.n0 % 128 : 0), half, p.K / 16);
+}
+
+template <bool EXPERTS>
+__device__ __attribute__((always_inline)) inline float total_scale(const GemmParams &p, int l)
+{
+    float scale = p.alpha;
+    if (p.scale_a)
+        scale *= p.scale_a[EXPERTS ? l : 0];
+    if (p.scale_b)
+        scale *= *p.scale_b;
+    return scale;
+}
+
+// Offset in c (and in a slice of partial sums) of the tile's row n, -1: not stored.
+template <bool EXPERTS>
+__device__ __attribute__((always_inline)) inline int64_t row_at(const GemmParams &p, const Where &w,
+                                                                const int32_t *s_slot, int n)
+{
+    if (n >= w.count)
+        return -1;
+    if constexpr (EXPERTS)
+        return s_slot[n] < 0 ? -1 : (int64_t)s_slot[n] * p.M;
+    else
+        return ((int64_t)w.l * p.N + w.n0 + n) * p.M;
+}
+
+// Takes the tile's ticket after this workgroup's partial sums; true for the
+// last of the tile's workgroups. All threads call it.
+__device__ __attribute__((always_inline)) inline bool last_of_tile(const GemmParams &p, uint32_t tile,
+                                                                   uint32_t *s_ticket)
+{
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");          // this wave's partial sums are out
+    barrier();
+    if (threadIdx.x == 0)
+        *s_ticket = __hip_atomic_fetch_add(&p.tickets[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (*s_ticket != (uint32_t)p.splits - 1)
+        return false;
+    if (threadIdx.x == 0)
+        __hip_atomic_store(&p.tickets[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return true;
+}
+
+// Sums of R values over the slices, in order: 4 slices' loads in flight.
+template <int R>
+__device__ __attribute__((always_inline)) inline void add_slices(const GemmParams &p, int64_t one,
+                                                                 const int64_t (&at)[R], float (&sum)[R])
+{
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        sum[r] = 0.0f;
+    for (int s0 = 0; s0 < p.splits; s0 += 4) {
+        float v[4][R];
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                v[s][r] = s0 + s < p.splits && at[r] >= 0
+                              ? __hip_atomic_load(&p.partials[(s0 + s) * one + at[r]], __ATOMIC_RELAXED,
+                                                  __HIP_MEMORY_SCOPE_AGENT)
+                              : 0.0f;
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                sum[r] += v[s][r];
+    }
+}
+
+// ------------------------------------------------------------------ wide kernel
+
+// FM x FN fragments of 32 x 32 per wave, WM x WN waves, NS stages in the ring,
+// registers for PER_CU workgroups per CU.
+template <int FM, int FN, int WM, int WN, int NS, int PER_CU>
+struct Tile {
+    static_assert(WM * WN == kWaves && NS >= 3);
+    static constexpr int kFM = FM, kFN = FN, kWM = WM, kWN = WN, kNS = NS, kPerCu = PER_CU;
+    static constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
+    // words per line of a scale tile: 32-row groups that share a line
+    static constexpr int LA = BM >= 128 ? 4 : BM / 32, LB = BN >= 128 ? 4 : BN / 32;
+    static constexpr int kCodesA = BM * 64, kCodesB = BN * 64;
+    static constexpr int kOffB = kCodesA, kOffSA = kCodesA + kCodesB;
+    // wave copies per stage: codes in 1 KiB, scale words in 256 bytes
+    static constexpr int TA = kCodesA / 1024, TB = kCodesB / 1024, TSA = BM * 8 / 256, TSB = BN * 8 / 256;
+    static_assert(TA % kWaves == 0 && TB % kWaves == 0 && TSA % kWaves == 0);
+    static_assert(TSB % kWaves == 0 || TSB < kWaves);
+    static constexpr int stage_bytes(bool odd) { return kOffSA + (BM + BN) * (odd ? 16 : 8); }
+    // one stage fewer where the halves of the words leave no room for NS
+    static constexpr int ring(bool odd) { return NS * stage_bytes(odd) + kStaticLds <= kLdsBytes ? NS : NS - 1; }
+    static constexpr int lds_bytes(bool odd) { return ring(odd) * stage_bytes(odd); }
+    static_assert(ring(true) >= 3 && lds_bytes(true) + kStaticLds <= kLdsBytes && ring(false) == NS);
+};
+
+template <class T, bool EXPERTS, bool ODD>
+__global__ __launch_bounds__(kThreads, T::kPerCu) void nvfp4_gemm_wide_kernel(GemmParams p)
+{
+    constexpr int FM = T::kFM, FN = T::kFN, NS = T::ring(ODD), BM = T::BM, BN = T::BN, F = FM + FN;
+    constexpr int kStage = T::stage_bytes(ODD), kWordsA = BM * 8, kWordsB = BN * 8;
+    constexpr int kOffSB = T::kOffSA + kWordsA * (ODD ? 2 : 1);
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    __shared__ int32_t s_slot[EXPERTS ? BN : 1];
+    __shared__ uint32_t s_ticket;
+    const int lane = threadIdx.x % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const Where w = locate<EXPERTS, BM, BN, kThreads>(p, s_slot);
+    if (EXPERTS && w.l < 0)
+        return;
+
+    // --- this wave's copies
+    const int first = w.split * p.stages_per_split;
     const int stages = min(p.stages_per_split, p.stages - first);
-    constexpr int CA = T::TA / kWaves, CB = (T::TB + kWaves - 1) / kWaves;
+    constexpr int CA = T::TA / kWaves, CB = T::TB / kWaves;
     constexpr int CSA = T::TSA / kWaves, CSB = (T::TSB + kWaves - 1) / kWaves;
-    const bool has_b = T::TB % kWaves == 0 || wave < T::TB;
-    const int wave_sb = T::TSB % kWaves == 0 ? wave : wave - (kWaves - T::TSB);      // B's words: the last waves
-    const bool has_sb = wave_sb >= 0;
-    const uint8_t *pa[CA], *pb[CB], *psa[CSA], *psb[CSB];
+    // where B's words are fewer than a copy per wave, the first TSB waves make them
+    const bool has_sb = T::TSB % kWaves == 0 || wave < T::TSB;
+    const uint32_t step_words = p.blocked ? 1024 : 8, back_words = p.blocked ? 512 : 4;
+    Source a = source_a(p, w), b = source_b<EXPERTS>(p, w);
+    a.codes += (int64_t)first * 64, b.codes += (int64_t)first * 64;
+    a.words += (int64_t)first * step_words, b.words += (int64_t)first * step_words;
+    uint32_t oa[CA], ob[CB], osa[CSA], osb[CSB];
+    int half_a[CSA], half_b[CSB];
     // lane's 16 bytes of a 1 KiB copy: row lane / 4 of 16, piece swizzled back
     const int piece = (lane % 4) ^ ((lane / 16) % 4);
 #pragma unroll
-    for (int i = 0; i < CA; ++i) {
-        const int r = (wave + kWaves * i) * 16 + lane / 4;
-        pa[i] = A + (int64_t)min(m0 + r, p.M - 1) * (p.K / 2) + (int64_t)first * 64 + piece * 16;
-    }
+    for (int i = 0; i < CA; ++i)
+        oa[i] = codes_at_a(p, w, (wave + kWaves * i) * 16 + lane / 4) + piece * 16;
 #pragma unroll
-    for (int i = 0; i < CB; ++i) {
-        const int r = has_b ? (wave + kWaves * i) * 16 + lane / 4 : 0;
-        pb[i] = B + (int64_t)row_b(r) * (p.K / 2) + (int64_t)first * 64 + piece * 16;
-    }
-    // word w of a stage's scale words: block of 32 * LW rows, half, line, word
-    auto word_row = [](int w, int LW) { return w / (LW * 64) * (LW * 32) + (w % LW) * 32 + (w / LW) % 32; };
-    auto word_half = [](int w, int LW) { return (w / (LW * 32)) % 2; };
-    const int64_t step_words = p.blocked ? 1024 : 8;
-    const int my_half_a = word_half(wave * 64 + lane, T::LA);
-    const int my_half_b = word_half(max(wave_sb, 0) * 64 + lane, T::LB);
+    for (int i = 0; i < CB; ++i)
+        ob[i] = codes_at_b<EXPERTS>(p, w, s_slot, (wave + kWaves * i) * 16 + lane / 4) + piece * 16;
+    // word v of a stage's scale words: block of 32 * LW rows, half, line, word
+    auto word_row = [](int v, int LW) { return v / (LW * 64) * (LW * 32) + (v % LW) * 32 + (v / LW) % 32; };
+    auto word_half = [](int v, int LW) { return (v / (LW * 32)) % 2; };
 #pragma unroll
     for (int i = 0; i < CSA; ++i) {
-        const int w = (wave + kWaves * i) * 64 + lane;
-        psa[i] = SA + scale_word_at(p.blocked, min(m0 + word_row(w, T::LA), p.M - 1), my_half_a, nkb) + first * step_words;
+        const int v = (wave + kWaves * i) * 64 + lane;
+        half_a[i] = word_half(v, T::LA);
+        osa[i] = words_at_a(p, w, word_row(v, T::LA), half_a[i]);
     }
 #pragma unroll
     for (int i = 0; i < CSB; ++i) {
-        const int w = (max(wave_sb, 0) + kWaves * i) * 64 + lane;
-        psb[i] = SB + scale_word_at(p.blocked, row_b(word_row(w, T::LB)), my_half_b, nkb) + first * step_words;
+        const int v = has_sb ? (wave + kWaves * i) * 64 + lane : 0;
+        half_b[i] = word_half(v, T::LB);
+        osb[i] = words_at_b<EXPERTS>(p, w, s_slot, word_row(v, T::LB), half_b[i]);
     }
     const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
 
-    uint32_t regs_a[CSA], regs_b[CSB];
-    // issues the copies of stage `st` (of all K) into ring slot `slot`
+    // issues the copies of the next stage, `st` of all K, into ring slot `slot`
     auto issue = [&](int st, int slot) {
-        const uint32_t base = lds_base + slot * T::kStage;
-        const bool ragged = (st + 1) * kStageK > p.K;
-        const int k_piece = st * kStageK + piece * 32;
-        const uint8_t *zero = (const uint8_t *)g_zeros;
-        if constexpr (REGS) {
-            // plain scales of 2-byte aligned rows: two 2-byte loads per word, written to LDS after the stage's work
-            const int ka = st * kStageK + my_half_a * 64, kb = st * kStageK + my_half_b * 64;
+        const uint32_t base = lds_base + slot * kStage;
+        const int left = p.K - st * kStageK;
+        // codes past K's end: the row's first of the stage (their scales are masked)
+        const uint32_t back = left <= piece * 32 ? piece * 16 : 0;
 #pragma unroll
-            for (int i = 0; i < CSA; ++i) {
-                const uint16_t *q = (const uint16_t *)psa[i];
-                regs_a[i] = (ka < p.K ? q[0] : 0u) | (ka + 32 < p.K ? (uint32_t)q[1] << 16 : 0u);
-                psa[i] += step_words;
-            }
+        for (int i = 0; i < CA; ++i)
+            copy16(a.codes, oa[i] - back, base + (wave + kWaves * i) * 1024);
 #pragma unroll
-            for (int i = 0; i < CSB; ++i) {
-                const uint16_t *q = (const uint16_t *)psb[i];
-                regs_b[i] = has_sb ? (kb < p.K ? q[0] : 0u) | (kb + 32 < p.K ? (uint32_t)q[1] << 16 : 0u) : 0u;
-                psb[i] += step_words;
-            }
+        for (int i = 0; i < CB; ++i)
+            copy16(b.codes, ob[i] - back, base + T::kOffB + (wave + kWaves * i) * 1024);
+#pragma unroll
+        for (int i = 0; i < CSA; ++i)
+            copy_words<ODD>(a.words, osa[i], left - half_a[i] * 64, back_words,
+                            base + T::kOffSA + (wave + kWaves * i) * 256, kWordsA);
+        if (has_sb) {
+#pragma unroll
+            for (int i = 0; i < CSB; ++i)
+                copy_words<ODD>(b.words, osb[i], left - half_b[i] * 64, back_words,
+                                base + kOffSB + (wave + kWaves * i) * 256, kWordsB);
         }
-#pragma unroll
-        for (int i = 0; i < CA; ++i) {
-            copy16(ragged && k_piece >= p.K ? zero : pa[i], base + (wave + kWaves * i) * 1024);
-            pa[i] += 64;
-        }
-        if (has_b) {
-#pragma unroll
-            for (int i = 0; i < CB; ++i) {
-                copy16(ragged && k_piece >= p.K ? zero : pb[i], base + T::kOffB + (wave + kWaves * i) * 1024);
-                pb[i] += 64;
-            }
-        }
-        if constexpr (!REGS) {
-            const bool past_a = ragged && st * kStageK + my_half_a * 64 >= p.K;
-            const bool past_b = ragged && st * kStageK + my_half_b * 64 >= p.K;
-#pragma unroll
-            for (int i = 0; i < CSA; ++i) {
-                copy4(past_a ? zero : psa[i], base + T::kOffSA + (wave + kWaves * i) * 256);
-                psa[i] += step_words;
-            }
-            if (has_sb) {
-#pragma unroll
-                for (int i = 0; i < CSB; ++i) {
-                    copy4(past_b ? zero : psb[i], base + T::kOffSB + (wave_sb + kWaves * i) * 256);
-                    psb[i] += step_words;
-                }
-            }
-        }
+        a.codes += 64, b.codes += 64;
+        a.words += step_words, b.words += step_words;
     };
-    auto write_regs = [&](int slot) {
-        if constexpr (REGS) {
-            uint8_t *base = lds + slot * T::kStage;
-#pragma unroll
-            for (int i = 0; i < CSA; ++i)
-                *(uint32_t *)(base + T::kOffSA + (wave + kWaves * i) * 256 + lane * 4) = regs_a[i];
-            if (has_sb) {
-#pragma unroll
-                for (int i = 0; i < CSB; ++i)
-                    *(uint32_t *)(base + T::kOffSB + (wave_sb + kWaves * i) * 256 + lane * 4) = regs_b[i];
-            }
-            asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
-        }
+    // waits until only the `younger` last stages' copies are out
+    constexpr int kW = ODD ? 2 : 1, kBase = CA + CB + CSA * kW + (T::TSB % kWaves == 0 ? CSB * kW : 0);
+    auto wait_stage = [&](auto younger) {
+        if (T::TSB % kWaves != 0 && has_sb)
+            wait_copies<younger() * (kBase + CSB * kW)>();
+        else
+            wait_copies<younger() * kBase>();
     };
+    typedef std::integral_constant<int, 0> None;
 
     // --- the product
     float16_t acc[FN][FM];
@@ -375,162 +508,360 @@ __global__ __launch_bounds__(kThreads, 1) void nvfp4_gemm_kernel(GemmParams p)
     const uint32_t codes_a = (ra0 + l32) * 64, codes_b = T::kOffB + (rb0 + l32) * 64;
     const uint32_t words_a = T::kOffSA + (ra0 / (32 * T::LA)) * (T::LA * 256) + half * (T::LA * 128) +
                              l32 * (T::LA * 4) + (ra0 / 32 % T::LA) * 4;
-    const uint32_t words_b = T::kOffSB + (rb0 / (32 * T::LB)) * (T::LB * 256) + half * (T::LB * 128) +
+    const uint32_t words_b = kOffSB + (rb0 / (32 * T::LB)) * (T::LB * 256) + half * (T::LB * 128) +
                              l32 * (T::LB * 4) + (rb0 / 32 % T::LB) * 4;
-    auto compute = [&](int st, int slot) {
-        const uint8_t *base = lds + slot * T::kStage;
-        uint32_t sa[FM], sb[FN];
-        read_words<FM>(base + words_a, sa);
-        read_words<FN>(base + words_b, sb);
-        // scales past K's end may be anything (blocked padding): cleared
-        const uint32_t valid = p.K - st * kStageK - half * 64 == 32 ? 0xFFFFu : ~0u;
+    // A stage is 8 steps of 16 k (per half of the lanes: one dword of codes per
+    // row), in two parts of 4 whose codes are read 16 bytes at a time. While a
+    // step's MFMAs run, the next step's fragments are decoded; the next part's
+    // codes are read a part ahead, across the stage's end: so the barrier that
+    // hands over stage i + 1 stands in the middle of stage i.
+    uint4_t q[2][F];                            // codes of the two parts, A's fragments first
+    half2_t sc[F][2];                           // the stage's 4 scales of each fragment
+    half8_t v[2][F];                            // decoded fragments of two steps
+    auto read_part = [&](int slot, int part) {
+        const uint8_t *base = lds + slot * kStage;
+        const uint32_t pc = ((2 * half + part) ^ swz) * 16;
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
-            sa[i] &= valid;
+        for (int f = 0; f < F; ++f)
+            q[part][f] = f < FM ? *(const uint4_t *)(base + codes_a + f * 2048 + pc)
+                                : *(const uint4_t *)(base + codes_b + (f - FM) * 2048 + pc);
+    };
+    auto read_scales = [&](int slot, int st) {
+        const uint8_t *base = lds + slot * kStage;
+        uint32_t sa[FM], sb[FN];
+        load_words<FM, ODD>(base + words_a, kWordsA, sa);
+        load_words<FN, ODD>(base + words_b, kWordsB, sb);
+        // past K's end: scales of 0
+        const uint32_t valid = word_mask(p.K - st * kStageK - half * 64);
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const uint32_t word = (f < FM ? sa[f < FM ? f : 0] : sb[f < FM ? 0 : f - FM]) & valid;
+            sc[f][0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word, 1.0f, false);
+            sc[f][1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word, 1.0f, true);
+        }
+    };
+    auto decode = [&](int part, int d, int into) {
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const half2_t two = sc[f][part];
+            const half2_t s = d < 2 ? (half2_t){two.x, two.x} : (half2_t){two.y, two.y};
+            const uint32_t codes[4] = {q[part][f].x, q[part][f].y, q[part][f].z, q[part][f].w};
+            v[into][f] = decode8(codes[d], s);
+        }
+    };
+    auto products = [&](int from) {
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-            sb[j] &= valid;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const uint32_t pc = ((2 * half + s) ^ swz) * 16;
-            uint4_t qa[FM], qb[FN];
-            half2_t fa[FM], fb[FN];
-#pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                qa[i] = *(const uint4_t *)(base + codes_a + i * 2048 + pc);
-                fa[i] = s ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sa[i], 1.0f, true)
-                          : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sa[i], 1.0f, false);
-            }
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                qb[j] = *(const uint4_t *)(base + codes_b + j * 2048 + pc);
-                fb[j] = s ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sb[j], 1.0f, true)
-                          : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sb[j], 1.0f, false);
-            }
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                half8_t va[FM], vb[FN];
-#pragma unroll
-                for (int i = 0; i < FM; ++i) {
-                    const half2_t sc = d < 2 ? (half2_t){fa[i].x, fa[i].x} : (half2_t){fa[i].y, fa[i].y};
-                    const uint32_t w[4] = {qa[i].x, qa[i].y, qa[i].z, qa[i].w};
-                    va[i] = decode8(w[d], sc);
-                }
-#pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    const half2_t sc = d < 2 ? (half2_t){fb[j].x, fb[j].x} : (half2_t){fb[j].y, fb[j].y};
-                    const uint32_t w[4] = {qb[j].x, qb[j].y, qb[j].z, qb[j].w};
-                    vb[j] = decode8(w[d], sc);
-                }
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-#pragma unroll
-                    for (int i = 0; i < FM; ++i)
-                        acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vb[j], va[i], acc[j][i], 0, 0, 0);
-            }
-        }
+            for (int i = 0; i < FM; ++i)
+                acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[from][FM + j], v[from][i], acc[j][i], 0, 0, 0);
     };
 
 #pragma unroll
-    for (int s = 0; s < NS - 1; ++s) {
-        if (s < stages) {
+    for (int s = 0; s < NS - 1; ++s)
+        if (s < stages)
             issue(first + s, s);
-            write_regs(s);
-        }
-    }
-    const bool more = (T::TB % kWaves != 0 && has_b) || (!REGS && T::TSB % kWaves != 0 && has_sb);
-    constexpr int kBase = REGS ? T::TA / kWaves + T::TB / kWaves : T::kBase;
+    if (stages >= NS - 1)
+        wait_stage(std::integral_constant<int, NS - 2>{});
+    else
+        wait_stage(None{});
+    barrier();
+    read_scales(0, first);
+    read_part(0, 0);
+    decode(0, 0, 0);
     int slot = 0;
-    int i = 0;
-    for (; i + NS - 1 < stages; ++i) {
-        // stage i has landed when only the NS - 2 younger stages' copies are out
-        if (more)
-            wait_copies<(NS - 2) * (kBase + 1)>();
-        else
-            wait_copies<(NS - 2) * kBase>();
-        barrier();
-        const int into = slot == 0 ? NS - 1 : slot - 1;
-        issue(first + i + NS - 1, into);
-        compute(first + i, slot);
-        write_regs(into);
-        slot = slot + 1 == NS ? 0 : slot + 1;
-    }
-    for (; i < stages; ++i) {
-        wait_copies<0>();
-        barrier();
-        compute(first + i, slot);
-        slot = slot + 1 == NS ? 0 : slot + 1;
+    for (int i = 0; i < stages; ++i) {
+        const int next = slot + 1 == NS ? 0 : slot + 1;
+        read_part(slot, 1);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            products(t % 2);
+            decode(t < 3 ? 0 : 1, (t + 1) % 4, (t + 1) % 2);
+        }
+        if (i + 1 < stages) {
+            // stage i + 1 has landed when only the stages after it are out
+            if (i + NS - 2 < stages)
+                wait_stage(std::integral_constant<int, NS - 3>{});
+            else
+                wait_stage(None{});
+            barrier();
+            if (i + NS - 1 < stages)
+                issue(first + i + NS - 1, slot == 0 ? NS - 1 : slot - 1);
+            read_part(next, 0);
+        }
+#pragma unroll
+        for (int t = 4; t < 8; ++t) {
+            products(t % 2);
+            if (t < 7)
+                decode(1, t - 3, (t + 1) % 2);
+        }
+        if (i + 1 < stages) {
+            read_scales(next, first + i + 1);
+            decode(0, 0, 0);
+        }
+        slot = next;
     }
 
     // --- results. Register r of fragment (j, i): row of B rb0 + 32 j + 8 (r / 4) + 4 (lane / 32) + r % 4,
     // row of A ra0 + 32 i + lane % 32.
-    const int64_t slot_base = EXPERTS ? 0 : (int64_t)l * p.N + n0;
     auto each = [&](auto f) {
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const int n = rb0 + 32 * j + 8 * (r / 4) + 4 * half + r % 4;
-                if (n >= count)
+                const int64_t row = row_at<EXPERTS>(p, w, s_slot, rb0 + 32 * j + 8 * (r / 4) + 4 * half + r % 4);
+                if (row < 0)
                     continue;
-                int64_t row = slot_base + n;
-                if constexpr (EXPERTS) {
-                    row = s_slot[n];
-                    if (row < 0)
-                        continue;
-                }
 #pragma unroll
                 for (int i = 0; i < FM; ++i) {
-                    const int m = m0 + ra0 + 32 * i + l32;
+                    const int m = w.m0 + ra0 + 32 * i + l32;
                     if (m < p.M)
-                        f(acc[j][i][r], row * p.M + m);
+                        f(acc[j][i][r], row + m);
                 }
             }
     };
-    auto total_scale = [&]() {
-        float scale = p.alpha;
-        if (p.scale_a)
-            scale *= p.scale_a[EXPERTS ? l : 0];
-        if (p.scale_b)
-            scale *= *p.scale_b;
-        return scale;
-    };
-    if (p.splits > 1) {
-        // partial sums: agent-scope stores (past this XCD's L2), then the ticket
-        const int64_t one = (int64_t)(EXPERTS ? p.N : p.N * (int64_t)p.L) * p.M;
-        each([&](float v, int64_t at) {
-            __hip_atomic_store(&p.partials[split * one + at], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        });
-        asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
-        barrier();
-        if (threadIdx.x == 0)
-            s_ticket = __hip_atomic_fetch_add(&p.tickets[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        if (s_ticket != (uint32_t)p.splits - 1)
-            return;
-        if (threadIdx.x == 0)
-            __hip_atomic_store(&p.tickets[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        const float scale = total_scale();
-        each([&](float, int64_t at) {
-            float sum = 0.0f;
-            for (int s = 0; s < p.splits; ++s)
-                sum += __hip_atomic_load(&p.partials[s * one + at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            store_value(p.c, at, sum * scale, p.dtype);
-        });
+    if (p.splits == 1) {
+        const float scale = total_scale<EXPERTS>(p, w.l);
+        each([&](float x, int64_t at) { store_value(p.c, at, x * scale, p.dtype); });
         return;
     }
-    const float scale = total_scale();
-    each([&](float v, int64_t at) { store_value(p.c, at, v * scale, p.dtype); });
+    // partial sums: agent-scope stores (past this XCD's L2), then the ticket
+    const int64_t one = (int64_t)(EXPERTS ? p.N : p.N * (int64_t)p.L) * p.M;
+    each([&](float x, int64_t at) {
+        __hip_atomic_store(&p.partials[w.split * one + at], x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    });
+    if (!last_of_tile(p, w.tile, &s_ticket))
+        return;
+    const float scale = total_scale<EXPERTS>(p, w.l);
+#pragma unroll 1
+    for (int g = 0; g < FN * FM * 2; ++g) {                     // 8 registers at a time
+        const int j = g / (FM * 2), i = g / 2 % FM, r0 = g % 2 * 8;
+        int64_t at[8];
+        float sum[8];
+        const int m = w.m0 + ra0 + 32 * i + l32;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const int r = r0 + x;
+            const int64_t row = row_at<EXPERTS>(p, w, s_slot, rb0 + 32 * j + 8 * (r / 4) + 4 * half + r % 4);
+            at[x] = row < 0 || m >= p.M ? -1 : row + m;
+        }
+        add_slices<8>(p, one, at, sum);
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            if (at[x] >= 0)
+                store_value(p.c, at[x], sum[x] * scale, p.dtype);
+    }
+}
+
+// ------------------------------------------------------------------ wave kernel
+
+// KW waves, each FM x FN fragments of the workgroup's tile over every KW-th
+// stage, NS stages in each wave's ring.
+template <int FM, int FN, int KW, int NS, int PER_CU>
+struct WaveTile {
+    static constexpr int kFM = FM, kFN = FN, kKW = KW, kNS = NS, kPerCu = PER_CU;
+    static constexpr int BM = 32 * FM, BN = 32 * FN, kThreads = 64 * KW;
+    static constexpr int kOffB = BM * 64, kOffSA = kOffB + BN * 64;
+    static constexpr int stage_bytes(bool odd) { return kOffSA + (BM + BN) * (odd ? 16 : 8); }
+    static constexpr int lds_bytes(bool odd) { return std::max(KW * NS * stage_bytes(odd), KW * FM * FN * 4096); }
+    static_assert(lds_bytes(true) + kStaticLds <= kLdsBytes);
+};
+
+template <class T, bool EXPERTS, bool ODD>
+__global__ __launch_bounds__(T::kThreads, T::kPerCu) void nvfp4_gemm_wave_kernel(GemmParams p)
+{
+    constexpr int FM = T::kFM, FN = T::kFN, KW = T::kKW, NS = T::kNS, BM = T::BM, BN = T::BN, F = FM + FN;
+    constexpr int kStage = T::stage_bytes(ODD), kWordsA = BM * 8, kWordsB = BN * 8;
+    constexpr int kOffSB = T::kOffSA + kWordsA * (ODD ? 2 : 1);
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    __shared__ int32_t s_slot[EXPERTS ? BN : 1];
+    __shared__ uint32_t s_ticket;
+    const int lane = threadIdx.x % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const Where w = locate<EXPERTS, BM, BN, T::kThreads>(p, s_slot);
+    if (EXPERTS && w.l < 0)
+        return;
+    // this wave's stages: first + wave, first + wave + KW, ..
+    const int first = w.split * p.stages_per_split + wave;
+    const int end = min((w.split + 1) * p.stages_per_split, p.stages);
+    const int stages = first < end ? (end - first + KW - 1) / KW : 0;
+    // copies of B's codes: 16 rows each, only those that hold rows of the tile
+    const int groups_b = (w.count + 15) / 16;
+    const uint32_t one_words = p.blocked ? 1024 : 8, back_words = p.blocked ? 512 : 4;
+    Source a = source_a(p, w), b = source_b<EXPERTS>(p, w);
+    a.codes += (int64_t)first * 64, b.codes += (int64_t)first * 64;
+    a.words += (int64_t)first * one_words, b.words += (int64_t)first * one_words;
+    uint32_t oa[2 * FM], ob[2 * FN], osa[FM], osb[FN];
+    const int piece = (lane % 4) ^ ((lane / 16) % 4);
+    const int half = lane / 32, l32 = lane % 32, swz = (l32 / 4) % 4;
+#pragma unroll
+    for (int i = 0; i < 2 * FM; ++i)
+        oa[i] = codes_at_a(p, w, i * 16 + lane / 4) + piece * 16;
+#pragma unroll
+    for (int i = 0; i < 2 * FN; ++i)
+        ob[i] = codes_at_b<EXPERTS>(p, w, s_slot, i * 16 + lane / 4) + piece * 16;
+    // words: fragment i's 64 words of a stage, half by half, row by row
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+        osa[i] = words_at_a(p, w, 32 * i + l32, half);
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+        osb[j] = words_at_b<EXPERTS>(p, w, s_slot, 32 * j + l32, half);
+    uint8_t *ring = lds + wave * (NS * kStage);
+    const uint32_t ring_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds + wave * (NS * kStage);
+
+    auto issue = [&](int n, int slot) {                         // the wave's n-th stage, the next one
+        const uint32_t base = ring_base + slot * kStage;
+        const int left = p.K - (first + n * KW) * kStageK;
+        const uint32_t back = left <= piece * 32 ? piece * 16 : 0;
+#pragma unroll
+        for (int i = 0; i < 2 * FM; ++i)
+            copy16(a.codes, oa[i] - back, base + i * 1024);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            copy_words<ODD>(a.words, osa[i], left - half * 64, back_words, base + T::kOffSA + i * 256, kWordsA);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            copy_words<ODD>(b.words, osb[j], left - half * 64, back_words, base + kOffSB + j * 256, kWordsB);
+#pragma unroll
+        for (int i = 0; i < 2 * FN; ++i)
+            if (i < groups_b)
+                copy16(b.codes, ob[i] - back, base + T::kOffB + i * 1024);
+        a.codes += 64 * KW, b.codes += 64 * KW;
+        a.words += one_words * KW, b.words += one_words * KW;
+    };
+    constexpr int kBase = 2 * FM + F * (ODD ? 2 : 1);
+    auto wait_younger = [&](auto younger) {
+        if (groups_b == 1)
+            wait_copies<younger() * (kBase + 1)>();
+        else if (2 * FN == 2 || groups_b == 2)
+            wait_copies<younger() * (kBase + 2)>();
+        else if (groups_b == 3)
+            wait_copies<younger() * (kBase + 3)>();
+        else
+            wait_copies<younger() * (kBase + 4)>();
+    };
+
+    float16_t acc[FN][FM];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                acc[j][i][r] = 0.0f;
+    auto compute = [&](int n, int slot) {
+        const uint8_t *base = ring + slot * kStage;
+        const uint32_t valid = word_mask(p.K - (first + n * KW) * kStageK - half * 64);
+        uint32_t word[F];
+        uint4_t q[F][2];
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const uint32_t row = f < FM ? f * 2048 : T::kOffB + (f - FM) * 2048;
+            uint32_t one[1];
+            load_words<1, ODD>(base + (f < FM ? T::kOffSA + f * 256 : kOffSB + (f - FM) * 256) + lane * 4,
+                               f < FM ? kWordsA : kWordsB, one);
+            word[f] = one[0] & valid;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                q[f][s] = *(const uint4_t *)(base + row + l32 * 64 + ((2 * half + s) ^ swz) * 16);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                half8_t v[F];
+#pragma unroll
+                for (int f = 0; f < F; ++f) {
+                    const half2_t two = s ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word[f], 1.0f, true)
+                                          : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word[f], 1.0f, false);
+                    const half2_t sc = d < 2 ? (half2_t){two.x, two.x} : (half2_t){two.y, two.y};
+                    const uint32_t codes[4] = {q[f][s].x, q[f][s].y, q[f][s].z, q[f][s].w};
+                    v[f] = decode8(codes[d], sc);
+                }
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int i = 0; i < FM; ++i)
+                        acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[FM + j], v[i], acc[j][i], 0, 0, 0);
+            }
+        }
+    };
+
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s)
+        if (s < stages)
+            issue(s, s);
+    int slot = 0, n = 0;
+    for (; n + NS - 1 < stages; ++n) {
+        // stage n has landed when only the NS - 2 younger ones are out; the
+        // slot of stage n - 1, read a turn ago, takes stage n + NS - 1
+        wait_younger(std::integral_constant<int, NS - 2>{});
+        asm volatile("" : : : "memory");
+        issue(n + NS - 1, slot == 0 ? NS - 1 : slot - 1);
+        compute(n, slot);
+        slot = slot + 1 == NS ? 0 : slot + 1;
+    }
+    wait_copies<0>();
+    asm volatile("" : : : "memory");
+    for (; n < stages; ++n) {
+        compute(n, slot);
+        slot = slot + 1 == NS ? 0 : slot + 1;
+    }
+
+    // --- the waves' sums through LDS, in the order of the waves: wave w takes
+    // registers w * R .. of the tile's FN * FM * 16
+    constexpr int R = FN * FM * 16 / KW;
+    __syncthreads();
+    float *sums = (float *)lds;                                 // [wave][register][lane]
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                sums[(wave * (FN * FM * 16) + (j * FM + i) * 16 + r) * 64 + lane] = acc[j][i][r];
+    __syncthreads();
+    float sum[R];
+    int64_t at[R];
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+        const int g = wave * R + x, f = g / 16, r = g % 16, j = f / FM, i = f % FM;
+        sum[x] = 0.0f;
+#pragma unroll
+        for (int o = 0; o < KW; ++o)
+            sum[x] += sums[(o * (FN * FM * 16) + g) * 64 + lane];
+        const int64_t row = row_at<EXPERTS>(p, w, s_slot, 32 * j + 8 * (r / 4) + 4 * half + r % 4);
+        const int m = w.m0 + 32 * i + l32;
+        at[x] = row < 0 || m >= p.M ? -1 : row + m;
+    }
+    if (p.splits > 1) {
+        const int64_t one = (int64_t)(EXPERTS ? p.N : p.N * (int64_t)p.L) * p.M;
+#pragma unroll
+        for (int x = 0; x < R; ++x)
+            if (at[x] >= 0)
+                __hip_atomic_store(&p.partials[w.split * one + at[x]], sum[x], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (!last_of_tile(p, w.tile, &s_ticket))
+            return;
+        add_slices<R>(p, one, at, sum);
+    }
+    const float scale = total_scale<EXPERTS>(p, w.l);
+#pragma unroll
+    for (int x = 0; x < R; ++x)
+        if (at[x] >= 0)
+            store_value(p.c, at[x], sum[x] * scale, p.dtype);
 }
 
 // ------------------------------------------------------------------ plans
 
-typedef Tile<4, 4, 2, 2, 3> TileLarge;          // 256 x 256
-typedef Tile<2, 2, 2, 2, 3> TileMid;            // 128 x 128
-typedef Tile<2, 1, 2, 2, 4> TileNarrow;         // 128 x 64
-typedef Tile<1, 1, 4, 1, 4> TileSkinny;         // 128 x 32
+typedef Tile<4, 4, 2, 2, 4, 1> TileLarge;       // 256 x 256
+typedef Tile<4, 2, 2, 2, 3, 1> TileTall;        // 256 x 128
+typedef Tile<2, 2, 2, 2, 3, 2> TileMid;         // 128 x 128
+typedef Tile<2, 1, 2, 2, 3, 2> TileNarrow;      // 128 x 64
+typedef WaveTile<2, 2, 4, 3, 1> TileWave2;         // 64 x 64
+typedef WaveTile<1, 1, 4, 4, 2> TileWave1;         // 32 x 32
 
-enum class Kind { Large, Mid, Narrow, Skinny };
+enum class Kind { Large, Tall, Mid, Narrow, Wave2, Wave1 };
 
 struct Plan {
     Kind kind;
@@ -570,11 +901,11 @@ Plan dense_plan(int64_t M, int64_t N, int64_t K, int64_t L)
         p.tiles = p.tiles_m * p.tiles_n * L;
     };
     if (N <= 32) {
-        p.kind = Kind::Skinny;
-        tiles(TileSkinny::BM, TileSkinny::BN);
+        p.kind = Kind::Wave1;
+        tiles(TileWave1::BM, TileWave1::BN);
     } else if (N <= 64) {
-        p.kind = Kind::Narrow;
-        tiles(TileNarrow::BM, TileNarrow::BN);
+        p.kind = Kind::Wave2;
+        tiles(TileWave2::BM, TileWave2::BN);
     } else {
         p.kind = Kind::Large;
         tiles(TileLarge::BM, TileLarge::BN);
@@ -598,11 +929,11 @@ Plan experts_plan(int64_t M, int64_t K, int64_t E, int64_t S)
     };
     const int64_t mean = ceil_div(S, E);
     if (mean <= 32) {
-        p.kind = Kind::Skinny;
-        tiles(TileSkinny::BM, TileSkinny::BN);
+        p.kind = Kind::Wave1;
+        tiles(TileWave1::BM, TileWave1::BN);
     } else if (mean <= 64) {
-        p.kind = Kind::Narrow;
-        tiles(TileNarrow::BM, TileNarrow::BN);
+        p.kind = Kind::Wave2;
+        tiles(TileWave2::BM, TileWave2::BN);
     } else {
         p.kind = Kind::Mid;
         tiles(TileMid::BM, TileMid::BN);
@@ -620,15 +951,25 @@ bool known_type(int dtype) { return dtype == NVFP4_F16 || dtype == NVFP4_BF16 ||
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 template <class T, bool EXPERTS>
-hipError_t launch(const GemmParams &p, int64_t grid, hipStream_t st)
+hipError_t launch_wide(const GemmParams &p, int64_t grid, hipStream_t st)
 {
-    // plain scales whose rows start at odd multiples of 2 bytes go through registers
-    const bool regs = !p.blocked && p.K % 64 != 0;
+    const bool odd = !p.blocked && p.K % 64 != 0;               // plain rows of 2-byte alignment
     auto go = [&](auto kern) {
-        hipLaunchKernelGGL(kern, dim3((uint32_t)grid), dim3(kThreads), T::kLds, st, p);
-        return hipGetLastError();
+        hipLaunchKernelGGL(kern, dim3((uint32_t)grid), dim3(kThreads), T::lds_bytes(odd), st, p);
     };
-    return regs ? go(nvfp4_gemm_kernel<T, EXPERTS, true>) : go(nvfp4_gemm_kernel<T, EXPERTS, false>);
+    odd ? go(nvfp4_gemm_wide_kernel<T, EXPERTS, true>) : go(nvfp4_gemm_wide_kernel<T, EXPERTS, false>);
+    return hipGetLastError();
+}
+
+template <class T, bool EXPERTS>
+hipError_t launch_wave(const GemmParams &p, int64_t grid, hipStream_t st)
+{
+    const bool odd = !p.blocked && p.K % 64 != 0;
+    auto go = [&](auto kern) {
+        hipLaunchKernelGGL(kern, dim3((uint32_t)grid), dim3(T::kThreads), T::lds_bytes(odd), st, p);
+    };
+    odd ? go(nvfp4_gemm_wave_kernel<T, EXPERTS, true>) : go(nvfp4_gemm_wave_kernel<T, EXPERTS, false>);
+    return hipGetLastError();
 }
 
 template <bool EXPERTS>
@@ -636,14 +977,13 @@ nvfp4_status_t run(const Plan &plan, const GemmParams &p, hipStream_t st)
 {
     const int64_t grid = plan.tiles * plan.splits;
     hipError_t e = hipSuccess;
-    auto typed = [&](auto tile) {
-        e = launch<decltype(tile), EXPERTS>(p, grid, st);
-    };
     switch (plan.kind) {
-    case Kind::Large: typed(TileLarge{}); break;
-    case Kind::Mid: typed(TileMid{}); break;
-    case Kind::Narrow: typed(TileNarrow{}); break;
-    case Kind::Skinny: typed(TileSkinny{}); break;
+    case Kind::Large: e = launch_wide<TileLarge, EXPERTS>(p, grid, st); break;
+    case Kind::Tall: e = launch_wide<TileTall, EXPERTS>(p, grid, st); break;
+    case Kind::Mid: e = launch_wide<TileMid, EXPERTS>(p, grid, st); break;
+    case Kind::Narrow: e = launch_wide<TileNarrow, EXPERTS>(p, grid, st); break;
+    case Kind::Wave2: e = launch_wave<TileWave2, EXPERTS>(p, grid, st); break;
+    case Kind::Wave1: e = launch_wave<TileWave1, EXPERTS>(p, grid, st); break;
     }
     if (e == hipSuccess)
         return NVFP4_OK;
@@ -753,7 +1093,7 @@ nvfp4_status_t nvfp4_gemm_experts(const void *a, const void *b, const void *sfa,
     if (!known_type(dtype))
         return NVFP4_ERR_INVALID_TYPE;
     if (rows < 1 || slots_per_row < 1 || E > kMaxExperts || rows > (INT64_C(1) << 30) / slots_per_row ||
-        !gemm_shape(M, rows * slots_per_row, K, E))
+        !gemm_shape(M, rows * slots_per_row, K, E) || rows > (INT64_C(1) << 32) / (K / 2))
         return NVFP4_ERR_INVALID_SHAPE;
     const nvfp4_status_t st = check_operands(a, b, sfa, sfb, c, dtype, sf_layout, alpha, scale_a, scale_b);
     if (st != NVFP4_OK)

@@ -1,13 +1,17 @@
 // Router and combine of a mixture of experts on MI355X (gfx950).
 //
-// Router. One wave per token: lane i holds the experts i, i + 64, ... . Scores
-// are float64 (64-bit exponentials cost less than a wrong pick: float32
-// scores of neighbouring experts collide or swap at their last bits); the k
-// picks are k argmaxima over the wave, ties to the lower index.
-// Lists. A stable counting sort of the slots by expert in three launches:
-// counts per chunk of slots, prefix sums, placement. Every rank is counted,
-// no atomic's order enters, so the lists are the same each time.
-// Combine. One thread per 8 (4 for float32) columns of a token, float32 sums.
+// Router. One wave per token: lane i holds the experts i, i + 64, ... . The
+// picks are the largest of the wave one after the other, ties to the lower index.
+//   Picks are compared in float64 by definition. Almost always float32 scores
+// with a bound on their error tell the same: the fast path takes the picks in
+// float32 and gives up where two neighbours in the ranking (or the last group
+// kept and the first one left) are closer than the bound, unless they are the
+// same number computed from the same logit and bias. Then the wave repeats the
+// token in float64. The weights are float64 in both.
+// Lists. A stable counting sort of the slots by expert: counts per chunk of
+// slots, then each chunk's places from the counts of the chunks before it. Every
+// rank is counted, no atomic's order enters: the lists are the same each time.
+// Combine. One thread per 16 bytes of a token's columns, float32 sums.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -25,8 +29,9 @@ constexpr int kRouteWaves = 4;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 64;
 constexpr int kMaxGroups = 64;
-constexpr int kChunkMin = 256;                 // slots a wave counts and places
-constexpr int kScanThreads = 1024;
+constexpr int kListThreads = 256;
+constexpr int kSmallThreads = 1024;
+constexpr int64_t kTicketBytes = 256;
 constexpr int64_t kMaxGrid = 0xFFFFFF;
 
 template <int DT>
@@ -62,200 +67,333 @@ __device__ __attribute__((always_inline)) inline double wave_sum(double v)
         v += __shfl_xor(v, d);
     return v;
 }
-// largest value and its lowest index over the wave, in every lane
-__device__ __attribute__((always_inline)) inline void wave_argmax(double &v, int &i)
+
+// Largest value over the wave, the same in every lane: rows of 16 lanes by
+// shifts, then across the rows; the last lane holds the result.
+template <int CTRL, int ROWS>
+__device__ __attribute__((always_inline)) inline float max_step(float v)
 {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-        const double ov = __shfl_xor(v, d);
-        const int oi = __shfl_xor(i, d);
-        if (ov > v || (ov == v && oi < i)) {
-            v = ov;
-            i = oi;
-        }
-    }
+    return fmaxf(v, as_f32(__builtin_amdgcn_update_dpp(as_i32(v), as_i32(v), CTRL, ROWS, 0xF, false)));
+}
+__device__ __attribute__((always_inline)) inline float wave_max(float v)
+{
+    v = max_step<0x111, 0xF>(v);                                // row_shr:1, 2, 4, 8
+    v = max_step<0x112, 0xF>(v);
+    v = max_step<0x114, 0xF>(v);
+    v = max_step<0x118, 0xF>(v);
+    v = max_step<0x142, 0xA>(v);                                // row_bcast:15, 31
+    v = max_step<0x143, 0xC>(v);
+    return as_f32(__builtin_amdgcn_readlane(as_i32(v), 63));
 }
 
 struct RouteParams {
     int32_t T, E, k, score, n_group, topk_group, group_top, renormalize;
     float scaling;
+    uint64_t group_magic;                                       // ceil(2^32 / group size): e / size = e * magic >> 32
 };
 
-// NL experts per lane (E <= 64 * NL).
+constexpr uint64_t kAllLanes = ~0ull;
+
+// The k picks of a token from the wave's picks (float or double), largest
+// first: lane j gets the j-th's expert, -1 where none is left. `close(m, e)` sees
+// each pick before it is taken, and the first that is left out; where it says
+// false, so does this.
+template <int NL, typename V, typename Close>
+__device__ __attribute__((always_inline)) inline bool pick_k(V (&pick)[NL], int k, int lane, int &id, Close close)
+{
+    const V none = -(V)__builtin_inff();
+    id = -1;
+    for (int j = 0; j <= k; ++j) {                              // one more: the first that is left out
+        V m = pick[0];
+#pragma unroll
+        for (int i = 1; i < NL; ++i)
+            m = pick[i] > m ? pick[i] : m;
+        m = wave_max(m);
+        if (!(m > none))
+            return true;
+        int e = -1;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const uint64_t at = __ballot(pick[i] == m);
+            if (e < 0 && at)
+                e = 64 * i + __ffsll((unsigned long long)at) - 1;
+        }
+        if (!close(m, e))
+            return false;
+        if (j == k)
+            return true;
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            if (e == lane + 64 * i)
+                pick[i] = none;
+        if (lane == j)
+            id = e;
+    }
+    return true;
+}
+
+// Masks the picks outside of the best groups. `picks`: the wave's picks in LDS.
+// Returns false where the border between kept and left groups is closer than `margin`.
+template <int NL, typename V>
+__device__ __attribute__((always_inline)) inline bool mask_groups(V (&pick)[NL], const V *picks, const RouteParams &p,
+                                                                  int lane, V margin)
+{
+    const V none = -(V)__builtin_inff();
+    const int size = p.E / p.n_group;
+    // lanes per group: the largest power of two that gives every group as many
+    int per = 1, shift = 0;
+    while (2 * per * p.n_group <= 64 && per < size)
+        per *= 2, ++shift;
+    const int g = lane >> shift, sub = lane & (per - 1);
+    V a = none, b = none;                                       // the two largest
+    if (g < p.n_group)
+        for (int j = sub; j < size; j += per) {
+            const V v = picks[g * size + j];
+            b = v > a ? a : (v > b ? v : b);
+            a = v > a ? v : a;
+        }
+    for (int d = 1; d < per; d *= 2) {
+        const V oa = __shfl_xor(a, d), ob = __shfl_xor(b, d);
+        const V low = oa > a ? a : oa, high = ob > b ? ob : b;
+        a = oa > a ? oa : a;
+        b = low > high ? low : high;
+    }
+    V value = p.group_top > 1 && b > none ? a + b : a;
+    if (g >= p.n_group || sub != 0)
+        value = none;
+    uint64_t keep = 0;
+    V last = none;
+    bool sure = true;
+    for (int j = 0; j <= p.topk_group; ++j) {
+        const V m = wave_max(value);
+        if (!(m > none))
+            break;                                              // groups without an expert left: nothing in them to mask
+        if (j == p.topk_group) {
+            sure = last - m > margin;
+            break;
+        }
+        last = m;
+        const int at = __ffsll((unsigned long long)__ballot(value == m)) - 1;
+        keep |= 1ull << (at >> shift);
+        if (lane == at)
+            value = none;
+    }
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const uint32_t e = (uint32_t)(lane + 64 * i);
+        const uint32_t of = min((uint32_t)((e * p.group_magic) >> 32), 63u);
+        if (!(keep >> of & 1ull))
+            pick[i] = none;
+    }
+    return sure;
+}
+
+// float32 path: x (masked: -inf), bias b -> id per lane. False: not certain.
+template <int NL>
+__device__ __attribute__((always_inline)) inline bool route_fast(const float (&x)[NL], const float (&b)[NL],
+                                                                 bool with_bias, float top, const RouteParams &p,
+                                                                 int lane, float *lds, int &id)
+{
+    const float none = -__builtin_inff();
+    float pick[NL], largest = none;
+    float score_top = 1.0f;
+    if (p.score == NVFP4_SCORE_SOFTMAX) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            pick[i] = __expf(x[i] - top);
+            sum += pick[i];
+        }
+#pragma unroll
+        for (int d = 32; d; d >>= 1)
+            sum += __shfl_xor(sum, d);
+        score_top = 1.0f / sum;                                 // the largest score: exp(0) / sum
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            pick[i] *= score_top;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            pick[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-x[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const float v = pick[i] + b[i];
+        pick[i] = x[i] > none && v == v ? v : none;
+        largest = pick[i] > none ? fmaxf(largest, fabsf(pick[i])) : largest;
+    }
+    // exp(-d) is off by at most (d + 2) 2^-23 of itself, so a softmax numerator (d e^-d
+    // <= 0.37) or a sigmoid by less than 2^-20 of the largest score. The softmax's sum
+    // scales every score alike and matters beside a bias only: it is off by at most
+    // (0.37 E + 16) 2^-23 of itself. The pick's own rounding is 2^-24 of the pick.
+    const float part = p.score == NVFP4_SCORE_SOFTMAX && with_bias ? (p.E > 64 ? 0x1p-13f : 0x1p-17f) : 0x1p-20f;
+    const float margin = 2.0f * (score_top * part + wave_max(largest) * 0x1p-23f);
+    if (!(margin < 1.0f))
+        return false;                                           // infinite picks: float64 sorts them out
+    if (p.n_group > 1) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            lds[lane + 64 * i] = pick[i];
+        wave_sync();
+        const bool sure = mask_groups<NL, float>(pick, lds, p, lane, 2.0f * margin);
+        wave_sync();
+        if (!sure)
+            return false;
+    }
+    float last = __builtin_inff(), last_x = 0.0f, last_b = 0.0f;
+    return pick_k<NL, float>(pick, p.k, lane, id, [&](float m, int e) {
+        float xe = 0.0f, be = 0.0f;
+        // the picked expert's logit and bias, and whether any other of the same pick has others
+        bool other = false;
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            if (e / 64 == i) {
+                xe = as_f32(__builtin_amdgcn_readlane(as_i32(x[i]), e % 64));
+                be = as_f32(__builtin_amdgcn_readlane(as_i32(b[i]), e % 64));
+            }
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            other |= pick[i] == m && (x[i] != xe || b[i] != be);
+        if (__ballot(other))
+            return false;
+        if (!(last - m > margin) && !(xe == last_x && be == last_b))
+            return false;
+        last = m, last_x = xe, last_b = be;
+        return true;
+    });
+}
+
+// An expert's logit and bias for lane `lane` of the i-th 64; masked and past the end: -inf.
+template <int DT, int NL>
+__device__ __attribute__((always_inline)) inline void load_token(const void *__restrict__ logits,
+                                                                 const float *__restrict__ bias, int64_t t, int32_t E,
+                                                                 int lane, float (&x)[NL], float (&b)[NL])
+{
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const int e = lane + 64 * i;
+        const float v = e < E ? load_value<DT>(logits, t * E + e) : -__builtin_inff();
+        b[i] = bias && e < E ? bias[e] : 0.0f;
+        x[i] = v == v ? v : -__builtin_inff();
+    }
+}
+
+struct Exact {
+    int id;
+    double sum;                                                 // softmax: of the exponentials
+};
+
+// float64 path, the definition itself. Not inlined: it is rarely taken, and its
+// registers would cost the fast path waves. It loads the token again.
+template <int DT, int NL>
+__device__ __attribute__((noinline)) Exact route_exact(const void *__restrict__ logits, const float *__restrict__ bias,
+                                                       int64_t t, RouteParams p, double *lds)
+{
+    const double none = -__builtin_inf();
+    const int lane = threadIdx.x % 64;
+    float x[NL], b[NL];
+    load_token<DT, NL>(logits, bias, t, p.E, lane, x, b);
+    int id;
+    double pick[NL], top = none, score_sum = 1.0;
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+        top = fmax(top, (double)x[i]);
+    if (p.score == NVFP4_SCORE_SOFTMAX) {
+        top = wave_max(top);
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            pick[i] = x[i] > none ? ((double)x[i] == top ? 1.0 : exp((double)x[i] - top)) : 0.0;
+            sum += pick[i];
+        }
+        score_sum = wave_sum(sum);
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            pick[i] = score_sum > 0.0 ? pick[i] / score_sum : 0.0;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            pick[i] = 1.0 / (1.0 + exp(-(double)x[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const double v = pick[i] + (double)b[i];
+        pick[i] = x[i] > none && v == v ? v : none;
+    }
+    if (p.n_group > 1) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            lds[lane + 64 * i] = pick[i];
+        wave_sync();
+        mask_groups<NL, double>(pick, lds, p, lane, 0.0);
+        wave_sync();
+    }
+    pick_k<NL, double>(pick, p.k, lane, id, [](double, int) { return true; });
+    return {id, score_sum};
+}
+
+// One token by one wave. `lds`: 64 * NL doubles of the wave's own.
+template <int DT, int NL>
+__device__ __attribute__((always_inline)) inline void route_token(const void *__restrict__ logits,
+                                                                  const float *__restrict__ bias,
+                                                                  int32_t *__restrict__ ids,
+                                                                  float *__restrict__ weights, const RouteParams &p,
+                                                                  int64_t t, int lane, double *lds)
+{
+    float x[NL], b[NL], top = -__builtin_inff();
+    load_token<DT, NL>(logits, bias, t, p.E, lane, x, b);
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+        top = fmaxf(top, x[i]);
+    top = wave_max(top);
+    // softmax weights that are not renormalised need the float64 sum over all
+    // experts, and infinite logits their own rule
+    const bool plain = top < __builtin_inff() && (p.score == NVFP4_SCORE_SIGMOID || p.renormalize);
+    int id;
+    double sum = 1.0;
+    if (!plain || !route_fast<NL>(x, b, bias != nullptr, top, p, lane, (float *)lds, id)) {
+        const Exact r = route_exact<DT, NL>(logits, bias, t, p, lds);
+        id = r.id;
+        sum = r.sum;
+    }
+    // weights: lane j has expert j's score, in float64
+    double w = 0.0;
+    if (id >= 0) {
+        const float v = load_value<DT>(logits, t * p.E + id);
+        if (p.score == NVFP4_SCORE_SIGMOID)
+            w = 1.0 / (1.0 + exp(-(double)v));
+        else                                                    // renormalised: the sum cancels
+            w = (v == top ? 1.0 : exp((double)v - (double)top)) / (p.renormalize ? 1.0 : sum);
+    }
+    if (p.renormalize) {
+        const double total = wave_sum(w);
+        w = total > 0.0 ? w / total : 0.0;
+    }
+    if (lane < p.k) {
+        ids[t * p.k + lane] = id;
+        weights[t * p.k + lane] = (float)(w * (double)p.scaling);
+    }
+}
+
 template <int DT, int NL>
 __global__ __launch_bounds__(64 * kRouteWaves) void nvfp4_route_kernel(const void *__restrict__ logits,
                                                                        const float *__restrict__ bias,
                                                                        int32_t *__restrict__ ids,
                                                                        float *__restrict__ weights, RouteParams p)
 {
-    __shared__ double s_score[kRouteWaves][64 * NL];
-    __shared__ double s_pick[kRouteWaves][64 * NL];
+    __shared__ double lds[kRouteWaves][64 * NL];
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
-    if (t >= p.T)
-        return;
-    const double none = -__builtin_inf();
-    double score[NL], pick[NL];
-    double top = none;
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-        const int e = lane + 64 * i;
-        const float x = e < p.E ? load_value<DT>(logits, t * p.E + e) : -__builtin_inff();
-        score[i] = x == x ? (double)x : none;
-        top = fmax(top, score[i]);
-    }
-    if (p.score == NVFP4_SCORE_SOFTMAX) {
-        top = wave_max(top);
-        double sum = 0.0;
-        uint32_t masked = 0u;
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            masked |= (uint32_t)(score[i] == none) << i;
-            // +inf: those logits share, the others get nothing
-            score[i] = (masked >> i & 1u) ? 0.0 : score[i] == top ? 1.0 : exp(score[i] - top);
-            sum += score[i];
-        }
-        sum = wave_sum(sum);
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            score[i] = sum > 0.0 ? score[i] / sum : 0.0;
-            pick[i] = (masked >> i & 1u) ? none : score[i];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const bool masked = score[i] == none;
-            score[i] = masked ? 0.0 : 1.0 / (1.0 + exp(-score[i]));
-            pick[i] = masked ? none : score[i];
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-        const int e = lane + 64 * i;
-        if (bias && e < p.E) {
-            const double v = pick[i] + (double)bias[e];
-            pick[i] = v == v ? v : none;
-        }
-        s_score[wave][e] = score[i];
-        s_pick[wave][e] = pick[i];
-    }
-    wave_sync();
-    if (p.n_group > 1) {
-        const int size = p.E / p.n_group;
-        double value = none;
-        if (lane < p.n_group) {
-            double a = none, b = none;                          // the two largest
-            for (int j = 0; j < size; ++j) {
-                const double v = s_pick[wave][lane * size + j];
-                b = v > a ? a : fmax(b, v);
-                a = fmax(a, v);
-            }
-            value = p.group_top > 1 && b > none ? a + b : a;
-        }
-        uint64_t keep = 0;
-        for (int j = 0; j < p.topk_group; ++j) {
-            const bool left = lane < p.n_group && !(keep >> lane & 1ull);
-            double v = left ? value : none;
-            int g = left ? lane : 64;
-            wave_argmax(v, g);
-            if (g < 64)
-                keep |= 1ull << g;
-        }
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int g = min((lane + 64 * i) / size, 63);
-            if (!(keep >> g & 1ull))
-                pick[i] = none;
-        }
-    }
-    int mine = -1;
-    double w = 0.0;
-    for (int j = 0; j < p.k; ++j) {
-        double v = none;
-        int e = kMaxExperts;
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            if (pick[i] > v) {
-                v = pick[i];
-                e = lane + 64 * i;
-            }
-        }
-        wave_argmax(v, e);
-        if (e >= p.E)
-            break;                                              // none left, in every lane
-#pragma unroll
-        for (int i = 0; i < NL; ++i)
-            if (e == lane + 64 * i)
-                pick[i] = none;
-        if (lane == j) {
-            mine = e;
-            w = s_score[wave][e];
-        }
-    }
-    if (p.renormalize) {
-        const double sum = wave_sum(w);
-        w = sum > 0.0 ? w / sum : 0.0;
-    }
-    if (lane < p.k) {
-        ids[t * p.k + lane] = mine;
-        weights[t * p.k + lane] = (float)(w * (double)p.scaling);
-    }
+    if (t < p.T)
+        route_token<DT, NL>(logits, bias, ids, weights, p, t, lane, lds[wave]);
 }
 
 // ------------------------------------------------------------------ lists
 
-// One wave counts `chunk` slots: counts[c][e].
-__global__ __launch_bounds__(64) void nvfp4_count_kernel(const int32_t *__restrict__ ids, int32_t *__restrict__ counts,
-                                                         int32_t S, int32_t E, int32_t chunk)
-{
-    __shared__ int32_t n[kMaxExperts];
-    const int lane = threadIdx.x;
-    for (int e = lane; e < E; e += 64)
-        n[e] = 0;
-    wave_sync();
-    const int32_t from = blockIdx.x * chunk, to = min(S, from + chunk);
-    for (int32_t s = from + lane; s < to; s += 64) {
-        const int32_t e = ids[s];
-        if (e >= 0 && e < E)
-            atomicAdd(&n[e], 1);
-    }
-    wave_sync();
-    for (int e = lane; e < E; e += 64)
-        counts[(int64_t)blockIdx.x * E + e] = n[e];
-}
-
-// Exclusive sums over the chunks of each expert (in place) and over the experts.
-__global__ __launch_bounds__(kScanThreads) void nvfp4_scan_kernel(int32_t *__restrict__ counts,
-                                                                  int32_t *__restrict__ offsets, int32_t nc,
-                                                                  int32_t E)
-{
-    __shared__ int32_t total[kScanThreads];
-    const int e = threadIdx.x;
-    int32_t sum = 0;
-    if (e < E)
-        for (int c = 0; c < nc; ++c) {
-            const int32_t v = counts[(int64_t)c * E + e];
-            counts[(int64_t)c * E + e] = sum;
-            sum += v;
-        }
-    total[e] = sum;
-    __syncthreads();
-    for (int d = 1; d < kScanThreads; d <<= 1) {
-        const int32_t v = e >= d ? total[e - d] : 0;
-        __syncthreads();
-        total[e] += v;
-        __syncthreads();
-    }
-    if (e < E)
-        offsets[e + 1] = total[e];
-    if (e == 0)
-        offsets[0] = 0;
-}
-
 // Lanes of the wave with the same key (bits key bits wide).
-__device__ inline uint64_t same_lanes(uint32_t key, int bits)
+__device__ __attribute__((always_inline)) inline uint64_t same_lanes(uint32_t key, int bits)
 {
-    uint64_t m = ~0ull;
+    uint64_t m = kAllLanes;
     for (int b = 0; b < bits; ++b) {
         const bool one = key >> b & 1u;
         const uint64_t v = __ballot(one);
@@ -264,38 +402,185 @@ __device__ inline uint64_t same_lanes(uint32_t key, int bits)
     return m;
 }
 
-// One wave places its chunk's slots in order, and leaves its counts zero (the
-// workspace may hold another call's counters there).
-__global__ __launch_bounds__(64) void nvfp4_place_kernel(const int32_t *__restrict__ ids,
-                                                         int32_t *__restrict__ counts,
-                                                         const int32_t *__restrict__ offsets,
-                                                         int32_t *__restrict__ order, int32_t S, int32_t E,
-                                                         int32_t chunk, int32_t bits)
+// Inclusive sums over a workgroup's threads (THREADS of them, `part` holds one
+// value per wave).
+template <int THREADS>
+__device__ __attribute__((always_inline)) inline int32_t sum_upto(int32_t v, int32_t *part)
 {
-    __shared__ int32_t at[kMaxExperts + 1];
-    const int lane = threadIdx.x;
-    for (int e = lane; e < E; e += 64) {
-        at[e] = counts[(int64_t)blockIdx.x * E + e] + offsets[e];
-        counts[(int64_t)blockIdx.x * E + e] = 0;
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int32_t o = __shfl_up(v, d);
+        v += lane >= d ? o : 0;
     }
-    wave_sync();
+    if (lane == 63)
+        part[wave] = v;
+    __syncthreads();
+    int32_t before = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w)
+        before += w < wave ? part[w] : 0;
+    __syncthreads();
+    return v + before;
+}
+
+// One workgroup counts a chunk of slots: counts[c][e].
+__global__ __launch_bounds__(kListThreads) void nvfp4_count_kernel(const int32_t *__restrict__ ids,
+                                                                   int32_t *__restrict__ counts, int32_t S, int32_t E,
+                                                                   int32_t chunk)
+{
+    __shared__ int32_t n[kMaxExperts];
+    for (int e = threadIdx.x; e < E; e += kListThreads)
+        n[e] = 0;
+    __syncthreads();
     const int32_t from = blockIdx.x * chunk, to = min(S, from + chunk);
-    for (int32_t s0 = from; s0 < to; s0 += 64) {
+    for (int32_t s = from + (int32_t)threadIdx.x; s < to; s += kListThreads) {
+        const int32_t e = ids[s];
+        if (e >= 0 && e < E)
+            atomicAdd(&n[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kListThreads)
+        counts[(int64_t)blockIdx.x * E + e] = n[e];
+}
+
+// A workgroup of THREADS places the slots [from, to) in order; base[e] is
+// where expert e's slots of this chunk start. at: LDS [waves][E] (per wave).
+template <int THREADS>
+__device__ __attribute__((always_inline)) inline void place_slots(const int32_t *__restrict__ ids,
+                                                                  int32_t *__restrict__ order, int32_t *at,
+                                                                  const int32_t *base, int32_t from, int32_t to,
+                                                                  int32_t E, int32_t bits)
+{
+    constexpr int W = THREADS / 64;
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    // each wave a run of whole groups of 64 slots
+    const int32_t run = ((to - from + 64 * W - 1) / (64 * W)) * 64;
+    const int32_t a = from + wave * run, z = min(to, a + run);
+    int32_t *mine = at + wave * E;
+    for (int e = threadIdx.x; e < W * E; e += THREADS)
+        at[e] = 0;
+    __syncthreads();
+    for (int32_t s = a + lane; s < z; s += 64) {
+        const int32_t e = ids[s];
+        if (e >= 0 && e < E)
+            atomicAdd(&mine[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += THREADS) {
+        int32_t sum = base[e];
+        for (int w = 0; w < W; ++w) {
+            const int32_t v = at[w * E + e];
+            at[w * E + e] = sum;
+            sum += v;
+        }
+    }
+    __syncthreads();
+    for (int32_t s0 = a; s0 < z; s0 += 64) {
         const int32_t s = s0 + lane;
-        int32_t e = s < to ? ids[s] : -1;
+        int32_t e = s < z ? ids[s] : -1;
         const bool in = e >= 0 && e < E;
         e = in ? e : E;                                         // one key for those in no list
         const uint64_t same = same_lanes((uint32_t)e, bits);
         const int before = __popcll(same & ((1ull << lane) - 1ull));
-        const int32_t base = in ? at[e] : 0;
+        const int32_t first = in ? mine[e] : 0;
         wave_sync();
         if (in) {
-            order[base + before] = s;
+            order[first + before] = s;
             if (before == 0)
-                at[e] = base + __popcll(same);
+                mine[e] = first + __popcll(same);
         }
         wave_sync();
     }
+}
+
+// Every workgroup sums the counts of all chunks (and of those before its own)
+// for itself: one launch fewer than a kernel for the sums, and the counts come
+// from L2. The last workgroup done with them (by ticket) clears them, as every
+// call leaves its workspace's counters.
+__global__ __launch_bounds__(kListThreads) void nvfp4_place_kernel(const int32_t *__restrict__ ids,
+                                                                   int32_t *counts, uint32_t *ticket,
+                                                                   int32_t *__restrict__ offsets,
+                                                                   int32_t *__restrict__ order, int32_t S, int32_t E,
+                                                                   int32_t chunk, int32_t nc, int32_t bits)
+{
+    __shared__ uint32_t taken;
+    extern __shared__ int32_t list_lds[];                       // base[E], at[waves][E]
+    __shared__ int32_t part[kListThreads / 64];
+    int32_t *base = list_lds, *at = list_lds + E;
+    int32_t start = 0;                                          // sum of the experts before this round's
+    for (int e0 = 0; e0 < E; e0 += kListThreads) {
+        const int e = e0 + (int)threadIdx.x;
+        int32_t all = 0, before = 0;
+        if (e < E) {
+#pragma unroll 16
+            for (int c = 0; c < nc; ++c) {
+                const int32_t v = counts[(int64_t)c * E + e];
+                all += v;
+                before += c < (int)blockIdx.x ? v : 0;
+            }
+        }
+        const int32_t upto = sum_upto<kListThreads>(all, part) + start;
+        if (e < E) {
+            base[e] = upto - all + before;
+            if (blockIdx.x == 0) {
+                offsets[e + 1] = upto;
+                if (e == 0)
+                    offsets[0] = 0;
+            }
+        }
+        __shared__ int32_t end;
+        if (threadIdx.x == kListThreads - 1)
+            end = upto;
+        __syncthreads();
+        start = end;
+        __syncthreads();
+    }
+    // every thread's counts have arrived (the barriers above follow their sums)
+    if (threadIdx.x == 0)
+        taken = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int32_t from = blockIdx.x * chunk;
+    place_slots<kListThreads>(ids, order, at, base, from, min(S, from + chunk), E, bits);
+    if (taken != (uint32_t)nc - 1)                              // place_slots has barriers of its own
+        return;
+    for (int64_t i = threadIdx.x; i < (int64_t)nc * E; i += kListThreads)
+        counts[i] = 0;
+    if (threadIdx.x == 0)
+        *ticket = 0u;
+}
+
+// Few tokens: the whole router in one workgroup of 16 waves.
+template <int DT, int NL>
+__global__ __launch_bounds__(kSmallThreads) void nvfp4_route_small_kernel(
+    const void *__restrict__ logits, const float *__restrict__ bias, int32_t *__restrict__ ids,
+    float *__restrict__ weights, int32_t *__restrict__ offsets, int32_t *__restrict__ order, RouteParams p, int32_t bits)
+{
+    extern __shared__ int32_t list_lds[];                       // route: the waves' picks; lists: base[E], at[waves][E]
+    __shared__ int32_t part[kSmallThreads / 64];
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    double *picks = (double *)list_lds + wave * (64 * NL);
+    for (int t = wave; t < p.T; t += kSmallThreads / 64)
+        route_token<DT, NL>(logits, bias, ids, weights, p, t, lane, picks);
+    __syncthreads();                                            // this workgroup's ids are in its reach
+    int32_t *base = list_lds, *at = list_lds + p.E;
+    const int e = threadIdx.x;
+    const int32_t S = p.T * p.k;
+    if (e < p.E)
+        base[e] = 0;
+    __syncthreads();
+    for (int s = threadIdx.x; s < S; s += kSmallThreads)
+        if (ids[s] >= 0)
+            atomicAdd(&base[ids[s]], 1);
+    __syncthreads();
+    const int32_t n = e < p.E ? base[e] : 0;
+    const int32_t upto = sum_upto<kSmallThreads>(n, part);
+    if (e < p.E) {
+        base[e] = upto - n;
+        offsets[e + 1] = upto;
+        if (e == 0)
+            offsets[0] = 0;
+    }
+    place_slots<kSmallThreads>(ids, order, at, base, 0, S, p.E, bits);
 }
 
 // ------------------------------------------------------------------ combine
@@ -328,7 +613,9 @@ __device__ __attribute__((always_inline)) inline uint32_t value_bits(float v)
 }
 
 // One thread per 16 bytes of a token's columns; the last piece of a row may be
-// partial. Rows have their type's alignment only.
+// partial. Rows have their type's alignment only. Eight slots at a time: their
+// ids and weights first, then all their values, so that the loads of a round
+// wait for one another once and not per slot.
 template <int DT>
 __global__ __launch_bounds__(256) void nvfp4_combine_kernel(const uint8_t *__restrict__ y,
                                                             const int32_t *__restrict__ ids,
@@ -336,36 +623,55 @@ __global__ __launch_bounds__(256) void nvfp4_combine_kernel(const uint8_t *__res
                                                             uint8_t *__restrict__ out, int64_t pieces, int32_t k,
                                                             int32_t M, int32_t per_row)
 {
-    constexpr int N = Piece<DT>::kN, SZ = DT == NVFP4_F32 ? 4 : 2;
+    constexpr int N = Piece<DT>::kN, SZ = DT == NVFP4_F32 ? 4 : 2, R = 8;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= pieces)
         return;
-    const int64_t t = i / per_row;
+    const int64_t t = pieces < INT32_MAX ? (int64_t)((uint32_t)i / (uint32_t)per_row) : i / per_row;
     const int32_t m = (int32_t)(i - t * per_row) * N;
     float sum[N];
 #pragma unroll
     for (int c = 0; c < N; ++c)
         sum[c] = 0.0f;
     const bool whole = m + N <= M;
-    for (int32_t j = 0; j < k; ++j) {
-        const int64_t s = t * k + j;
-        if (ids[s] < 0)
-            continue;
-        const float w = weights[s];
-        const uint8_t *p = y + (s * M + m) * SZ;
-        uint32_t v[4] = {0u, 0u, 0u, 0u};
-        if (whole) {
-            __builtin_memcpy(v, p, 16);
-        } else if constexpr (SZ == 4) {
-            for (int c = 0; c < M - m; ++c)
-                v[c] = ((const uint32_t *)p)[c];
-        } else {
-            for (int c = 0; c < M - m; ++c)
-                v[c / 2] |= (uint32_t)((const uint16_t *)p)[c] << (16 * (c % 2));
+    const uint8_t *row = y + (t * k * M + m) * SZ;
+    for (int32_t j0 = 0; j0 < k; j0 += R) {
+        float w[R];
+        uint32_t used = 0u, v[R][4];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            const int64_t s = t * k + min(j0 + j, k - 1);
+            w[j] = weights[s];
+            used |= (uint32_t)(j0 + j < k && ids[s] >= 0) << j;
         }
 #pragma unroll
-        for (int c = 0; c < N; ++c)
-            sum[c] = fmaf(w, to_float<DT>(v, c), sum[c]);
+        for (int j = 0; j < R; ++j) {
+            v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0u;
+            if (!(used >> j & 1u))
+                continue;
+            const uint8_t *p = row + (int64_t)(j0 + j) * M * SZ;
+            if (whole) {
+                __builtin_memcpy(v[j], p, 16);
+            } else if constexpr (SZ == 4) {
+#pragma unroll
+                for (int c = 0; c < 3; ++c)
+                    if (c < M - m)
+                        v[j][c] = ((const uint32_t *)p)[c];
+            } else {
+#pragma unroll
+                for (int c = 0; c < 7; ++c)
+                    if (c < M - m)
+                        v[j][c / 2] |= (uint32_t)((const uint16_t *)p)[c] << (16 * (c % 2));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            if (!(used >> j & 1u))
+                continue;
+#pragma unroll
+            for (int c = 0; c < N; ++c)
+                sum[c] = fmaf(w[j], to_float<DT>(v[j], c), sum[c]);
+        }
     }
     uint8_t *o = out + (t * M + m) * SZ;
     if (whole) {
@@ -424,14 +730,11 @@ bool route_shape(int64_t T, int64_t E, int64_t k)
     return T >= 1 && E >= 1 && E <= kMaxExperts && k >= 1 && k <= E && k <= kMaxTopK && T <= (INT64_C(1) << 30) / k;
 }
 
-// slots per wave of the lists' kernels: at most about 256 chunks
-int64_t list_chunk(int64_t S)
-{
-    int64_t chunk = kChunkMin;
-    while (S > chunk * 256)
-        chunk *= 2;
-    return chunk;
-}
+// Few tokens run in one workgroup: at most 4 tokens per wave, and LDS for the lists.
+bool route_small(int64_t T, int64_t E, int64_t k) { return T <= 64 && T * k <= 2048 && E <= kSmallThreads; }
+
+// slots per workgroup of the lists' kernels: at most 128 chunks of at least 512
+int64_t list_chunk(int64_t S) { return std::max<int64_t>(512, (S + 127) / 128); }
 
 } // namespace
 
@@ -439,10 +742,10 @@ extern "C" {
 
 size_t nvfp4_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t k)
 {
-    if (!route_shape(T, E, k))
+    if (!route_shape(T, E, k) || route_small(T, E, k))
         return 0;
     const int64_t S = T * k, chunk = list_chunk(S);
-    return (size_t)((((S + chunk - 1) / chunk) * E * 4 + 255) / 256 * 256);
+    return (size_t)(kTicketBytes + (((S + chunk - 1) / chunk) * E * 4 + 255) / 256 * 256);
 }
 
 nvfp4_status_t nvfp4_moe_route(const void *logits, int dtype, const float *bias, int32_t *ids, float *weights,
@@ -465,38 +768,51 @@ nvfp4_status_t nvfp4_moe_route(const void *logits, int dtype, const float *bias,
     if (!aligned(logits, type_size(dtype)) || (bias && !aligned(bias, 4)) || !aligned(ids, 4) || !aligned(weights, 4) ||
         !aligned(offsets, 4) || !aligned(order, 4))
         return NVFP4_ERR_MISALIGNED;
-    if (!workspace || workspace_bytes < nvfp4_moe_route_workspace_bytes(T, E, k) || !aligned(workspace, 256))
+    const size_t need = nvfp4_moe_route_workspace_bytes(T, E, k);
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
         return NVFP4_ERR_WORKSPACE;
-    const hipStream_t st = (hipStream_t)stream;
-    RouteParams p{(int32_t)T, (int32_t)E, (int32_t)k, r.score, r.n_group, r.topk_group, r.group_top, r.renormalize,
-                  r.scaling};
     const int64_t grid = (T + kRouteWaves - 1) / kRouteWaves;
     if (grid > kMaxGrid)
         return NVFP4_ERR_INVALID_SHAPE;
-    by_type(dtype, [&](auto dt) {
-        auto go = [&](auto kern) {
-            hipLaunchKernelGGL(kern, dim3((uint32_t)grid), dim3(64 * kRouteWaves), 0, st, logits, bias, ids, weights, p);
-        };
-        if (E <= 64)
-            go(nvfp4_route_kernel<dt(), 1>);
-        else if (E <= 128)
-            go(nvfp4_route_kernel<dt(), 2>);
-        else if (E <= 256)
-            go(nvfp4_route_kernel<dt(), 4>);
-        else if (E <= 512)
-            go(nvfp4_route_kernel<dt(), 8>);
-        else
-            go(nvfp4_route_kernel<dt(), 16>);
-    });
-    const int32_t S = (int32_t)(T * k), chunk = (int32_t)list_chunk(S), nc = (S + chunk - 1) / chunk;
+    const hipStream_t st = (hipStream_t)stream;
+    const int64_t size = E / r.n_group;
+    RouteParams p{(int32_t)T, (int32_t)E, (int32_t)k, r.score, r.n_group, r.topk_group, r.group_top, r.renormalize,
+                  r.scaling, (uint64_t)(((INT64_C(1) << 32) + size - 1) / size)};
+    const int32_t S = (int32_t)(T * k);
     int32_t bits = 1;
     while ((E >> bits) != 0)
         ++bits;                                                 // E itself is a key too
-    int32_t *counts = (int32_t *)workspace;
-    hipLaunchKernelGGL(nvfp4_count_kernel, dim3(nc), dim3(64), 0, st, (const int32_t *)ids, counts, S, (int32_t)E, chunk);
-    hipLaunchKernelGGL(nvfp4_scan_kernel, dim3(1), dim3(kScanThreads), 0, st, counts, offsets, nc, (int32_t)E);
-    hipLaunchKernelGGL(nvfp4_place_kernel, dim3(nc), dim3(64), 0, st, (const int32_t *)ids, counts,
-                       (const int32_t *)offsets, order, S, (int32_t)E, chunk, bits);
+    const bool small = route_small(T, E, k);
+    by_type(dtype, [&](auto dt) {
+        auto go = [&](auto nl) {
+            if (small) {
+                const size_t lds = std::max<size_t>(kSmallThreads / 64 * 64 * nl() * 8, (1 + kSmallThreads / 64) * E * 4);
+                hipLaunchKernelGGL((nvfp4_route_small_kernel<dt(), nl()>), dim3(1), dim3(kSmallThreads), lds, st, logits,
+                                   bias, ids, weights, offsets, order, p, bits);
+            } else {
+                hipLaunchKernelGGL((nvfp4_route_kernel<dt(), nl()>), dim3((uint32_t)grid), dim3(64 * kRouteWaves), 0, st,
+                                   logits, bias, ids, weights, p);
+            }
+        };
+        if (E <= 64)
+            go(std::integral_constant<int, 1>{});
+        else if (E <= 128)
+            go(std::integral_constant<int, 2>{});
+        else if (E <= 256)
+            go(std::integral_constant<int, 4>{});
+        else if (E <= 512)
+            go(std::integral_constant<int, 8>{});
+        else
+            go(std::integral_constant<int, 16>{});
+    });
+    if (!small) {
+        const int32_t chunk = (int32_t)list_chunk(S), nc = (S + chunk - 1) / chunk;
+        int32_t *counts = (int32_t *)((uint8_t *)workspace + kTicketBytes);
+        hipLaunchKernelGGL(nvfp4_count_kernel, dim3(nc), dim3(kListThreads), 0, st, (const int32_t *)ids, counts, S,
+                           (int32_t)E, chunk);
+        hipLaunchKernelGGL(nvfp4_place_kernel, dim3(nc), dim3(kListThreads), (1 + kListThreads / 64) * E * 4, st,
+                           (const int32_t *)ids, counts, (uint32_t *)workspace, offsets, order, S, (int32_t)E, chunk, nc, bits);
+    }
     return finish();
 }
 

@@ -60,58 +60,116 @@ __device__ __attribute__((always_inline)) inline void load16(const uint8_t *p, f
 }
 
 template <int DT>
-__device__ __attribute__((always_inline)) inline uint32_t load_bits(const uint8_t *p)
-{
-    if constexpr (DT == NVFP4_F32) {
-        uint32_t w;
-        __builtin_memcpy(&w, p, 4);
-        return w;
-    } else {
-        uint16_t h;
-        __builtin_memcpy(&h, p, 2);
-        if constexpr (DT == NVFP4_BF16)
-            return (uint32_t)h << 16;
-        return __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(_Float16, h));
-    }
-}
-
-template <int DT>
 constexpr int kSize = DT == NVFP4_F32 ? 4 : 2;
 
 // ------------------------------------------------------------------ global scale
 
-// |x| as an ordered integer, 0 for NaN and infinities
-__device__ __attribute__((always_inline)) inline uint32_t finite_size(uint32_t bits)
+typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
+
+// Largest size in `top`: 16-bit types two at a time, their sizes being ordered
+// as integers. Infinities and NaN are the largest integers and win.
+template <int DT>
+__device__ __attribute__((always_inline)) inline uint32_t max_size(uint32_t top, uint32_t w)
 {
-    const uint32_t a = bits & 0x7FFFFFFFu;
-    return a < 0x7F800000u ? a : 0u;
+    if constexpr (DT == NVFP4_F32)
+        return max(top, w & 0x7FFFFFFFu);
+    const ushort2_t m = __builtin_elementwise_max(__builtin_bit_cast(ushort2_t, top),
+                                                  __builtin_bit_cast(ushort2_t, w & 0x7FFF7FFFu));
+    return __builtin_bit_cast(uint32_t, m);
 }
 
-// Grid-stride over pieces of 16 elements of every row; maxima are joined with
-// an atomic maximum (any order gives the same result), the last workgroup (by
-// ticket) writes the scale and clears the two counters.
+// The same, values that are not finite passed over.
+template <int DT>
+__device__ __attribute__((always_inline)) inline uint32_t max_finite(uint32_t top, uint32_t w)
+{
+    if constexpr (DT == NVFP4_F32)
+        return (w & 0x7FFFFFFFu) < 0x7F800000u ? max_size<DT>(top, w) : top;
+    constexpr uint32_t inf = DT == NVFP4_BF16 ? 0x7F80u : 0x7C00u;
+    w &= 0x7FFF7FFFu;
+    w = (w & 0xFFFFu) >= inf ? w & 0xFFFF0000u : w;
+    w = (w >> 16) >= inf ? w & 0xFFFFu : w;
+    return max_size<DT>(top, w);
+}
+
+template <int DT>
+__device__ __attribute__((always_inline)) inline bool all_finite(uint32_t top)
+{
+    if constexpr (DT == NVFP4_F32)
+        return top < 0x7F800000u;
+    constexpr uint32_t inf = DT == NVFP4_BF16 ? 0x7F80u : 0x7C00u;
+    return (top & 0xFFFFu) < inf && (top >> 16) < inf;
+}
+
+// One thread's share: 16-byte pieces i, i + step, .. of `rows` rows of `per_row`
+// pieces (the last of a row may be partial), U loads in flight. FINITE: passes
+// over what is not finite.
+template <int DT, bool FINITE>
+__device__ __attribute__((always_inline)) inline uint32_t scan_share(const uint8_t *__restrict__ x, int64_t i,
+                                                                     int64_t step, int64_t pieces, int64_t per_row,
+                                                                     int64_t K, int64_t rows, int64_t row_bytes,
+                                                                     int64_t batch_bytes)
+{
+    constexpr int U = 8, N = 16 / kSize<DT>;
+    uint32_t top = 0;
+    auto take = [&](uint32_t w) { top = FINITE ? max_finite<DT>(top, w) : max_size<DT>(top, w); };
+    for (; i < pieces; i += U * step) {
+        uint32_t v[U][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t at = min(i + u * step, pieces - 1);      // past the end: the last piece again
+            int64_t r = 0, k = at;
+            if (per_row != pieces) {
+                r = pieces < INT32_MAX ? (int64_t)((uint32_t)at / (uint32_t)per_row) : at / per_row;
+                k = at - r * per_row;
+            }
+            int64_t l = 0;
+            if (r >= rows) {
+                l = r / rows;
+                r -= l * rows;
+            }
+            const uint8_t *p = x + l * batch_bytes + r * row_bytes + k * 16;
+            if (k * N + N <= K) {
+                __builtin_memcpy(v[u], p, 16);
+            } else {
+                v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0u;
+#pragma unroll
+                for (int j = 0; j < N - 1; ++j) {
+                    if (k * N + j < K) {
+                        if constexpr (DT == NVFP4_F32)
+                            v[u][j] = ((const uint32_t *)p)[j];
+                        else
+                            v[u][j / 2] |= (uint32_t)((const uint16_t *)p)[j] << (16 * (j % 2));
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                take(v[u][j]);
+    }
+    return top;
+}
+
+// A thread that meets a value that is not finite reads its share again.
+// Maxima are joined with an atomic maximum (any order gives the same result);
+// the last workgroup (by ticket) writes the scale and clears the two counters.
+// 8192x7168 bf16: 117 MB, bound by HBM.
 template <int DT>
 __global__ __launch_bounds__(kAmaxThreads) void nvfp4_global_scale_kernel(
-    const uint8_t *__restrict__ x, float *__restrict__ scale, uint32_t *__restrict__ ws, int64_t pieces, int64_t K,
-    int64_t rows, int64_t row_bytes, int64_t batch_bytes, int32_t per_row)
+    const uint8_t *__restrict__ x, float *__restrict__ scale, uint32_t *__restrict__ ws, int64_t pieces,
+    int64_t per_row, int64_t K, int64_t rows, int64_t row_bytes, int64_t batch_bytes)
 {
-    uint32_t top = 0;
-    const int64_t step = (int64_t)gridDim.x * kAmaxThreads;
-    for (int64_t i = (int64_t)blockIdx.x * kAmaxThreads + threadIdx.x; i < pieces; i += step) {
-        const int64_t r = i / per_row, k = (i - r * per_row) * 16;
-        const int64_t l = r / rows;
-        const uint8_t *p = x + l * batch_bytes + (r - l * rows) * row_bytes + k * kSize<DT>;
-        if (k + 16 <= K) {
-            float v[16];
-            load16<DT>(p, v);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                top = max(top, finite_size(__builtin_bit_cast(uint32_t, v[j])));
-        } else {
-            for (int64_t j = k; j < K; ++j)
-                top = max(top, finite_size(load_bits<DT>(p + (j - k) * kSize<DT>)));
-        }
-    }
+    const int64_t step = (int64_t)gridDim.x * kAmaxThreads, i = (int64_t)blockIdx.x * kAmaxThreads + threadIdx.x;
+    uint32_t top = scan_share<DT, false>(x, i, step, pieces, per_row, K, rows, row_bytes, batch_bytes);
+    if (!all_finite<DT>(top))
+        top = scan_share<DT, true>(x, i, step, pieces, per_row, K, rows, row_bytes, batch_bytes);
+    // as float32 bits
+    if constexpr (DT == NVFP4_BF16)
+        top = max(top & 0xFFFFu, top >> 16) << 16;
+    else if constexpr (DT == NVFP4_F16)
+        top = __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(_Float16, (uint16_t)max(top & 0xFFFFu, top >> 16)));
 #pragma unroll
     for (int d = 32; d; d >>= 1)
         top = max(top, (uint32_t)__shfl_xor((int)top, d));
@@ -182,6 +240,15 @@ __device__ __attribute__((always_inline)) inline uint32_t value_code(float x, fl
     return n | ((__builtin_bit_cast(uint32_t, x) >> 31) << 3);
 }
 
+// 8 values times r -> 8 codes
+__device__ __attribute__((always_inline)) inline void convert8(const float *v, float r, uint32_t &w)
+{
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0] * r, v[1] * r, 1.0f, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2] * r, v[3] * r, 1.0f, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4] * r, v[5] * r, 1.0f, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6] * r, v[7] * r, 1.0f, 3);
+}
+
 // One block of 16 values -> 8 bytes of codes and the scale code.
 __device__ __attribute__((always_inline)) inline uint2_t quantize_block(const float (&v)[16], float g, bool g_good,
                                                                         uint32_t &scale)
@@ -201,6 +268,19 @@ __device__ __attribute__((always_inline)) inline uint2_t quantize_block(const fl
     if (scale == 0u)
         return (uint2_t){0u, 0u};
     const float s = e4m3_value(scale);
+    // The reciprocal, the products and s * g are off by less than 2^-21 together:
+    // the exact quotients lie between the products with r (1 -+ 2^-21). Where the
+    // conversion (nearest, ties to even) gives both ends the same codes, those
+    // are the exact quotients' codes; else a quotient is close to a midpoint.
+    const float u = s * g, r = __builtin_amdgcn_rcpf(u);
+    const float r0 = r * (1.0f - 0x1p-21f), r1 = r * (1.0f + 0x1p-21f);
+    uint32_t w0[2] = {0u, 0u}, w1[2] = {0u, 0u};
+    convert8(v, r0, w0[0]);
+    convert8(v + 8, r0, w0[1]);
+    convert8(v, r1, w1[0]);
+    convert8(v + 8, r1, w1[1]);
+    if (w0[0] == w1[0] && w0[1] == w1[1] && u < 0x1p100f && amax < __builtin_inff())
+        return (uint2_t){w0[0], w0[1]};
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
     for (int i = 0; i < 16; ++i)
@@ -389,12 +469,16 @@ nvfp4_status_t nvfp4_global_scale(const void *x, int dtype, float *scale, int64_
         return NVFP4_ERR_MISALIGNED;
     if (!workspace || workspace_bytes < nvfp4_global_scale_workspace_bytes() || !aligned(workspace, 256))
         return NVFP4_ERR_WORKSPACE;
-    const int64_t per_row = (K + 15) / 16, pieces = rows * L * per_row;
+    const int64_t n = 16 / size;
+    // a dense tensor is one row
+    const bool dense = (rows == 1 || row_stride == K) && (L == 1 || batch_stride == rows * K);
+    const int64_t cols = dense ? L * rows * K : K, lines = dense ? 1 : rows;
+    const int64_t per_row = (cols + n - 1) / n, pieces = dense ? per_row : rows * L * per_row;
     const int64_t grid = std::min<int64_t>(kAmaxMaxGrid, (pieces + kAmaxThreads - 1) / kAmaxThreads);
     by_type(dtype, [&](auto dt) {
         hipLaunchKernelGGL((nvfp4_global_scale_kernel<dt()>), dim3((uint32_t)grid), dim3(kAmaxThreads), 0,
-                           (hipStream_t)stream, (const uint8_t *)x, scale, (uint32_t *)workspace, pieces, K, rows,
-                           row_stride * size, batch_stride * size, (int32_t)per_row);
+                           (hipStream_t)stream, (const uint8_t *)x, scale, (uint32_t *)workspace, pieces, per_row, cols,
+                           lines, row_stride * size, batch_stride * size);
     });
     return finish();
 }

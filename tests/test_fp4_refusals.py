@@ -32,7 +32,7 @@ def experts(a=P, b=P, sfa=P, sfb=P, c=P, dtype=1, M=64, K=64, E=4, rows=8, per=2
                                       n, None)
 
 
-def route(logits=P, dtype=1, bias=P, ids=P, weights=P, off=P, order=P, T=4, E=8, k=2, score=0, n_group=1, topk_group=1,
+def route(logits=P, dtype=1, bias=P, ids=P, weights=P, off=P, order=P, T=400, E=8, k=2, score=0, n_group=1, topk_group=1,
           group_top=1, renorm=1, scaling=1.0, ws=P, n=1 << 20, opts=True):
     o = g.Routing(score, n_group, topk_group, group_top, renorm, scaling)
     return g.lib().nvfp4_moe_route(logits, dtype, bias, ids, weights, off, order, T, E, k,

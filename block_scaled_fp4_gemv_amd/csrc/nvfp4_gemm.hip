@@ -655,15 +655,15 @@ __global__ __launch_bounds__(kThreads, T::kPerCu) void nvfp4_gemm_wide_kernel(Ge
 
 // ------------------------------------------------------------------ wave kernel
 
-// KW waves, each FM x FN fragments of the workgroup's tile over every KW-th
-// stage, NS stages in each wave's ring.
-template <int FM, int FN, int KW, int NS, int PER_CU>
+// WM x KW waves: WM of them share the rows of A, each with FM x FN fragments, and
+// KW take a row range's stages in turn; NS stages in each wave's ring.
+template <int FM, int FN, int WM, int KW, int NS, int PER_CU>
 struct WaveTile {
-    static constexpr int kFM = FM, kFN = FN, kKW = KW, kNS = NS, kPerCu = PER_CU;
-    static constexpr int BM = 32 * FM, BN = 32 * FN, kThreads = 64 * KW;
-    static constexpr int kOffB = BM * 64, kOffSA = kOffB + BN * 64;
-    static constexpr int stage_bytes(bool odd) { return kOffSA + (BM + BN) * (odd ? 16 : 8); }
-    static constexpr int lds_bytes(bool odd) { return std::max(KW * NS * stage_bytes(odd), KW * FM * FN * 4096); }
+    static constexpr int kFM = FM, kFN = FN, kWM = WM, kKW = KW, kNS = NS, kPerCu = PER_CU;
+    static constexpr int kWaveM = 32 * FM, BM = kWaveM * WM, BN = 32 * FN, kThreads = 64 * WM * KW;
+    static constexpr int kOffB = kWaveM * 64, kOffSA = kOffB + BN * 64;
+    static constexpr int stage_bytes(bool odd) { return kOffSA + (kWaveM + BN) * (odd ? 16 : 8); }
+    static constexpr int lds_bytes(bool odd) { return std::max(WM * KW * NS * stage_bytes(odd), KW > 1 ? WM * KW * FM * FN * 4096 : 0); }
     static_assert(lds_bytes(true) + kStaticLds <= kLdsBytes);
 };
 
@@ -671,18 +671,21 @@ template <class T, bool EXPERTS, bool ODD>
 __global__ __launch_bounds__(T::kThreads, T::kPerCu) void nvfp4_gemm_wave_kernel(GemmParams p)
 {
     constexpr int FM = T::kFM, FN = T::kFN, KW = T::kKW, NS = T::kNS, BM = T::BM, BN = T::BN, F = FM + FN;
-    constexpr int kStage = T::stage_bytes(ODD), kWordsA = BM * 8, kWordsB = BN * 8;
+    constexpr int kStage = T::stage_bytes(ODD), kWordsA = T::kWaveM * 8, kWordsB = BN * 8;
     constexpr int kOffSB = T::kOffSA + kWordsA * (ODD ? 2 : 1);
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     __shared__ int32_t s_slot[EXPERTS ? BN : 1];
     __shared__ uint32_t s_ticket;
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const Where w = locate<EXPERTS, BM, BN, T::kThreads>(p, s_slot);
+    Where w = locate<EXPERTS, BM, BN, T::kThreads>(p, s_slot);
     if (EXPERTS && w.l < 0)
         return;
-    // this wave's stages: first + wave, first + wave + KW, ..
-    const int first = w.split * p.stages_per_split + wave;
+    // this wave's rows (its first may lie past M: then it works on row M - 1 and stores nothing)
+    const int wk = wave % KW, rows0 = w.m0 + wave / KW * T::kWaveM;
+    w.m0 = min(rows0, p.M - 1);
+    // and stages: first, first + KW, ..
+    const int first = w.split * p.stages_per_split + wk;
     const int end = min((w.split + 1) * p.stages_per_split, p.stages);
     const int stages = first < end ? (end - first + KW - 1) / KW : 0;
     // copies of B's codes: 16 rows each, only those that hold rows of the tile
@@ -809,30 +812,39 @@ __global__ __launch_bounds__(T::kThreads, T::kPerCu) void nvfp4_gemm_wave_kernel
         slot = slot + 1 == NS ? 0 : slot + 1;
     }
 
-    // --- the waves' sums through LDS, in the order of the waves: wave w takes
-    // registers w * R .. of the tile's FN * FM * 16
+    // --- the waves' sums through LDS, in the order of the waves: of the KW waves
+    // of a row range, wave wk takes registers wk * R .. of its FN * FM * 16
     constexpr int R = FN * FM * 16 / KW;
-    __syncthreads();
-    float *sums = (float *)lds;                                 // [wave][register][lane]
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                sums[(wave * (FN * FM * 16) + (j * FM + i) * 16 + r) * 64 + lane] = acc[j][i][r];
-    __syncthreads();
     float sum[R];
+    if constexpr (KW > 1) {
+        __syncthreads();
+        float *sums = (float *)lds + wave / KW * KW * (FN * FM * 1024);      // [wave][register][lane]
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    sums[(wk * (FN * FM * 16) + (j * FM + i) * 16 + r) * 64 + lane] = acc[j][i][r];
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < R; ++x) {
+            sum[x] = 0.0f;
+#pragma unroll
+            for (int o = 0; o < KW; ++o)
+                sum[x] += sums[(o * (FN * FM * 16) + wk * R + x) * 64 + lane];
+        }
+    } else {
+#pragma unroll
+        for (int x = 0; x < R; ++x)
+            sum[x] = acc[x / 16 / FM][x / 16 % FM][x % 16];
+    }
     int64_t at[R];
 #pragma unroll
     for (int x = 0; x < R; ++x) {
-        const int g = wave * R + x, f = g / 16, r = g % 16, j = f / FM, i = f % FM;
-        sum[x] = 0.0f;
-#pragma unroll
-        for (int o = 0; o < KW; ++o)
-            sum[x] += sums[(o * (FN * FM * 16) + g) * 64 + lane];
+        const int g = wk * R + x, f = g / 16, r = g % 16, j = f / FM, i = f % FM;
         const int64_t row = row_at<EXPERTS>(p, w, s_slot, 32 * j + 8 * (r / 4) + 4 * half + r % 4);
-        const int m = w.m0 + 32 * i + l32;
+        const int m = rows0 + 32 * i + l32;
         at[x] = row < 0 || m >= p.M ? -1 : row + m;
     }
     if (p.splits > 1) {
@@ -843,7 +855,19 @@ __global__ __launch_bounds__(T::kThreads, T::kPerCu) void nvfp4_gemm_wave_kernel
                 __hip_atomic_store(&p.partials[w.split * one + at[x]], sum[x], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         if (!last_of_tile(p, w.tile, &s_ticket))
             return;
-        add_slices<R>(p, one, at, sum);
+#pragma unroll
+        for (int g = 0; g < R; g += R < 8 ? R : 8) {
+            constexpr int G = R < 8 ? R : 8;
+            int64_t some[G];
+            float part[G];
+#pragma unroll
+            for (int x = 0; x < G; ++x)
+                some[x] = at[g + x];
+            add_slices<G>(p, one, some, part);
+#pragma unroll
+            for (int x = 0; x < G; ++x)
+                sum[g + x] = part[x];
+        }
     }
     const float scale = total_scale<EXPERTS>(p, w.l);
 #pragma unroll
@@ -858,10 +882,12 @@ typedef Tile<4, 4, 2, 2, 4, 1> TileLarge;       // 256 x 256
 typedef Tile<4, 2, 2, 2, 3, 1> TileTall;        // 256 x 128
 typedef Tile<2, 2, 2, 2, 3, 2> TileMid;         // 128 x 128
 typedef Tile<2, 1, 2, 2, 3, 2> TileNarrow;      // 128 x 64
-typedef WaveTile<2, 2, 4, 3, 1> TileWave2;         // 64 x 64
-typedef WaveTile<1, 1, 4, 4, 2> TileWave1;         // 32 x 32
+typedef WaveTile<1, 2, 4, 1, 3, 1> TileWave64;  // 128 x 64
+typedef WaveTile<1, 2, 1, 4, 3, 1> TileWave64K; // 32 x 64, 4 waves along K
+typedef WaveTile<1, 1, 4, 1, 4, 2> TileWave32;  // 128 x 32
+typedef WaveTile<1, 1, 1, 4, 4, 2> TileWave32K; // 32 x 32, 4 waves along K
 
-enum class Kind { Large, Tall, Mid, Narrow, Wave2, Wave1 };
+enum class Kind { Large, Tall, Mid, Narrow, Wave64, Wave64K, Wave32, Wave32K };
 
 struct Plan {
     Kind kind;
@@ -901,11 +927,11 @@ Plan dense_plan(int64_t M, int64_t N, int64_t K, int64_t L)
         p.tiles = p.tiles_m * p.tiles_n * L;
     };
     if (N <= 32) {
-        p.kind = Kind::Wave1;
-        tiles(TileWave1::BM, TileWave1::BN);
+        p.kind = Kind::Wave32K;
+        tiles(TileWave32K::BM, TileWave32K::BN);
     } else if (N <= 64) {
-        p.kind = Kind::Wave2;
-        tiles(TileWave2::BM, TileWave2::BN);
+        p.kind = Kind::Wave64K;
+        tiles(TileWave64K::BM, TileWave64K::BN);
     } else {
         p.kind = Kind::Large;
         tiles(TileLarge::BM, TileLarge::BN);
@@ -929,11 +955,11 @@ Plan experts_plan(int64_t M, int64_t K, int64_t E, int64_t S)
     };
     const int64_t mean = ceil_div(S, E);
     if (mean <= 32) {
-        p.kind = Kind::Wave1;
-        tiles(TileWave1::BM, TileWave1::BN);
+        p.kind = Kind::Wave32K;
+        tiles(TileWave32K::BM, TileWave32K::BN);
     } else if (mean <= 64) {
-        p.kind = Kind::Wave2;
-        tiles(TileWave2::BM, TileWave2::BN);
+        p.kind = Kind::Wave64K;
+        tiles(TileWave64K::BM, TileWave64K::BN);
     } else {
         p.kind = Kind::Mid;
         tiles(TileMid::BM, TileMid::BN);
@@ -982,8 +1008,10 @@ nvfp4_status_t run(const Plan &plan, const GemmParams &p, hipStream_t st)
     case Kind::Tall: e = launch_wide<TileTall, EXPERTS>(p, grid, st); break;
     case Kind::Mid: e = launch_wide<TileMid, EXPERTS>(p, grid, st); break;
     case Kind::Narrow: e = launch_wide<TileNarrow, EXPERTS>(p, grid, st); break;
-    case Kind::Wave2: e = launch_wave<TileWave2, EXPERTS>(p, grid, st); break;
-    case Kind::Wave1: e = launch_wave<TileWave1, EXPERTS>(p, grid, st); break;
+    case Kind::Wave64: e = launch_wave<TileWave64, EXPERTS>(p, grid, st); break;
+    case Kind::Wave64K: e = launch_wave<TileWave64K, EXPERTS>(p, grid, st); break;
+    case Kind::Wave32: e = launch_wave<TileWave32, EXPERTS>(p, grid, st); break;
+    case Kind::Wave32K: e = launch_wave<TileWave32K, EXPERTS>(p, grid, st); break;
     }
     if (e == hipSuccess)
         return NVFP4_OK;

@@ -35,28 +35,31 @@ constexpr int64_t kMaxGrid = 0xFFFFFF;           // workgroups of 256 threads in
 
 // ------------------------------------------------------------------ loads
 
-// 16 consecutive elements as float32 (exact for every type). The address has
-// the type's own alignment only: gfx950 takes 16-byte global loads at any.
+// 16 consecutive elements, as loaded. The address has the type's own alignment
+// only: gfx950 takes 16-byte global loads at any.
 template <int DT>
-__device__ __attribute__((always_inline)) inline void load16(const uint8_t *p, float (&v)[16])
+struct Block {
+    uint32_t w[DT == NVFP4_F32 ? 16 : 8];
+};
+
+template <int DT>
+__device__ __attribute__((always_inline)) inline Block<DT> load_block(const uint8_t *p)
 {
-    if constexpr (DT == NVFP4_F32) {
-        __builtin_memcpy(v, p, 64);
-    } else {
-        uint32_t w[8];
-        __builtin_memcpy(w, p, 32);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if constexpr (DT == NVFP4_BF16) {
-                v[2 * i] = __builtin_bit_cast(float, w[i] << 16);
-                v[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xFFFF0000u);
-            } else {
-                const half2_t h = as_h2(w[i]);
-                v[2 * i] = (float)h.x;
-                v[2 * i + 1] = (float)h.y;
-            }
-        }
-    }
+    Block<DT> b;
+    __builtin_memcpy(&b, p, sizeof(b));
+    return b;
+}
+
+// element i as float32 (exact for every type)
+template <int DT>
+__device__ __attribute__((always_inline)) inline float element(const Block<DT> &b, int i)
+{
+    if constexpr (DT == NVFP4_F32)
+        return __builtin_bit_cast(float, b.w[i]);
+    else if constexpr (DT == NVFP4_BF16)
+        return __builtin_bit_cast(float, i % 2 ? b.w[i / 2] & 0xFFFF0000u : b.w[i / 2] << 16);
+    else
+        return i % 2 ? (float)as_h2(b.w[i / 2]).y : (float)as_h2(b.w[i / 2]).x;
 }
 
 template <int DT>
@@ -100,54 +103,66 @@ __device__ __attribute__((always_inline)) inline bool all_finite(uint32_t top)
     return (top & 0xFFFFu) < inf && (top >> 16) < inf;
 }
 
-// One thread's share: 16-byte pieces i, i + step, .. of `rows` rows of `per_row`
-// pieces (the last of a row may be partial), U loads in flight. FINITE: passes
-// over what is not finite.
-template <int DT, bool FINITE>
-__device__ __attribute__((always_inline)) inline uint32_t scan_share(const uint8_t *__restrict__ x, int64_t i,
-                                                                     int64_t step, int64_t pieces, int64_t per_row,
-                                                                     int64_t K, int64_t rows, int64_t row_bytes,
-                                                                     int64_t batch_bytes)
+// A size as max_size leaves it (16-bit types: the larger half) -> float32 bits
+template <int DT>
+__device__ __attribute__((always_inline)) inline uint32_t size_bits(uint32_t top)
+{
+    if constexpr (DT == NVFP4_BF16)
+        return max(top & 0xFFFFu, top >> 16) << 16;
+    else if constexpr (DT == NVFP4_F16)
+        return __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(_Float16, (uint16_t)max(top & 0xFFFFu, top >> 16)));
+    else
+        return top;
+}
+
+struct ScanParams {
+    int64_t pieces, per_row;                    // whole 16-byte pieces of all rows, of one
+    int64_t K, rows, lines;                     // rows per batch, rows of all batches
+    int64_t row_bytes, batch_bytes;
+};
+
+// One thread's share: pieces i, i + step, .., U loads in flight, then the rows'
+// last elements that fill no piece. FINITE: passes over what is not finite.
+// FLAT: one row.
+template <int DT, bool FINITE, bool FLAT>
+__device__ __attribute__((always_inline)) inline uint32_t scan_share(const uint8_t *__restrict__ x, const ScanParams &p,
+                                                                     int64_t i, int64_t step)
 {
     constexpr int U = 8, N = 16 / kSize<DT>;
     uint32_t top = 0;
     auto take = [&](uint32_t w) { top = FINITE ? max_finite<DT>(top, w) : max_size<DT>(top, w); };
-    for (; i < pieces; i += U * step) {
-        uint32_t v[U][4];
+    auto row_at = [&](int64_t r) {
+        const int64_t l = r < p.rows ? 0 : r / p.rows;
+        return x + l * p.batch_bytes + (r - l * p.rows) * p.row_bytes;
+    };
+    for (int64_t at = i; at < p.pieces; at += U * step) {
+        uint4_t v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t at = min(i + u * step, pieces - 1);      // past the end: the last piece again
-            int64_t r = 0, k = at;
-            if (per_row != pieces) {
-                r = pieces < INT32_MAX ? (int64_t)((uint32_t)at / (uint32_t)per_row) : at / per_row;
-                k = at - r * per_row;
+            const int64_t k = min(at + u * step, p.pieces - 1);    // past the end: the last piece again
+            const uint8_t *q = x + k * 16;
+            if constexpr (!FLAT) {
+                const int64_t r = p.pieces < INT32_MAX ? (int64_t)((uint32_t)k / (uint32_t)p.per_row) : k / p.per_row;
+                q = row_at(r) + (k - r * p.per_row) * 16;
             }
-            int64_t l = 0;
-            if (r >= rows) {
-                l = r / rows;
-                r -= l * rows;
-            }
-            const uint8_t *p = x + l * batch_bytes + r * row_bytes + k * 16;
-            if (k * N + N <= K) {
-                __builtin_memcpy(v[u], p, 16);
-            } else {
-                v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0u;
-#pragma unroll
-                for (int j = 0; j < N - 1; ++j) {
-                    if (k * N + j < K) {
-                        if constexpr (DT == NVFP4_F32)
-                            v[u][j] = ((const uint32_t *)p)[j];
-                        else
-                            v[u][j / 2] |= (uint32_t)((const uint16_t *)p)[j] << (16 * (j % 2));
-                    }
-                }
-            }
+            __builtin_memcpy(&v[u], q, 16);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                take(v[u][j]);
+        for (int u = 0; u < U; ++u) {
+            take(v[u].x);
+            take(v[u].y);
+            take(v[u].z);
+            take(v[u].w);
+        }
+    }
+    const int64_t rest = p.K - p.per_row * N;
+    for (int64_t at = i; at < p.lines * rest; at += step) {
+        const int64_t r = at / rest;
+        const uint8_t *q = row_at(r) + (p.per_row * N + (at - r * rest)) * kSize<DT>;
+        if constexpr (DT == NVFP4_F32)
+            take(*(const uint32_t *)q);
+        else
+            take(*(const uint16_t *)q);
     }
     return top;
 }
@@ -155,21 +170,16 @@ __device__ __attribute__((always_inline)) inline uint32_t scan_share(const uint8
 // A thread that meets a value that is not finite reads its share again.
 // Maxima are joined with an atomic maximum (any order gives the same result);
 // the last workgroup (by ticket) writes the scale and clears the two counters.
-// 8192x7168 bf16: 117 MB, bound by HBM.
-template <int DT>
-__global__ __launch_bounds__(kAmaxThreads) void nvfp4_global_scale_kernel(
-    const uint8_t *__restrict__ x, float *__restrict__ scale, uint32_t *__restrict__ ws, int64_t pieces,
-    int64_t per_row, int64_t K, int64_t rows, int64_t row_bytes, int64_t batch_bytes)
+template <int DT, bool FLAT>
+__global__ __launch_bounds__(kAmaxThreads) void nvfp4_global_scale_kernel(const uint8_t *__restrict__ x,
+                                                                         float *__restrict__ scale,
+                                                                         uint32_t *__restrict__ ws, ScanParams p)
 {
     const int64_t step = (int64_t)gridDim.x * kAmaxThreads, i = (int64_t)blockIdx.x * kAmaxThreads + threadIdx.x;
-    uint32_t top = scan_share<DT, false>(x, i, step, pieces, per_row, K, rows, row_bytes, batch_bytes);
+    uint32_t top = scan_share<DT, false, FLAT>(x, p, i, step);
     if (!all_finite<DT>(top))
-        top = scan_share<DT, true>(x, i, step, pieces, per_row, K, rows, row_bytes, batch_bytes);
-    // as float32 bits
-    if constexpr (DT == NVFP4_BF16)
-        top = max(top & 0xFFFFu, top >> 16) << 16;
-    else if constexpr (DT == NVFP4_F16)
-        top = __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(_Float16, (uint16_t)max(top & 0xFFFFu, top >> 16)));
+        top = scan_share<DT, true, FLAT>(x, p, i, step);
+    top = size_bits<DT>(top);
 #pragma unroll
     for (int d = 32; d; d >>= 1)
         top = max(top, (uint32_t)__shfl_xor((int)top, d));
@@ -205,12 +215,25 @@ __device__ __attribute__((always_inline)) inline float e4m3_value(uint32_t code)
     return __builtin_amdgcn_cvt_f32_fp8((int)code, 0);
 }
 
+// What the blocks need of the global scale.
+struct Global {
+    float g, per_g;                             // g and about 1 / (6 g), 0 where that is no normal number
+    bool good;
+};
+
+__device__ __attribute__((always_inline)) inline Global global_of(const float *gp)
+{
+    const float g = gp ? *gp : 1.0f;
+    return {g, g < 0x1p100f ? __builtin_amdgcn_rcpf(g) * (1.0f / 6.0f) : 0.0f, g >= kMinScale && g < __builtin_inff()};
+}
+
 // E4M3 code of the exact quotient amax / (6 g), amax finite or infinite, >= 0.
 // The float32 quotient is within a few units of its last place, so its code is
 // the right one or a neighbour; the two midpoints around it decide.
-__device__ __attribute__((always_inline)) inline uint32_t scale_code(float amax, float g)
+__device__ __attribute__((always_inline)) inline uint32_t scale_code(float amax, const Global &gl)
 {
-    const float v = fminf((amax / g) * (1.0f / 6.0f), 448.0f);
+    const float g = gl.g;
+    const float v = fminf(gl.per_g != 0.0f ? amax * gl.per_g : (amax / g) * (1.0f / 6.0f), 448.0f);
     uint32_t c = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xFFu;
     const float here = e4m3_value(c);
     const float above = e4m3_value(c < 126u ? c + 1 : c), below = e4m3_value(c > 0u ? c - 1 : c);
@@ -240,31 +263,33 @@ __device__ __attribute__((always_inline)) inline uint32_t value_code(float x, fl
     return n | ((__builtin_bit_cast(uint32_t, x) >> 31) << 3);
 }
 
-// 8 values times r -> 8 codes
-__device__ __attribute__((always_inline)) inline void convert8(const float *v, float r, uint32_t &w)
+// 8 values (from element i on) times r -> 8 codes
+template <int DT>
+__device__ __attribute__((always_inline)) inline uint32_t convert8(const Block<DT> &b, int i, float r)
 {
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0] * r, v[1] * r, 1.0f, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2] * r, v[3] * r, 1.0f, 1);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4] * r, v[5] * r, 1.0f, 2);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6] * r, v[7] * r, 1.0f, 3);
+    uint32_t w = 0u;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, element<DT>(b, i) * r, element<DT>(b, i + 1) * r, 1.0f, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, element<DT>(b, i + 2) * r, element<DT>(b, i + 3) * r, 1.0f, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, element<DT>(b, i + 4) * r, element<DT>(b, i + 5) * r, 1.0f, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, element<DT>(b, i + 6) * r, element<DT>(b, i + 7) * r, 1.0f, 3);
+    return w;
 }
 
 // One block of 16 values -> 8 bytes of codes and the scale code.
-__device__ __attribute__((always_inline)) inline uint2_t quantize_block(const float (&v)[16], float g, bool g_good,
+template <int DT>
+__device__ __attribute__((always_inline)) inline uint2_t quantize_block(const Block<DT> &b, const Global &gl,
                                                                         uint32_t &scale)
 {
-    float amax = 0.0f;
-    bool nan = !g_good;
+    uint32_t top = 0u;                          // sizes ordered as integers: NaN above infinity
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        amax = fmaxf(amax, fabsf(v[i]));
-        nan |= v[i] != v[i];
-    }
-    if (nan) {
+    for (int i = 0; i < (DT == NVFP4_F32 ? 16 : 8); ++i)
+        top = max_size<DT>(top, b.w[i]);
+    const float amax = __builtin_bit_cast(float, size_bits<DT>(top));
+    if (!gl.good || amax != amax) {
         scale = 0x7Fu;
         return (uint2_t){0u, 0u};
     }
-    scale = scale_code(amax, g);
+    scale = scale_code(amax, gl);
     if (scale == 0u)
         return (uint2_t){0u, 0u};
     const float s = e4m3_value(scale);
@@ -272,19 +297,16 @@ __device__ __attribute__((always_inline)) inline uint2_t quantize_block(const fl
     // the exact quotients lie between the products with r (1 -+ 2^-21). Where the
     // conversion (nearest, ties to even) gives both ends the same codes, those
     // are the exact quotients' codes; else a quotient is close to a midpoint.
-    const float u = s * g, r = __builtin_amdgcn_rcpf(u);
+    const float u = s * gl.g, r = __builtin_amdgcn_rcpf(u);
     const float r0 = r * (1.0f - 0x1p-21f), r1 = r * (1.0f + 0x1p-21f);
-    uint32_t w0[2] = {0u, 0u}, w1[2] = {0u, 0u};
-    convert8(v, r0, w0[0]);
-    convert8(v + 8, r0, w0[1]);
-    convert8(v, r1, w1[0]);
-    convert8(v + 8, r1, w1[1]);
-    if (w0[0] == w1[0] && w0[1] == w1[1] && u < 0x1p100f && amax < __builtin_inff())
-        return (uint2_t){w0[0], w0[1]};
+    const uint2_t w0 = {convert8<DT>(b, 0, r0), convert8<DT>(b, 8, r0)};
+    const uint2_t w1 = {convert8<DT>(b, 0, r1), convert8<DT>(b, 8, r1)};
+    if (w0.x == w1.x && w0.y == w1.y && u < 0x1p100f && amax < __builtin_inff())
+        return w0;
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-        w[i / 8] |= value_code(v[i], s, g) << (4 * (i % 8));
+        w[i / 8] |= value_code(element<DT>(b, i), s, gl.g) << (4 * (i % 8));
     return (uint2_t){w[0], w[1]};
 }
 
@@ -295,28 +317,23 @@ struct QParams {
     int32_t bands;                   // bands of rows per batch (blocked)
 };
 
-__device__ __attribute__((always_inline)) inline bool good_scale(float g)
-{
-    return g >= kMinScale && g < __builtin_inff();
-}
-
 // Plain scales: one thread per block, blocks of a batch in order.
 template <int DT>
 __global__ __launch_bounds__(kQThreads) void nvfp4_quantize_plain_kernel(
     const uint8_t *__restrict__ x, const float *__restrict__ gp, uint8_t *__restrict__ codes,
     uint8_t *__restrict__ scales, QParams p)
 {
-    const float g = gp ? *gp : 1.0f;
+    const Global gl = global_of(gp);
     const int64_t l = blockIdx.x / (uint32_t)p.wg_per_band;
-    const int64_t i = (int64_t)(blockIdx.x % (uint32_t)p.wg_per_band) * kQThreads + threadIdx.x;
+    // the grid keeps every index of a block below 2^32
+    const uint32_t i = (blockIdx.x % (uint32_t)p.wg_per_band) * kQThreads + threadIdx.x;
     if (i >= p.rows * p.nkb)
         return;
-    const int64_t r = i / p.nkb;
-    const int32_t kb = (int32_t)(i - r * p.nkb);
-    float v[16];
-    load16<DT>(x + l * p.batch_bytes + r * p.row_bytes + (int64_t)kb * 16 * kSize<DT>, v);
+    const int64_t r = i / (uint32_t)p.nkb;
+    const uint32_t kb = i % (uint32_t)p.nkb;
     uint32_t s;
-    const uint2_t q = quantize_block(v, g, good_scale(g), s);
+    const uint2_t q = quantize_block<DT>(
+        load_block<DT>(x + l * p.batch_bytes + r * p.row_bytes + (int64_t)kb * 16 * kSize<DT>), gl, s);
     const int64_t o = l * p.rows * p.nkb + i;
     *(uint2_t *)(codes + o * 8) = q;
     scales[o] = (uint8_t)s;
@@ -331,7 +348,7 @@ __global__ __launch_bounds__(kQThreads) void nvfp4_quantize_blocked_kernel(
     const uint8_t *__restrict__ x, const float *__restrict__ gp, uint8_t *__restrict__ codes,
     uint8_t *__restrict__ scales, QParams p)
 {
-    const float g = gp ? *gp : 1.0f;
+    const Global gl = global_of(gp);
     const int32_t t = threadIdx.x;
     const uint32_t band = blockIdx.x / (uint32_t)p.wg_per_band;            // batch * bands + 16-row band
     const int32_t kb = (int32_t)(blockIdx.x % (uint32_t)p.wg_per_band) * 16 + t % 16;
@@ -343,9 +360,8 @@ __global__ __launch_bounds__(kQThreads) void nvfp4_quantize_blocked_kernel(
     const int32_t ncb = (p.nkb + 3) / 4;
     uint32_t s = 0u;
     if (r < p.rows && kb < p.nkb) {
-        float v[16];
-        load16<DT>(x + l * p.batch_bytes + r * p.row_bytes + (int64_t)kb * 16 * kSize<DT>, v);
-        const uint2_t q = quantize_block(v, g, good_scale(g), s);
+        const uint2_t q = quantize_block<DT>(
+            load_block<DT>(x + l * p.batch_bytes + r * p.row_bytes + (int64_t)kb * 16 * kSize<DT>), gl, s);
         *(uint2_t *)(codes + ((l * p.rows + r) * p.nkb + kb) * 8) = q;
     }
     // four lanes' scales in one word, lane 0 of the four stores it
@@ -381,21 +397,21 @@ __device__ __attribute__((always_inline)) inline void store16(uint8_t *p, const 
 template <int DT, int LAYOUT>
 __global__ __launch_bounds__(kQThreads) void nvfp4_dequantize_kernel(
     const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, const float *__restrict__ gp,
-    uint8_t *__restrict__ out, int64_t rows, int64_t blocks, int32_t nkb)
+    uint8_t *__restrict__ out, uint32_t rows, int64_t blocks, uint32_t nkb)
 {
-    const int64_t i = (int64_t)blockIdx.x * kQThreads + threadIdx.x;
+    // the grid keeps every index of a block below 2^32
+    const uint32_t i = blockIdx.x * kQThreads + threadIdx.x;
     if (i >= blocks)
         return;
     const float g = gp ? *gp : 1.0f;
-    const int64_t lr = i / nkb;
-    const int32_t kb = (int32_t)(i - lr * nkb);
+    const uint32_t lr = i / nkb, kb = i % nkb;
     int64_t at = i;
     if constexpr (LAYOUT == NVFP4_SF_BLOCKED) {
-        const int64_t l = lr / rows, r = lr - l * rows;
-        const int64_t nrb = (rows + 127) / 128, ncb = (nkb + 3) / 4;
+        const uint32_t l = lr / rows, r = lr % rows, ncb = (nkb + 3) / 4;
+        const int64_t nrb = (rows + 127) / 128;
         at = ((l * nrb + r / 128) * ncb + kb / 4) * 512 + (r % 32) * 16 + ((r % 128) / 32) * 4 + kb % 4;
     }
-    const uint2_t q = *(const uint2_t *)(codes + i * 8);
+    const uint2_t q = *(const uint2_t *)(codes + (int64_t)i * 8);
     const float s = e4m3_value(scales[at]);
     float v[16];
     const uint32_t w[2] = {q.x, q.y};
@@ -408,7 +424,7 @@ __global__ __launch_bounds__(kQThreads) void nvfp4_dequantize_kernel(
             v[8 * d + 2 * j + 1] = (float)h[j].y * s * g;
         }
     }
-    store16<DT>(out + i * 16 * kSize<DT>, v);
+    store16<DT>(out + (int64_t)i * 16 * kSize<DT>, v);
 }
 
 // ------------------------------------------------------------------ host
@@ -471,14 +487,23 @@ nvfp4_status_t nvfp4_global_scale(const void *x, int dtype, float *scale, int64_
         return NVFP4_ERR_WORKSPACE;
     const int64_t n = 16 / size;
     // a dense tensor is one row
-    const bool dense = (rows == 1 || row_stride == K) && (L == 1 || batch_stride == rows * K);
-    const int64_t cols = dense ? L * rows * K : K, lines = dense ? 1 : rows;
-    const int64_t per_row = (cols + n - 1) / n, pieces = dense ? per_row : rows * L * per_row;
-    const int64_t grid = std::min<int64_t>(kAmaxMaxGrid, (pieces + kAmaxThreads - 1) / kAmaxThreads);
+    const bool flat = (rows == 1 || row_stride == K) && (L == 1 || batch_stride == rows * K);
+    ScanParams p{};
+    p.K = flat ? L * rows * K : K;
+    p.rows = flat ? 1 : rows;
+    p.lines = flat ? 1 : rows * L;
+    p.per_row = p.K / n;
+    p.pieces = p.lines * p.per_row;
+    p.row_bytes = row_stride * size;
+    p.batch_bytes = batch_stride * size;
+    const int64_t units = std::max<int64_t>(p.pieces, p.lines);
+    const int64_t grid = std::min<int64_t>(kAmaxMaxGrid, (units + kAmaxThreads - 1) / kAmaxThreads);
     by_type(dtype, [&](auto dt) {
-        hipLaunchKernelGGL((nvfp4_global_scale_kernel<dt()>), dim3((uint32_t)grid), dim3(kAmaxThreads), 0,
-                           (hipStream_t)stream, (const uint8_t *)x, scale, (uint32_t *)workspace, pieces, per_row, cols,
-                           lines, row_stride * size, batch_stride * size);
+        auto go = [&](auto kern) {
+            hipLaunchKernelGGL(kern, dim3((uint32_t)grid), dim3(kAmaxThreads), 0, (hipStream_t)stream,
+                               (const uint8_t *)x, scale, (uint32_t *)workspace, p);
+        };
+        flat ? go(nvfp4_global_scale_kernel<dt(), true>) : go(nvfp4_global_scale_kernel<dt(), false>);
     });
     return finish();
 }
@@ -552,8 +577,8 @@ nvfp4_status_t nvfp4_dequantize(const void *codes, const void *scales, const flo
     by_type(dtype, [&](auto dt) {
         auto go = [&](auto kern) {
             hipLaunchKernelGGL(kern, dim3((uint32_t)grid), dim3(kQThreads), 0, (hipStream_t)stream,
-                               (const uint8_t *)codes, (const uint8_t *)scales, global_scale, (uint8_t *)out, rows,
-                               blocks, (int32_t)nkb);
+                               (const uint8_t *)codes, (const uint8_t *)scales, global_scale, (uint8_t *)out,
+                               (uint32_t)rows, blocks, (uint32_t)nkb);
         };
         sf_layout == NVFP4_SF_BLOCKED ? go(nvfp4_dequantize_kernel<dt(), NVFP4_SF_BLOCKED>)
                                       : go(nvfp4_dequantize_kernel<dt(), NVFP4_SF_PLAIN>);

@@ -48,8 +48,6 @@ namespace {
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float16_t __attribute__((ext_vector_type(16)));
 
-constexpr int kThreads = 256;                   // wide kernel
-constexpr int kWaves = 4;
 constexpr int kLdsBytes = 160 * 1024;           // LDS of a CU
 constexpr int kStaticLds = 2048;                // slot table and ticket, at most
 constexpr int kStageK = 128;                    // k per stage
@@ -62,6 +60,15 @@ constexpr int64_t kMaxGrid = 0xFFFFFF;          // workgroups of 256 threads in 
 
 // ------------------------------------------------------------------ copies to LDS
 
+// A pointer that is the same in every lane, in scalar registers (nothing to do
+// where the compiler has it there).
+__device__ __attribute__((always_inline)) inline const uint8_t *uniform_ptr(const uint8_t *p)
+{
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uintptr_t)p >> 32));
+    return (const uint8_t *)(uintptr_t)((uint64_t)hi << 32 | lo);
+}
+
 // 16, 4 or 2 bytes per lane from base + off into LDS at dst + lane * 16 (lane *
 // 4; 2 bytes land in the low half of a dword). The base is uniform and steps
 // along K in scalar registers, the lane's offset stays. The compiler does not
@@ -70,15 +77,15 @@ constexpr int64_t kMaxGrid = 0xFFFFFF;          // workgroups of 256 threads in 
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __attribute__((always_inline)) inline void copy16(const uint8_t *base, uint32_t off, uint32_t dst)
 {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "s"(dst) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(uniform_ptr(base)), "s"(dst) : "memory", "m0");
 }
 __device__ __attribute__((always_inline)) inline void copy4(const uint8_t *base, uint32_t off, uint32_t dst)
 {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(base), "s"(dst) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(uniform_ptr(base)), "s"(dst) : "memory", "m0");
 }
 __device__ __attribute__((always_inline)) inline void copy2(const uint8_t *base, uint32_t off, uint32_t dst)
 {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_ushort %0, %1" : : "v"(off), "s"(base), "s"(dst) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_ushort %0, %1" : : "v"(off), "s"(uniform_ptr(base)), "s"(dst) : "memory", "m0");
 }
 #pragma clang diagnostic pop
 
@@ -205,57 +212,86 @@ struct Where {
     int split;
 };
 
+// The experts e0 .. e0 + 63, one per lane: start and length of the list, and the
+// lists' tiles summed up to and including the lane's.
+struct Lists {
+    int from, n, tiles, upto;
+};
+
+template <int BN>
+__device__ __attribute__((always_inline)) inline Lists lists_at(const GemmParams &p, int e0)
+{
+    const int lane = threadIdx.x % 64, e = e0 + lane;
+    Lists s{};
+    if (e < p.L) {
+        s.from = min(max(p.offsets[e], 0), p.N);
+        s.n = max(min(max(p.offsets[e + 1], 0), p.N) - s.from, 0);
+    }
+    s.tiles = s.upto = (s.n + BN - 1) / BN;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(s.upto, d);
+        s.upto += lane >= d ? v : 0;
+    }
+    return s;
+}
+
 template <bool EXPERTS, int BM, int BN, int THREADS>
 __device__ __attribute__((always_inline)) inline Where locate(const GemmParams &p, int32_t *s_slot)
 {
-    const int lane = threadIdx.x % 64;
     Where w;
-    uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
-    w.split = (int)(id % (uint32_t)p.splits);
-    id /= (uint32_t)p.splits;
-    w.tile = id;
     if constexpr (EXPERTS) {
-        w.m0 = (int)(id % (uint32_t)p.tiles_m) * BM;
-        int want = (int)(id / (uint32_t)p.tiles_m);
-        // the expert whose list holds tile `want` of all lists' tiles: 64 experts at a time
-        int found = -1;
+        // The grid holds as many workgroups as any lists may need; the first
+        // `total` of them work, so that all XCDs get their share of these.
+        const Lists head = lists_at<BN>(p, 0);
+        int64_t total = __shfl(head.upto, 63);
+        for (int e0 = 64; e0 < p.L; e0 += 64)
+            total += __shfl(lists_at<BN>(p, e0).upto, 63);
+        const uint32_t wgs = __builtin_amdgcn_readfirstlane((uint32_t)min(total * p.tiles_m * p.splits, (int64_t)gridDim.x));
+        w.l = -1;
+        if (blockIdx.x >= wgs)
+            return w;                           // the whole workgroup
+        uint32_t id = xcd_remap(blockIdx.x, wgs);
+        w.split = (int)(id % (uint32_t)p.splits);
+        id /= (uint32_t)p.splits;
+        w.tile = id;
+        // Tiles in the order of experts, then rows of A, then the list's tiles, so
+        // that neighbours share the expert's weights.
+        int64_t want = id;
+        int found = -1, row = 0;
         w.n0 = w.count = 0;
         for (int e0 = 0; e0 < p.L; e0 += 64) {
-            const int e = e0 + lane;
-            int from = 0, n = 0;
-            if (e < p.L) {
-                from = min(max(p.offsets[e], 0), p.N);
-                n = max(min(max(p.offsets[e + 1], 0), p.N) - from, 0);
-            }
-            const int tiles = (n + BN - 1) / BN;
-            int upto = tiles;                   // inclusive sum over the lanes
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int v = __shfl_up(upto, d);
-                upto += lane >= d ? v : 0;
-            }
-            const uint64_t past = __ballot(upto > want);
+            const Lists s = e0 == 0 ? head : lists_at<BN>(p, e0);
+            const uint64_t past = __ballot((int64_t)s.upto * p.tiles_m > want);
             if (past) {
                 const int src = __ffsll((unsigned long long)past) - 1;
-                const int in_list = want - (__shfl(upto, src) - __shfl(tiles, src));
+                const int own = __shfl(s.tiles, src);
+                const uint32_t in_list = (uint32_t)(want - (int64_t)(__shfl(s.upto, src) - own) * p.tiles_m);
                 found = e0 + src;
-                w.n0 = __shfl(from, src) + in_list * BN;
-                w.count = min(BN, __shfl(n, src) - in_list * BN);
+                row = (int)(in_list / (uint32_t)own);
+                const int at = (int)(in_list % (uint32_t)own) * BN;
+                w.n0 = __shfl(s.from, src) + at;
+                w.count = min(BN, __shfl(s.n, src) - at);
                 break;
             }
-            want -= __shfl(upto, 63);
+            want -= (int64_t)__shfl(s.upto, 63) * p.tiles_m;
         }
+        w.m0 = __builtin_amdgcn_readfirstlane(row) * BM;
         w.l = __builtin_amdgcn_readfirstlane(found);
         w.n0 = __builtin_amdgcn_readfirstlane(w.n0);
         w.count = __builtin_amdgcn_readfirstlane(w.count);
         if (w.l < 0)
-            return w;                           // past the last tile (the whole workgroup)
+            return w;
         for (int i = threadIdx.x; i < BN; i += THREADS) {
             const int s = i < w.count ? p.order[w.n0 + i] : -1;
             s_slot[i] = s >= 0 && s < p.N ? s : -1;
         }
         __syncthreads();
     } else {
+        uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
+        w.split = (int)(id % (uint32_t)p.splits);
+        id /= (uint32_t)p.splits;
+        w.tile = id;
         // bands of 8 tiles along n, so that one XCD's tiles share rows of both
         const uint32_t per = (uint32_t)p.tiles_m * (uint32_t)p.tiles_n;
         w.l = (int)(id / per);
@@ -314,6 +350,8 @@ __device__ __attribute__((always_inline)) inline uint32_t words_at_b(const GemmP
     return (uint32_t)scale_word_at(p.blocked, min(i, w.count - 1) + (p.blocked ? w.n0 % 128 : 0), half, p.K / 16);
 }
 
+// alpha and the global scales. Loaded before the product and kept: read at the
+// end, they would add a memory round trip to every tile.
 template <bool EXPERTS>
 __device__ __attribute__((always_inline)) inline float total_scale(const GemmParams &p, int l)
 {
@@ -387,7 +425,8 @@ __device__ __attribute__((always_inline)) inline void add_slices(const GemmParam
 // registers for PER_CU workgroups per CU.
 template <int FM, int FN, int WM, int WN, int NS, int PER_CU>
 struct Tile {
-    static_assert(WM * WN == kWaves && NS >= 3);
+    static_assert(NS >= 2);
+    static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves, kPerSimd = PER_CU * kWaves / 4;
     static constexpr int kFM = FM, kFN = FN, kWM = WM, kWN = WN, kNS = NS, kPerCu = PER_CU;
     static constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
     // words per line of a scale tile: 32-row groups that share a line
@@ -401,14 +440,16 @@ struct Tile {
     static constexpr int stage_bytes(bool odd) { return kOffSA + (BM + BN) * (odd ? 16 : 8); }
     // one stage fewer where the halves of the words leave no room for NS
     static constexpr int ring(bool odd) { return NS * stage_bytes(odd) + kStaticLds <= kLdsBytes ? NS : NS - 1; }
-    static constexpr int lds_bytes(bool odd) { return ring(odd) * stage_bytes(odd); }
-    static_assert(ring(true) >= 3 && lds_bytes(true) + kStaticLds <= kLdsBytes && ring(false) == NS);
+    // results of one fragment row per wave pass through LDS: 32 rows of FM * 32 values
+    static constexpr int kPitch = FM * 128 + 16, kOutLds = kWaves * 32 * kPitch;
+    static constexpr int lds_bytes(bool odd) { return std::max(ring(odd) * stage_bytes(odd), kOutLds); }
+    static_assert(ring(true) >= 2 && PER_CU * (lds_bytes(false) + kStaticLds) <= kLdsBytes && lds_bytes(true) + kStaticLds <= kLdsBytes && ring(false) == NS);
 };
 
 template <class T, bool EXPERTS, bool ODD>
-__global__ __launch_bounds__(kThreads, T::kPerCu) void nvfp4_gemm_wide_kernel(GemmParams p)
+__global__ __launch_bounds__(T::kThreads, T::kPerSimd) void nvfp4_gemm_wide_kernel(GemmParams p)
 {
-    constexpr int FM = T::kFM, FN = T::kFN, NS = T::ring(ODD), BM = T::BM, BN = T::BN, F = FM + FN;
+    constexpr int FM = T::kFM, FN = T::kFN, NS = T::ring(ODD), BM = T::BM, BN = T::BN, F = FM + FN, kWaves = T::kWaves;
     constexpr int kStage = T::stage_bytes(ODD), kWordsA = BM * 8, kWordsB = BN * 8;
     constexpr int kOffSB = T::kOffSA + kWordsA * (ODD ? 2 : 1);
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -416,7 +457,7 @@ __global__ __launch_bounds__(kThreads, T::kPerCu) void nvfp4_gemm_wide_kernel(Ge
     __shared__ uint32_t s_ticket;
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const Where w = locate<EXPERTS, BM, BN, kThreads>(p, s_slot);
+    const Where w = locate<EXPERTS, BM, BN, T::kThreads>(p, s_slot);
     if (EXPERTS && w.l < 0)
         return;
 
@@ -511,95 +552,67 @@ __global__ __launch_bounds__(kThreads, T::kPerCu) void nvfp4_gemm_wide_kernel(Ge
     const uint32_t words_b = kOffSB + (rb0 / (32 * T::LB)) * (T::LB * 256) + half * (T::LB * 128) +
                              l32 * (T::LB * 4) + (rb0 / 32 % T::LB) * 4;
     // A stage is 8 steps of 16 k (per half of the lanes: one dword of codes per
-    // row), in two parts of 4 whose codes are read 16 bytes at a time. While a
-    // step's MFMAs run, the next step's fragments are decoded; the next part's
-    // codes are read a part ahead, across the stage's end: so the barrier that
-    // hands over stage i + 1 stands in the middle of stage i.
-    uint4_t q[2][F];                            // codes of the two parts, A's fragments first
-    half2_t sc[F][2];                           // the stage's 4 scales of each fragment
-    half8_t v[2][F];                            // decoded fragments of two steps
-    auto read_part = [&](int slot, int part) {
+    // row), codes being read 16 bytes at a time.
+    auto compute = [&](int st, int slot) {
         const uint8_t *base = lds + slot * kStage;
-        const uint32_t pc = ((2 * half + part) ^ swz) * 16;
-#pragma unroll
-        for (int f = 0; f < F; ++f)
-            q[part][f] = f < FM ? *(const uint4_t *)(base + codes_a + f * 2048 + pc)
-                                : *(const uint4_t *)(base + codes_b + (f - FM) * 2048 + pc);
-    };
-    auto read_scales = [&](int slot, int st) {
-        const uint8_t *base = lds + slot * kStage;
-        uint32_t sa[FM], sb[FN];
+        uint32_t word[F], sa[FM], sb[FN];
         load_words<FM, ODD>(base + words_a, kWordsA, sa);
         load_words<FN, ODD>(base + words_b, kWordsB, sb);
         // past K's end: scales of 0
         const uint32_t valid = word_mask(p.K - st * kStageK - half * 64);
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-            const uint32_t word = (f < FM ? sa[f < FM ? f : 0] : sb[f < FM ? 0 : f - FM]) & valid;
-            sc[f][0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word, 1.0f, false);
-            sc[f][1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word, 1.0f, true);
+        for (int f = 0; f < F; ++f)
+            word[f] = (f < FM ? sa[f < FM ? f : 0] : sb[f < FM ? 0 : f - FM]) & valid;
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            const uint32_t pc = ((2 * half + part) ^ swz) * 16;
+            uint4_t q[F];
+            half2_t sc[F];
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                q[f] = f < FM ? *(const uint4_t *)(base + codes_a + f * 2048 + pc)
+                              : *(const uint4_t *)(base + codes_b + (f - FM) * 2048 + pc);
+                sc[f] = part ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word[f], 1.0f, true)
+                             : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word[f], 1.0f, false);
+            }
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                half8_t v[F];
+#pragma unroll
+                for (int f = 0; f < F; ++f) {
+                    const half2_t s = d < 2 ? (half2_t){sc[f].x, sc[f].x} : (half2_t){sc[f].y, sc[f].y};
+                    const uint32_t codes[4] = {q[f].x, q[f].y, q[f].z, q[f].w};
+                    v[f] = decode8(codes[d], s);
+                }
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int i = 0; i < FM; ++i)
+                        acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[FM + j], v[i], acc[j][i], 0, 0, 0);
+            }
         }
-    };
-    auto decode = [&](int part, int d, int into) {
-#pragma unroll
-        for (int f = 0; f < F; ++f) {
-            const half2_t two = sc[f][part];
-            const half2_t s = d < 2 ? (half2_t){two.x, two.x} : (half2_t){two.y, two.y};
-            const uint32_t codes[4] = {q[part][f].x, q[part][f].y, q[part][f].z, q[part][f].w};
-            v[into][f] = decode8(codes[d], s);
-        }
-    };
-    auto products = [&](int from) {
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-                acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[from][FM + j], v[from][i], acc[j][i], 0, 0, 0);
     };
 
 #pragma unroll
     for (int s = 0; s < NS - 1; ++s)
         if (s < stages)
             issue(first + s, s);
-    if (stages >= NS - 1)
+    const float scale = total_scale<EXPERTS>(p, w.l);
+    int slot = 0, i = 0;
+    for (; i + NS - 1 < stages; ++i) {
+        // stage i has landed when only the NS - 2 younger ones are out; past the
+        // barrier every wave has done with stage i - 1, whose slot is next
         wait_stage(std::integral_constant<int, NS - 2>{});
-    else
+        barrier();
+        issue(first + i + NS - 1, slot == 0 ? NS - 1 : slot - 1);
+        compute(first + i, slot);
+        slot = slot + 1 == NS ? 0 : slot + 1;
+    }
+    for (; i < stages; ++i) {
         wait_stage(None{});
-    barrier();
-    read_scales(0, first);
-    read_part(0, 0);
-    decode(0, 0, 0);
-    int slot = 0;
-    for (int i = 0; i < stages; ++i) {
-        const int next = slot + 1 == NS ? 0 : slot + 1;
-        read_part(slot, 1);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            products(t % 2);
-            decode(t < 3 ? 0 : 1, (t + 1) % 4, (t + 1) % 2);
-        }
-        if (i + 1 < stages) {
-            // stage i + 1 has landed when only the stages after it are out
-            if (i + NS - 2 < stages)
-                wait_stage(std::integral_constant<int, NS - 3>{});
-            else
-                wait_stage(None{});
-            barrier();
-            if (i + NS - 1 < stages)
-                issue(first + i + NS - 1, slot == 0 ? NS - 1 : slot - 1);
-            read_part(next, 0);
-        }
-#pragma unroll
-        for (int t = 4; t < 8; ++t) {
-            products(t % 2);
-            if (t < 7)
-                decode(1, t - 3, (t + 1) % 2);
-        }
-        if (i + 1 < stages) {
-            read_scales(next, first + i + 1);
-            decode(0, 0, 0);
-        }
-        slot = next;
+        barrier();
+        compute(first + i, slot);
+        slot = slot + 1 == NS ? 0 : slot + 1;
     }
 
     // --- results. Register r of fragment (j, i): row of B rb0 + 32 j + 8 (r / 4) + 4 (lane / 32) + r % 4,
@@ -621,8 +634,41 @@ __global__ __launch_bounds__(kThreads, T::kPerCu) void nvfp4_gemm_wide_kernel(Ge
             }
     };
     if (p.splits == 1) {
-        const float scale = total_scale<EXPERTS>(p, w.l);
-        each([&](float x, int64_t at) { store_value(p.c, at, x * scale, p.dtype); });
+        // Through LDS, so that a lane stores 16 bytes of a row at a time (2-byte
+        // stores of 32 neighbours took 17 us per 256 x 256 tile, most of it these).
+        barrier();                              // all waves have read their last stage
+        uint8_t *const out = lds + wave * (32 * T::kPitch);
+        const int size = p.dtype == NVFP4_F32 ? 4 : 2;
+        const int per_row = FM * 32 * size / 16, rows_at_once = 64 / per_row, per_piece = 16 / size;
+        const int piece_n = lane / per_row, piece_m = lane % per_row * per_piece;
+        const int m = w.m0 + ra0 + piece_m;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+                    store_value(out + (8 * (r / 4) + 4 * half + r % 4) * T::kPitch, 32 * i + l32, acc[j][i][r] * scale, p.dtype);
+            asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+            for (int n = piece_n; n < 32; n += rows_at_once) {
+                const uint4_t v = *(const uint4_t *)(out + n * T::kPitch + piece_m * size);
+                const int64_t row = row_at<EXPERTS>(p, w, s_slot, rb0 + 32 * j + n);
+                if (row < 0 || m >= p.M)
+                    continue;
+                uint8_t *c = p.c + (row + m) * size;
+                if (m + per_piece <= p.M) {
+                    __builtin_memcpy(c, &v, 16);
+                } else {
+                    for (int x = 0; x < p.M - m; ++x) {
+                        if (size == 4)
+                            ((uint32_t *)c)[x] = *(const uint32_t *)(out + n * T::kPitch + (piece_m + x) * 4);
+                        else
+                            ((uint16_t *)c)[x] = *(const uint16_t *)(out + n * T::kPitch + (piece_m + x) * 2);
+                    }
+                }
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+        }
         return;
     }
     // partial sums: agent-scope stores (past this XCD's L2), then the ticket
@@ -632,7 +678,6 @@ __global__ __launch_bounds__(kThreads, T::kPerCu) void nvfp4_gemm_wide_kernel(Ge
     });
     if (!last_of_tile(p, w.tile, &s_ticket))
         return;
-    const float scale = total_scale<EXPERTS>(p, w.l);
 #pragma unroll 1
     for (int g = 0; g < FN * FM * 2; ++g) {                     // 8 registers at a time
         const int j = g / (FM * 2), i = g / 2 % FM, r0 = g % 2 * 8;
@@ -656,10 +701,11 @@ __global__ __launch_bounds__(kThreads, T::kPerCu) void nvfp4_gemm_wide_kernel(Ge
 // ------------------------------------------------------------------ wave kernel
 
 // WM x KW waves: WM of them share the rows of A, each with FM x FN fragments, and
-// KW take a row range's stages in turn; NS stages in each wave's ring.
-template <int FM, int FN, int WM, int KW, int NS, int PER_CU>
+// KW take a row range's stages in turn, RUN (1 or 2) neighbouring ones at a time;
+// NS stages in each wave's ring.
+template <int FM, int FN, int WM, int KW, int NS, int PER_CU, int RUN>
 struct WaveTile {
-    static constexpr int kFM = FM, kFN = FN, kWM = WM, kKW = KW, kNS = NS, kPerCu = PER_CU;
+    static constexpr int kRun = RUN, kFM = FM, kFN = FN, kWM = WM, kKW = KW, kNS = NS, kPerCu = PER_CU;
     static constexpr int kWaveM = 32 * FM, BM = kWaveM * WM, BN = 32 * FN, kThreads = 64 * WM * KW;
     static constexpr int kOffB = kWaveM * 64, kOffSA = kOffB + BN * 64;
     static constexpr int stage_bytes(bool odd) { return kOffSA + (kWaveM + BN) * (odd ? 16 : 8); }
@@ -684,10 +730,12 @@ __global__ __launch_bounds__(T::kThreads, T::kPerCu) void nvfp4_gemm_wave_kernel
     // this wave's rows (its first may lie past M: then it works on row M - 1 and stores nothing)
     const int wk = wave % KW, rows0 = w.m0 + wave / KW * T::kWaveM;
     w.m0 = min(rows0, p.M - 1);
-    // and stages: first, first + KW, ..
-    const int first = w.split * p.stages_per_split + wk;
-    const int end = min((w.split + 1) * p.stages_per_split, p.stages);
-    const int stages = first < end ? (end - first + KW - 1) / KW : 0;
+    // and stages: RUN from first on, then those RUN * KW further
+    constexpr int RUN = T::kRun;
+    const int begin = w.split * p.stages_per_split, count = min(p.stages_per_split, p.stages - begin);
+    const int stages = count / (RUN * KW) * RUN + min(max(count % (RUN * KW) - RUN * wk, 0), RUN);
+    const int first = begin + RUN * wk;
+    auto stage_at = [&](int n) { return first + n / RUN * (RUN * KW) + n % RUN; };
     // copies of B's codes: 16 rows each, only those that hold rows of the tile
     const int groups_b = (w.count + 15) / 16;
     const uint32_t one_words = p.blocked ? 1024 : 8, back_words = p.blocked ? 512 : 4;
@@ -715,7 +763,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerCu) void nvfp4_gemm_wave_kernel
 
     auto issue = [&](int n, int slot) {                         // the wave's n-th stage, the next one
         const uint32_t base = ring_base + slot * kStage;
-        const int left = p.K - (first + n * KW) * kStageK;
+        const int left = p.K - stage_at(n) * kStageK;
         const uint32_t back = left <= piece * 32 ? piece * 16 : 0;
 #pragma unroll
         for (int i = 0; i < 2 * FM; ++i)
@@ -730,8 +778,9 @@ __global__ __launch_bounds__(T::kThreads, T::kPerCu) void nvfp4_gemm_wave_kernel
         for (int i = 0; i < 2 * FN; ++i)
             if (i < groups_b)
                 copy16(b.codes, ob[i] - back, base + T::kOffB + i * 1024);
-        a.codes += 64 * KW, b.codes += 64 * KW;
-        a.words += one_words * KW, b.words += one_words * KW;
+        const int step = RUN == 1 ? KW : (n % 2 ? 2 * KW - 1 : 1);
+        a.codes += 64 * step, b.codes += 64 * step;
+        a.words += one_words * step, b.words += one_words * step;
     };
     constexpr int kBase = 2 * FM + F * (ODD ? 2 : 1);
     auto wait_younger = [&](auto younger) {
@@ -755,7 +804,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerCu) void nvfp4_gemm_wave_kernel
                 acc[j][i][r] = 0.0f;
     auto compute = [&](int n, int slot) {
         const uint8_t *base = ring + slot * kStage;
-        const uint32_t valid = word_mask(p.K - (first + n * KW) * kStageK - half * 64);
+        const uint32_t valid = word_mask(p.K - stage_at(n) * kStageK - half * 64);
         uint32_t word[F];
         uint4_t q[F][2];
 #pragma unroll
@@ -795,13 +844,15 @@ __global__ __launch_bounds__(T::kThreads, T::kPerCu) void nvfp4_gemm_wave_kernel
     for (int s = 0; s < NS - 1; ++s)
         if (s < stages)
             issue(s, s);
+    const float scale = total_scale<EXPERTS>(p, w.l);
     int slot = 0, n = 0;
     for (; n + NS - 1 < stages; ++n) {
-        // stage n has landed when only the NS - 2 younger ones are out; the
-        // slot of stage n - 1, read a turn ago, takes stage n + NS - 1
-        wait_younger(std::integral_constant<int, NS - 2>{});
-        asm volatile("" : : : "memory");
+        // the slot of stage n - 1, whose reads are done, takes stage n + NS - 1;
+        // stage n has landed when only the NS - 1 younger ones are out
+        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
         issue(n + NS - 1, slot == 0 ? NS - 1 : slot - 1);
+        wait_younger(std::integral_constant<int, NS - 1>{});
+        asm volatile("" : : : "memory");
         compute(n, slot);
         slot = slot + 1 == NS ? 0 : slot + 1;
     }
@@ -869,7 +920,6 @@ __global__ __launch_bounds__(T::kThreads, T::kPerCu) void nvfp4_gemm_wave_kernel
                 sum[g + x] = part[x];
         }
     }
-    const float scale = total_scale<EXPERTS>(p, w.l);
 #pragma unroll
     for (int x = 0; x < R; ++x)
         if (at[x] >= 0)
@@ -878,16 +928,15 @@ __global__ __launch_bounds__(T::kThreads, T::kPerCu) void nvfp4_gemm_wave_kernel
 
 // ------------------------------------------------------------------ plans
 
-typedef Tile<4, 4, 2, 2, 4, 1> TileLarge;       // 256 x 256
-typedef Tile<4, 2, 2, 2, 3, 1> TileTall;        // 256 x 128
-typedef Tile<2, 2, 2, 2, 3, 2> TileMid;         // 128 x 128
-typedef Tile<2, 1, 2, 2, 3, 2> TileNarrow;      // 128 x 64
-typedef WaveTile<1, 2, 4, 1, 3, 1> TileWave64;  // 128 x 64
-typedef WaveTile<1, 2, 1, 4, 3, 1> TileWave64K; // 32 x 64, 4 waves along K
-typedef WaveTile<1, 1, 4, 1, 4, 2> TileWave32;  // 128 x 32
-typedef WaveTile<1, 1, 1, 4, 4, 2> TileWave32K; // 32 x 32, 4 waves along K
+typedef Tile<2, 4, 4, 2, 3, 1> TileLarge;       // 256 x 256, 8 waves
+typedef Tile<4, 2, 2, 2, 2, 2> TileTall;        // 256 x 128
+typedef WaveTile<2, 2, 1, 4, 2, 2, 2> TileSquare;  // 64 x 64, 4 waves along K
+typedef WaveTile<2, 1, 2, 2, 2, 3, 1> TileFew;     // 128 x 32, 2 waves along K
+typedef WaveTile<2, 1, 1, 4, 2, 3, 1> TileFewK;    // 64 x 32, 4 waves along K
+typedef WaveTile<1, 1, 1, 4, 2, 3, 1> TileOne;     // 32 x 32, 4 waves along K
+typedef WaveTile<1, 1, 1, 8, 3, 1, 1> TileOneK;    // 32 x 32, 8 waves along K
 
-enum class Kind { Large, Tall, Mid, Narrow, Wave64, Wave64K, Wave32, Wave32K };
+enum class Kind { Large, Tall, Square, Few, FewK, One, OneK };
 
 struct Plan {
     Kind kind;
@@ -926,20 +975,8 @@ Plan dense_plan(int64_t M, int64_t N, int64_t K, int64_t L)
         p.tiles_m = ceil_div(M, bm), p.tiles_n = ceil_div(N, bn);
         p.tiles = p.tiles_m * p.tiles_n * L;
     };
-    if (N <= 32) {
-        p.kind = Kind::Wave32K;
-        tiles(TileWave32K::BM, TileWave32K::BN);
-    } else if (N <= 64) {
-        p.kind = Kind::Wave64K;
-        tiles(TileWave64K::BM, TileWave64K::BN);
-    } else {
-        p.kind = Kind::Large;
-        tiles(TileLarge::BM, TileLarge::BN);
-        if (p.tiles < 160) {
-            p.kind = Kind::Mid;
-            tiles(TileMid::BM, TileMid::BN);
-        }
-    }
+    p.kind = N <= 32 ? Kind::One : Kind::Square;
+    N <= 32 ? tiles(32, 32) : tiles(64, 64);
     split_k(p, p.kind == Kind::Large ? 256 : 512, 4, N * L, M);
     return p;
 }
@@ -954,16 +991,8 @@ Plan experts_plan(int64_t M, int64_t K, int64_t E, int64_t S)
         p.tiles = p.tiles_m * p.tiles_n;
     };
     const int64_t mean = ceil_div(S, E);
-    if (mean <= 32) {
-        p.kind = Kind::Wave32K;
-        tiles(TileWave32K::BM, TileWave32K::BN);
-    } else if (mean <= 64) {
-        p.kind = Kind::Wave64K;
-        tiles(TileWave64K::BM, TileWave64K::BN);
-    } else {
-        p.kind = Kind::Mid;
-        tiles(TileMid::BM, TileMid::BN);
-    }
+    p.kind = mean <= 32 ? Kind::Few : Kind::Tall;
+    mean <= 32 ? tiles(128, 32) : tiles(256, 128);
     split_k(p, 512, 4, S, M);
     return p;
 }
@@ -981,7 +1010,7 @@ hipError_t launch_wide(const GemmParams &p, int64_t grid, hipStream_t st)
 {
     const bool odd = !p.blocked && p.K % 64 != 0;               // plain rows of 2-byte alignment
     auto go = [&](auto kern) {
-        hipLaunchKernelGGL(kern, dim3((uint32_t)grid), dim3(kThreads), T::lds_bytes(odd), st, p);
+        hipLaunchKernelGGL(kern, dim3((uint32_t)grid), dim3(T::kThreads), T::lds_bytes(odd), st, p);
     };
     odd ? go(nvfp4_gemm_wide_kernel<T, EXPERTS, true>) : go(nvfp4_gemm_wide_kernel<T, EXPERTS, false>);
     return hipGetLastError();
@@ -1006,12 +1035,11 @@ nvfp4_status_t run(const Plan &plan, const GemmParams &p, hipStream_t st)
     switch (plan.kind) {
     case Kind::Large: e = launch_wide<TileLarge, EXPERTS>(p, grid, st); break;
     case Kind::Tall: e = launch_wide<TileTall, EXPERTS>(p, grid, st); break;
-    case Kind::Mid: e = launch_wide<TileMid, EXPERTS>(p, grid, st); break;
-    case Kind::Narrow: e = launch_wide<TileNarrow, EXPERTS>(p, grid, st); break;
-    case Kind::Wave64: e = launch_wave<TileWave64, EXPERTS>(p, grid, st); break;
-    case Kind::Wave64K: e = launch_wave<TileWave64K, EXPERTS>(p, grid, st); break;
-    case Kind::Wave32: e = launch_wave<TileWave32, EXPERTS>(p, grid, st); break;
-    case Kind::Wave32K: e = launch_wave<TileWave32K, EXPERTS>(p, grid, st); break;
+    case Kind::Square: e = launch_wave<TileSquare, EXPERTS>(p, grid, st); break;
+    case Kind::Few: e = launch_wave<TileFew, EXPERTS>(p, grid, st); break;
+    case Kind::FewK: e = launch_wave<TileFewK, EXPERTS>(p, grid, st); break;
+    case Kind::One: e = launch_wave<TileOne, EXPERTS>(p, grid, st); break;
+    case Kind::OneK: e = launch_wave<TileOneK, EXPERTS>(p, grid, st); break;
     }
     if (e == hipSuccess)
         return NVFP4_OK;

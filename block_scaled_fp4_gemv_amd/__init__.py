@@ -503,7 +503,10 @@ def _strided(x, name, rows, K, L, row_stride, batch_stride):
         return x, row_stride, batch_stride
     if not x.is_cuda:
         raise ValueError("operands must be device tensors")
-    if min(rows, K, L) >= 1 and min(row_stride, batch_stride) >= 0:
+    if row_stride == K and batch_stride == rows * K and x.is_contiguous():
+        if rows * K * L > x.numel():
+            raise ValueError(f"{name} holds {x.numel()} elements, the shape needs {rows * K * L}")
+    elif min(rows, K, L) >= 1 and min(row_stride, batch_stride) >= 0:
         held = x.untyped_storage().nbytes() // x.element_size() - x.storage_offset()
         need = (L - 1) * batch_stride + (rows - 1) * row_stride + K
         if held < need:

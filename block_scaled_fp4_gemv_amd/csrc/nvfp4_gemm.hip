@@ -954,47 +954,84 @@ bool gemm_shape(int64_t M, int64_t N, int64_t K, int64_t L)
            L <= (INT64_C(1) << 61) / K / std::max(M, N) && L <= (INT64_C(1) << 60) / M / N;
 }
 
-// slices of K that bring the grid to about `want` workgroups, at least `least` stages each
-void split_k(Plan &p, int64_t want, int64_t least, int64_t rows, int64_t M)
+// The tile shapes and what they cost, from which the plans choose. us on one
+// MI355X, measured over 40 shapes (M and N 16 .. 7168, K 512 .. 16384, 1 to 16
+// slices): `alone`, a workgroup's time per stage (128 k) with its CU to itself;
+// `each`, what a stage adds to the CU's time per workgroup when more share it;
+// `start`, what a workgroup of routed experts adds besides.
+//   Large tiles decode less per product (6 vector instructions per MFMA for 256 x
+// 256 and 256 x 128, 8 for 64 x 64, 12 for 32 wide, 16 for 32 x 32) and need
+// many tiles to fill the GPU; small ones put their waves along K. E.g. 4096 x 333
+// x 7168: 64 x 64 33 us, 64 x 32 33, 128 x 32 37, 256 x 128 above 100; 7168 x
+// 4096 x 16384: 256 x 256 760, 256 x 128 810, 64 x 64 970; 4096 x 128 x 7168: 64
+// x 32 14.4, 32 x 32 15.4, 64 x 64 18.2; 7168 x 16 x 16384: 32 x 32 with 8
+// waves along K 17.3, with 4 20.2, 64 x 32 in two slices 19.1.
+struct Shape {
+    Kind kind;
+    int bm, bn;
+    double alone, each, start;
+};
+constexpr Shape kShapes[] = {
+    {Kind::Large, TileLarge::BM, TileLarge::BN, 2.85, 2.95, 8.0},
+    {Kind::Tall, TileTall::BM, TileTall::BN, 2.03, 1.58, 4.0},
+    {Kind::Square, TileSquare::BM, TileSquare::BN, 0.28, 0.27, 2.0},
+    {Kind::Few, TileFew::BM, TileFew::BN, 0.35, 0.35, 1.6},
+    {Kind::FewK, TileFewK::BM, TileFewK::BN, 0.15, 0.185, 1.2},
+    {Kind::One, TileOne::BM, TileOne::BN, 0.115, 0.095, 0.9},
+    {Kind::OneK, TileOneK::BM, TileOneK::BN, 0.085, 0.10, 1.5},
+};
+constexpr double kCus = 256.0, kSplitUs = 1.0, kSliceUs = 0.15, kPartialBytesPerUs = 2.0e6;
+
+// Cheapest shape and number of K slices. tiles_of(shape, plan) fills the tile
+// counts and returns the expected number of tiles; rows: of the result.
+template <typename F>
+Plan choose(int64_t M, int64_t K, int64_t rows, bool experts, F tiles_of)
 {
-    int64_t s = std::min<int64_t>(want / std::max<int64_t>(p.tiles, 1), kMaxSplits);
-    s = std::min<int64_t>(s, p.stages / least);
-    s = std::min<int64_t>(s, kMaxPartialBytes / 4 / rows / M);
-    if (s < 2 || p.tiles > kMaxTickets)
-        s = 1;
-    p.per_split = (int32_t)ceil_div(p.stages, s);
-    p.splits = (int32_t)ceil_div(p.stages, p.per_split);
+    Plan best{};
+    double best_us = 0.0;
+    for (const Shape &s : kShapes) {
+        Plan p{};
+        p.kind = s.kind, p.bm = s.bm, p.bn = s.bn;
+        p.stages = (int32_t)ceil_div(K, kStageK);
+        p.tiles_m = ceil_div(M, s.bm);
+        const double tiles = tiles_of(s, p);
+        for (int64_t splits = 1; splits <= kMaxSplits && splits <= p.stages; splits *= 2) {
+            p.per_split = (int32_t)ceil_div(p.stages, splits);
+            p.splits = (int32_t)ceil_div(p.stages, p.per_split);
+            if (p.splits > 1 && (p.tiles > kMaxTickets || p.splits * rows > kMaxPartialBytes / 4 / M))
+                break;
+            const double n = tiles * p.splits / kCus, load = experts ? std::max(n, 1.0) : std::ceil(n);
+            double us = p.per_split * std::max(s.alone, s.each * load) + (experts ? s.start * load : 0.0);
+            if (p.splits > 1)
+                us += kSplitUs + p.splits * (kSliceUs + 8.0 * rows * M / kPartialBytesPerUs);
+            if (best_us == 0.0 || us < best_us) {
+                best = p;
+                best_us = us;
+            }
+        }
+    }
+    return best;
 }
 
 Plan dense_plan(int64_t M, int64_t N, int64_t K, int64_t L)
 {
-    Plan p{};
-    p.stages = (int32_t)ceil_div(K, kStageK);
-    auto tiles = [&](int bm, int bn) {
-        p.bm = bm, p.bn = bn;
-        p.tiles_m = ceil_div(M, bm), p.tiles_n = ceil_div(N, bn);
+    return choose(M, K, N * L, false, [&](const Shape &s, Plan &p) {
+        p.tiles_n = ceil_div(N, s.bn);
         p.tiles = p.tiles_m * p.tiles_n * L;
-    };
-    p.kind = N <= 32 ? Kind::One : Kind::Square;
-    N <= 32 ? tiles(32, 32) : tiles(64, 64);
-    split_k(p, p.kind == Kind::Large ? 256 : 512, 4, N * L, M);
-    return p;
+        return (double)p.tiles;
+    });
 }
 
+// The lists are on the device: the grid has room for the most tiles that S slots
+// can make, the choice goes by what S slots spread over the experts make.
 Plan experts_plan(int64_t M, int64_t K, int64_t E, int64_t S)
 {
-    Plan p{};
-    p.stages = (int32_t)ceil_div(K, kStageK);
-    auto tiles = [&](int bm, int bn) {
-        p.bm = bm, p.bn = bn;
-        p.tiles_m = ceil_div(M, bm), p.tiles_n = std::min<int64_t>(S, S / bn + std::min(E, S));
+    const double mean = (double)S / E, hit = E * (1.0 - std::exp(-mean));
+    return choose(M, K, S, true, [&](const Shape &s, Plan &p) {
+        p.tiles_n = std::min<int64_t>(S, S / s.bn + std::min(E, S));
         p.tiles = p.tiles_m * p.tiles_n;
-    };
-    const int64_t mean = ceil_div(S, E);
-    p.kind = mean <= 32 ? Kind::Few : Kind::Tall;
-    mean <= 32 ? tiles(128, 32) : tiles(256, 128);
-    split_k(p, 512, 4, S, M);
-    return p;
+        return std::max(hit, (double)S / s.bn + 0.5 * hit) * p.tiles_m;
+    });
 }
 
 size_t plan_workspace(const Plan &p, int64_t rows, int64_t M)

@@ -26,10 +26,12 @@
 namespace {
 
 constexpr int kRouteWaves = 4;
+constexpr int kSimds = 1024;                   // of the GPU: 256 CUs of 4
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 64;
 constexpr int kMaxGroups = 64;
-constexpr int kListThreads = 256;
+constexpr int kListThreads = 1024;
+static_assert(kListThreads >= kMaxExperts);
 constexpr int kSmallThreads = 1024;
 constexpr int64_t kTicketBytes = 256;
 constexpr int64_t kMaxGrid = 0xFFFFFF;
@@ -94,40 +96,65 @@ struct RouteParams {
 
 constexpr uint64_t kAllLanes = ~0ull;
 
-// The k picks of a token from the wave's picks (float or double), largest
-// first: lane j gets the j-th's expert, -1 where none is left. `close(m, e)` sees
-// each pick before it is taken, and the first that is left out; where it says
-// false, so does this.
+// lowest value over the wave
+__device__ __attribute__((always_inline)) inline int wave_min(int v)
+{
+#pragma unroll
+    for (int d = 32; d; d >>= 1)
+        v = min(v, __shfl_xor(v, d));
+    return v;
+}
+
+// The k picks of a token from the wave's picks (float or double), largest first:
+// lane at + j gets the j-th's expert in `id`; lanes past the last keep theirs.
+// Each lane's picks are sorted first, so that a round looks at one per lane.
+// `close(m, e, last, last_e)` sees each pick before it is taken, beside the one
+// before it, and also the first that is left out; where it says false, so does this.
 template <int NL, typename V, typename Close>
-__device__ __attribute__((always_inline)) inline bool pick_k(V (&pick)[NL], int k, int lane, int &id, Close close)
+__device__ __attribute__((always_inline)) inline bool pick_k(V (&v)[NL], int k, int lane, int at, int &id, Close close)
 {
     const V none = -(V)__builtin_inff();
-    id = -1;
-    for (int j = 0; j <= k; ++j) {                              // one more: the first that is left out
-        V m = pick[0];
+    int of[NL];                                                 // v[i] is expert lane + 64 * of[i]
 #pragma unroll
-        for (int i = 1; i < NL; ++i)
-            m = pick[i] > m ? pick[i] : m;
-        m = wave_max(m);
+    for (int i = 0; i < NL; ++i)
+        of[i] = i;
+#pragma unroll
+    for (int n = NL - 1; n > 0; --n)
+#pragma unroll
+        for (int i = 0; i < n; ++i) {                           // equal picks keep their order
+            const bool swap = v[i + 1] > v[i];
+            const V hi = swap ? v[i + 1] : v[i], lo = swap ? v[i] : v[i + 1];
+            const int a = swap ? of[i + 1] : of[i], b = swap ? of[i] : of[i + 1];
+            v[i] = hi, v[i + 1] = lo;
+            of[i] = a, of[i + 1] = b;
+        }
+    V last = (V)__builtin_inff();
+    int last_e = -1;
+    for (int j = 0; j <= k; ++j) {                              // one more: the first that is left out
+        const V m = wave_max(v[0]);
         if (!(m > none))
             return true;
-        int e = -1;
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const uint64_t at = __ballot(pick[i] == m);
-            if (e < 0 && at)
-                e = 64 * i + __ffsll((unsigned long long)at) - 1;
+        const uint64_t best = __ballot(v[0] == m);
+        int e;
+        if (best & (best - 1))                                  // the same pick in several lanes: the lowest expert
+            e = __builtin_amdgcn_readfirstlane(wave_min(v[0] == m ? lane + 64 * of[0] : kMaxExperts));
+        else {
+            const int l = __ffsll((unsigned long long)best) - 1;
+            e = l + 64 * __builtin_amdgcn_readlane(of[0], l);
         }
-        if (!close(m, e))
+        if (!close(m, e, last, last_e))
             return false;
         if (j == k)
             return true;
-#pragma unroll
-        for (int i = 0; i < NL; ++i)
-            if (e == lane + 64 * i)
-                pick[i] = none;
-        if (lane == j)
+        if (lane == at + j)
             id = e;
+        if (lane == e % 64) {
+#pragma unroll
+            for (int i = 0; i + 1 < NL; ++i)
+                v[i] = v[i + 1], of[i] = of[i + 1];
+            v[NL - 1] = none;
+        }
+        last = m, last_e = e;
     }
     return true;
 }
@@ -188,11 +215,12 @@ __device__ __attribute__((always_inline)) inline bool mask_groups(V (&pick)[NL],
     return sure;
 }
 
-// float32 path: x (masked: -inf), bias b -> id per lane. False: not certain.
-template <int NL>
+// float32 path: x (masked: -inf), bias b -> the picks in lanes at, at + 1, ..
+// False: not certain. `same(e, f)`: whether two experts have equal logits and biases.
+template <int NL, typename Same>
 __device__ __attribute__((always_inline)) inline bool route_fast(const float (&x)[NL], const float (&b)[NL],
                                                                  bool with_bias, float top, const RouteParams &p,
-                                                                 int lane, float *lds, int &id)
+                                                                 int lane, int at, float *lds, int &id, Same same)
 {
     const float none = -__builtin_inff();
     float pick[NL], largest = none;
@@ -240,26 +268,8 @@ __device__ __attribute__((always_inline)) inline bool route_fast(const float (&x
         if (!sure)
             return false;
     }
-    float last = __builtin_inff(), last_x = 0.0f, last_b = 0.0f;
-    return pick_k<NL, float>(pick, p.k, lane, id, [&](float m, int e) {
-        float xe = 0.0f, be = 0.0f;
-        // the picked expert's logit and bias, and whether any other of the same pick has others
-        bool other = false;
-#pragma unroll
-        for (int i = 0; i < NL; ++i)
-            if (e / 64 == i) {
-                xe = as_f32(__builtin_amdgcn_readlane(as_i32(x[i]), e % 64));
-                be = as_f32(__builtin_amdgcn_readlane(as_i32(b[i]), e % 64));
-            }
-#pragma unroll
-        for (int i = 0; i < NL; ++i)
-            other |= pick[i] == m && (x[i] != xe || b[i] != be);
-        if (__ballot(other))
-            return false;
-        if (!(last - m > margin) && !(xe == last_x && be == last_b))
-            return false;
-        last = m, last_x = xe, last_b = be;
-        return true;
+    return pick_k<NL, float>(pick, p.k, lane, at, id, [&](float m, int e, float last, int last_e) {
+        return last - m > margin || same(e, last_e);
     });
 }
 
@@ -278,22 +288,17 @@ __device__ __attribute__((always_inline)) inline void load_token(const void *__r
     }
 }
 
-struct Exact {
-    int id;
-    double sum;                                                 // softmax: of the exponentials
-};
-
-// float64 path, the definition itself. Not inlined: it is rarely taken, and its
+// float64 path, the definition itself: the picks in lanes at, at + 1, .. of
+// *picked; returns the softmax's sum. Not inlined: it is rarely taken, and its
 // registers would cost the fast path waves. It loads the token again.
 template <int DT, int NL>
-__device__ __attribute__((noinline)) Exact route_exact(const void *__restrict__ logits, const float *__restrict__ bias,
-                                                       int64_t t, RouteParams p, double *lds)
+__device__ __attribute__((noinline)) double route_exact(const void *__restrict__ logits, const float *__restrict__ bias,
+                                                       int64_t t, RouteParams p, int at, int *picked, double *lds)
 {
     const double none = -__builtin_inf();
     const int lane = threadIdx.x % 64;
     float x[NL], b[NL];
     load_token<DT, NL>(logits, bias, t, p.E, lane, x, b);
-    int id;
     double pick[NL], top = none, score_sum = 1.0;
 #pragma unroll
     for (int i = 0; i < NL; ++i)
@@ -328,64 +333,93 @@ __device__ __attribute__((noinline)) Exact route_exact(const void *__restrict__ 
         mask_groups<NL, double>(pick, lds, p, lane, 0.0);
         wave_sync();
     }
-    pick_k<NL, double>(pick, p.k, lane, id, [](double, int) { return true; });
-    return {id, score_sum};
+    int id = -1;
+    pick_k<NL, double>(pick, p.k, lane, at, id, [](double, int, double, int) { return true; });
+    *picked = id;
+    return score_sum;
 }
 
-// One token by one wave. `lds`: 64 * NL doubles of the wave's own.
-template <int DT, int NL>
-__device__ __attribute__((always_inline)) inline void route_token(const void *__restrict__ logits,
-                                                                  const float *__restrict__ bias,
-                                                                  int32_t *__restrict__ ids,
-                                                                  float *__restrict__ weights, const RouteParams &p,
-                                                                  int64_t t, int lane, double *lds)
+// Lanes that hold one token's picks: the power of two from k on.
+__device__ __attribute__((always_inline)) inline int pick_lanes(int k)
 {
-    float x[NL], b[NL], top = -__builtin_inff();
-    load_token<DT, NL>(logits, bias, t, p.E, lane, x, b);
+    return k <= 1 ? 1 : 1 << (32 - __builtin_clz(k - 1));
+}
+
+// `n` tokens from t on by one wave (n * pick_lanes(k) <= 64): the picks of one
+// after the other, then the float64 weights of all at once. `lds`: 64 * NL
+// doubles of the wave's own.
+template <int DT, int NL>
+__device__ __attribute__((always_inline)) inline void route_tokens(const void *__restrict__ logits,
+                                                                   const float *__restrict__ bias,
+                                                                   int32_t *__restrict__ ids,
+                                                                   float *__restrict__ weights, const RouteParams &p,
+                                                                   int64_t t, int n, int lane, double *lds)
+{
+    const int width = pick_lanes(p.k), mine = lane / width;    // the token whose pick this lane holds
+    int id = -1;
+    float my_top = 0.0f;
+    double my_sum = 1.0;
+    for (int q = 0; q < n; ++q) {
+        const int at = q * width;
+        float x[NL], b[NL], top = -__builtin_inff();
+        load_token<DT, NL>(logits, bias, t + q, p.E, lane, x, b);
 #pragma unroll
-    for (int i = 0; i < NL; ++i)
-        top = fmaxf(top, x[i]);
-    top = wave_max(top);
-    // softmax weights that are not renormalised need the float64 sum over all
-    // experts, and infinite logits their own rule
-    const bool plain = top < __builtin_inff() && (p.score == NVFP4_SCORE_SIGMOID || p.renormalize);
-    int id;
-    double sum = 1.0;
-    if (!plain || !route_fast<NL>(x, b, bias != nullptr, top, p, lane, (float *)lds, id)) {
-        const Exact r = route_exact<DT, NL>(logits, bias, t, p, lds);
-        id = r.id;
-        sum = r.sum;
+        for (int i = 0; i < NL; ++i)
+            top = fmaxf(top, x[i]);
+        top = wave_max(top);
+        // softmax weights that are not renormalised need the float64 sum over all
+        // experts, and infinite logits their own rule
+        const bool plain = top < __builtin_inff() && (p.score == NVFP4_SCORE_SIGMOID || p.renormalize);
+        int got = -1;
+        double sum = 1.0;
+        auto same = [&](int e, int f) {
+            const int64_t row = (t + q) * p.E;
+            return f >= 0 && load_value<DT>(logits, row + e) == load_value<DT>(logits, row + f) &&
+                   (!bias || bias[e] == bias[f]);
+        };
+        if (!plain || !route_fast<NL>(x, b, bias != nullptr, top, p, lane, at, (float *)lds, got, same))
+            sum = route_exact<DT, NL>(logits, bias, t + q, p, at, &got, lds);
+        if (mine == q) {
+            id = got;
+            my_top = top;
+            my_sum = sum;
+        }
     }
-    // weights: lane j has expert j's score, in float64
+    const int64_t token = t + mine;
     double w = 0.0;
     if (id >= 0) {
-        const float v = load_value<DT>(logits, t * p.E + id);
+        const float v = load_value<DT>(logits, token * p.E + id);
         if (p.score == NVFP4_SCORE_SIGMOID)
             w = 1.0 / (1.0 + exp(-(double)v));
         else                                                    // renormalised: the sum cancels
-            w = (v == top ? 1.0 : exp((double)v - (double)top)) / (p.renormalize ? 1.0 : sum);
+            w = (v == my_top ? 1.0 : exp((double)v - (double)my_top)) / (p.renormalize ? 1.0 : my_sum);
     }
     if (p.renormalize) {
-        const double total = wave_sum(w);
+        double total = w;
+        for (int d = 1; d < width; d *= 2)
+            total += __shfl_xor(total, d);
         w = total > 0.0 ? w / total : 0.0;
     }
-    if (lane < p.k) {
-        ids[t * p.k + lane] = id;
-        weights[t * p.k + lane] = (float)(w * (double)p.scaling);
+    const int j = lane % width;
+    if (mine < n && j < p.k) {
+        ids[token * p.k + j] = id;
+        weights[token * p.k + j] = (float)(w * (double)p.scaling);
     }
 }
 
+// per_wave tokens per wave.
 template <int DT, int NL>
 __global__ __launch_bounds__(64 * kRouteWaves) void nvfp4_route_kernel(const void *__restrict__ logits,
                                                                        const float *__restrict__ bias,
                                                                        int32_t *__restrict__ ids,
-                                                                       float *__restrict__ weights, RouteParams p)
+                                                                       float *__restrict__ weights, RouteParams p,
+                                                                       int32_t per_wave)
 {
     __shared__ double lds[kRouteWaves][64 * NL];
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int64_t t = ((int64_t)blockIdx.x * kRouteWaves + wave) * per_wave;
     if (t < p.T)
-        route_token<DT, NL>(logits, bias, ids, weights, p, t, lane, lds[wave]);
+        route_tokens<DT, NL>(logits, bias, ids, weights, p, t, (int)min((int64_t)per_wave, p.T - t), lane, lds[wave]);
 }
 
 // ------------------------------------------------------------------ lists
@@ -507,35 +541,41 @@ __global__ __launch_bounds__(kListThreads) void nvfp4_place_kernel(const int32_t
     __shared__ uint32_t taken;
     extern __shared__ int32_t list_lds[];                       // base[E], at[waves][E]
     __shared__ int32_t part[kListThreads / 64];
+    __shared__ int32_t s_all[kListThreads], s_before[kListThreads];
     int32_t *base = list_lds, *at = list_lds + E;
-    int32_t start = 0;                                          // sum of the experts before this round's
-    for (int e0 = 0; e0 < E; e0 += kListThreads) {
-        const int e = e0 + (int)threadIdx.x;
-        int32_t all = 0, before = 0;
-        if (e < E) {
+    // kListThreads / width threads per expert, each every so many chunks
+    int width = 64;
+    while (width < E)
+        width *= 2;
+    const int e = threadIdx.x % width, share = threadIdx.x / width, shares = kListThreads / width;
+    int32_t all = 0, before = 0;
+    if (e < E) {
 #pragma unroll 16
-            for (int c = 0; c < nc; ++c) {
-                const int32_t v = counts[(int64_t)c * E + e];
-                all += v;
-                before += c < (int)blockIdx.x ? v : 0;
-            }
+        for (int c = share; c < nc; c += shares) {
+            const int32_t v = counts[(int64_t)c * E + e];
+            all += v;
+            before += c < (int)blockIdx.x ? v : 0;
         }
-        const int32_t upto = sum_upto<kListThreads>(all, part) + start;
-        if (e < E) {
-            base[e] = upto - all + before;
-            if (blockIdx.x == 0) {
-                offsets[e + 1] = upto;
-                if (e == 0)
-                    offsets[0] = 0;
-            }
-        }
-        __shared__ int32_t end;
-        if (threadIdx.x == kListThreads - 1)
-            end = upto;
-        __syncthreads();
-        start = end;
-        __syncthreads();
     }
+    s_all[threadIdx.x] = all;
+    s_before[threadIdx.x] = before;
+    __syncthreads();
+    all = before = 0;
+    if (share == 0)
+        for (int h = 0; h < shares; ++h) {
+            all += s_all[h * width + e];
+            before += s_before[h * width + e];
+        }
+    const int32_t upto = sum_upto<kListThreads>(all, part);
+    if (share == 0 && e < E) {
+        base[e] = upto - all + before;
+        if (blockIdx.x == 0) {
+            offsets[e + 1] = upto;
+            if (e == 0)
+                offsets[0] = 0;
+        }
+    }
+    __syncthreads();
     // every thread's counts have arrived (the barriers above follow their sums)
     if (threadIdx.x == 0)
         taken = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -557,10 +597,10 @@ __global__ __launch_bounds__(kSmallThreads) void nvfp4_route_small_kernel(
 {
     extern __shared__ int32_t list_lds[];                       // route: the waves' picks; lists: base[E], at[waves][E]
     __shared__ int32_t part[kSmallThreads / 64];
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     double *picks = (double *)list_lds + wave * (64 * NL);
     for (int t = wave; t < p.T; t += kSmallThreads / 64)
-        route_token<DT, NL>(logits, bias, ids, weights, p, t, lane, picks);
+        route_tokens<DT, NL>(logits, bias, ids, weights, p, t, 1, lane, picks);
     __syncthreads();                                            // this workgroup's ids are in its reach
     int32_t *base = list_lds, *at = list_lds + p.E;
     const int e = threadIdx.x;
@@ -771,7 +811,12 @@ nvfp4_status_t nvfp4_moe_route(const void *logits, int dtype, const float *bias,
     const size_t need = nvfp4_moe_route_workspace_bytes(T, E, k);
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
         return NVFP4_ERR_WORKSPACE;
-    const int64_t grid = (T + kRouteWaves - 1) / kRouteWaves;
+    // tokens per wave: as many as its lanes hold picks for, but 4 waves per SIMD
+    int64_t width = 1;
+    while (width < k)
+        width *= 2;
+    const int64_t per_wave = std::max<int64_t>(1, std::min<int64_t>(64 / width, T / (4 * kSimds)));
+    const int64_t per_wg = per_wave * kRouteWaves, grid = (T + per_wg - 1) / per_wg;
     if (grid > kMaxGrid)
         return NVFP4_ERR_INVALID_SHAPE;
     const hipStream_t st = (hipStream_t)stream;
@@ -791,7 +836,7 @@ nvfp4_status_t nvfp4_moe_route(const void *logits, int dtype, const float *bias,
                                    bias, ids, weights, offsets, order, p, bits);
             } else {
                 hipLaunchKernelGGL((nvfp4_route_kernel<dt(), nl()>), dim3((uint32_t)grid), dim3(64 * kRouteWaves), 0, st,
-                                   logits, bias, ids, weights, p);
+                                   logits, bias, ids, weights, p, (int32_t)per_wave);
             }
         };
         if (E <= 64)

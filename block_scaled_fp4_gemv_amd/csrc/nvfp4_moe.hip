@@ -1,13 +1,15 @@
 // Router and combine of a mixture of experts on MI355X (gfx950).
 //
-// Router. One wave per token: lane i holds the experts i, i + 64, ... . The
-// picks are the largest of the wave one after the other, ties to the lower index.
-//   Picks are compared in float64 by definition. Almost always float32 scores
-// with a bound on their error tell the same: the fast path takes the picks in
-// float32 and gives up where two neighbours in the ranking (or the last group
-// kept and the first one left) are closer than the bound, unless they are the
-// same number computed from the same logit and bias. Then the wave repeats the
-// token in float64. The weights are float64 in both.
+// Router. Picks are compared in float64 by definition. Almost always float32
+// picks with a bound on their error tell the same, and much cheaper: the fast path
+// gives 16 lanes to a token (64 for many experts), 4 tokens to a wave, and turns
+// each pick into one 32-bit key, its value in fixed point above the expert's index
+// counted down, so that the largest key is the pick and ties go to the lower
+// index. Each lane sorts its keys; a round takes the largest head of the lanes.
+// Where two neighbours in the ranking (or the last group kept and the first one
+// left) are closer than the bound, unless they come from the same logit and bias,
+// the wave repeats the token in float64. The weights are float64 in both. 16384
+// tokens of 256 experts: float64 alone 58 us; float32 with a wave per token 44.
 // Lists. A stable counting sort of the slots by expert: counts per chunk of
 // slots, then each chunk's places from the counts of the chunks before it. Every
 // rank is counted, no atomic's order enters: the lists are the same each time.
@@ -26,7 +28,6 @@
 namespace {
 
 constexpr int kRouteWaves = 4;
-constexpr int kSimds = 1024;                   // of the GPU: 256 CUs of 4
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 64;
 constexpr int kMaxGroups = 64;
@@ -69,34 +70,6 @@ __device__ __attribute__((always_inline)) inline double wave_sum(double v)
         v += __shfl_xor(v, d);
     return v;
 }
-
-// Largest value over the wave, the same in every lane: rows of 16 lanes by
-// shifts, then across the rows; the last lane holds the result.
-template <int CTRL, int ROWS>
-__device__ __attribute__((always_inline)) inline float max_step(float v)
-{
-    return fmaxf(v, as_f32(__builtin_amdgcn_update_dpp(as_i32(v), as_i32(v), CTRL, ROWS, 0xF, false)));
-}
-__device__ __attribute__((always_inline)) inline float wave_max(float v)
-{
-    v = max_step<0x111, 0xF>(v);                                // row_shr:1, 2, 4, 8
-    v = max_step<0x112, 0xF>(v);
-    v = max_step<0x114, 0xF>(v);
-    v = max_step<0x118, 0xF>(v);
-    v = max_step<0x142, 0xA>(v);                                // row_bcast:15, 31
-    v = max_step<0x143, 0xC>(v);
-    return as_f32(__builtin_amdgcn_readlane(as_i32(v), 63));
-}
-
-struct RouteParams {
-    int32_t T, E, k, score, n_group, topk_group, group_top, renormalize;
-    float scaling;
-    uint64_t group_magic;                                       // ceil(2^32 / group size): e / size = e * magic >> 32
-};
-
-constexpr uint64_t kAllLanes = ~0ull;
-
-// lowest value over the wave
 __device__ __attribute__((always_inline)) inline int wave_min(int v)
 {
 #pragma unroll
@@ -105,200 +78,107 @@ __device__ __attribute__((always_inline)) inline int wave_min(int v)
     return v;
 }
 
-// The k picks of a token from the wave's picks (float or double), largest first:
-// lane at + j gets the j-th's expert in `id`; lanes past the last keep theirs.
-// Each lane's picks are sorted first, so that a round looks at one per lane.
-// `close(m, e, last, last_e)` sees each pick before it is taken, beside the one
-// before it, and also the first that is left out; where it says false, so does this.
-template <int NL, typename V, typename Close>
-__device__ __attribute__((always_inline)) inline bool pick_k(V (&v)[NL], int k, int lane, int at, int &id, Close close)
+struct RouteParams {
+    int32_t T, E, k, score, n_group, topk_group, group_top, renormalize;
+    float scaling;
+};
+
+constexpr uint64_t kAllLanes = ~0ull;
+
+// ------------------------------------------------------------------ float64: the definition
+
+// The k picks of a token from the wave's picks v[i] (expert lane + 64 i), largest
+// first, ties to the lower expert: lane at + j gets the j-th in `id`.
+template <int NL>
+__device__ __attribute__((always_inline)) inline void pick_k(double (&v)[NL], int k, int lane, int at, int &id)
 {
-    const V none = -(V)__builtin_inff();
-    int of[NL];                                                 // v[i] is expert lane + 64 * of[i]
+    const double none = -__builtin_inf();
+    for (int j = 0; j < k; ++j) {
+        double best = none;
+        int e = kMaxExperts;
 #pragma unroll
-    for (int i = 0; i < NL; ++i)
-        of[i] = i;
-#pragma unroll
-    for (int n = NL - 1; n > 0; --n)
-#pragma unroll
-        for (int i = 0; i < n; ++i) {                           // equal picks keep their order
-            const bool swap = v[i + 1] > v[i];
-            const V hi = swap ? v[i + 1] : v[i], lo = swap ? v[i] : v[i + 1];
-            const int a = swap ? of[i + 1] : of[i], b = swap ? of[i] : of[i + 1];
-            v[i] = hi, v[i + 1] = lo;
-            of[i] = a, of[i + 1] = b;
-        }
-    V last = (V)__builtin_inff();
-    int last_e = -1;
-    for (int j = 0; j <= k; ++j) {                              // one more: the first that is left out
-        const V m = wave_max(v[0]);
+        for (int i = 0; i < NL; ++i)
+            if (v[i] > best)
+                best = v[i], e = lane + 64 * i;
+        const double m = wave_max(best);
         if (!(m > none))
-            return true;
-        const uint64_t best = __ballot(v[0] == m);
-        int e;
-        if (best & (best - 1))                                  // the same pick in several lanes: the lowest expert
-            e = __builtin_amdgcn_readfirstlane(wave_min(v[0] == m ? lane + 64 * of[0] : kMaxExperts));
-        else {
-            const int l = __ffsll((unsigned long long)best) - 1;
-            e = l + 64 * __builtin_amdgcn_readlane(of[0], l);
-        }
-        if (!close(m, e, last, last_e))
-            return false;
-        if (j == k)
-            return true;
+            return;
+        e = __builtin_amdgcn_readfirstlane(wave_min(best == m ? e : kMaxExperts));
         if (lane == at + j)
             id = e;
-        if (lane == e % 64) {
 #pragma unroll
-            for (int i = 0; i + 1 < NL; ++i)
-                v[i] = v[i + 1], of[i] = of[i + 1];
-            v[NL - 1] = none;
-        }
-        last = m, last_e = e;
+        for (int i = 0; i < NL; ++i)
+            v[i] = e == lane + 64 * i ? none : v[i];
     }
-    return true;
 }
 
-// Masks the picks outside of the best groups. `picks`: the wave's picks in LDS.
-// Returns false where the border between kept and left groups is closer than `margin`.
-template <int NL, typename V>
-__device__ __attribute__((always_inline)) inline bool mask_groups(V (&pick)[NL], const V *picks, const RouteParams &p,
-                                                                  int lane, V margin)
+// Masks the picks outside of the best groups; `picks`: the wave's picks in LDS.
+template <int NL>
+__device__ __attribute__((always_inline)) inline void mask_groups(double (&pick)[NL], const double *picks,
+                                                                  const RouteParams &p, int lane)
 {
-    const V none = -(V)__builtin_inff();
+    const double none = -__builtin_inf();
     const int size = p.E / p.n_group;
-    // lanes per group: the largest power of two that gives every group as many
-    int per = 1, shift = 0;
-    while (2 * per * p.n_group <= 64 && per < size)
-        per *= 2, ++shift;
-    const int g = lane >> shift, sub = lane & (per - 1);
-    V a = none, b = none;                                       // the two largest
-    if (g < p.n_group)
-        for (int j = sub; j < size; j += per) {
-            const V v = picks[g * size + j];
+    double value = none;
+    if (lane < p.n_group) {
+        double a = none, b = none;                              // the two largest
+        for (int j = 0; j < size; ++j) {
+            const double v = picks[lane * size + j];
             b = v > a ? a : (v > b ? v : b);
             a = v > a ? v : a;
         }
-    for (int d = 1; d < per; d *= 2) {
-        const V oa = __shfl_xor(a, d), ob = __shfl_xor(b, d);
-        const V low = oa > a ? a : oa, high = ob > b ? ob : b;
-        a = oa > a ? oa : a;
-        b = low > high ? low : high;
+        value = p.group_top > 1 && b > none ? a + b : a;
     }
-    V value = p.group_top > 1 && b > none ? a + b : a;
-    if (g >= p.n_group || sub != 0)
-        value = none;
     uint64_t keep = 0;
-    V last = none;
-    bool sure = true;
-    for (int j = 0; j <= p.topk_group; ++j) {
-        const V m = wave_max(value);
+    for (int j = 0; j < p.topk_group; ++j) {
+        const double m = wave_max(value);
         if (!(m > none))
-            break;                                              // groups without an expert left: nothing in them to mask
-        if (j == p.topk_group) {
-            sure = last - m > margin;
-            break;
-        }
-        last = m;
-        const int at = __ffsll((unsigned long long)__ballot(value == m)) - 1;
-        keep |= 1ull << (at >> shift);
-        if (lane == at)
-            value = none;
+            break;                                              // the other groups have no expert left
+        const int g = __ffsll((unsigned long long)__ballot(value == m)) - 1;
+        keep |= 1ull << g;
+        value = lane == g ? none : value;
     }
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-        const uint32_t e = (uint32_t)(lane + 64 * i);
-        const uint32_t of = min((uint32_t)((e * p.group_magic) >> 32), 63u);
-        if (!(keep >> of & 1ull))
+    for (int i = 0; i < NL; ++i)
+        if (!(keep >> min((lane + 64 * i) / size, 63) & 1ull))
             pick[i] = none;
-    }
-    return sure;
 }
 
-// float32 path: x (masked: -inf), bias b -> the picks in lanes at, at + 1, ..
-// False: not certain. `same(e, f)`: whether two experts have equal logits and biases.
-template <int NL, typename Same>
-__device__ __attribute__((always_inline)) inline bool route_fast(const float (&x)[NL], const float (&b)[NL],
-                                                                 bool with_bias, float top, const RouteParams &p,
-                                                                 int lane, int at, float *lds, int &id, Same same)
+// Logits (masked and past the end: -inf) and biases of the experts l, l + STEP, ..
+// Nothing branches but on `bias`: all loads are in flight together.
+template <int DT, int N, int STEP>
+__device__ __attribute__((always_inline)) inline void load_experts(const void *__restrict__ logits,
+                                                                   const float *__restrict__ bias, int64_t t, int32_t E,
+                                                                   int l, float (&x)[N], float (&b)[N])
 {
-    const float none = -__builtin_inff();
-    float pick[NL], largest = none;
-    float score_top = 1.0f;
-    if (p.score == NVFP4_SCORE_SOFTMAX) {
-        float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            pick[i] = __expf(x[i] - top);
-            sum += pick[i];
-        }
+    for (int i = 0; i < N; ++i)
+        x[i] = load_value<DT>(logits, t * E + min(l + STEP * i, E - 1));
+    if (bias) {
 #pragma unroll
-        for (int d = 32; d; d >>= 1)
-            sum += __shfl_xor(sum, d);
-        score_top = 1.0f / sum;                                 // the largest score: exp(0) / sum
-#pragma unroll
-        for (int i = 0; i < NL; ++i)
-            pick[i] *= score_top;
+        for (int i = 0; i < N; ++i)
+            b[i] = bias[min(l + STEP * i, E - 1)];
     } else {
 #pragma unroll
-        for (int i = 0; i < NL; ++i)
-            pick[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-x[i]));
+        for (int i = 0; i < N; ++i)
+            b[i] = 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-        const float v = pick[i] + b[i];
-        pick[i] = x[i] > none && v == v ? v : none;
-        largest = pick[i] > none ? fmaxf(largest, fabsf(pick[i])) : largest;
-    }
-    // exp(-d) is off by at most (d + 2) 2^-23 of itself, so a softmax numerator (d e^-d
-    // <= 0.37) or a sigmoid by less than 2^-20 of the largest score. The softmax's sum
-    // scales every score alike and matters beside a bias only: it is off by at most
-    // (0.37 E + 16) 2^-23 of itself. The pick's own rounding is 2^-24 of the pick.
-    const float part = p.score == NVFP4_SCORE_SOFTMAX && with_bias ? (p.E > 64 ? 0x1p-13f : 0x1p-17f) : 0x1p-20f;
-    const float margin = 2.0f * (score_top * part + wave_max(largest) * 0x1p-23f);
-    if (!(margin < 1.0f))
-        return false;                                           // infinite picks: float64 sorts them out
-    if (p.n_group > 1) {
-#pragma unroll
-        for (int i = 0; i < NL; ++i)
-            lds[lane + 64 * i] = pick[i];
-        wave_sync();
-        const bool sure = mask_groups<NL, float>(pick, lds, p, lane, 2.0f * margin);
-        wave_sync();
-        if (!sure)
-            return false;
-    }
-    return pick_k<NL, float>(pick, p.k, lane, at, id, [&](float m, int e, float last, int last_e) {
-        return last - m > margin || same(e, last_e);
-    });
+    for (int i = 0; i < N; ++i)
+        x[i] = x[i] == x[i] && l + STEP * i < E ? x[i] : -__builtin_inff();
 }
 
-// An expert's logit and bias for lane `lane` of the i-th 64; masked and past the end: -inf.
-template <int DT, int NL>
-__device__ __attribute__((always_inline)) inline void load_token(const void *__restrict__ logits,
-                                                                 const float *__restrict__ bias, int64_t t, int32_t E,
-                                                                 int lane, float (&x)[NL], float (&b)[NL])
-{
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-        const int e = lane + 64 * i;
-        const float v = e < E ? load_value<DT>(logits, t * E + e) : -__builtin_inff();
-        b[i] = bias && e < E ? bias[e] : 0.0f;
-        x[i] = v == v ? v : -__builtin_inff();
-    }
-}
-
-// float64 path, the definition itself: the picks in lanes at, at + 1, .. of
-// *picked; returns the softmax's sum. Not inlined: it is rarely taken, and its
-// registers would cost the fast path waves. It loads the token again.
+// One token by the wave: its picks in lanes at, at + 1, .. of *picked; returns
+// the softmax's sum. Not inlined: it is rarely taken, and its registers would
+// cost the fast path waves. `lds`: 64 * NL doubles.
 template <int DT, int NL>
 __device__ __attribute__((noinline)) double route_exact(const void *__restrict__ logits, const float *__restrict__ bias,
-                                                       int64_t t, RouteParams p, int at, int *picked, double *lds)
+                                                        int64_t t, RouteParams p, int at, int *picked, double *lds)
 {
     const double none = -__builtin_inf();
     const int lane = threadIdx.x % 64;
     float x[NL], b[NL];
-    load_token<DT, NL>(logits, bias, t, p.E, lane, x, b);
+    load_experts<DT, NL, 64>(logits, bias, t, p.E, lane, x, b);
     double pick[NL], top = none, score_sum = 1.0;
 #pragma unroll
     for (int i = 0; i < NL; ++i)
@@ -308,6 +188,7 @@ __device__ __attribute__((noinline)) double route_exact(const void *__restrict__
         double sum = 0.0;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
+            // +inf: those logits share, the others get nothing
             pick[i] = x[i] > none ? ((double)x[i] == top ? 1.0 : exp((double)x[i] - top)) : 0.0;
             sum += pick[i];
         }
@@ -330,96 +211,306 @@ __device__ __attribute__((noinline)) double route_exact(const void *__restrict__
         for (int i = 0; i < NL; ++i)
             lds[lane + 64 * i] = pick[i];
         wave_sync();
-        mask_groups<NL, double>(pick, lds, p, lane, 0.0);
+        mask_groups<NL>(pick, lds, p, lane);
         wave_sync();
     }
     int id = -1;
-    pick_k<NL, double>(pick, p.k, lane, at, id, [](double, int, double, int) { return true; });
+    pick_k<NL>(pick, p.k, lane, at, id);
     *picked = id;
     return score_sum;
 }
 
-// Lanes that hold one token's picks: the power of two from k on.
-__device__ __attribute__((always_inline)) inline int pick_lanes(int k)
+// ------------------------------------------------------------------ float32 with a bound
+
+// The value of another lane of the same 16; one instruction with the operation that takes it.
+template <int CTRL>
+__device__ __attribute__((always_inline)) inline uint32_t from_lane(uint32_t v)
 {
-    return k <= 1 ? 1 : 1 << (32 - __builtin_clz(k - 1));
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
 }
 
-// `n` tokens from t on by one wave (n * pick_lanes(k) <= 64): the picks of one
-// after the other, then the float64 weights of all at once. `lds`: 64 * NL
-// doubles of the wave's own.
-template <int DT, int NL>
+// Largest value over the token's LPT lanes, in all of them.
+template <int LPT>
+__device__ __attribute__((always_inline)) inline uint32_t token_max(uint32_t v)
+{
+    v = max(v, from_lane<0x128>(v));                            // row_ror:8, 4, 2, 1
+    v = max(v, from_lane<0x124>(v));
+    v = max(v, from_lane<0x122>(v));
+    v = max(v, from_lane<0x121>(v));
+    if constexpr (LPT == 64) {
+        v = max(max((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16)),
+                max((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48)));
+    }
+    return v;
+}
+template <int LPT>
+__device__ __attribute__((always_inline)) inline float token_max(float v)                  // v >= 0
+{
+    return __builtin_bit_cast(float, token_max<LPT>(__builtin_bit_cast(uint32_t, v)));
+}
+template <int LPT>
+__device__ __attribute__((always_inline)) inline float token_sum(float v)
+{
+    v += as_f32((int)from_lane<0x128>((uint32_t)as_i32(v)));
+    v += as_f32((int)from_lane<0x124>((uint32_t)as_i32(v)));
+    v += as_f32((int)from_lane<0x122>((uint32_t)as_i32(v)));
+    v += as_f32((int)from_lane<0x121>((uint32_t)as_i32(v)));
+    if constexpr (LPT == 64) {
+        v += __shfl_xor(v, 16);
+        v += __shfl_xor(v, 32);
+    }
+    return v;
+}
+// The two largest of the token's lanes: at each step the other lane's set is
+// another one.
+__device__ __attribute__((always_inline)) inline void join_two(uint32_t &a, uint32_t &b, uint32_t oa, uint32_t ob)
+{
+    b = max(min(a, oa), max(b, ob));
+    a = max(a, oa);
+}
+template <int LPT>
+__device__ __attribute__((always_inline)) inline void token_two(uint32_t &a, uint32_t &b)
+{
+    join_two(a, b, from_lane<0x128>(a), from_lane<0x128>(b));
+    join_two(a, b, from_lane<0x124>(a), from_lane<0x124>(b));
+    join_two(a, b, from_lane<0x122>(a), from_lane<0x122>(b));
+    join_two(a, b, from_lane<0x121>(a), from_lane<0x121>(b));
+    if constexpr (LPT == 64) {
+        join_two(a, b, (uint32_t)__shfl_xor((int)a, 16), (uint32_t)__shfl_xor((int)b, 16));
+        join_two(a, b, (uint32_t)__shfl_xor((int)a, 32), (uint32_t)__shfl_xor((int)b, 32));
+    }
+}
+
+// Descending, by merging (Batcher's odd-even merge sort); N a power of two.
+template <int N>
+__device__ __attribute__((always_inline)) inline void sort_down(uint32_t (&v)[N])
+{
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (j + i + k < N && (j + i) / (2 * p) == (j + i + k) / (2 * p)) {
+                        const uint32_t a = v[j + i], b = v[j + i + k];
+                        v[j + i] = max(a, b);
+                        v[j + i + k] = min(a, b);
+                    }
+}
+
+// The wave's 64 / LPT tokens t, t + 1, .. (those below t_end): lane j of a
+// token's lanes gets its j-th pick, or -1; `top` its largest logit. Returns
+// whether the token's picks are certain (the same in its lanes).
+// Expert of key i of lane l: i * LPT + l. Groups have to be whole runs of LPT.
+template <int DT, int LPT, int NL>
+__device__ __attribute__((always_inline)) inline bool route_fast(const void *__restrict__ logits,
+                                                                 const float *__restrict__ bias, const RouteParams &p,
+                                                                 int64_t t, bool here, int l, int &id, float &top)
+{
+    constexpr int IB = LPT * NL <= 64 ? 6 : LPT * NL <= 128 ? 7 : LPT * NL <= 256 ? 8 : LPT * NL <= 512 ? 9 : 10;
+    constexpr uint32_t kIndex = (1u << IB) - 1;
+    constexpr uint32_t kGroup = LPT - 1;                        // a group's value stands above its index
+    constexpr int GB = LPT == 16 ? 4 : 6;
+    constexpr float kSteps = (float)((1u << (31 - IB)) - 16);   // steps for a pick of the token's largest size
+    const float none = -__builtin_inff();
+    float x[NL], b[NL], v[NL];
+    top = none;
+    load_experts<DT, NL, LPT>(logits, bias, here ? t : 0, p.E, l, x, b);
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+        top = fmaxf(top, x[i]);
+    // the largest logit: by its order as an integer
+    const uint32_t bits = __builtin_bit_cast(uint32_t, top);
+    const uint32_t high = token_max<LPT>(bits >> 31 ? ~bits : bits | 0x80000000u);
+    top = __builtin_bit_cast(float, high >> 31 ? high & 0x7FFFFFFFu : ~high);
+    float score_top = 1.0f;
+    if (p.score == NVFP4_SCORE_SOFTMAX) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            v[i] = __expf(x[i] - top);
+            sum += v[i];
+        }
+        score_top = 1.0f / token_sum<LPT>(sum);                 // the largest score: exp(0) / sum
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            v[i] *= score_top;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            v[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-x[i]));
+    }
+    float largest = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const float pick = v[i] + b[i];
+        v[i] = x[i] > none && pick > none ? pick : none;        // NaN too
+        largest = v[i] > none ? fmaxf(largest, fabsf(v[i])) : largest;
+    }
+    largest = token_max<LPT>(largest);
+    // exp(-d) is off by at most (d + 2) 2^-23 of itself, so a softmax numerator (d e^-d
+    // <= 0.37) or a sigmoid by less than 2^-20 of the largest score. The softmax's sum
+    // scales every score alike and matters beside a bias only: it is off by at most
+    // (0.37 E + 16) 2^-23 of itself. A pick's own rounding is 2^-24 of the largest, its
+    // way to a key two steps of 2^-23 and one of the key's.
+    const float part = p.score == NVFP4_SCORE_SOFTMAX && bias ? (p.E > 64 ? 0x1p-13f : 0x1p-17f) : 0x1p-20f;
+    const float margin = 2.0f * (score_top / largest * part + 0x1p-22f) * kSteps + 3.0f;
+    bool sure = largest > 0.0f && largest < __builtin_inff() && margin < 0.25f * kSteps;
+    const uint32_t close = sure ? (uint32_t)margin : 0u;
+    const float scale = kSteps / largest;
+    uint32_t key[NL];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const uint32_t step = (uint32_t)(fmaf(v[i], scale, kSteps) + 1.0f);
+        key[i] = v[i] > none ? step << IB | (kIndex - (uint32_t)(i * LPT + l)) : 0u;
+    }
+    if (p.n_group > 1) {
+        const int runs = p.E / p.n_group / LPT;                 // keys per group and lane
+        uint32_t mine = 0u;                                     // lane g: group g's value above its index
+        uint32_t a = 0u, c = 0u;
+        int g = 0, in_group = 0;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            join_two(a, c, key[i], 0u);
+            if (++in_group == runs) {
+                token_two<LPT>(a, c);
+                // a second value that is missing counts as 0
+                const uint32_t two = (a >> IB) + (p.group_top > 1 ? (c ? c >> IB : (uint32_t)kSteps + 1u) : 0u);
+                if (l == g)
+                    mine = a ? two << GB | (kGroup - (uint32_t)g) : 0u;
+                a = c = 0u;
+                in_group = 0;
+                ++g;
+            }
+        }
+        uint64_t keep = 0;
+        uint32_t last = 0u;
+        for (int j = 0; j <= p.topk_group; ++j) {
+            const uint32_t m = token_max<LPT>(mine);
+            if (j == p.topk_group) {
+                sure = sure && !(m && (last >> GB) - (m >> GB) <= 2u * close);
+            } else {
+                keep |= m ? 1ull << (kGroup - (m & kGroup)) : 0ull;
+                mine = mine == m ? 0u : mine;
+                last = m;
+            }
+        }
+        in_group = 0;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            key[i] = keep & 1ull ? key[i] : 0u;
+            if (++in_group == runs) {
+                keep >>= 1;
+                in_group = 0;
+            }
+        }
+    }
+    sort_down<NL>(key);
+    uint32_t got = 0u;
+    for (int j = 0; j <= p.k; ++j) {                            // one more: the first that is left out
+        const uint32_t m = token_max<LPT>(key[0]);
+        got = l == j ? m : got;
+        const bool pop = key[0] == m;
+#pragma unroll
+        for (int i = 0; i + 1 < NL; ++i) {
+            uint32_t next = key[i + 1];
+            asm("" : "+v"(next));                               // a choice of values, not of an index into key
+            key[i] = pop ? next : key[i];
+        }
+        key[NL - 1] = pop ? 0u : key[NL - 1];
+    }
+    id = got ? (int)(kIndex - (got & kIndex)) : -1;
+    // neighbours in the ranking closer than the bound: from the same logit and bias?
+    const uint32_t next = LPT == 16 ? from_lane<0x101>(got) : (uint32_t)__shfl_down((int)got, 1);      // row_shl:1
+    bool doubt = here && l < p.k && got && next && (got >> IB) - (next >> IB) <= close;
+    if (__ballot(doubt)) {
+        if (doubt) {
+            const int other = (int)(kIndex - (next & kIndex));
+            doubt = load_value<DT>(logits, t * p.E + id) != load_value<DT>(logits, t * p.E + other) ||
+                    (bias && bias[id] != bias[other]);
+        }
+        const uint32_t any = token_max<LPT>(doubt ? 1u : 0u);
+        sure = sure && any == 0u;
+    }
+    if (l >= p.k)
+        id = -1;
+    return sure;
+}
+
+// The tokens t .. t + 64 / LPT - 1 (below T) by one wave. NX: experts per lane of
+// the float64 path. `lds`: 64 * NX doubles of the wave's own.
+template <int DT, int LPT, int NL, int NX>
 __device__ __attribute__((always_inline)) inline void route_tokens(const void *__restrict__ logits,
                                                                    const float *__restrict__ bias,
                                                                    int32_t *__restrict__ ids,
                                                                    float *__restrict__ weights, const RouteParams &p,
-                                                                   int64_t t, int n, int lane, double *lds)
+                                                                   int64_t t0, int lane, double *lds)
 {
-    const int width = pick_lanes(p.k), mine = lane / width;    // the token whose pick this lane holds
+    const int l = lane % LPT;
+    const int64_t t = t0 + lane / LPT;
+    const bool here = t < p.T;
     int id = -1;
-    float my_top = 0.0f;
-    double my_sum = 1.0;
-    for (int q = 0; q < n; ++q) {
-        const int at = q * width;
-        float x[NL], b[NL], top = -__builtin_inff();
-        load_token<DT, NL>(logits, bias, t + q, p.E, lane, x, b);
-#pragma unroll
-        for (int i = 0; i < NL; ++i)
-            top = fmaxf(top, x[i]);
-        top = wave_max(top);
-        // softmax weights that are not renormalised need the float64 sum over all
-        // experts, and infinite logits their own rule
-        const bool plain = top < __builtin_inff() && (p.score == NVFP4_SCORE_SIGMOID || p.renormalize);
+    float top = 0.0f;
+    double sum = 1.0;
+    bool sure = false;
+    // the fast path's lanes hold one pick more than k
+    if (p.k < LPT && (p.n_group == 1 || (p.E / p.n_group % LPT == 0 && p.n_group <= LPT)))
+        sure = route_fast<DT, LPT, NL>(logits, bias, p, t, here, l, id, top);
+    else {
+        top = -__builtin_inff();
+        for (int e = l; e < p.E; e += LPT)
+            top = fmaxf(top, load_value<DT>(logits, (here ? t : 0) * p.E + e));         // skips NaN
+        for (int d = 1; d < LPT; d *= 2)
+            top = fmaxf(top, __shfl_xor(top, d));
+    }
+    // softmax weights that are not renormalised need the float64 sum over all
+    // experts, and infinite logits their own rule
+    sure = sure && top < __builtin_inff() && (p.score == NVFP4_SCORE_SIGMOID || p.renormalize);
+    uint64_t again = __ballot(here && !sure && l == 0);
+    while (again) {
+        const int at = __ffsll((unsigned long long)again) - 1;
+        again &= again - 1;
         int got = -1;
-        double sum = 1.0;
-        auto same = [&](int e, int f) {
-            const int64_t row = (t + q) * p.E;
-            return f >= 0 && load_value<DT>(logits, row + e) == load_value<DT>(logits, row + f) &&
-                   (!bias || bias[e] == bias[f]);
-        };
-        if (!plain || !route_fast<NL>(x, b, bias != nullptr, top, p, lane, at, (float *)lds, got, same))
-            sum = route_exact<DT, NL>(logits, bias, t + q, p, at, &got, lds);
-        if (mine == q) {
+        const double s = route_exact<DT, NX>(logits, bias, t0 + at / LPT, p, at, &got, lds);
+        if (lane / LPT == at / LPT) {
             id = got;
-            my_top = top;
-            my_sum = sum;
+            sum = s;
         }
     }
-    const int64_t token = t + mine;
     double w = 0.0;
     if (id >= 0) {
-        const float v = load_value<DT>(logits, token * p.E + id);
+        const float v = load_value<DT>(logits, t * p.E + id);
         if (p.score == NVFP4_SCORE_SIGMOID)
             w = 1.0 / (1.0 + exp(-(double)v));
         else                                                    // renormalised: the sum cancels
-            w = (v == my_top ? 1.0 : exp((double)v - (double)my_top)) / (p.renormalize ? 1.0 : my_sum);
+            w = (v == top ? 1.0 : exp((double)v - (double)top)) / (p.renormalize ? 1.0 : sum);
     }
     if (p.renormalize) {
         double total = w;
-        for (int d = 1; d < width; d *= 2)
+#pragma unroll
+        for (int d = 1; d < LPT; d *= 2)
             total += __shfl_xor(total, d);
         w = total > 0.0 ? w / total : 0.0;
     }
-    const int j = lane % width;
-    if (mine < n && j < p.k) {
-        ids[token * p.k + j] = id;
-        weights[token * p.k + j] = (float)(w * (double)p.scaling);
+    if (here && l < p.k) {
+        ids[t * p.k + l] = id;
+        weights[t * p.k + l] = (float)(w * (double)p.scaling);
     }
 }
 
-// per_wave tokens per wave.
-template <int DT, int NL>
+template <int DT, int LPT, int NL, int NX>
 __global__ __launch_bounds__(64 * kRouteWaves) void nvfp4_route_kernel(const void *__restrict__ logits,
                                                                        const float *__restrict__ bias,
                                                                        int32_t *__restrict__ ids,
-                                                                       float *__restrict__ weights, RouteParams p,
-                                                                       int32_t per_wave)
+                                                                       float *__restrict__ weights, RouteParams p)
 {
-    __shared__ double lds[kRouteWaves][64 * NL];
+    __shared__ double lds[kRouteWaves][64 * NX];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int64_t t = ((int64_t)blockIdx.x * kRouteWaves + wave) * per_wave;
+    const int64_t t = ((int64_t)blockIdx.x * kRouteWaves + wave) * (64 / LPT);
     if (t < p.T)
-        route_tokens<DT, NL>(logits, bias, ids, weights, p, t, (int)min((int64_t)per_wave, p.T - t), lane, lds[wave]);
+        route_tokens<DT, LPT, NL, NX>(logits, bias, ids, weights, p, t, lane, lds[wave]);
 }
 
 // ------------------------------------------------------------------ lists
@@ -590,7 +681,7 @@ __global__ __launch_bounds__(kListThreads) void nvfp4_place_kernel(const int32_t
 }
 
 // Few tokens: the whole router in one workgroup of 16 waves.
-template <int DT, int NL>
+template <int DT, int LPT, int NL, int NX>
 __global__ __launch_bounds__(kSmallThreads) void nvfp4_route_small_kernel(
     const void *__restrict__ logits, const float *__restrict__ bias, int32_t *__restrict__ ids,
     float *__restrict__ weights, int32_t *__restrict__ offsets, int32_t *__restrict__ order, RouteParams p, int32_t bits)
@@ -598,9 +689,9 @@ __global__ __launch_bounds__(kSmallThreads) void nvfp4_route_small_kernel(
     extern __shared__ int32_t list_lds[];                       // route: the waves' picks; lists: base[E], at[waves][E]
     __shared__ int32_t part[kSmallThreads / 64];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    double *picks = (double *)list_lds + wave * (64 * NL);
-    for (int t = wave; t < p.T; t += kSmallThreads / 64)
-        route_tokens<DT, NL>(logits, bias, ids, weights, p, t, 1, lane, picks);
+    double *picks = (double *)list_lds + wave * (64 * NX);
+    for (int t = wave * (64 / LPT); t < p.T; t += kSmallThreads / LPT)
+        route_tokens<DT, LPT, NL, NX>(logits, bias, ids, weights, p, t, lane, picks);
     __syncthreads();                                            // this workgroup's ids are in its reach
     int32_t *base = list_lds, *at = list_lds + p.E;
     const int e = threadIdx.x;
@@ -811,44 +902,46 @@ nvfp4_status_t nvfp4_moe_route(const void *logits, int dtype, const float *bias,
     const size_t need = nvfp4_moe_route_workspace_bytes(T, E, k);
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
         return NVFP4_ERR_WORKSPACE;
-    // tokens per wave: as many as its lanes hold picks for, but 4 waves per SIMD
-    int64_t width = 1;
-    while (width < k)
-        width *= 2;
-    const int64_t per_wave = std::max<int64_t>(1, std::min<int64_t>(64 / width, T / (4 * kSimds)));
-    const int64_t per_wg = per_wave * kRouteWaves, grid = (T + per_wg - 1) / per_wg;
+    // 16 lanes per token where they hold its picks and at most 16 experts each, and
+    // not where a wave per token ends sooner (one token: 9 against 10.5 us)
+    const bool narrow = k < 16 && E <= 256 && T > kSmallThreads / 64;
+    const int64_t per_wg = kRouteWaves * (narrow ? 4 : 1), grid = (T + per_wg - 1) / per_wg;
     if (grid > kMaxGrid)
         return NVFP4_ERR_INVALID_SHAPE;
     const hipStream_t st = (hipStream_t)stream;
-    const int64_t size = E / r.n_group;
     RouteParams p{(int32_t)T, (int32_t)E, (int32_t)k, r.score, r.n_group, r.topk_group, r.group_top, r.renormalize,
-                  r.scaling, (uint64_t)(((INT64_C(1) << 32) + size - 1) / size)};
+                  r.scaling};
     const int32_t S = (int32_t)(T * k);
     int32_t bits = 1;
     while ((E >> bits) != 0)
         ++bits;                                                 // E itself is a key too
     const bool small = route_small(T, E, k);
     by_type(dtype, [&](auto dt) {
-        auto go = [&](auto nl) {
+        auto go = [&](auto lpt, auto nl, auto nx) {
             if (small) {
-                const size_t lds = std::max<size_t>(kSmallThreads / 64 * 64 * nl() * 8, (1 + kSmallThreads / 64) * E * 4);
-                hipLaunchKernelGGL((nvfp4_route_small_kernel<dt(), nl()>), dim3(1), dim3(kSmallThreads), lds, st, logits,
-                                   bias, ids, weights, offsets, order, p, bits);
+                const size_t lds = std::max<size_t>(kSmallThreads / 64 * 64 * nx() * 8, (1 + kSmallThreads / 64) * E * 4);
+                hipLaunchKernelGGL((nvfp4_route_small_kernel<dt(), lpt(), nl(), nx()>), dim3(1), dim3(kSmallThreads), lds,
+                                   st, logits, bias, ids, weights, offsets, order, p, bits);
             } else {
-                hipLaunchKernelGGL((nvfp4_route_kernel<dt(), nl()>), dim3((uint32_t)grid), dim3(64 * kRouteWaves), 0, st,
-                                   logits, bias, ids, weights, p, (int32_t)per_wave);
+                hipLaunchKernelGGL((nvfp4_route_kernel<dt(), lpt(), nl(), nx()>), dim3((uint32_t)grid),
+                                   dim3(64 * kRouteWaves), 0, st, logits, bias, ids, weights, p);
             }
         };
-        if (E <= 64)
-            go(std::integral_constant<int, 1>{});
-        else if (E <= 128)
-            go(std::integral_constant<int, 2>{});
+        auto n = [](auto v) { return v; };
+#define NVFP4_N(v) n(std::integral_constant<int, v>{})
+        if (narrow && E <= 64)
+            go(NVFP4_N(16), NVFP4_N(4), NVFP4_N(1));
+        else if (narrow && E <= 128)
+            go(NVFP4_N(16), NVFP4_N(8), NVFP4_N(2));
+        else if (narrow)
+            go(NVFP4_N(16), NVFP4_N(16), NVFP4_N(4));
         else if (E <= 256)
-            go(std::integral_constant<int, 4>{});
+            go(NVFP4_N(64), NVFP4_N(4), NVFP4_N(4));
         else if (E <= 512)
-            go(std::integral_constant<int, 8>{});
+            go(NVFP4_N(64), NVFP4_N(8), NVFP4_N(8));
         else
-            go(std::integral_constant<int, 16>{});
+            go(NVFP4_N(64), NVFP4_N(16), NVFP4_N(16));
+#undef NVFP4_N
     });
     if (!small) {
         const int32_t chunk = (int32_t)list_chunk(S), nc = (S + chunk - 1) / chunk;

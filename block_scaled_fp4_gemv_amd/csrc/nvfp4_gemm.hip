@@ -56,7 +56,7 @@ constexpr int kMaxTickets = 16384;              // tiles of a split product
 constexpr int64_t kTicketBytes = kMaxTickets * 4;
 constexpr int64_t kMaxPartialBytes = INT64_C(64) << 20;
 constexpr int kMaxSplits = 16;
-constexpr int64_t kMaxGrid = 0xFFFFFF;          // workgroups of 256 threads in 2^32 work items
+constexpr int64_t kMaxGrid = 0x7FFFFF;          // workgroups of up to 512 threads in 2^32 work items
 
 // ------------------------------------------------------------------ copies to LDS
 
@@ -454,7 +454,6 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void nvfp4_gemm_wide_kern
     constexpr int kOffSB = T::kOffSA + kWordsA * (ODD ? 2 : 1);
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     __shared__ int32_t s_slot[EXPERTS ? BN : 1];
-    __shared__ uint32_t s_ticket;
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const Where w = locate<EXPERTS, BM, BN, T::kThreads>(p, s_slot);
@@ -462,16 +461,13 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void nvfp4_gemm_wide_kern
         return;
 
     // --- this wave's copies
-    const int first = w.split * p.stages_per_split;
-    const int stages = min(p.stages_per_split, p.stages - first);
+    const int stages = p.stages;
     constexpr int CA = T::TA / kWaves, CB = T::TB / kWaves;
     constexpr int CSA = T::TSA / kWaves, CSB = (T::TSB + kWaves - 1) / kWaves;
     // where B's words are fewer than a copy per wave, the first TSB waves make them
     const bool has_sb = T::TSB % kWaves == 0 || wave < T::TSB;
     const uint32_t step_words = p.blocked ? 1024 : 8, back_words = p.blocked ? 512 : 4;
     Source a = source_a(p, w), b = source_b<EXPERTS>(p, w);
-    a.codes += (int64_t)first * 64, b.codes += (int64_t)first * 64;
-    a.words += (int64_t)first * step_words, b.words += (int64_t)first * step_words;
     uint32_t oa[CA], ob[CB], osa[CSA], osb[CSB];
     int half_a[CSA], half_b[CSB];
     // lane's 16 bytes of a 1 KiB copy: row lane / 4 of 16, piece swizzled back
@@ -596,7 +592,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void nvfp4_gemm_wide_kern
 #pragma unroll
     for (int s = 0; s < NS - 1; ++s)
         if (s < stages)
-            issue(first + s, s);
+            issue(s, s);
     const float scale = total_scale<EXPERTS>(p, w.l);
     int slot = 0, i = 0;
     for (; i + NS - 1 < stages; ++i) {
@@ -604,97 +600,53 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void nvfp4_gemm_wide_kern
         // barrier every wave has done with stage i - 1, whose slot is next
         wait_stage(std::integral_constant<int, NS - 2>{});
         barrier();
-        issue(first + i + NS - 1, slot == 0 ? NS - 1 : slot - 1);
-        compute(first + i, slot);
+        issue(i + NS - 1, slot == 0 ? NS - 1 : slot - 1);
+        compute(i, slot);
         slot = slot + 1 == NS ? 0 : slot + 1;
     }
     for (; i < stages; ++i) {
         wait_stage(None{});
         barrier();
-        compute(first + i, slot);
+        compute(i, slot);
         slot = slot + 1 == NS ? 0 : slot + 1;
     }
 
     // --- results. Register r of fragment (j, i): row of B rb0 + 32 j + 8 (r / 4) + 4 (lane / 32) + r % 4,
     // row of A ra0 + 32 i + lane % 32.
-    auto each = [&](auto f) {
+    // Through LDS, so that a lane stores 16 bytes of a row at a time (2-byte
+    // stores of 32 neighbours took 17 us per 256 x 256 tile, most of it these).
+    barrier();                                  // all waves have read their last stage
+    uint8_t *const out = lds + wave * (32 * T::kPitch);
+    const int size = p.dtype == NVFP4_F32 ? 4 : 2;
+    const int per_row = FM * 32 * size / 16, rows_at_once = 64 / per_row, per_piece = 16 / size;
+    const int piece_n = lane / per_row, piece_m = lane % per_row * per_piece;
+    const int m = w.m0 + ra0 + piece_m;
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
+    for (int j = 0; j < FN; ++j) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int64_t row = row_at<EXPERTS>(p, w, s_slot, rb0 + 32 * j + 8 * (r / 4) + 4 * half + r % 4);
-                if (row < 0)
-                    continue;
+        for (int r = 0; r < 16; ++r)
 #pragma unroll
-                for (int i = 0; i < FM; ++i) {
-                    const int m = w.m0 + ra0 + 32 * i + l32;
-                    if (m < p.M)
-                        f(acc[j][i][r], row + m);
+            for (int i = 0; i < FM; ++i)
+                store_value(out + (8 * (r / 4) + 4 * half + r % 4) * T::kPitch, 32 * i + l32, acc[j][i][r] * scale, p.dtype);
+        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+        for (int n = piece_n; n < 32; n += rows_at_once) {
+            const uint4_t v = *(const uint4_t *)(out + n * T::kPitch + piece_m * size);
+            const int64_t row = row_at<EXPERTS>(p, w, s_slot, rb0 + 32 * j + n);
+            if (row < 0 || m >= p.M)
+                continue;
+            uint8_t *c = p.c + (row + m) * size;
+            if (m + per_piece <= p.M) {
+                __builtin_memcpy(c, &v, 16);
+            } else {
+                for (int x = 0; x < p.M - m; ++x) {
+                    if (size == 4)
+                        ((uint32_t *)c)[x] = *(const uint32_t *)(out + n * T::kPitch + (piece_m + x) * 4);
+                    else
+                        ((uint16_t *)c)[x] = *(const uint16_t *)(out + n * T::kPitch + (piece_m + x) * 2);
                 }
             }
-    };
-    if (p.splits == 1) {
-        // Through LDS, so that a lane stores 16 bytes of a row at a time (2-byte
-        // stores of 32 neighbours took 17 us per 256 x 256 tile, most of it these).
-        barrier();                              // all waves have read their last stage
-        uint8_t *const out = lds + wave * (32 * T::kPitch);
-        const int size = p.dtype == NVFP4_F32 ? 4 : 2;
-        const int per_row = FM * 32 * size / 16, rows_at_once = 64 / per_row, per_piece = 16 / size;
-        const int piece_n = lane / per_row, piece_m = lane % per_row * per_piece;
-        const int m = w.m0 + ra0 + piece_m;
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-#pragma unroll
-                for (int i = 0; i < FM; ++i)
-                    store_value(out + (8 * (r / 4) + 4 * half + r % 4) * T::kPitch, 32 * i + l32, acc[j][i][r] * scale, p.dtype);
-            asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
-            for (int n = piece_n; n < 32; n += rows_at_once) {
-                const uint4_t v = *(const uint4_t *)(out + n * T::kPitch + piece_m * size);
-                const int64_t row = row_at<EXPERTS>(p, w, s_slot, rb0 + 32 * j + n);
-                if (row < 0 || m >= p.M)
-                    continue;
-                uint8_t *c = p.c + (row + m) * size;
-                if (m + per_piece <= p.M) {
-                    __builtin_memcpy(c, &v, 16);
-                } else {
-                    for (int x = 0; x < p.M - m; ++x) {
-                        if (size == 4)
-                            ((uint32_t *)c)[x] = *(const uint32_t *)(out + n * T::kPitch + (piece_m + x) * 4);
-                        else
-                            ((uint16_t *)c)[x] = *(const uint16_t *)(out + n * T::kPitch + (piece_m + x) * 2);
-                    }
-                }
-            }
-            asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
         }
-        return;
-    }
-    // partial sums: agent-scope stores (past this XCD's L2), then the ticket
-    const int64_t one = (int64_t)(EXPERTS ? p.N : p.N * (int64_t)p.L) * p.M;
-    each([&](float x, int64_t at) {
-        __hip_atomic_store(&p.partials[w.split * one + at], x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    });
-    if (!last_of_tile(p, w.tile, &s_ticket))
-        return;
-#pragma unroll 1
-    for (int g = 0; g < FN * FM * 2; ++g) {                     // 8 registers at a time
-        const int j = g / (FM * 2), i = g / 2 % FM, r0 = g % 2 * 8;
-        int64_t at[8];
-        float sum[8];
-        const int m = w.m0 + ra0 + 32 * i + l32;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            const int r = r0 + x;
-            const int64_t row = row_at<EXPERTS>(p, w, s_slot, rb0 + 32 * j + 8 * (r / 4) + 4 * half + r % 4);
-            at[x] = row < 0 || m >= p.M ? -1 : row + m;
-        }
-        add_slices<8>(p, one, at, sum);
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-            if (at[x] >= 0)
-                store_value(p.c, at[x], sum[x] * scale, p.dtype);
+        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
     }
 }
 
@@ -930,13 +882,14 @@ __global__ __launch_bounds__(T::kThreads, T::kPerCu) void nvfp4_gemm_wave_kernel
 
 typedef Tile<2, 4, 4, 2, 3, 1> TileLarge;       // 256 x 256, 8 waves
 typedef Tile<4, 2, 2, 2, 2, 2> TileTall;        // 256 x 128
+typedef Tile<2, 2, 2, 2, 4, 2> TileMid;         // 128 x 128
 typedef WaveTile<2, 2, 1, 4, 2, 2, 2> TileSquare;  // 64 x 64, 4 waves along K
 typedef WaveTile<2, 1, 2, 2, 2, 3, 1> TileFew;     // 128 x 32, 2 waves along K
 typedef WaveTile<2, 1, 1, 4, 2, 3, 1> TileFewK;    // 64 x 32, 4 waves along K
 typedef WaveTile<1, 1, 1, 4, 2, 3, 1> TileOne;     // 32 x 32, 4 waves along K
 typedef WaveTile<1, 1, 1, 8, 3, 1, 1> TileOneK;    // 32 x 32, 8 waves along K
 
-enum class Kind { Large, Tall, Square, Few, FewK, One, OneK };
+enum class Kind { Large, Tall, Mid, Square, Few, FewK, One, OneK };
 
 struct Plan {
     Kind kind;
@@ -955,30 +908,41 @@ bool gemm_shape(int64_t M, int64_t N, int64_t K, int64_t L)
 }
 
 // The tile shapes and what they cost, from which the plans choose. us on one
-// MI355X, measured over 40 shapes (M and N 16 .. 7168, K 512 .. 16384, 1 to 16
-// slices): `alone`, a workgroup's time per stage (128 k) with its CU to itself;
+// MI355X, measured over 60 shapes (M and N 16 .. 7168, K 512 .. 16384, 1 to 16
+// slices; 1 to 16384 tokens of 8 to 64 experts): `alone`, a workgroup's time per
+// stage (128 k) with its CU to itself;
 // `each`, what a stage adds to the CU's time per workgroup when more share it;
-// `start`, what a workgroup of routed experts adds besides.
+// `start`, what a workgroup adds besides (its first copies and its results);
+// `listed`, what one of routed experts adds to that (its list and weights that
+// nobody has read yet).
 //   Large tiles decode less per product (6 vector instructions per MFMA for 256 x
-// 256 and 256 x 128, 8 for 64 x 64, 12 for 32 wide, 16 for 32 x 32) and need
-// many tiles to fill the GPU; small ones put their waves along K. E.g. 4096 x 333
-// x 7168: 64 x 64 33 us, 64 x 32 33, 128 x 32 37, 256 x 128 above 100; 7168 x
-// 4096 x 16384: 256 x 256 760, 256 x 128 810, 64 x 64 970; 4096 x 128 x 7168: 64
-// x 32 14.4, 32 x 32 15.4, 64 x 64 18.2; 7168 x 16 x 16384: 32 x 32 with 8
-// waves along K 17.3, with 4 20.2, 64 x 32 in two slices 19.1.
+// 256 and 256 x 128, 8 for 128 x 128 and 64 x 64, 12 for 32 wide, 16 for 32 x 32)
+// and need many tiles to fill the GPU; small ones put their waves along K. E.g.
+// 4096 x 333 x 7168: 64 x 32 33 us, 64 x 64 34, 128 x 32 37, 128 x 128 56, 256 x
+// 128 above 100; 4096 x 1024 x 4096: 128 x 128 40, 64 x 64 45, 64 x 32 52, 256 x
+// 128 64; 7168 x 4096 x 16384: 256 x 256 760, 256 x 128 810, 64 x 64 970; 4096 x
+// 128 x 7168: 64 x 32 14.4, 32 x 32 15.4, 64 x 64 18.2; 7168 x 16 x 16384: 32 x 32
+// with 8 waves along K 17.3, with 4 20.2, 64 x 32 in two slices 19.1.
+//   A shape that is never fastest in a use is not built for it: 256 x 256 against
+// 256 x 128 for 16384 slots of 32 experts, 7168 x 4096: 1068 against 970 us; 256 x
+// 128 against 128 x 128 and 256 x 256 in dense products: at most 2 % ahead of the
+// better one. The wide kernel has no slices: they would be used where few tiles
+// have a long K, and there 64 x 64 in slices is ahead.
+enum Use { kDense = 1, kExperts = 2, kBoth = 3 };
 struct Shape {
     Kind kind;
-    int bm, bn;
-    double alone, each, start;
+    int bm, bn, uses, max_splits;
+    double alone, each, start, listed;
 };
 constexpr Shape kShapes[] = {
-    {Kind::Large, TileLarge::BM, TileLarge::BN, 2.85, 2.95, 8.0},
-    {Kind::Tall, TileTall::BM, TileTall::BN, 2.03, 1.58, 4.0},
-    {Kind::Square, TileSquare::BM, TileSquare::BN, 0.28, 0.27, 2.0},
-    {Kind::Few, TileFew::BM, TileFew::BN, 0.35, 0.35, 1.6},
-    {Kind::FewK, TileFewK::BM, TileFewK::BN, 0.15, 0.185, 1.2},
-    {Kind::One, TileOne::BM, TileOne::BN, 0.115, 0.095, 0.9},
-    {Kind::OneK, TileOneK::BM, TileOneK::BN, 0.085, 0.10, 1.5},
+    {Kind::Large, TileLarge::BM, TileLarge::BN, kDense, 1, 2.85, 2.88, 8.0, 0.0},
+    {Kind::Tall, TileTall::BM, TileTall::BN, kExperts, 1, 2.03, 1.58, 5.0, 9.0},
+    {Kind::Mid, TileMid::BM, TileMid::BN, kBoth, 1, 1.05, 0.98, 1.0, 4.0},
+    {Kind::Square, TileSquare::BM, TileSquare::BN, kBoth, kMaxSplits, 0.38, 0.30, 0.3, 1.7},
+    {Kind::Few, TileFew::BM, TileFew::BN, kBoth, kMaxSplits, 0.40, 0.35, 0.3, 1.5},
+    {Kind::FewK, TileFewK::BM, TileFewK::BN, kBoth, kMaxSplits, 0.19, 0.185, 0.3, 0.9},
+    {Kind::One, TileOne::BM, TileOne::BN, kBoth, kMaxSplits, 0.115, 0.095, 0.2, 0.7},
+    {Kind::OneK, TileOneK::BM, TileOneK::BN, kDense, kMaxSplits, 0.085, 0.10, 0.2, 0.0},
 };
 constexpr double kCus = 256.0, kSplitUs = 1.0, kSliceUs = 0.15, kPartialBytesPerUs = 2.0e6;
 
@@ -990,18 +954,20 @@ Plan choose(int64_t M, int64_t K, int64_t rows, bool experts, F tiles_of)
     Plan best{};
     double best_us = 0.0;
     for (const Shape &s : kShapes) {
+        if (!(s.uses & (experts ? kExperts : kDense)))
+            continue;
         Plan p{};
         p.kind = s.kind, p.bm = s.bm, p.bn = s.bn;
         p.stages = (int32_t)ceil_div(K, kStageK);
         p.tiles_m = ceil_div(M, s.bm);
         const double tiles = tiles_of(s, p);
-        for (int64_t splits = 1; splits <= kMaxSplits && splits <= p.stages; splits *= 2) {
+        for (int64_t splits = 1; splits <= s.max_splits && splits <= p.stages; splits *= 2) {
             p.per_split = (int32_t)ceil_div(p.stages, splits);
             p.splits = (int32_t)ceil_div(p.stages, p.per_split);
             if (p.splits > 1 && (p.tiles > kMaxTickets || p.splits * rows > kMaxPartialBytes / 4 / M))
                 break;
             const double n = tiles * p.splits / kCus, load = experts ? std::max(n, 1.0) : std::ceil(n);
-            double us = p.per_split * std::max(s.alone, s.each * load) + (experts ? s.start * load : 0.0);
+            double us = p.per_split * std::max(s.alone, s.each * load) + (s.start + (experts ? s.listed : 0.0)) * load;
             if (p.splits > 1)
                 us += kSplitUs + p.splits * (kSliceUs + 8.0 * rows * M / kPartialBytesPerUs);
             if (best_us == 0.0 || us < best_us) {
@@ -1070,13 +1036,23 @@ nvfp4_status_t run(const Plan &plan, const GemmParams &p, hipStream_t st)
     const int64_t grid = plan.tiles * plan.splits;
     hipError_t e = hipSuccess;
     switch (plan.kind) {
-    case Kind::Large: e = launch_wide<TileLarge, EXPERTS>(p, grid, st); break;
-    case Kind::Tall: e = launch_wide<TileTall, EXPERTS>(p, grid, st); break;
+    case Kind::Large:
+        if constexpr (!EXPERTS)
+            e = launch_wide<TileLarge, EXPERTS>(p, grid, st);
+        break;
+    case Kind::Tall:
+        if constexpr (EXPERTS)
+            e = launch_wide<TileTall, EXPERTS>(p, grid, st);
+        break;
+    case Kind::Mid: e = launch_wide<TileMid, EXPERTS>(p, grid, st); break;
     case Kind::Square: e = launch_wave<TileSquare, EXPERTS>(p, grid, st); break;
     case Kind::Few: e = launch_wave<TileFew, EXPERTS>(p, grid, st); break;
     case Kind::FewK: e = launch_wave<TileFewK, EXPERTS>(p, grid, st); break;
     case Kind::One: e = launch_wave<TileOne, EXPERTS>(p, grid, st); break;
-    case Kind::OneK: e = launch_wave<TileOneK, EXPERTS>(p, grid, st); break;
+    case Kind::OneK:
+        if constexpr (!EXPERTS)
+            e = launch_wave<TileOneK, EXPERTS>(p, grid, st);
+        break;
     }
     if (e == hipSuccess)
         return NVFP4_OK;

@@ -902,9 +902,8 @@ nvfp4_status_t nvfp4_moe_route(const void *logits, int dtype, const float *bias,
     const size_t need = nvfp4_moe_route_workspace_bytes(T, E, k);
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
         return NVFP4_ERR_WORKSPACE;
-    // 16 lanes per token where they hold its picks and at most 16 experts each, and
-    // not where a wave per token ends sooner (one token: 9 against 10.5 us)
-    const bool narrow = k < 16 && E <= 256 && T > kSmallThreads / 64;
+    // 16 lanes per token where they hold its picks and at most 16 experts each
+    const bool narrow = k < 16 && E <= 256;
     const int64_t per_wg = kRouteWaves * (narrow ? 4 : 1), grid = (T + per_wg - 1) / per_wg;
     if (grid > kMaxGrid)
         return NVFP4_ERR_INVALID_SHAPE;

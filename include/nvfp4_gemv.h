@@ -478,7 +478,8 @@ nvfp4_status_t nvfp4_moe_route(const void *logits, int dtype, const float *bias,
  *   scale_a  float32 [E] on the device (NULL: 1), scale_b float32 (NULL: 1)
  *   c        dtype [S][M]; rows of slots in no list are not written
  * Rounding, order of summation and requirements as for nvfp4_gemm; E <= 1024,
- * rows, slots_per_row >= 1, S <= 2^30.
+ * rows, slots_per_row >= 1, S <= 2^30, rows * K / 2 <= 2^32 (B's rows are gathered
+ * by 32-bit offsets).
  */
 size_t nvfp4_gemm_experts_workspace_bytes(int64_t M, int64_t K, int64_t E, int64_t S);
 nvfp4_status_t nvfp4_gemm_experts(const void *a, const void *b, const void *sfa, const void *sfb,

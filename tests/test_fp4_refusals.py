@@ -108,6 +108,12 @@ def test_products_that_split_k_want_a_workspace():
     assert experts(M=M, K=K, rows=8, per=2, ws=P, n=need - 256) == WORK
 
 
+def test_experts_rows_within_32_bit_offsets():
+    """The rows are gathered by 32-bit offsets: rows * K / 2 is at most 2^32 bytes."""
+    assert experts(M=1, K=64, E=1, rows=2 ** 27 + 1, per=1) == SHAPE
+    assert experts(M=1, K=64, E=1, rows=2 ** 27, per=1, a=P + 4) == ALIGN
+
+
 SHAPES = [(1, 1, 32, 1), (7168, 1, 16384, 1), (128, 16, 2048, 1), (7168, 16, 2048, 1), (1000, 33, 4096, 3),
           (4096, 64, 7168, 8), (4096, 333, 7168, 1), (7168, 4096, 16384, 1), (127, 1000, 64, 1), (513, 129, 160, 2),
           (8192, 4096, 16352, 2), (1, 4096, 16384, 1), (20000, 1, 32, 1), (64, 64, 1 << 22, 1), (1 << 20, 64, 64, 1)]

@@ -74,6 +74,28 @@ def test_product(M, N, K, L):
         assert torch.equal(got["plain"].view(torch.uint8), got["blocked"].view(torch.uint8)), dtype
 
 
+# every tile, K of 64 and of 32, several batches, slices of K
+TILES = [(7168, 2050, 544, 1, 256, 256, 1), (3285, 1349, 448, 3, 256, 256, 1), (1500, 1030, 224, 2, 128, 128, 1),
+         (521, 1836, 256, 3, 128, 128, 1), (513, 1000, 96, 1, 64, 64, 1), (1025, 513, 192, 1, 64, 64, 1),
+         (1074, 38, 22944, 2, 64, 64, 15), (3077, 101, 11520, 2, 64, 64, 2), (4100, 200, 96, 1, 128, 32, 1),
+         (4100, 200, 320, 1, 128, 32, 1), (1062, 1, 12512, 2, 128, 32, 14), (2050, 100, 96, 1, 64, 32, 1),
+         (2050, 100, 448, 1, 64, 32, 1), (1067, 1, 18912, 1, 64, 32, 15), (1074, 2, 5184, 2, 64, 32, 7),
+         (513, 1000, 544, 1, 32, 32, 1), (1025, 513, 576, 1, 32, 32, 1), (2105, 1, 12064, 1, 32, 32, 8)]
+
+
+@pytest.mark.parametrize("M,N,K,L,tile_m,tile_n,splits", TILES)
+def test_every_tile(M, N, K, L, tile_m, tile_n, splits):
+    plan = g.nvfp4_gemm_plan(M, N, K, L)
+    assert (plan["tile_m"], plan["tile_n"], plan["k_splits"]) == (tile_m, tile_n, splits)
+    rng = np.random.default_rng([M, N, K, L])
+    (a, sfa), (b, sfb) = operand(rng, L, M, K), operand(rng, L, N, K)
+    want, size = reference(a, sfa, b, sfb)
+    for dtype in DTYPES:
+        got = {lay: run(a, sfa, b, sfb, dtype, lay) for lay in ("plain", "blocked")}
+        ref.check_product(got["blocked"], want, size, K, dtype, "blocked")
+        assert torch.equal(got["plain"], got["blocked"])
+
+
 @pytest.mark.parametrize("M,N,K", [(70, 5, 512), (70, 40, 512), (300, 200, 544), (3000, 3500, 96)])
 def test_scales_and_edge_codes(M, N, K):
     """alpha and the device's global scales; zero, subnormal and largest block scales; sums past float16's range."""

@@ -84,6 +84,41 @@ def test_route_ties_and_masks(score):
     check_route(logits[:30], 8, bias, score=score)
 
 
+# experts per lane and lanes per token; groups of 16 and 64 experts (and others), up to the largest k
+FORMS = [(66, 64, 15, dict(n_group=4, topk_group=2, group_top=2)), (70, 128, 9, dict(n_group=8, topk_group=7)),
+         (90, 256, 15, dict(n_group=16, topk_group=5, group_top=2)), (65, 256, 16, dict()), (90, 250, 4, dict()),
+         (67, 256, 33, dict(n_group=4, topk_group=3, group_top=2)), (80, 512, 12, dict(n_group=8, topk_group=2)),
+         (70, 1024, 20, dict(n_group=16, topk_group=9, group_top=2)), (70, 1024, 63, dict()), (70, 512, 64, dict()),
+         (3, 16, 15, dict()), (9, 256, 8, dict(n_group=2, topk_group=1, group_top=2)), (129, 17, 16, dict())]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,kw", FORMS)
+def test_route_forms(T, E, k, kw, score):
+    gen = torch.Generator().manual_seed(T * E + k)
+    logits = torch.randn(T, E, generator=gen) * 1.5
+    logits[::5] = torch.where(torch.rand(logits[::5].shape, generator=gen) < 0.7, float("-inf"), logits[::5])
+    check_route(logits, k, None, score=score, **kw)
+    check_route(logits, k, torch.randn(E, generator=gen) * 0.2, score=score, **kw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,kw", [(64, dict()), (256, dict(n_group=8, topk_group=4, group_top=2)), (512, dict()),
+                                  (1024, dict(n_group=16, topk_group=4, group_top=2))])
+def test_route_close_picks(E, kw, score):
+    """Logits a few float32 steps apart, biases that bring unlike scores together or drown them: float32 cannot
+    tell these picks."""
+    rng = np.random.default_rng(E)
+    T = 150
+    x = rng.choice(np.array([0.5, 1.25, -0.75], np.float32), (T, E))
+    x = x * (1 + rng.integers(-3, 4, (T, E)) * 2.0 ** -23)
+    x[100:] = rng.standard_normal((50, E))
+    logits = torch.from_numpy(x).float()
+    near = torch.from_numpy(-1 / (1 + np.exp(-x[120]))).float()             # row 120: every sum near zero
+    for bias in (None, near, torch.from_numpy(rng.standard_normal(E) * 1e5).float(), torch.full((E,), 3e4)):
+        check_route(logits, 8, bias, score=score, **kw)
+
+
 @pytest.mark.parametrize("T,E,k", [(16384, 256, 8), (9000, 1024, 2), (70000, 8, 2), (40000, 60, 4)])
 def test_lists_of_many_slots(T, E, k):
     gen = torch.Generator().manual_seed(T)
@@ -158,6 +193,23 @@ def test_experts(T, E, k, M, K, per_token):
     for dtype in DTYPES:
         got = {lay: run_experts(a, sfa, b, sfb, ids, per, dtype, lay) for lay in ("plain", "blocked")}
         check_experts(got["blocked"], a, sfa, b, sfb, ids, per, dtype)
+        assert torch.equal(got["plain"], got["blocked"])
+
+
+# longer lists and rows: every tile, slices of K
+TILES = [(1606, 64, 4, 897, 1408), (1606, 64, 4, 897, 1440), (4000, 4, 4, 130, 96), (1220, 1, 1, 2346, 256),
+         (4000, 4, 4, 33, 96), (619, 16, 8, 133, 256), (1103, 1, 1, 618, 22976), (20, 64, 4, 513, 96),
+         (980, 1, 1, 851, 256), (144, 64, 2, 39, 8992), (64, 64, 1, 260, 96), (64, 64, 1, 300, 320), (9, 64, 8, 33, 3008)]
+
+
+@pytest.mark.parametrize("T,E,k,M,K", TILES)
+def test_experts_every_tile(T, E, k, M, K):
+    rng = np.random.default_rng([T, E, M])
+    (a, sfa), (b, sfb) = operand(rng, E, M, K), operand(rng, 1, T, K)
+    ids = routed(rng, T, E, k, drop=0.02)
+    for dtype in DTYPES:
+        got = {lay: run_experts(a, sfa, b, sfb, ids, k, dtype, lay) for lay in ("plain", "blocked")}
+        check_experts(got["blocked"], a, sfa, b, sfb, ids, k, dtype)
         assert torch.equal(got["plain"], got["blocked"])
 
 

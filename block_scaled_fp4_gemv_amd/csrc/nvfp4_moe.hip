@@ -2,17 +2,21 @@
 //
 // Router. Picks are compared in float64 by definition. Almost always float32
 // picks with a bound on their error tell the same, and much cheaper: the fast path
-// gives 16 lanes to a token (64 for many experts), 4 tokens to a wave, and turns
-// each pick into one 32-bit key, its value in fixed point above the expert's index
+// gives 16 lanes to a token (64 for many experts or few tokens), 4 tokens to a
+// wave, and turns each pick into one 32-bit key, its value in fixed point above the expert's index
 // counted down, so that the largest key is the pick and ties go to the lower
 // index. Each lane sorts its keys; a round takes the largest head of the lanes.
 // Where two neighbours in the ranking (or the last group kept and the first one
 // left) are closer than the bound, unless they come from the same logit and bias,
-// the wave repeats the token in float64. The weights are float64 in both. 16384
-// tokens of 256 experts: float64 alone 58 us; float32 with a wave per token 44.
+// the wave repeats the token in float64. The weights are float64 in both. What
+// bounds it: vector instructions, about 1300 per wave; the logits would take 4 us.
+// 16384 tokens of 256 experts, 8 of them from 4 of 8 groups: float64 alone 58 us;
+// float32 with a wave per token 44; four tokens per wave 23.
 // Lists. A stable counting sort of the slots by expert: counts per chunk of
 // slots, then each chunk's places from the counts of the chunks before it. Every
 // rank is counted, no atomic's order enters: the lists are the same each time.
+// Bound by latency: 131072 slots of 256 experts 5 us and 9 (three launches; up to
+// 64 tokens the router's one workgroup makes the lists too, in the same launch).
 // Combine. One thread per 16 bytes of a token's columns, float32 sums.
 #include <hip/hip_runtime.h>
 
@@ -303,7 +307,8 @@ __device__ __attribute__((always_inline)) inline void sort_down(uint32_t (&v)[N]
 // The wave's 64 / LPT tokens t, t + 1, .. (those below t_end): lane j of a
 // token's lanes gets its j-th pick, or -1; `top` its largest logit. Returns
 // whether the token's picks are certain (the same in its lanes).
-// Expert of key i of lane l: i * LPT + l. Groups have to be whole runs of LPT.
+// Expert of key i of lane l: i * LPT + l. Groups have to be whole runs of LPT lanes
+// (for LPT = 64 also 16 or 32).
 template <int DT, int LPT, int NL>
 __device__ __attribute__((always_inline)) inline bool route_fast(const void *__restrict__ logits,
                                                                  const float *__restrict__ bias, const RouteParams &p,
@@ -367,22 +372,38 @@ __device__ __attribute__((always_inline)) inline bool route_fast(const void *__r
         key[i] = v[i] > none ? step << IB | (kIndex - (uint32_t)(i * LPT + l)) : 0u;
     }
     if (p.n_group > 1) {
-        const int runs = p.E / p.n_group / LPT;                 // keys per group and lane
+        const int size = p.E / p.n_group, runs = size / LPT;    // keys per group and lane
         uint32_t mine = 0u;                                     // lane g: group g's value above its index
-        uint32_t a = 0u, c = 0u;
-        int g = 0, in_group = 0;
+        // a second value that is missing counts as 0
+        auto value = [&](uint32_t a, uint32_t c, int g) {
+            const uint32_t two = (a >> IB) + (p.group_top > 1 ? (c ? c >> IB : (uint32_t)kSteps + 1u) : 0u);
+            return a ? two << GB | (kGroup - (uint32_t)g) : 0u;
+        };
+        if (LPT == 64 && runs == 0) {                           // several groups of 16 or 32 lanes in a key
+            const int per = LPT / size;
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            join_two(a, c, key[i], 0u);
-            if (++in_group == runs) {
-                token_two<LPT>(a, c);
-                // a second value that is missing counts as 0
-                const uint32_t two = (a >> IB) + (p.group_top > 1 ? (c ? c >> IB : (uint32_t)kSteps + 1u) : 0u);
-                if (l == g)
-                    mine = a ? two << GB | (kGroup - (uint32_t)g) : 0u;
-                a = c = 0u;
-                in_group = 0;
-                ++g;
+            for (int i = 0; i < NL; ++i) {
+                uint32_t a = key[i], c = 0u;
+                token_two<16>(a, c);
+                if (size == 32)
+                    join_two(a, c, (uint32_t)__shfl_xor((int)a, 16), (uint32_t)__shfl_xor((int)c, 16));
+                const uint32_t v = value(a, c, i * per + l / size);
+                const uint32_t of_mine = (uint32_t)__shfl((int)v, l % per * size);
+                mine = l / per == i ? of_mine : mine;
+            }
+        } else {
+            uint32_t a = 0u, c = 0u;
+            int g = 0, in_group = 0;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                join_two(a, c, key[i], 0u);
+                if (++in_group == runs) {
+                    token_two<LPT>(a, c);
+                    mine = l == g ? value(a, c, g) : mine;
+                    a = c = 0u;
+                    in_group = 0;
+                    ++g;
+                }
             }
         }
         uint64_t keep = 0;
@@ -397,13 +418,17 @@ __device__ __attribute__((always_inline)) inline bool route_fast(const void *__r
                 last = m;
             }
         }
-        in_group = 0;
+        int in_group = 0;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            key[i] = keep & 1ull ? key[i] : 0u;
-            if (++in_group == runs) {
-                keep >>= 1;
-                in_group = 0;
+            if (LPT == 64 && runs == 0) {
+                key[i] = keep >> (i * (LPT / size) + l / size) & 1ull ? key[i] : 0u;
+            } else {
+                key[i] = keep & 1ull ? key[i] : 0u;
+                if (++in_group == runs) {
+                    keep >>= 1;
+                    in_group = 0;
+                }
             }
         }
     }
@@ -456,7 +481,8 @@ __device__ __attribute__((always_inline)) inline void route_tokens(const void *_
     double sum = 1.0;
     bool sure = false;
     // the fast path's lanes hold one pick more than k
-    if (p.k < LPT && (p.n_group == 1 || (p.E / p.n_group % LPT == 0 && p.n_group <= LPT)))
+    const int size = p.E / p.n_group;
+    if (p.k < LPT && (p.n_group == 1 || (size % LPT == 0 && p.n_group <= LPT) || (LPT == 64 && (size == 16 || size == 32))))
         sure = route_fast<DT, LPT, NL>(logits, bias, p, t, here, l, id, top);
     else {
         top = -__builtin_inff();
@@ -902,8 +928,9 @@ nvfp4_status_t nvfp4_moe_route(const void *logits, int dtype, const float *bias,
     const size_t need = nvfp4_moe_route_workspace_bytes(T, E, k);
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
         return NVFP4_ERR_WORKSPACE;
-    // 16 lanes per token where they hold its picks and at most 16 experts each
-    const bool narrow = k < 16 && E <= 256;
+    // 16 lanes per token where they hold its picks and at most 16 experts each,
+    // and where a wave per token would not do at once (a single token)
+    const bool narrow = k < 16 && E <= 256 && T > kSmallThreads / 64;
     const int64_t per_wg = kRouteWaves * (narrow ? 4 : 1), grid = (T + per_wg - 1) / per_wg;
     if (grid > kMaxGrid)
         return NVFP4_ERR_INVALID_SHAPE;

@@ -89,7 +89,10 @@ FORMS = [(66, 64, 15, dict(n_group=4, topk_group=2, group_top=2)), (70, 128, 9, 
          (90, 256, 15, dict(n_group=16, topk_group=5, group_top=2)), (65, 256, 16, dict()), (90, 250, 4, dict()),
          (67, 256, 33, dict(n_group=4, topk_group=3, group_top=2)), (80, 512, 12, dict(n_group=8, topk_group=2)),
          (70, 1024, 20, dict(n_group=16, topk_group=9, group_top=2)), (70, 1024, 63, dict()), (70, 512, 64, dict()),
-         (3, 16, 15, dict()), (9, 256, 8, dict(n_group=2, topk_group=1, group_top=2)), (129, 17, 16, dict())]
+         (3, 16, 15, dict()), (9, 256, 8, dict(n_group=2, topk_group=1, group_top=2)), (129, 17, 16, dict()),
+         (7, 256, 8, dict(n_group=8, topk_group=4, group_top=2)), (16, 128, 6, dict(n_group=8, topk_group=3)),
+         (5, 160, 4, dict(n_group=5, topk_group=2, group_top=2)), (66, 256, 40, dict(n_group=16, topk_group=6, group_top=2)),
+         (70, 512, 20, dict(n_group=16, topk_group=4, group_top=2)), (66, 1024, 30, dict(n_group=64, topk_group=9))]
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])

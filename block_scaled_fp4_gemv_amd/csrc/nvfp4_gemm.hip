@@ -663,6 +663,8 @@ struct WaveTile {
     static constexpr int stage_bytes(bool odd) { return kOffSA + (kWaveM + BN) * (odd ? 16 : 8); }
     static constexpr int lds_bytes(bool odd) { return std::max(WM * KW * NS * stage_bytes(odd), KW > 1 ? WM * KW * FM * FN * 4096 : 0); }
     static_assert(lds_bytes(true) + kStaticLds <= kLdsBytes);
+    // the KW waves share the registers of a range evenly, and slices are added 8 at a time
+    static_assert(FN * FM * 16 % KW == 0 && (FN * FM * 16 / KW < 8 || FN * FM * 16 / KW % 8 == 0));
 };
 
 template <class T, bool EXPERTS, bool ODD>

@@ -265,6 +265,59 @@ def test_combine(T, k, M, dtype):
     assert (np.abs(got - want) <= tol).all()
 
 
+def test_far_logits():
+    """Logits past 2^32 bytes, and as many tokens: every token's expert and every list."""
+    T, E = (1 << 21) + 5, 1024
+    want = (torch.arange(T, device="cuda") * 7 % E).int()
+    logits = torch.zeros(T, E, device="cuda")
+    logits.scatter_(1, want[:, None].long(), 1.0)
+    z = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    ids, offsets, order, weights = z(T), z(E + 1), z(T), torch.zeros(T, device="cuda")
+    ws = torch.zeros(g.nvfp4_moe_route_workspace_bytes(T, E, 1), dtype=torch.uint8, device="cuda")
+    g.nvfp4_moe_route(logits, ids, weights, offsets, order, T, E, 1, workspace=ws)
+    assert torch.equal(ids, want) and (weights == 1).all()
+    assert torch.equal(order, torch.argsort(want, stable=True).int())
+    assert torch.equal(offsets[1:], torch.bincount(want, minlength=E).cumsum(0).int()) and offsets[0] == 0
+
+
+def test_far_experts():
+    """Weights and results past 2^32 bytes: the last expert's rows and the last slot are their own."""
+    E, M, K, T = 3, 1 << 18, 16384, 2
+    codes = torch.zeros(E, M, K // 2, dtype=torch.uint8, device="cuda")
+    sfa = torch.zeros(E * M * (K // 16), dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(2)
+    (a, sa), (b, sfb) = operand(rng, 1, 64, K), operand(rng, 1, T, K)
+    codes[E - 1, M - 64:] = dev(a[0])
+    sfa[-64 * (K // 16):] = dev(sa.reshape(-1))
+    per = 2100                                                              # 4200 slots of 2^18 float32: 4.4 GB
+    S = T * per
+    offsets = dev(np.array([0, 1, 1, 3], np.int32))
+    order = dev(np.array([5, 17, S - 1] + [S] * (S - 3), np.int32))
+    c = torch.full((S, M), 7.0, device="cuda")
+    ws = torch.zeros(g.nvfp4_gemm_experts_workspace_bytes(M, K, E, S), dtype=torch.uint8, device="cuda")
+    g.nvfp4_gemm_experts(codes, dev(b), sfa, dev(sfb), c, M, K, E, T, per, "plain", offsets, order,
+                         workspace=ws if ws.numel() else None)
+    va, vb = dev(ref.values(a[0], sa[0])), dev(ref.values(b[0], sfb[0]))
+    want, size = (vb @ va.t().contiguous()).cpu().numpy(), (vb.abs() @ va.abs().t().contiguous()).cpu().numpy()
+    ref.check_product(c[[17, S - 1], M - 64:], want, size, K, torch.float32, "last expert")
+    assert not c[[17, S - 1], :M - 64].any() and not c[5].any()
+    assert (c[6:17] == 7).all() and (c[S - 2] == 7).all()
+
+
+def test_far_slots():
+    """Rows to combine past 2^32 elements: the last token gets its own."""
+    T, k, M = 70000, 8, 8192
+    y = torch.zeros(T * k, M, dtype=torch.float16, device="cuda")
+    y[-k:] = torch.randn(k, M, device="cuda")
+    ids = torch.zeros(T, k, dtype=torch.int32, device="cuda")
+    weights = torch.rand(T, k, device="cuda")
+    out = torch.full((T, M), 7.0, dtype=torch.float16, device="cuda")
+    g.nvfp4_moe_combine(y, ids, weights, out, T, k, M)
+    terms = y[-k:].double() * weights[-1, :, None].double()
+    tol = terms.abs().sum(0) * (k + 1) * 2.0 ** -24 + terms.sum(0).abs() * 2.0 ** -11 + 2.0 ** -25
+    assert ((out[-1].double() - terms.sum(0)).abs() <= tol).all() and not out[:-1].any()
+
+
 def test_layer_in_a_graph():
     """Route, quantise, both products and the combine captured together; replays
     with other inputs agree with the eager chain bit for bit."""

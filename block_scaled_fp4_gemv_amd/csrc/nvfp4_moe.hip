@@ -3,20 +3,22 @@
 // Router. Picks are compared in float64 by definition. Almost always float32
 // picks with a bound on their error tell the same, and much cheaper: the fast path
 // gives 16 lanes to a token (64 for many experts or few tokens), 4 tokens to a
-// wave, and turns each pick into one 32-bit key, its value in fixed point above the expert's index
-// counted down, so that the largest key is the pick and ties go to the lower
-// index. Each lane sorts its keys; a round takes the largest head of the lanes.
+// wave, and turns each pick into one 32-bit key, its value in fixed point above
+// the expert's index counted down, so that the largest key is the pick and ties
+// go to the lower index. Each lane sorts its keys; a round takes the largest head of the lanes.
 // Where two neighbours in the ranking (or the last group kept and the first one
 // left) are closer than the bound, unless they come from the same logit and bias,
 // the wave repeats the token in float64. The weights are float64 in both. What
-// bounds it: vector instructions, about 1300 per wave; the logits would take 4 us.
+// bounds it: vector instructions, about 1270 per wave, 10 us at 4 per SIMD, after
+// the logits have come (4 us) and the waves have started.
 // 16384 tokens of 256 experts, 8 of them from 4 of 8 groups: float64 alone 58 us;
-// float32 with a wave per token 44; four tokens per wave 23.
+// float32 with a wave per token 44; four tokens per wave 23 with the experts of a
+// lane 16 apart, 21 with neighbours: groups are then a few lanes, and loads wide.
 // Lists. A stable counting sort of the slots by expert: counts per chunk of
 // slots, then each chunk's places from the counts of the chunks before it. Every
 // rank is counted, no atomic's order enters: the lists are the same each time.
-// Bound by latency: 131072 slots of 256 experts 5 us and 9 (three launches; up to
-// 64 tokens the router's one workgroup makes the lists too, in the same launch).
+// Bound by latency: 131072 slots of 256 experts 5 us and 9 (up to 64 tokens the
+// router's one workgroup makes the lists too, in the same launch).
 // Combine. One thread per 16 bytes of a token's columns, float32 sums.
 #include <hip/hip_runtime.h>
 
@@ -172,6 +174,48 @@ __device__ __attribute__((always_inline)) inline void load_experts(const void *_
         x[i] = x[i] == x[i] && l + STEP * i < E ? x[i] : -__builtin_inff();
 }
 
+// The same of the experts l * N, l * N + 1, ..; whole rows (E = LPT * N) by 16-byte
+// loads, at any address of the type's alignment.
+template <int DT, int N, int LPT>
+__device__ __attribute__((always_inline)) inline void load_run(const void *__restrict__ logits,
+                                                               const float *__restrict__ bias, int64_t t, int32_t E,
+                                                               int l, float (&x)[N], float (&b)[N])
+{
+    using Value = std::conditional_t<DT == NVFP4_F32, float, uint16_t>;
+    if (E == LPT * N) {
+        Value raw[N];
+        __builtin_memcpy(raw, (const Value *)logits + t * E + l * N, sizeof raw);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (DT == NVFP4_F32)
+                x[i] = raw[i];
+            else if constexpr (DT == NVFP4_BF16)
+                x[i] = __builtin_bit_cast(float, (uint32_t)raw[i] << 16);
+            else
+                x[i] = (float)__builtin_bit_cast(_Float16, raw[i]);
+        }
+        if (bias)
+            __builtin_memcpy(b, bias + l * N, sizeof b);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            x[i] = load_value<DT>(logits, t * E + min(l * N + i, E - 1));
+        if (bias) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                b[i] = bias[min(l * N + i, E - 1)];
+        }
+    }
+    if (!bias) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            b[i] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        x[i] = x[i] == x[i] && l * N + i < E ? x[i] : -__builtin_inff();
+}
+
 // One token by the wave: its picks in lanes at, at + 1, .. of *picked; returns
 // the softmax's sum. Not inlined: it is rarely taken, and its registers would
 // cost the fast path waves. `lds`: 64 * NL doubles.
@@ -265,26 +309,12 @@ __device__ __attribute__((always_inline)) inline float token_sum(float v)
     }
     return v;
 }
-// The two largest of the token's lanes: at each step the other lane's set is
-// another one.
+// The two largest of two sets.
 __device__ __attribute__((always_inline)) inline void join_two(uint32_t &a, uint32_t &b, uint32_t oa, uint32_t ob)
 {
     b = max(min(a, oa), max(b, ob));
     a = max(a, oa);
 }
-template <int LPT>
-__device__ __attribute__((always_inline)) inline void token_two(uint32_t &a, uint32_t &b)
-{
-    join_two(a, b, from_lane<0x128>(a), from_lane<0x128>(b));
-    join_two(a, b, from_lane<0x124>(a), from_lane<0x124>(b));
-    join_two(a, b, from_lane<0x122>(a), from_lane<0x122>(b));
-    join_two(a, b, from_lane<0x121>(a), from_lane<0x121>(b));
-    if constexpr (LPT == 64) {
-        join_two(a, b, (uint32_t)__shfl_xor((int)a, 16), (uint32_t)__shfl_xor((int)b, 16));
-        join_two(a, b, (uint32_t)__shfl_xor((int)a, 32), (uint32_t)__shfl_xor((int)b, 32));
-    }
-}
-
 // Descending, by merging (Batcher's odd-even merge sort); N a power of two.
 template <int N>
 __device__ __attribute__((always_inline)) inline void sort_down(uint32_t (&v)[N])
@@ -307,8 +337,8 @@ __device__ __attribute__((always_inline)) inline void sort_down(uint32_t (&v)[N]
 // The wave's 64 / LPT tokens t, t + 1, .. (those below t_end): lane j of a
 // token's lanes gets its j-th pick, or -1; `top` its largest logit. Returns
 // whether the token's picks are certain (the same in its lanes).
-// Expert of key i of lane l: i * LPT + l. Groups have to be whole runs of LPT lanes
-// (for LPT = 64 also 16 or 32).
+// Expert of key i of lane l: l * NL + i. Groups have to be the experts of 1, 2, 4,
+// .. lanes.
 template <int DT, int LPT, int NL>
 __device__ __attribute__((always_inline)) inline bool route_fast(const void *__restrict__ logits,
                                                                  const float *__restrict__ bias, const RouteParams &p,
@@ -322,7 +352,7 @@ __device__ __attribute__((always_inline)) inline bool route_fast(const void *__r
     const float none = -__builtin_inff();
     float x[NL], b[NL], v[NL];
     top = none;
-    load_experts<DT, NL, LPT>(logits, bias, here ? t : 0, p.E, l, x, b);
+    load_run<DT, NL, LPT>(logits, bias, here ? t : 0, p.E, l, x, b);
 #pragma unroll
     for (int i = 0; i < NL; ++i)
         top = fmaxf(top, x[i]);
@@ -369,43 +399,29 @@ __device__ __attribute__((always_inline)) inline bool route_fast(const void *__r
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
         const uint32_t step = (uint32_t)(fmaf(v[i], scale, kSteps) + 1.0f);
-        key[i] = v[i] > none ? step << IB | (kIndex - (uint32_t)(i * LPT + l)) : 0u;
+        key[i] = v[i] > none ? step << IB | (kIndex - (uint32_t)(l * NL + i)) : 0u;
     }
     if (p.n_group > 1) {
-        const int size = p.E / p.n_group, runs = size / LPT;    // keys per group and lane
-        uint32_t mine = 0u;                                     // lane g: group g's value above its index
-        // a second value that is missing counts as 0
-        auto value = [&](uint32_t a, uint32_t c, int g) {
-            const uint32_t two = (a >> IB) + (p.group_top > 1 ? (c ? c >> IB : (uint32_t)kSteps + 1u) : 0u);
-            return a ? two << GB | (kGroup - (uint32_t)g) : 0u;
-        };
-        if (LPT == 64 && runs == 0) {                           // several groups of 16 or 32 lanes in a key
-            const int per = LPT / size;
+        const int lanes = p.E / p.n_group / NL, g = l / lanes;  // lanes per group, this lane's group
+        uint32_t a = 0u, c = 0u;                                // the group's two largest
 #pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                uint32_t a = key[i], c = 0u;
-                token_two<16>(a, c);
-                if (size == 32)
-                    join_two(a, c, (uint32_t)__shfl_xor((int)a, 16), (uint32_t)__shfl_xor((int)c, 16));
-                const uint32_t v = value(a, c, i * per + l / size);
-                const uint32_t of_mine = (uint32_t)__shfl((int)v, l % per * size);
-                mine = l / per == i ? of_mine : mine;
-            }
-        } else {
-            uint32_t a = 0u, c = 0u;
-            int g = 0, in_group = 0;
-#pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                join_two(a, c, key[i], 0u);
-                if (++in_group == runs) {
-                    token_two<LPT>(a, c);
-                    mine = l == g ? value(a, c, g) : mine;
-                    a = c = 0u;
-                    in_group = 0;
-                    ++g;
-                }
-            }
-        }
+        for (int i = 0; i < NL; ++i)
+            join_two(a, c, key[i], 0u);
+        // each step joins neighbouring halves, whose lanes agree among themselves
+        if (lanes > 1)
+            join_two(a, c, from_lane<0xB1>(a), from_lane<0xB1>(c));         // quad_perm [1, 0, 3, 2]
+        if (lanes > 2)
+            join_two(a, c, from_lane<0x4E>(a), from_lane<0x4E>(c));         // quad_perm [2, 3, 0, 1]
+        if (lanes > 4)
+            join_two(a, c, from_lane<0x141>(a), from_lane<0x141>(c));       // row_half_mirror
+        if (lanes > 8)
+            join_two(a, c, from_lane<0x140>(a), from_lane<0x140>(c));       // row_mirror
+        if (lanes > 16)
+            join_two(a, c, (uint32_t)__shfl_xor((int)a, 16), (uint32_t)__shfl_xor((int)c, 16));
+        // the group's first lane: its value above its index; a second value that is
+        // missing counts as 0
+        const uint32_t two = (a >> IB) + (p.group_top > 1 ? (c ? c >> IB : (uint32_t)kSteps + 1u) : 0u);
+        uint32_t mine = a && l % lanes == 0 ? two << GB | (kGroup - (uint32_t)g) : 0u;
         uint64_t keep = 0;
         uint32_t last = 0u;
         for (int j = 0; j <= p.topk_group; ++j) {
@@ -418,19 +434,10 @@ __device__ __attribute__((always_inline)) inline bool route_fast(const void *__r
                 last = m;
             }
         }
-        int in_group = 0;
+        const bool kept = keep >> g & 1ull;
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            if (LPT == 64 && runs == 0) {
-                key[i] = keep >> (i * (LPT / size) + l / size) & 1ull ? key[i] : 0u;
-            } else {
-                key[i] = keep & 1ull ? key[i] : 0u;
-                if (++in_group == runs) {
-                    keep >>= 1;
-                    in_group = 0;
-                }
-            }
-        }
+        for (int i = 0; i < NL; ++i)
+            key[i] = kept ? key[i] : 0u;
     }
     sort_down<NL>(key);
     uint32_t got = 0u;
@@ -481,8 +488,8 @@ __device__ __attribute__((always_inline)) inline void route_tokens(const void *_
     double sum = 1.0;
     bool sure = false;
     // the fast path's lanes hold one pick more than k
-    const int size = p.E / p.n_group;
-    if (p.k < LPT && (p.n_group == 1 || (size % LPT == 0 && p.n_group <= LPT) || (LPT == 64 && (size == 16 || size == 32))))
+    const int size = p.E / p.n_group, lanes = size / NL;
+    if (p.k < LPT && (p.n_group == 1 || (size % NL == 0 && (lanes & (lanes - 1)) == 0)))
         sure = route_fast<DT, LPT, NL>(logits, bias, p, t, here, l, id, top);
     else {
         top = -__builtin_inff();
@@ -970,6 +977,9 @@ nvfp4_status_t nvfp4_moe_route(const void *logits, int dtype, const float *bias,
 #undef NVFP4_N
     });
     if (!small) {
+        // the router could count its picks as it goes (10 us against 5 + 9 for 131072
+        // slots), but then the counts had to be zero before the call, which partial
+        // sums of a product may have left otherwise in a shared workspace
         const int32_t chunk = (int32_t)list_chunk(S), nc = (S + chunk - 1) / chunk;
         int32_t *counts = (int32_t *)((uint8_t *)workspace + kTicketBytes);
         hipLaunchKernelGGL(nvfp4_count_kernel, dim3(nc), dim3(kListThreads), 0, st, (const int32_t *)ids, counts, S,

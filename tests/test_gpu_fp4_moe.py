@@ -318,6 +318,26 @@ def test_far_slots():
     assert ((out[-1].double() - terms.sum(0)).abs() <= tol).all() and not out[:-1].any()
 
 
+def test_router_after_a_split_product_in_one_workspace():
+    """The partial sums that a product leaves in the workspace do not reach the lists."""
+    T, E, k, M, K = 300, 1024, 4, 128, 16384
+    assert g.nvfp4_gemm_plan(M, 16, K, 1)["k_splits"] > 1
+    rng = np.random.default_rng(5)
+    (a, sfa), (b, sfb) = operand(rng, 1, M, K), operand(rng, 1, 16, K)
+    ws = torch.zeros(max(g.nvfp4_gemm_workspace_bytes(M, 16, K, 1), g.nvfp4_moe_route_workspace_bytes(T, E, k)),
+                     dtype=torch.uint8, device="cuda")
+    c = torch.empty(16 * M, device="cuda")
+    logits = torch.randn(T, E, device="cuda")
+    z = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    ids, offsets, order, weights = z(T, k), z(E + 1), z(T * k), torch.zeros(T, k, device="cuda")
+    for _ in range(2):
+        g.nvfp4_gemm(dev(a), dev(b), dev(sfa), dev(sfb), c, M, 16, K, 1, "plain", workspace=ws)
+        assert ws[65536:].any() and not ws[:65536].any()
+        g.nvfp4_moe_route(logits, ids, weights, offsets, order, T, E, k, workspace=ws)
+        wo, wl = ref.lists(ids.cpu().numpy(), E)
+        assert np.array_equal(offsets.cpu().numpy(), wo) and np.array_equal(order.cpu().numpy(), wl)
+
+
 def test_layer_in_a_graph():
     """Route, quantise, both products and the combine captured together; replays
     with other inputs agree with the eager chain bit for bit."""

@@ -513,7 +513,7 @@ __device__ __attribute__((always_inline)) inline void route_tokens(const void *_
         }
     }
     double w = 0.0;
-    if (id >= 0) {
+    if (here && id >= 0) {                                      // lanes without a token carry token 0's picks
         const float v = load_value<DT>(logits, t * p.E + id);
         if (p.score == NVFP4_SCORE_SIGMOID)
             w = 1.0 / (1.0 + exp(-(double)v));

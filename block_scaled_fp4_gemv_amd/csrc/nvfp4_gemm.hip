@@ -101,9 +101,12 @@ __device__ __attribute__((always_inline)) inline void wait_copies()
     __builtin_amdgcn_s_waitcnt((0x0F70 & ~0xC00F) | (N & 15) | ((N >> 4) << 14));
 }
 
+// Past it, what any wave has read from LDS before may be overwritten: each waits
+// for its own reads to return. The compiler waits where it uses a read, which may
+// be after a barrier that it does not know to free the place that was read.
 __device__ __attribute__((always_inline)) inline void barrier()
 {
-    asm volatile("" : : : "memory");
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" : : : "memory");
 }

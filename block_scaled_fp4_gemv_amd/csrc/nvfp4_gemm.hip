@@ -357,17 +357,35 @@ __device__ __attribute__((always_inline)) inline uint32_t words_at_b(const GemmP
     return (uint32_t)scale_word_at(p.blocked, min(i, w.count - 1) + (p.blocked ? w.n0 % 128 : 0), half, p.K / 16);
 }
 
-// alpha and the global scales. Loaded before the product and kept: read at the
-// end, they would add a memory round trip to every tile.
+// alpha and the global scales, as a size of 1/8 to 1 and a power of two: their
+// product may leave float32's range where the scaled sum does not (two scales of
+// 2^-75, or 2^100 and 2^100 beside a sum of zero), and the sum, 2^-20 to 2^46 or
+// zero, times the size does not leave it. Rounds as the product of the floats.
+// Loaded before the product and kept: read at the end, they would add a memory
+// round trip to every tile.
+struct Scale {
+    float size;
+    int power;
+
+    __device__ __attribute__((always_inline)) inline void times(float v)
+    {
+        size *= __builtin_amdgcn_frexp_mantf(v);
+        power += __builtin_amdgcn_frexp_expf(v);
+    }
+    // the one rounding of the scaled sum (two where it is subnormal)
+    __device__ __attribute__((always_inline)) inline float of(float sum) const { return __builtin_ldexpf(sum * size, power); }
+};
+
 template <bool EXPERTS>
-__device__ __attribute__((always_inline)) inline float total_scale(const GemmParams &p, int l)
+__device__ __attribute__((always_inline)) inline Scale total_scale(const GemmParams &p, int l)
 {
-    float scale = p.alpha;
+    Scale s{1.0f, 0};
+    s.times(p.alpha);
     if (p.scale_a)
-        scale *= p.scale_a[EXPERTS ? l : 0];
+        s.times(p.scale_a[EXPERTS ? l : 0]);
     if (p.scale_b)
-        scale *= *p.scale_b;
-    return scale;
+        s.times(*p.scale_b);
+    return s;
 }
 
 // Offset in c (and in a slice of partial sums) of the tile's row n, -1: not stored.
@@ -600,7 +618,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void nvfp4_gemm_wide_kern
     for (int s = 0; s < NS - 1; ++s)
         if (s < stages)
             issue(s, s);
-    const float scale = total_scale<EXPERTS>(p, w.l);
+    const Scale scale = total_scale<EXPERTS>(p, w.l);
     int slot = 0, i = 0;
     for (; i + NS - 1 < stages; ++i) {
         // stage i has landed when only the NS - 2 younger ones are out; past the
@@ -634,7 +652,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void nvfp4_gemm_wide_kern
         for (int r = 0; r < 16; ++r)
 #pragma unroll
             for (int i = 0; i < FM; ++i)
-                store_value(out + (8 * (r / 4) + 4 * half + r % 4) * T::kPitch, 32 * i + l32, acc[j][i][r] * scale, p.dtype);
+                store_value(out + (8 * (r / 4) + 4 * half + r % 4) * T::kPitch, 32 * i + l32, scale.of(acc[j][i][r]), p.dtype);
         asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
         for (int n = piece_n; n < 32; n += rows_at_once) {
             const uint4_t v = *(const uint4_t *)(out + n * T::kPitch + piece_m * size);
@@ -805,7 +823,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerCu) void nvfp4_gemm_wave_kernel
     for (int s = 0; s < NS - 1; ++s)
         if (s < stages)
             issue(s, s);
-    const float scale = total_scale<EXPERTS>(p, w.l);
+    const Scale scale = total_scale<EXPERTS>(p, w.l);
     int slot = 0, n = 0;
     for (; n + NS - 1 < stages; ++n) {
         // the slot of stage n - 1, whose reads are done, takes stage n + NS - 1;
@@ -884,7 +902,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerCu) void nvfp4_gemm_wave_kernel
 #pragma unroll
     for (int x = 0; x < R; ++x)
         if (at[x] >= 0)
-            store_value(p.c, at[x], sum[x] * scale, p.dtype);
+            store_value(p.c, at[x], scale.of(sum[x]), p.dtype);
 }
 
 // ------------------------------------------------------------------ plans

@@ -386,7 +386,8 @@ nvfp4_status_t nvfp4_dequantize(const void *codes, const void *scales, const flo
  *   scale_a, scale_b           float32 on the device, ga and gb (NULL: 1)
  *   c      dtype [L][N][M], written; aligned to its type
  * Accumulation is float32 (the products are exact), one rounding of the scaled
- * sum to float32 and one to dtype; float16 overflows to +-inf. The order of
+ * sum to float32 and one to dtype; float16 overflows to +-inf. The product
+ * alpha * ga * gb itself may leave float32's range. The order of
  * summation is fixed for a shape, so equal calls give equal bits.
  * Requirements: M, N, L >= 1; K % 32 == 0; M, N <= 2^30; K <= 2^22; a, b, sfa
  * and sfb 16-byte aligned; alpha finite.

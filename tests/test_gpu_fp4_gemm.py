@@ -217,3 +217,36 @@ def test_far_rows():
     want, size = reference(a, sa, b[L - 1:], sfb[L - 1:])
     ref.check_product(c[L - 1:, :, M - 64:], want, size, K, torch.float32)
     assert not c[:L - 1].any() and not c[L - 1, :, :M - 64].any()
+
+
+# alpha, ga, gb whose product, or part of it, is no normal float32: below its
+# range, subnormal, above it on the way, above it beside sums of zero
+FAR_SCALES = [(1.0, 2.0 ** -75 * 1.3, 2.0 ** -75 * 1.7), (1.0, 2.0 ** -70 * 1.1, 2.0 ** -70 * 1.3), (2.0 ** 60, 2.0 ** 100, 2.0 ** -120),
+              (-2.0 ** -100, 2.0 ** -60, 2.0 ** 120), (1.0, 1e-40, 2.0 ** 20), (2.0 ** -149, 2.0 ** 127, 2.0 ** 20)]
+
+
+def check_far(got, want, size, K, dtype, what):
+    """check_product's bound on each result. Its bound on their norm is relative and does not
+    hold here: many results lie below the type's normal numbers, where steps are absolute."""
+    off = np.abs(got.double().cpu().numpy().reshape(want.shape) - want) - ref.product_tolerance(K, size, want, dtype)
+    fine = np.abs(want) < torch.finfo(dtype).max * 0.99
+    assert off[fine].max() <= 0, f"{what}: worst by {off[fine].max():.3g}"
+
+
+@pytest.mark.parametrize("M,N,K", [(70, 5, 512), (70, 40, 512), (300, 200, 544), (3000, 3500, 96), (128, 16, 16384)])
+def test_scales_far_from_one(M, N, K):
+    """Scales whose product leaves float32's range where the scaled sums do not (product_tolerance counts four
+    float32 roundings and half of the least step); sums of zero stay zero beside a product that overflows."""
+    rng = np.random.default_rng([M, N, K, 2])
+    (a, sfa), (b, sfb) = operand(rng, 1, M, K, "edge"), operand(rng, 1, N, K, "edge")
+    sfa[0, M // 2] = 0
+    want, size = reference(a, sfa, b, sfb)
+    for alpha, ga, gb in FAR_SCALES:
+        f = np.float64(np.float32(alpha)) * np.float64(np.float32(ga)) * np.float64(np.float32(gb))
+        for dtype in DTYPES:
+            got = run(a, sfa, b, sfb, dtype, "blocked", alpha, ga, gb)
+            check_far(got, want * f, size * abs(f), K, dtype, f"{dtype} {alpha} {ga} {gb}")
+    got = run(a, sfa, b, sfb, torch.float32, "plain", 1.0, 2.0 ** 100, 2.0 ** 100).double().cpu().numpy()
+    assert (got[0, :, M // 2] == 0).all()
+    sure = np.abs(want) > ref.product_tolerance(K, size, want, torch.float32)      # the sum's sign
+    assert sure.any() and np.array_equal(got[sure], np.sign(want[sure]) * np.inf)

@@ -382,3 +382,23 @@ def test_layer_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+def test_experts_scales_far_from_one():
+    """Each expert's scale times the rows' leaves float32's range where the scaled sums do not."""
+    rng = np.random.default_rng(18)
+    T, E, k, M, K = 50, 6, 2, 140, 1024
+    (a, sfa), (b, sfb) = operand(rng, E, M, K, "edge"), operand(rng, 1, T, K, "edge")
+    ids = routed(rng, T, E, k)
+    for alpha, ga, gb in ((1.0, 2.0 ** -75, 2.0 ** -75), (1.0, 2.0 ** -70, 2.0 ** -70), (2.0 ** 60, 2.0 ** 100, 2.0 ** -120)):
+        ga = (ga * rng.uniform(0.5, 2, E)).astype(np.float32)
+        f = alpha * ga.astype(np.float64) * gb
+        for dtype in DTYPES:
+            got = run_experts(a, sfa, b, sfb, ids, k, dtype, "blocked", alpha, ga, np.array([gb], np.float32))
+            for e in range(E):
+                slots = np.nonzero(ids.reshape(-1) == e)[0]
+                va, vb = ref.values(a[e], sfa[e]), ref.values(b[0], sfb[0])[slots // k]
+                want, size = vb @ va.T * f[e], np.abs(vb) @ np.abs(va).T * f[e]
+                off = np.abs(got[dev(slots)].double().cpu().numpy() - want) - ref.product_tolerance(K, size, want, dtype)
+                fine = np.abs(want) < torch.finfo(dtype).max * 0.99
+                assert not fine.any() or off[fine].max() <= 0, f"{dtype} expert {e}: worst by {off[fine].max():.3g}"

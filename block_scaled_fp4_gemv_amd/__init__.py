@@ -495,6 +495,7 @@ def _workspace(x, nbytes):
 def _strided(x, name, rows, K, L, row_stride, batch_stride):
     """Pointer of an [L][rows][K] tensor and its strides in elements, checked
     against what the tensor's memory holds behind its first element."""
+    given = row_stride is not None or batch_stride is not None
     if row_stride is None:
         row_stride = K
     if batch_stride is None:
@@ -503,6 +504,8 @@ def _strided(x, name, rows, K, L, row_stride, batch_stride):
         return x, row_stride, batch_stride
     if not x.is_cuda:
         raise ValueError("operands must be device tensors")
+    if not given and not x.is_contiguous():
+        raise ValueError(f"{name} is not contiguous: give its strides")
     if row_stride == K and batch_stride == rows * K and x.is_contiguous():
         if rows * K * L > x.numel():
             raise ValueError(f"{name} holds {x.numel()} elements, the shape needs {rows * K * L}")

@@ -186,3 +186,35 @@ def test_binding_checks_types_and_sizes():
         g.nvfp4_moe_route(f32, i32, Fake(7, "torch.float32", 4), i32, i32, 4, 8, 2, workspace=u8)
     with pytest.raises(ValueError, match="codes holds"):
         g.nvfp4_dequantize(Fake(10), u8, bf, 4, 64, 1, "plain")
+
+
+class FakeView(Fake):
+    """A view that is not contiguous, over `held` elements of memory from its first on."""
+
+    def __init__(self, n, dtype, size, held):
+        super().__init__(n, dtype, size)
+        self.held = held
+
+    def is_contiguous(self):
+        return False
+
+    def storage_offset(self):
+        return 0
+
+    def untyped_storage(self):
+        return self
+
+    def nbytes(self):
+        return self.held * self.size
+
+
+@pytest.mark.parametrize("call", [
+    lambda x, **kw: g.nvfp4_global_scale(x, Fake(1, "torch.float32", 4), 4, 64, 1, Fake(256), **kw),
+    lambda x, **kw: g.nvfp4_quantize(x, Fake(128), Fake(16), 4, 64, 1, "plain", **kw)], ids=["global_scale", "quantize"])
+def test_a_view_wants_its_strides(call):
+    """Rows 80 apart, taken as dense ones for want of strides, would be read wrongly without a word."""
+    x = FakeView(4 * 64, "torch.bfloat16", 2, 3 * 80 + 64)
+    with pytest.raises(ValueError, match="not contiguous"):
+        call(x)
+    with pytest.raises(ValueError, match="x holds 304 elements, the shape needs 307"):
+        call(x, row_stride=81)

@@ -492,9 +492,9 @@ def _workspace(x, nbytes):
     return _op(x, 0, "workspace"), nbytes
 
 
-def _strided(x, name, rows, K, L, row_stride, batch_stride):
-    """Pointer of an [L][rows][K] tensor and its strides in elements, checked
-    against what the tensor's memory holds behind its first element."""
+def _strided(x, name, dt, rows, K, L, row_stride, batch_stride):
+    """Pointer of an [L][rows][K] tensor of type ``dt`` and its strides in elements,
+    checked against what the tensor's memory holds behind its first element."""
     given = row_stride is not None or batch_stride is not None
     if row_stride is None:
         row_stride = K
@@ -506,11 +506,13 @@ def _strided(x, name, rows, K, L, row_stride, batch_stride):
         raise ValueError("operands must be device tensors")
     if not given and not x.is_contiguous():
         raise ValueError(f"{name} is not contiguous: give its strides")
+    size = 4 if dt == NVFP4_F32 else 2                       # of the elements that are read, whatever x's type
     if row_stride == K and batch_stride == rows * K and x.is_contiguous():
-        if rows * K * L > x.numel():
-            raise ValueError(f"{name} holds {x.numel()} elements, the shape needs {rows * K * L}")
+        held = x.numel() * x.element_size() // size
+        if rows * K * L > held:
+            raise ValueError(f"{name} holds {held} elements, the shape needs {rows * K * L}")
     elif min(rows, K, L) >= 1 and min(row_stride, batch_stride) >= 0:
-        held = x.untyped_storage().nbytes() // x.element_size() - x.storage_offset()
+        held = (x.untyped_storage().nbytes() - x.storage_offset() * x.element_size()) // size
         need = (L - 1) * batch_stride + (rows - 1) * row_stride + K
         if held < need:
             raise ValueError(f"{name} holds {held} elements, the shape needs {need}")
@@ -534,9 +536,10 @@ def nvfp4_global_scale(x, scale, rows: int, K: int, L: int, workspace, workspace
                        row_stride: int | None = None, batch_stride: int | None = None, dtype=None,
                        stream=None) -> None:
     """Enqueue scale[0] = max finite |x| * (1 / 2688) (strides in elements; dense by default)."""
-    px, rs, bs = _strided(x, "x", rows, K, L, row_stride, batch_stride)
+    dt = _dtype_id(x, dtype)
+    px, rs, bs = _strided(x, "x", dt, rows, K, L, row_stride, batch_stride)
     pw, nw = _workspace(workspace, workspace_bytes)
-    _done(lib().nvfp4_global_scale(px, _dtype_id(x, dtype), _op(scale, 4, "scale", _F32), rows, K, L, rs, bs, pw, nw,
+    _done(lib().nvfp4_global_scale(px, dt, _op(scale, 4, "scale", _F32), rows, K, L, rs, bs, pw, nw,
                                    _stream_handle(stream)), "nvfp4_global_scale")
 
 
@@ -545,10 +548,11 @@ def nvfp4_quantize(x, codes, scales, rows: int, K: int, L: int, sf_layout, globa
                    stream=None) -> None:
     """Enqueue the quantisation of x [L][rows][K] (strides in elements; dense by
     default) to NVFP4 codes and scales; global_scale: float32 on the device."""
-    px, rs, bs = _strided(x, "x", rows, K, L, row_stride, batch_stride)
+    dt = _dtype_id(x, dtype)
+    px, rs, bs = _strided(x, "x", dt, rows, K, L, row_stride, batch_stride)
     lay = layout_id(sf_layout)
     on = 1 if min(rows, K, L) >= 1 else 0                   # the library reports shape errors itself
-    _done(lib().nvfp4_quantize(px, _dtype_id(x, dtype), _op(global_scale, 4, "global_scale", _F32),
+    _done(lib().nvfp4_quantize(px, dt, _op(global_scale, 4, "global_scale", _F32),
                                _op(codes, on * L * rows * K // 2, "codes"),
                                _op(scales, on * _scale_bytes(rows, K, L, lay), "scales"), rows, K, L, rs, bs, lay,
                                _stream_handle(stream)), "nvfp4_quantize")

@@ -218,3 +218,15 @@ def test_a_view_wants_its_strides(call):
         call(x)
     with pytest.raises(ValueError, match="x holds 304 elements, the shape needs 307"):
         call(x, row_stride=81)
+
+
+@pytest.mark.parametrize("call", [
+    lambda x, **kw: g.nvfp4_global_scale(x, Fake(1, "torch.float32", 4), 4, 64, 1, Fake(256), dtype="torch.float32", **kw),
+    lambda x, **kw: g.nvfp4_quantize(x, Fake(128), Fake(16), 4, 64, 1, "plain", dtype="torch.float32", **kw)],
+    ids=["global_scale", "quantize"])
+def test_a_given_type_counts_in_the_tensors_bytes(call):
+    """float32 read from a tensor of 2-byte elements: half as many fit."""
+    with pytest.raises(ValueError, match="x holds 255 elements, the shape needs 256"):
+        call(Fake(511, "torch.bfloat16", 2))
+    with pytest.raises(ValueError, match="x holds 303 elements, the shape needs 304"):
+        call(FakeView(256, "torch.bfloat16", 2, 607), row_stride=80)

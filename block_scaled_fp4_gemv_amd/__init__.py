@@ -489,7 +489,9 @@ def _workspace(x, nbytes):
     """(pointer, bytes) of a workspace, its own size by default."""
     if nbytes is None:
         nbytes = 0 if x is None or isinstance(x, int) else x.numel() * x.element_size()
-    return _op(x, 0, "workspace"), nbytes
+    if nbytes < 0:
+        raise ValueError(f"workspace_bytes is {nbytes}")
+    return _op(x, nbytes, "workspace"), nbytes
 
 
 def _strided(x, name, dt, rows, K, L, row_stride, batch_stride):

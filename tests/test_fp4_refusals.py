@@ -230,3 +230,23 @@ def test_a_given_type_counts_in_the_tensors_bytes(call):
         call(Fake(511, "torch.bfloat16", 2))
     with pytest.raises(ValueError, match="x holds 303 elements, the shape needs 304"):
         call(FakeView(256, "torch.bfloat16", 2, 607), row_stride=80)
+
+
+@pytest.mark.parametrize("call", [
+    lambda **kw: g.nvfp4_global_scale(Fake(256, "torch.float32", 4), Fake(1, "torch.float32", 4), 4, 64, 1, **kw),
+    lambda **kw: g.nvfp4_gemm(*[Fake(1 << 20)] * 4, Fake(2048, "torch.float32", 4), 128, 16, 16384, 1, "plain", **kw),
+    lambda **kw: g.nvfp4_gemm_experts(*[Fake(1 << 22)] * 4, Fake(2048, "torch.float32", 4), 128, 16384, 4, 8, 2, "plain",
+                                      Fake(5, "torch.int32", 4), Fake(16, "torch.int32", 4), **kw),
+    lambda **kw: g.nvfp4_moe_route(Fake(3200, "torch.float32", 4), *[Fake(800, t, 4) for t in (
+        "torch.int32", "torch.float32", "torch.int32", "torch.int32")], 400, 8, 2, **kw)],
+    ids=["global_scale", "gemm", "gemm_experts", "moe_route"])
+def test_workspace_bytes_are_the_tensors(call):
+    """A size given beside the tensor is no larger than it: the library believes the size."""
+    with pytest.raises(ValueError, match="workspace holds 128 bytes, the shape needs"):
+        call(workspace=Fake(128), workspace_bytes=1 << 30)
+    for ws in (Fake(128), P):
+        with pytest.raises(ValueError, match="workspace_bytes is -1"):
+            call(workspace=ws, workspace_bytes=-1)
+    with pytest.raises(g.Nvfp4Error) as e:
+        call(workspace=Fake(128), stream=0)
+    assert e.value.status == WORK

@@ -52,6 +52,7 @@ NVFP4_BF16 = 1
 NVFP4_F32 = 2
 NVFP4_SCORE_SOFTMAX = 0
 NVFP4_SCORE_SIGMOID = 1
+NVFP4_WORKSPACE_MAX_BYTES = 67174400        # serves any call of the FP4 linear layers and routed experts
 
 EXPORTED_SYMBOLS = (
     "nvfp4_gemv",
@@ -586,7 +587,8 @@ def nvfp4_gemm(a, b, sfa, sfb, c, M: int, N: int, K: int, L: int, sf_layout, alp
                scale_b=None, workspace=None, workspace_bytes: int | None = None, dtype=None, stream=None) -> None:
     """Enqueue c[l][n][m] = alpha * ga * gb * sum_k A*SFA*B_n*SFB_n for any N; c
     float16, bfloat16 or float32; scale_a, scale_b: float32 on the device; a
-    (zero-initialised) workspace of nvfp4_gemm_workspace_bytes."""
+    (zero-initialised) workspace of nvfp4_gemm_workspace_bytes, which fewer rows
+    may raise, or of NVFP4_WORKSPACE_MAX_BYTES."""
     lay, dt = layout_id(sf_layout), _dtype_id(c, dtype)
     pw, nw = _workspace(workspace, workspace_bytes)
     on = 1 if min(M, N, K, L) >= 1 else 0

@@ -59,6 +59,7 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxTickets = 16384;              // tiles of a split product
 constexpr int64_t kTicketBytes = kMaxTickets * 4;
 constexpr int64_t kMaxPartialBytes = INT64_C(64) << 20;
+static_assert(kTicketBytes + kMaxPartialBytes == NVFP4_WORKSPACE_MAX_BYTES && NVFP4_WORKSPACE_MAX_BYTES % 256 == 0);
 constexpr int kMaxSplits = 16;
 constexpr int64_t kMaxGrid = 0x7FFFFF;          // workgroups of up to 512 threads in 2^32 work items
 

@@ -897,8 +897,10 @@ bool route_shape(int64_t T, int64_t E, int64_t k)
 // Few tokens run in one workgroup: at most 4 tokens per wave, and LDS for the lists.
 bool route_small(int64_t T, int64_t E, int64_t k) { return T <= 64 && T * k <= 2048 && E <= kSmallThreads; }
 
-// slots per workgroup of the lists' kernels: at most 128 chunks of at least 512
-int64_t list_chunk(int64_t S) { return std::max<int64_t>(512, (S + 127) / 128); }
+// slots per workgroup of the lists' kernels: at most kMaxChunks chunks, of at least 512
+constexpr int64_t kMaxChunks = 128;
+int64_t list_chunk(int64_t S) { return std::max<int64_t>(512, (S + kMaxChunks - 1) / kMaxChunks); }
+static_assert(kTicketBytes + kMaxChunks * kMaxExperts * 4 <= NVFP4_WORKSPACE_MAX_BYTES);
 
 } // namespace
 

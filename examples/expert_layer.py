@@ -64,12 +64,9 @@ class ExpertLayer:
         self.routing = dict(score=score, **routing)
         device = w1.device
         empty = lambda *s, dtype: torch.empty(*s, dtype=dtype, device=device)  # noqa: E731
-        # one zero-filled workspace serves every call in turn: each leaves its counters zero
-        self.workspace = torch.zeros(max(g.nvfp4_global_scale_workspace_bytes(),
-                                         *(g.nvfp4_moe_route_workspace_bytes(t, E, top) for t in (1, tokens)),
-                                         *(g.nvfp4_gemm_experts_workspace_bytes(M, K, E, t * top)
-                                           for t in range(1, tokens + 1) for M, K in ((F2, H), (H, self.F)))),
-                                     dtype=torch.uint8, device=device)
+        # one zero-filled workspace serves every call in turn: each leaves its counters
+        # zero. Fewer tokens may need more of it, so it has the size that serves any
+        self.workspace = torch.zeros(g.NVFP4_WORKSPACE_MAX_BYTES, dtype=torch.uint8, device=device)
         self.w1 = Quantized(F2, H, E, device).take(w1, self.workspace)
         self.w2 = Quantized(H, self.F, E, device).take(w2, self.workspace)
         # the products take a scale per expert; here all share the tensor's

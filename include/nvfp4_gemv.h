@@ -317,9 +317,14 @@ size_t nvfp4_blocked_scales_bytes(int64_t rows, int64_t K, int64_t L);
  * Workspaces of this part: device memory of at least the bytes that the
  * matching _workspace_bytes function gives, 256-byte aligned, zero-filled
  * before its first use. Every completed call leaves its counters zero, so one
- * workspace serves any later call of this part without clearing, on one stream.
- * A size of 0 means none is needed (NULL is then accepted).
+ * workspace serves any later call of this part without clearing, on one stream,
+ * if it is large enough for that call. A product's size does not rise with its
+ * rows N (or slots S): fewer rows may be split along K and then need more. No
+ * call of this part needs more than NVFP4_WORKSPACE_MAX_BYTES, so a program that
+ * does not know its row counts beforehand takes one workspace of that size. A
+ * size of 0 means none is needed (NULL is then accepted).
  */
+#define NVFP4_WORKSPACE_MAX_BYTES 67174400  /* 64 KiB of counters, 64 MiB of partial sums */
 
 /*
  * Global scale of a tensor for nvfp4_quantize: the largest block of x then

@@ -1,6 +1,10 @@
 """CPU checks of the FP4 linear layers' C ABI: every refusal comes before any HIP
 call, the binding checks types and sizes, plans and workspaces are consistent."""
 import ctypes
+import math
+import os
+import random
+import re
 
 import pytest
 
@@ -250,3 +254,23 @@ def test_workspace_bytes_are_the_tensors(call):
     with pytest.raises(g.Nvfp4Error) as e:
         call(workspace=Fake(128), stream=0)
     assert e.value.status == WORK
+
+
+def test_workspace_max_serves_every_shape():
+    """A product's workspace does not rise with its rows; the documented size holds all of them."""
+    text = open(os.path.join(os.path.dirname(g.PKG_DIR), "include", "nvfp4_gemv.h")).read()
+    most = int(re.search(r"#define NVFP4_WORKSPACE_MAX_BYTES (\d+)", text).group(1))
+    assert most == g.NVFP4_WORKSPACE_MAX_BYTES and most % 256 == 0
+    assert g.nvfp4_gemm_workspace_bytes(2048, 64, 7168, 1) > g.nvfp4_gemm_workspace_bytes(2048, 256, 7168, 1)
+    rng = random.Random(5)
+    log = lambda lo, hi: int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))  # noqa: E731
+    near = 0
+    for _ in range(4000):
+        M, N, K = log(1, 1 << 20), log(1, 1 << 16), 32 * log(1, 1 << 17)
+        got = max(g.nvfp4_gemm_workspace_bytes(M, N, K, log(1, 64)), g.nvfp4_gemm_experts_workspace_bytes(M, K, log(1, 1024), N),
+                  g.nvfp4_moe_route_workspace_bytes(N, log(64, 1024), log(1, 64)))
+        near = max(near, got)
+        assert got <= most, (M, N, K)
+    assert near > most // 2, "the sweep does not come near the size"
+    assert g.nvfp4_moe_route_workspace_bytes(1 << 24, 1024, 64) <= most
+    assert g.nvfp4_global_scale_workspace_bytes() <= most

@@ -365,7 +365,9 @@ nvfp4_status_t nvfp4_global_scale(const void *x, int dtype, float *scale, int64_
  *           written as 0 (4-byte aligned)
  * The outputs are operands of nvfp4_gemv (rows = 1 or M), nvfp4_gemm_small_n
  * and nvfp4_gemm: those want 16-byte aligned codes. Requirements: rows, L >= 1;
- * K % 32 == 0; codes and scales do not overlap x.
+ * K % 32 == 0; codes and scales do not overlap x; and at most 2^24 - 1
+ * workgroups, which are L * ceil(rows * K / 4096) for plain scales and
+ * L * 8 * ceil(rows / 128) * ceil(K / 256) for blocked ones.
  */
 nvfp4_status_t nvfp4_quantize(const void *x, int dtype, const float *global_scale, void *codes,
                               void *scales, int64_t rows, int64_t K, int64_t L, int64_t row_stride,
@@ -375,6 +377,7 @@ nvfp4_status_t nvfp4_quantize(const void *x, int dtype, const float *global_scal
  * The values that codes and scales stand for: out[l][r][k] = q * s * g, out
  * of type dtype, dense [L][rows][K]. q * s is exact; the product with g is
  * rounded to float32 and then to dtype (so at most half a step and 2^-24 off).
+ * Requirements: rows, L >= 1; K % 32 == 0; L * rows * K <= 4096 * (2^24 - 1).
  */
 nvfp4_status_t nvfp4_dequantize(const void *codes, const void *scales, const float *global_scale,
                                 void *out, int dtype, int64_t rows, int64_t K, int64_t L,
@@ -395,7 +398,8 @@ nvfp4_status_t nvfp4_dequantize(const void *codes, const void *scales, const flo
  * alpha * ga * gb itself may leave float32's range. The order of
  * summation is fixed for a shape, so equal calls give equal bits.
  * Requirements: M, N, L >= 1; K % 32 == 0; M, N <= 2^30; K <= 2^22; a, b, sfa
- * and sfb 16-byte aligned; alpha finite.
+ * and sfb 16-byte aligned; alpha finite; at most 2^23 - 1 workgroups (a shape
+ * that needs more is refused by nvfp4_gemm_plan too).
  */
 size_t nvfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t L);
 nvfp4_status_t nvfp4_gemm(const void *a, const void *b, const void *sfa, const void *sfb, void *c,
@@ -444,7 +448,8 @@ nvfp4_status_t nvfp4_gemm_plan(int64_t M, int64_t N, int64_t K, int64_t L, nvfp4
  *
  *   logits dtype [T][E] dense, bias float32 [E], ids int32 [T][k], weights
  *   float32 [T][k]; all aligned to their types.
- * Requirements: T >= 1, T * k <= 2^30; 1 <= E <= 1024; 1 <= k <= min(E, 64);
+ * Requirements: T >= 1, T * k <= 2^30, T <= 16 * (2^24 - 1) where k < 16 and
+ * E <= 256, T <= 4 * (2^24 - 1) elsewhere; 1 <= E <= 1024; 1 <= k <= min(E, 64);
  * n_group divides E and is at most 64; 1 <= topk_group <= n_group; 1 <= group_top
  * <= E / n_group, at most 2; scaling finite.
  */
@@ -485,7 +490,8 @@ nvfp4_status_t nvfp4_moe_route(const void *logits, int dtype, const float *bias,
  *   c        dtype [S][M]; rows of slots in no list are not written
  * Rounding, order of summation and requirements as for nvfp4_gemm; E <= 1024,
  * rows, slots_per_row >= 1, S <= 2^30, rows * K / 2 <= 2^32 (B's rows are gathered
- * by 32-bit offsets).
+ * by 32-bit offsets); workgroups as for nvfp4_gemm, for the most tiles that any
+ * lists of S slots have.
  */
 size_t nvfp4_gemm_experts_workspace_bytes(int64_t M, int64_t K, int64_t E, int64_t S);
 nvfp4_status_t nvfp4_gemm_experts(const void *a, const void *b, const void *sfa, const void *sfb,
@@ -502,7 +508,7 @@ nvfp4_status_t nvfp4_gemm_experts(const void *a, const void *b, const void *sfa,
  * j. Slots with a negative id are not read (their rows may hold anything).
  *   y dtype [T * k][M], out dtype [T][M], ids int32 and weights float32 [T][k];
  * all aligned to their types. Requirements: T, k, M >= 1; k <= 64; T * k <= 2^30;
- * M <= 2^30.
+ * M <= 2^30; T * ceil(M / 8) (float32: M / 4) <= 256 * (2^24 - 1).
  */
 nvfp4_status_t nvfp4_moe_combine(const void *y, int dtype, const int32_t *ids, const float *weights,
                                  void *out, int64_t T, int64_t k, int64_t M, void *stream);

@@ -9,6 +9,7 @@ import re
 import pytest
 
 import block_scaled_fp4_gemv_amd as g
+from conftest import no_gpu_only
 
 P = 0x100000        # fake, aligned device addresses (never dereferenced: every call here is refused)
 INF, NAN = float("inf"), float("nan")
@@ -274,3 +275,34 @@ def test_workspace_max_serves_every_shape():
     assert near > most // 2, "the sweep does not come near the size"
     assert g.nvfp4_moe_route_workspace_bytes(1 << 24, 1024, 64) <= most
     assert g.nvfp4_global_scale_workspace_bytes() <= most
+
+
+G = 2 ** 24 - 1         # workgroups of 256 threads that a launch holds
+# (call, arguments, largest value of one of them, that argument): the header's limits
+LIMITS = [(quantize, dict(K=32, rs=32, bs=0, lay=1), 128 * (G // 8), "rows"), (quantize, dict(K=64, bs=0, lay=0), 64 * G, "rows"),
+          (quantize, dict(rows=1, bs=0, lay=0), G, "L"), (dequantize, dict(rows=64, K=64), G, "L"),
+          (route, dict(E=8, k=2), 16 * G, "T"), (route, dict(E=8, k=1), 16 * G, "T"), (route, dict(E=257, k=2), 4 * G, "T"),
+          (route, dict(E=64, k=16), 4 * G, "T"), (combine, dict(k=2, M=512), 4 * G, "T"),
+          (combine, dict(k=2, M=512, dtype=2), 2 * G, "T"), (combine, dict(T=256, k=1), 8 * G, "M")]
+
+
+@pytest.mark.parametrize("call,args,most,name", LIMITS,
+                         ids=lambda v: v.__name__ if callable(v) else str(v) if isinstance(v, (int, str)) else "")
+def test_documented_limits_past_the_end(call, args, most, name):
+    assert call(**args, **{name: most + 1}) == SHAPE
+
+
+@no_gpu_only
+@pytest.mark.parametrize("call,args,most,name", LIMITS,
+                         ids=lambda v: v.__name__ if callable(v) else str(v) if isinstance(v, (int, str)) else "")
+def test_documented_limits_are_reached(call, args, most, name):
+    assert call(**args, **{name: most}) == g.NVFP4_ERR_HIP
+
+
+def test_product_limits():
+    """Workgroups of a product: the plan and the product refuse alike."""
+    assert gemm(M=2 ** 30, N=2 ** 12, K=32) == SHAPE
+    with pytest.raises(g.Nvfp4Error) as e:
+        g.nvfp4_gemm_plan(2 ** 30, 2 ** 12, 32, 1)
+    assert e.value.status == SHAPE
+    assert experts(M=2 ** 30, K=32, E=4, rows=2 ** 12, per=1) == SHAPE

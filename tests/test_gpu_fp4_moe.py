@@ -402,3 +402,12 @@ def test_experts_scales_far_from_one():
                 off = np.abs(got[dev(slots)].double().cpu().numpy() - want) - ref.product_tolerance(K, size, want, dtype)
                 fine = np.abs(want) < torch.finfo(dtype).max * 0.99
                 assert not fine.any() or off[fine].max() <= 0, f"{dtype} expert {e}: worst by {off[fine].max():.3g}"
+
+
+# a tile in slices that the lists above do not reach: 128 x 32
+SLICED_TILES = [(52, 37, 4, 240, 32160)]
+
+
+@pytest.mark.parametrize("T,E,k,M,K", SLICED_TILES)
+def test_experts_more_tiles_in_slices(T, E, k, M, K):
+    test_experts_every_tile(T, E, k, M, K)

@@ -1,54 +1,36 @@
-"""CPU run of the router's source: nvfp4_moe_route, its launches and kernels
-compiled for the host (tests/cpu_wave), on buffers that end where their mapping
-ends, and once more on ones that start where it starts. A read or write outside
-ends the run with a segmentation fault; what it writes is the definition's.
+"""CPU run of the source of router and combine (nvfp4_moe.hip): their launches and
+kernels compiled for the host (tests/cpu_wave), on buffers that end where their
+mapping ends, and once more on ones that start where it starts. A read or write
+outside ends the run with a segmentation fault; what it writes is the definition's.
 
 The rows of T tokens are packed four to a wave where k < 16, E <= 256 and T > 16,
 so the token counts stand around multiples of 4, of a workgroup's 16 tokens, and
 of 64, up to which one workgroup does it all.
 """
-import os
-import shutil
-import subprocess
-
 import numpy as np
 import pytest
 
 import block_scaled_fp4_gemv_amd as g
+import cpu_wave_util as cpu_wave
 import fp4_reference as ref
 
 torch = pytest.importorskip("torch")
 
-HERE = os.path.dirname(os.path.abspath(__file__))
-CLANG = next((c for c in ("/opt/rocm/llvm/bin/clang++", shutil.which("clang++")) if c and os.path.exists(c)), None)
 DTYPES = {g.NVFP4_F16: torch.float16, g.NVFP4_BF16: torch.bfloat16, g.NVFP4_F32: torch.float32}
 
 
 @pytest.fixture(scope="module")
 def program(tmp_path_factory):
-    if CLANG is None:
-        pytest.skip("no clang++ (ROCm's)")
-    out = str(tmp_path_factory.mktemp("route") / "route")
-    root = os.path.dirname(HERE)
-    subprocess.run([CLANG, "-x", "c++", "-std=c++17", "-O2", "-Wall", "-Wno-unused-function", "-I", os.path.join(HERE, "cpu_wave"),
-                    "-I", os.path.join(root, "block_scaled_fp4_gemv_amd", "csrc"), "-I", os.path.join(root, "include"),
-                    os.path.join(HERE, "cpu_wave", "route.cpp"), "-o", out], check=True)
-    return out
+    return cpu_wave.build(tmp_path_factory.mktemp("route"), "route")
 
 
-def run(program, tmp_path, logits, dtype, k, score, bias, n_group, topk_group, group_top, renormalize, scaling):
+def run(program, folder, logits, dtype, k, score, bias, n_group, topk_group, group_top, renormalize, scaling):
     """The router's outputs for logits [T][E], a tensor of the type `dtype`."""
     T, E = logits.shape
-    head = np.array([dtype, T, E, k, score, n_group, topk_group, group_top, renormalize, bias is not None], np.int32)
-    src, dst = str(tmp_path / "in"), str(tmp_path / "out")
-    with open(src, "wb") as f:
-        f.write(head.tobytes() + np.float32(scaling).tobytes() + logits.contiguous().view(torch.uint8).numpy().tobytes() +
-                (np.zeros(E, np.float32) if bias is None else bias).tobytes())
-    done = subprocess.run([program, src, dst], capture_output=True, text=True, timeout=120)
-    assert done.returncode == 0, (f"status {done.returncode}" + (" (an access outside a buffer)" if done.returncode == -11 else "") +
-                                  done.stderr)
-    words = np.fromfile(dst, np.int32)
-    S = T * k
+    head = np.array([0, dtype, T, E, k, score, n_group, topk_group, group_top, renormalize, bias is not None], np.int32)
+    out, _ = cpu_wave.run(program, folder, [head, np.float32(scaling), logits.contiguous().view(torch.uint8).numpy()] +
+                          ([] if bias is None else [bias]))
+    words, S = out.view(np.int32), T * k
     ids, weights = words[:S].reshape(T, k), words[S:2 * S].view(np.float32).reshape(T, k)
     return ids, weights, words[2 * S:2 * S + E + 1], words[2 * S + E + 1:]
 
@@ -89,3 +71,19 @@ def test_last_wave_reads_no_token_past_the_end(program, tmp_path, T, dtype):
     for score in (0, 1):
         ids, _, _, _ = run(program, tmp_path, logits, dtype, k, score, None, 1, 1, 1, 1, 1.0)
         assert np.array_equal(ids, ref.route(logits.double().numpy(), None, k, "sigmoid" if score else "softmax")[0])
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("T,k,M", [(1, 1, 1), (3, 2, 7), (5, 4, 130), (2, 9, 33), (7, 64, 8), (1, 8, 1001)])
+def test_combine_stays_inside_its_buffers(program, tmp_path, T, k, M, dtype):
+    rng = np.random.default_rng([T, k, M])
+    y = torch.from_numpy(rng.standard_normal((T * k, M))).to(DTYPES[dtype])
+    w = rng.uniform(-1, 1, (T, k)).astype(np.float32)
+    ids = rng.integers(-1, 4, (T, k)).astype(np.int32)
+    y[torch.from_numpy(ids.reshape(-1) < 0)] = float("nan")          # never read
+    out, _ = cpu_wave.run(program, tmp_path, [np.array([1, dtype, T, k, M], np.int32), y.view(torch.uint8).numpy(), ids, w])
+    terms = np.where(ids < 0, 0.0, w.astype(np.float64))[:, :, None] * np.nan_to_num(y.double().numpy()).reshape(T, k, M)
+    got = torch.from_numpy(out).view(DTYPES[dtype]).double().numpy().reshape(T, M)
+    want, size = terms.sum(1), np.abs(terms).sum(1)
+    tol = k * 2.0 ** -24 * size + ref.HALF_STEP[DTYPES[dtype]] * (1 + 2.0 ** -10) * np.abs(want) + ref.LEAST[DTYPES[dtype]]
+    assert (np.abs(got - want) <= tol).all()

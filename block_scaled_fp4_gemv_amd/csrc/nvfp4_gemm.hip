@@ -574,7 +574,8 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void nvfp4_gemm_wide_kern
     const uint32_t words_b = kOffSB + (rb0 / (32 * T::LB)) * (T::LB * 256) + half * (T::LB * 128) +
                              l32 * (T::LB * 4) + (rb0 / 32 % T::LB) * 4;
     // A stage is 8 steps of 16 k (per half of the lanes: one dword of codes per
-    // row), codes being read 16 bytes at a time.
+    // row), codes being read 16 bytes at a time. A wave whose rows of B all lie past
+    // the list's end works as the others do (12% of the rows of 16384 slots of 32 experts).
     auto compute = [&](int st, int slot) {
         const uint8_t *base = lds + slot * kStage;
         uint32_t word[F], sa[FM], sb[FN];
@@ -951,6 +952,10 @@ bool gemm_shape(int64_t M, int64_t N, int64_t K, int64_t L)
 // 128 64; 7168 x 4096 x 16384: 256 x 256 760, 256 x 128 810, 64 x 64 970; 4096 x
 // 128 x 7168: 64 x 32 14.4, 32 x 32 15.4, 64 x 64 18.2; 7168 x 16 x 16384: 32 x 32
 // with 8 waves along K 17.3, with 4 20.2, 64 x 32 in two slices 19.1.
+//   The table does not know the result's bytes, and was not measured below K = 512:
+// there the result bounds the time, and 128 x 128 tiles with a lone stage or few
+// are taken. 4096 x 4096 x 128: 28 us to float32, 22 to bfloat16 (67 and 34 MB
+// stored); 8192 x 2900 x 128: 39 and 31 (95 and 48 MB); 4096 x 4096 x 32 as x 128.
 //   A shape that is never fastest in a use is not built for it: 256 x 256 against
 // 256 x 128 for 16384 slots of 32 experts, 7168 x 4096: 1068 against 970 us; 256 x
 // 128 against 128 x 128 and 256 x 256 in dense products: at most 2 % ahead of the

@@ -14,6 +14,16 @@
 // 16384 tokens of 256 experts, 8 of them from 4 of 8 groups: float64 alone 58 us;
 // float32 with a wave per token 44; four tokens per wave 23 with the experts of a
 // lane 16 apart, 21 with neighbours: groups are then a few lanes, and loads wide.
+//   Some routers take float64 for every token, those of a wave one after another:
+// softmax weights that are not renormalised (they need the float64 sum over all
+// experts), groups that are not the experts of 1, 2, 4, .. whole lanes, and as many
+// picks as a token has lanes. 16384 tokens, softmax: 8 of 256 experts 17 us
+// renormalised, 51 not; 6 of 64 11 and 32; 6 of 160 in 8 groups 56; 8 of 384 33, in
+// 4 groups 105.
+//   The one workgroup of up to 64 tokens has 128 registers a thread; its kernels
+// spill 41 of them for 129 to 256 experts and more than 16 tokens, 27 for 257 to 512
+// experts and 106 beyond. 64 tokens: 8 of 128 experts 8.5 us, of 256 14, of 384 29,
+// of 1024 48.
 // Lists. A stable counting sort of the slots by expert: counts per chunk of
 // slots, then each chunk's places from the counts of the chunks before it. Every
 // rank is counted, no atomic's order enters: the lists are the same each time.
@@ -979,9 +989,11 @@ nvfp4_status_t nvfp4_moe_route(const void *logits, int dtype, const float *bias,
 #undef NVFP4_N
     });
     if (!small) {
-        // the router could count its picks as it goes (10 us against 5 + 9 for 131072
-        // slots), but then the counts had to be zero before the call, which partial
-        // sums of a product may have left otherwise in a shared workspace
+        // The router does not count its picks as it goes. By atomics (10 us for the
+        // lists against 5 + 9, 131072 slots) the counts would have to be zero before
+        // the call, and partial sums of a product may stand there in a shared
+        // workspace; counts per chunk in LDS, stored as this kernel stores them, would
+        // need no zero and are not built.
         const int32_t chunk = (int32_t)list_chunk(S), nc = (S + chunk - 1) / chunk;
         int32_t *counts = (int32_t *)((uint8_t *)workspace + kTicketBytes);
         hipLaunchKernelGGL(nvfp4_count_kernel, dim3(nc), dim3(kListThreads), 0, st, (const int32_t *)ids, counts, S,

@@ -6,9 +6,9 @@
 // wave, and turns each pick into one 32-bit key, its value in fixed point above
 // the expert's index counted down, so that the largest key is the pick and ties
 // go to the lower index. Each lane sorts its keys; a round takes the largest head of the lanes.
-// Where two neighbours in the ranking (or the last group kept and the first one
-// left) are closer than the bound, unless they come from the same logit and bias,
-// the wave repeats the token in float64. The weights are float64 in both. What
+// Where two neighbours in the ranking (or the last pick and any that is left, or the
+// last group kept and the first one left) are closer than the bound, unless they come
+// from the same logit and bias, the wave repeats the token in float64. The weights are float64 in both. What
 // bounds it: vector instructions, about 1270 per wave, 10 us at 4 per SIMD, after
 // the logits have come (4 us) and the waves have started.
 // 16384 tokens of 256 experts, 8 of them from 4 of 8 groups: float64 alone 58 us;
@@ -464,14 +464,27 @@ __device__ __attribute__((always_inline)) inline bool route_fast(const void *__r
         key[NL - 1] = pop ? 0u : key[NL - 1];
     }
     id = got ? (int)(kIndex - (got & kIndex)) : -1;
-    // neighbours in the ranking closer than the bound: from the same logit and bias?
+    // Neighbours in the ranking closer than the bound: from the same logit and bias? Of
+    // those that are left, all within the bound of the last pick have to be its equals:
+    // the first one may be, and stand before a larger one by its index.
     const uint32_t next = LPT == 16 ? from_lane<0x101>(got) : (uint32_t)__shfl_down((int)got, 1);      // row_shl:1
     bool doubt = here && l < p.k && got && next && (got >> IB) - (next >> IB) <= close;
     if (__ballot(doubt)) {
-        if (doubt) {
-            const int other = (int)(kIndex - (next & kIndex));
-            doubt = load_value<DT>(logits, t * p.E + id) != load_value<DT>(logits, t * p.E + other) ||
-                    (bias && bias[id] != bias[other]);
+        auto differs = [&](uint32_t a, uint32_t b) {
+            const int ea = (int)(kIndex - (a & kIndex)), eb = (int)(kIndex - (b & kIndex));
+            return load_value<DT>(logits, t * p.E + ea) != load_value<DT>(logits, t * p.E + eb) ||
+                   (bias && bias[ea] != bias[eb]);
+        };
+        doubt = doubt && differs(got, next);
+        const uint32_t last = token_max<LPT>(here && l == p.k - 1 ? got : 0u);
+        auto left = [&] { return last && key[0] && (last >> IB) - (key[0] >> IB) <= close; };
+        while (__ballot(left())) {                              // a lane's keys fall
+            if (left())
+                doubt = doubt || differs(last, key[0]);
+#pragma unroll
+            for (int i = 0; i + 1 < NL; ++i)
+                key[i] = key[i + 1];
+            key[NL - 1] = 0u;
         }
         const uint32_t any = token_max<LPT>(doubt ? 1u : 0u);
         sure = sure && any == 0u;

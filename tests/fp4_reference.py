@@ -153,3 +153,18 @@ def check_product(got, ref, sum_abs, K, dtype, what=""):
         rel = np.linalg.norm((g - ref)[fine]) / norm
         scale = np.linalg.norm(sum_abs[fine]) / norm
         assert rel <= HALF_STEP[dtype] + 2.0 ** -22 + np.sqrt(K) * 2.0 ** -23 * max(1.0, scale / np.sqrt(K)), f"{what}: {rel:.3g} off"
+
+
+def equals_at_the_last_pick(rng, T, E, k, sigmoid):
+    """Logits (float32 tensor) whose order float32 scores cannot tell at the last of k picks:
+    there, two or three experts of one logit stand among others of a larger one, all of the
+    same float32 score."""
+    x = torch.full((T, E), -8.0)
+    for t in range(T):
+        at = torch.from_numpy(rng.permutation(E))
+        x[t, at[:k - 1]] = 60.0 if sigmoid else 30.0        # picked before; softmax: they take all of the sum
+        close = at[k - 1:k + 3].sort().values
+        low, high = (20.0, 24.0) if sigmoid else (2.0, 2.25) if k > 1 else (2.0, 2.0 + 2.0 ** -20)
+        x[t, close] = low
+        x[t, close[2 + t % 2]] = high
+    return x

@@ -411,3 +411,46 @@ SLICED_TILES = [(52, 37, 4, 240, 32160)]
 @pytest.mark.parametrize("T,E,k,M,K", SLICED_TILES)
 def test_experts_more_tiles_in_slices(T, E, k, M, K):
     test_experts_every_tile(T, E, k, M, K)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", [(19, 64, 1), (200, 64, 2), (18, 128, 8), (301, 256, 8), (66, 256, 15), (5, 256, 6), (90, 512, 4), (70, 1024, 8)])
+def test_equals_at_the_last_pick_hide_no_larger_one(T, E, k, score):
+    """The expert of the last pick and the next share a logit: what stands behind them, as
+    close in float32, may be larger."""
+    rng = np.random.default_rng([T, E, k])
+    logits = ref.equals_at_the_last_pick(rng, T, E, k, score == "sigmoid")
+    for bias in (None, np.full(E, 0.03125, np.float32)):
+        z = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+        ids, offsets, order, weights = z(T, k), z(E + 1), z(T * k), torch.zeros(T, k, device="cuda")
+        ws = torch.zeros(max(256, g.nvfp4_moe_route_workspace_bytes(T, E, k)), dtype=torch.uint8, device="cuda")
+        g.nvfp4_moe_route(logits.cuda(), ids, weights, offsets, order, T, E, k, score=score,
+                          bias=None if bias is None else dev(bias), workspace=ws)
+        want, _ = ref.route(logits.double().numpy(), bias, k, score)
+        assert np.array_equal(ids.cpu().numpy(), want), np.argwhere(ids.cpu().numpy() != want)[:4]
+
+
+@pytest.mark.parametrize("k,score,biased", [(1, "sigmoid", True), (2, "softmax", False), (8, "sigmoid", False), (8, "softmax", True)])
+def test_ids_of_many_near_ties(k, score, biased):
+    """Logits on a coarse grid, some a few 2^-20 off it: 20000 tokens against 64 bits."""
+    T, E = 20000, 64
+    gen = torch.Generator(device="cuda").manual_seed(k)
+    x = (torch.randn(T, E, device="cuda", generator=gen) * (12 if k < 8 else 2) * 16).round() / 16
+    x += torch.randint(-2, 3, (T, E), device="cuda", generator=gen) * 2.0 ** -20
+    bias = (torch.randn(E, device="cuda", generator=gen) * 2).round() / 64 if biased else None
+    z = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    ids, offsets, order, weights = z(T, k), z(E + 1), z(T * k), torch.zeros(T, k, device="cuda")
+    ws = torch.zeros(g.nvfp4_moe_route_workspace_bytes(T, E, k), dtype=torch.uint8, device="cuda")
+    g.nvfp4_moe_route(x, ids, weights, offsets, order, T, E, k, score=score, bias=bias, workspace=ws)
+    v = x.double()
+    if score == "softmax":
+        pick = torch.exp(v - v.amax(1, keepdim=True))
+        pick = pick / pick.sum(1, keepdim=True)
+    else:
+        pick = 1 / (1 + torch.exp(-v))
+    if biased:
+        pick = pick + bias.double()
+    # both sides' float64 scores are a few 2^-53 off: an id that differs is of such a pick
+    want = pick.sort(dim=1, descending=True, stable=True).indices[:, :k]
+    off = (pick.gather(1, ids.long()) - pick.gather(1, want)).abs()
+    assert off.max() <= 2.0 ** -50, (int((off > 2.0 ** -50).sum()), off.max())

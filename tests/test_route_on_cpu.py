@@ -87,3 +87,17 @@ def test_combine_stays_inside_its_buffers(program, tmp_path, T, k, M, dtype):
     want, size = terms.sum(1), np.abs(terms).sum(1)
     tol = k * 2.0 ** -24 * size + ref.HALF_STEP[DTYPES[dtype]] * (1 + 2.0 ** -10) * np.abs(want) + ref.LEAST[DTYPES[dtype]]
     assert (np.abs(got - want) <= tol).all()
+
+
+@pytest.mark.parametrize("score", [0, 1], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", [(19, 64, 1), (19, 64, 2), (18, 128, 8), (17, 256, 8), (66, 256, 15), (5, 256, 6), (3, 512, 4), (2, 1024, 8)])
+def test_equals_at_the_last_pick_hide_no_larger_one(program, tmp_path, T, E, k, score):
+    """Expert of the last pick and the next share a logit: what stands behind them, as close
+    in float32, may be larger."""
+    rng = np.random.default_rng([T, E, k, score])
+    for biased in (False, True):
+        logits = ref.equals_at_the_last_pick(rng, T, E, k, score)
+        bias = np.full(E, 0.03125, np.float32) if biased else None
+        ids, _, offsets, order = run(program, tmp_path, logits, g.NVFP4_F32, k, score, bias, 1, 1, 1, 1, 1.0)
+        want, _ = ref.route(logits.double().numpy(), bias, k, "sigmoid" if score else "softmax")
+        assert np.array_equal(ids, want), np.argwhere(ids != want)[:4]

@@ -18,6 +18,15 @@ FP4 linear layers and routed experts (last part of the header):
     nvfp4_gemm_experts(a, b, sfa, sfb, c, M, K, E, rows, slots_per_row, sf_layout, offsets, order)
     nvfp4_moe_combine(y, ids, weights, out, T, k, M)
 
+Attention over a paged NVFP4 key/value cache:
+
+    nvfp4_rope_frequencies(R, base, method="unscaled", ...)
+    nvfp4_rope(x, out, positions, frequencies, T, H, D, R, layout="half")
+    Nvfp4Cache(k_codes, k_scales, v_codes, v_scales, pages, page_size, heads, head_size)
+    nvfp4_cache_write(cache, k, v, slots, T)
+    nvfp4_cache_read(cache, k, v, slots, T)
+    nvfp4_cache_attention(cache, q, out, offsets, lengths, table, T, H, B, max_q, max_length, workspace=...)
+
     a   uint8 [L, M, K/2]   packed E2M1, low nibble = even k
     b   uint8 [L, K/2]
     sfa uint8 plain [L, M, K/16] or blocked [L, ceil(M/128)*ceil(K/64)*512]
@@ -47,12 +56,21 @@ NVFP4_ERR_INVALID_SCALE = 7
 NVFP4_ERR_INVALID_STRIDE = 8
 NVFP4_ERR_INVALID_TYPE = 9
 NVFP4_ERR_INVALID_ROUTING = 10
+NVFP4_ERR_INVALID_ROTATION = 11
+NVFP4_ERR_INVALID_CACHE = 12
 NVFP4_F16 = 0
 NVFP4_BF16 = 1
 NVFP4_F32 = 2
 NVFP4_SCORE_SOFTMAX = 0
 NVFP4_SCORE_SIGMOID = 1
-NVFP4_WORKSPACE_MAX_BYTES = 67174400        # serves any call of the FP4 linear layers and routed experts
+NVFP4_ROPE_HALF = 0
+NVFP4_ROPE_INTERLEAVED = 1
+NVFP4_ROPE_UNSCALED = 0
+NVFP4_ROPE_LINEAR = 1
+NVFP4_ROPE_BASE = 2
+NVFP4_ROPE_BANDS = 3
+NVFP4_ROPE_RAMP = 4
+NVFP4_WORKSPACE_MAX_BYTES = 67174400        # serves any call that takes one of the layers', experts' and attention's
 
 EXPORTED_SYMBOLS = (
     "nvfp4_gemv",
@@ -81,6 +99,12 @@ EXPORTED_SYMBOLS = (
     "nvfp4_gemm_experts",
     "nvfp4_gemm_experts_workspace_bytes",
     "nvfp4_moe_combine",
+    "nvfp4_rope",
+    "nvfp4_rope_frequencies",
+    "nvfp4_cache_write",
+    "nvfp4_cache_read",
+    "nvfp4_cache_attention",
+    "nvfp4_cache_attention_workspace_bytes",
     "nvfp4_status_string",
     "nvfp4_last_hip_error",
 )
@@ -134,6 +158,28 @@ class Routing(ctypes.Structure):
     """nvfp4_routing_t."""
     _fields_ = [("score", ctypes.c_int32), ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
                 ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scaling", ctypes.c_float)]
+
+
+class RopeScaling(ctypes.Structure):
+    """nvfp4_rope_scaling_t."""
+    _fields_ = [("method", ctypes.c_int32), ("factor", ctypes.c_double), ("length", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+class CacheStruct(ctypes.Structure):
+    """nvfp4_cache_t."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page_size", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("head_size", ctypes.c_int64), ("code_page_stride", ctypes.c_int64),
+                ("scale_page_stride", ctypes.c_int64)]
+
+
+class Attention(ctypes.Structure):
+    """nvfp4_attention_t."""
+    _fields_ = [("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64), ("max_q", ctypes.c_int64),
+                ("max_length", ctypes.c_int64), ("window", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("causal", ctypes.c_int32)]
 
 
 _lib = None
@@ -206,6 +252,20 @@ def lib():
     L.nvfp4_gemm_experts_workspace_bytes.argtypes = [i64, i64, i64, i64]
     L.nvfp4_moe_combine.restype = i32
     L.nvfp4_moe_combine.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, vp]
+    L.nvfp4_rope.restype = i32
+    L.nvfp4_rope.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i64, i32, f32, i32, vp]
+    L.nvfp4_rope_frequencies.restype = i32
+    L.nvfp4_rope_frequencies.argtypes = [ctypes.POINTER(ctypes.c_double), i64, ctypes.c_double,
+                                         ctypes.POINTER(RopeScaling)]
+    cache, att = ctypes.POINTER(CacheStruct), ctypes.POINTER(Attention)
+    L.nvfp4_cache_write.restype = i32
+    L.nvfp4_cache_write.argtypes = [cache, vp, vp, i32, vp, i64, i64, i64, i64, i64, vp]
+    L.nvfp4_cache_read.restype = i32
+    L.nvfp4_cache_read.argtypes = [cache, vp, vp, i32, vp, i64, vp]
+    L.nvfp4_cache_attention.restype = i32
+    L.nvfp4_cache_attention.argtypes = [cache, vp, i32, vp, vp, vp, vp, vp, i64, i64, i64, i64, att, vp, size, vp]
+    L.nvfp4_cache_attention_workspace_bytes.restype = size
+    L.nvfp4_cache_attention_workspace_bytes.argtypes = [cache, i32, i64, i64, i64, att]
     L.nvfp4_status_string.restype = ctypes.c_char_p
     L.nvfp4_status_string.argtypes = [i32]
     L.nvfp4_last_hip_error.restype = i32
@@ -658,6 +718,176 @@ def nvfp4_moe_combine(y, ids, weights, out, T: int, k: int, M: int, dtype=None, 
     _done(lib().nvfp4_moe_combine(_op(y, k * n, "y"), dt, _op(ids, slots, "ids", _I32),
                                   _op(weights, slots, "weights", _F32), _op(out, n, "out"), T, k, M,
                                   _stream_handle(stream)), "nvfp4_moe_combine")
+
+
+# ---------------------------------------------------------------- attention over a paged cache
+
+_LAYOUTS = {"half": NVFP4_ROPE_HALF, "interleaved": NVFP4_ROPE_INTERLEAVED}
+_METHODS = {"unscaled": NVFP4_ROPE_UNSCALED, "linear": NVFP4_ROPE_LINEAR, "base": NVFP4_ROPE_BASE,
+            "bands": NVFP4_ROPE_BANDS, "ramp": NVFP4_ROPE_RAMP}
+_I64, _F64, _U8 = "torch.int64", "torch.float64", "torch.uint8"
+
+
+_current_device = None
+
+
+def _check_device(x, name):
+    """Kernels are launched on the current device: a tensor of another is refused."""
+    global _current_device
+    if not x.is_cuda:
+        raise ValueError("operands must be device tensors")
+    if _current_device is None:
+        import torch
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    if x.get_device() != _current_device():
+        raise ValueError(f"{name} is on {x.device}, not on the current device")
+
+
+def _rows(x, name, dt, T, H, D, token_stride, head_stride):
+    """Pointer of a [T][H][D] tensor of type ``dt`` and its strides in elements (dense
+    by default), checked against what its memory holds behind its first element."""
+    given = token_stride is not None or head_stride is not None
+    if head_stride is None:
+        head_stride = D
+    if token_stride is None:
+        token_stride = H * head_stride
+    if x is None or isinstance(x, int):
+        return x, token_stride, head_stride
+    _check_device(x, name)
+    if _dtype_id(x, None) != dt:
+        raise ValueError(f"{name} is {x.dtype}, not of the call's type")
+    if not given and not x.is_contiguous():
+        raise ValueError(f"{name} is not contiguous: give its strides")
+    if given and x.dim() and x.stride(-1) != 1 and x.shape[-1] > 1:
+        raise ValueError(f"rows of {name} are not contiguous")
+    if min(T, H, D) >= 1 and min(token_stride, head_stride) >= 0:
+        size = x.element_size()
+        need = (T - 1) * token_stride + (H - 1) * head_stride + D
+        held = x.untyped_storage().nbytes() // size - x.storage_offset() if given else x.numel()
+        if held < need:
+            raise ValueError(f"{name} holds {held} elements, the shape needs {need}")
+    return x.data_ptr(), token_stride, head_stride
+
+
+def nvfp4_rope_frequencies(R: int, base: float, method="unscaled", factor: float = 1.0, length: float = 0.0,
+                           low: float = 0.0, high: float = 0.0) -> list:
+    """The R / 2 frequencies of the pairs, as a list of floats (float64 on the device for nvfp4_rope)."""
+    f = (ctypes.c_double * max(1, R // 2))()
+    opts = RopeScaling(_METHODS.get(method, method), factor, length, low, high)
+    _done(lib().nvfp4_rope_frequencies(f, R, base, ctypes.byref(opts)), "nvfp4_rope_frequencies")
+    return list(f)
+
+
+def nvfp4_rope(x, out, positions, frequencies, T: int, H: int, D: int, R: int, layout="half", factor: float = 1.0,
+               transpose: bool = False, token_stride: int | None = None, head_stride: int | None = None,
+               out_token_stride: int | None = None, out_head_stride: int | None = None, dtype=None, stream=None) -> None:
+    """Enqueue out = x [T][H][D] with the pairs of each head's first R values turned by
+    positions[t] * frequencies[j] (``transpose``: back, the gradient). Strides in
+    elements, dense by default; out may be x (with x's strides then)."""
+    dt = _dtype_id(x, dtype)
+    px, ts, hs = _rows(x, "x", dt, T, H, D, token_stride, head_stride)
+    if out_token_stride is None and out_head_stride is None and out is x:
+        out_token_stride, out_head_stride = ts, hs
+    po, ots, ohs = _rows(out, "out", dt, T, H, D, out_token_stride, out_head_stride)
+    on = 1 if min(T, R) >= 1 else 0                          # the library reports shape errors itself
+    _done(lib().nvfp4_rope(px, dt, po, _op(positions, on * 8 * T, "positions", _I64),
+                           _op(frequencies, on * 4 * R, "frequencies", _F64), T, H, D, R, ts, hs, ots, ohs,
+                           _LAYOUTS.get(layout, layout), factor, int(transpose), _stream_handle(stream)), "nvfp4_rope")
+
+
+class Nvfp4Cache:
+    """nvfp4_cache_t of device tensors (which it keeps alive): codes uint8 [pages][heads][page_size]
+    [head_size / 2] and scales uint8 [..][head_size / 16] of keys and of values, k_scale and v_scale
+    float32 on the device (None: 1). Page strides in bytes, dense by default; with them the tensors
+    may be views whose pages are dense."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, pages: int, page_size: int, heads: int, head_size: int,
+                 k_scale=None, v_scale=None, code_page_stride: int | None = None, scale_page_stride: int | None = None):
+        self.pages, self.page_size, self.heads, self.head_size = pages, page_size, heads, head_size
+        self.tensors = (k_codes, k_scales, v_codes, v_scales, k_scale, v_scale)
+        row = heads * page_size
+        strides, pointers = [], []
+        for given, each in ((code_page_stride, row * head_size // 2), (scale_page_stride, row * head_size // 16)):
+            strides.append(each if given is None else given)
+        for name, x, stride, given, each in (
+                ("k_codes", k_codes, strides[0], code_page_stride, row * head_size // 2),
+                ("k_scales", k_scales, strides[1], scale_page_stride, row * head_size // 16),
+                ("v_codes", v_codes, strides[0], code_page_stride, row * head_size // 2),
+                ("v_scales", v_scales, strides[1], scale_page_stride, row * head_size // 16)):
+            if given is None or x is None or isinstance(x, int):
+                pointers.append(_op(x, max(0, pages * each), name, _U8))
+                continue
+            if not x.is_cuda:
+                raise ValueError("operands must be device tensors")
+            if str(x.dtype) != _U8:
+                raise ValueError(f"{name} is {x.dtype}, not uint8")
+            need, held = (pages - 1) * stride + each, x.untyped_storage().nbytes() - x.storage_offset()
+            if min(pages, stride) >= 1 and held < need:
+                raise ValueError(f"{name} holds {held} bytes, the shape needs {need}")
+            pointers.append(x.data_ptr())
+        self.struct = CacheStruct(*pointers, _op(k_scale, 4, "k_scale", _F32), _op(v_scale, 4, "v_scale", _F32), pages,
+                                  page_size, heads, head_size, *strides)
+        self._ref = ctypes.byref(self.struct)
+
+
+def nvfp4_cache_write(cache, k, v, slots, T: int, k_strides=None, v_strides=None, dtype=None, stream=None) -> None:
+    """Enqueue the quantisation of k, v [T][heads][head_size] (strides: (token, head) in elements,
+    dense by default) into the cache's rows ``slots`` (int64 [T]; outside the cache: not written)."""
+    dt = _dtype_id(k, dtype)
+    pk, kt, kh = _rows(k, "k", dt, T, cache.heads, cache.head_size, *(k_strides or (None, None)))
+    pv, vt, vh = _rows(v, "v", dt, T, cache.heads, cache.head_size, *(v_strides or (None, None)))
+    _done(lib().nvfp4_cache_write(cache._ref, pk, pv, dt, _op(slots, 8 * max(T, 0), "slots", _I64), T, kt, kh, vt, vh,
+                                  _stream_handle(stream)), "nvfp4_cache_write")
+
+
+def nvfp4_cache_read(cache, k, v, slots, T: int, dtype=None, stream=None) -> None:
+    """Enqueue k, v [T][heads][head_size] = the values of the cache's rows ``slots`` (int64 [T];
+    outside the cache: zeros)."""
+    dt = _dtype_id(k, dtype)
+    pk, _, _ = _rows(k, "k", dt, T, cache.heads, cache.head_size, None, None)
+    pv, _, _ = _rows(v, "v", dt, T, cache.heads, cache.head_size, None, None)
+    _done(lib().nvfp4_cache_read(cache._ref, pk, pv, dt, _op(slots, 8 * max(T, 0), "slots", _I64), T,
+                                 _stream_handle(stream)), "nvfp4_cache_read")
+
+
+def _attention(cache, H, max_q, max_length, scale, causal, window, token_stride, head_stride):
+    if scale is None:
+        scale = max(cache.head_size, 1) ** -0.5
+    return Attention(token_stride, head_stride, max_q, max_length, window, scale, int(causal))
+
+
+def nvfp4_cache_attention_workspace_bytes(cache, dtype, T: int, H: int, B: int, max_q: int, max_length: int) -> int:
+    """Bytes of a workspace for such a call (0: none needed, or a call that is refused); ``dtype`` as q's."""
+    opts = _attention(cache, H, max_q, max_length, None, True, 0, 0, 0)
+    return int(lib().nvfp4_cache_attention_workspace_bytes(cache._ref, _dtype_id(None, dtype), T, H, B,
+                                                           ctypes.byref(opts)))
+
+
+def nvfp4_cache_attention(cache, q, out, offsets, lengths, table, T: int, H: int, B: int, max_q: int, max_length: int,
+                          scale: float | None = None, causal: bool = True, window: int = 0, lse=None, workspace=None,
+                          workspace_bytes: int | None = None, token_stride: int | None = None,
+                          head_stride: int | None = None, table_width: int | None = None, dtype=None,
+                          stream=None) -> None:
+    """Enqueue the attention of q [T][H][head_size] (strides in elements, dense by default): rows
+    offsets[b] .. offsets[b + 1] are the last of the lengths[b] positions of sequence b, which are in
+    the pages table[b] (int32 [B][table_width]; its last dimension by default). scale None:
+    head_size ** -0.5; lse: float32 [T][H]; a (zero-initialised) workspace of
+    nvfp4_cache_attention_workspace_bytes or of NVFP4_WORKSPACE_MAX_BYTES."""
+    D, dt = cache.head_size, _dtype_id(q, dtype)
+    pq, ts, hs = _rows(q, "q", dt, T, H, D, token_stride, head_stride)
+    po, _, _ = _rows(out, "out", dt, T, H, D, None, None)
+    if table_width is None:
+        if isinstance(table, int) or table is None:
+            raise ValueError("raw pointers need table_width=")
+        table_width = table.shape[-1]
+    pw, nw = _workspace(workspace, workspace_bytes)
+    opts = _attention(cache, H, max_q, max_length, scale, causal, window, ts, hs)
+    on = 1 if min(T, H, B, table_width) >= 1 else 0
+    _done(lib().nvfp4_cache_attention(cache._ref, pq, dt, po, _op(lse, on * 4 * T * H, "lse", _F32),
+                                      _op(offsets, on * 4 * (B + 1), "offsets", _I32),
+                                      _op(lengths, on * 4 * B, "lengths", _I32),
+                                      _op(table, on * 4 * B * table_width, "table", _I32), T, H, B, table_width,
+                                      ctypes.byref(opts), pw, nw, _stream_handle(stream)), "nvfp4_cache_attention")
 
 
 def nvfp4_status_string(status: int) -> str:

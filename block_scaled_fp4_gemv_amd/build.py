@@ -14,7 +14,8 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", f) for f in ("nvfp4_gemv.hip", "nvfp4_reblock.hip", "nvfp4_gemm_small_n.hip",
-                                              "nvfp4_quantize.hip", "nvfp4_gemm.hip", "nvfp4_moe.hip")]
+                                              "nvfp4_quantize.hip", "nvfp4_gemm.hip", "nvfp4_moe.hip",
+                                              "nvfp4_rope.hip", "nvfp4_cache.hip", "nvfp4_attention.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libnvfp4gemv.so")
 # the measurement helper (streaming-read reference for the bench): its own library

@@ -1713,6 +1713,8 @@ const char *nvfp4_status_string(int status)
     case NVFP4_ERR_INVALID_STRIDE: return "operand stride out of range or misaligned";
     case NVFP4_ERR_INVALID_TYPE: return "unknown element type";
     case NVFP4_ERR_INVALID_ROUTING: return "router option out of range";
+    case NVFP4_ERR_INVALID_ROTATION: return "rope layout or scaling out of range";
+    case NVFP4_ERR_INVALID_CACHE: return "option of a cache or of attention out of range";
     default: return "unknown status";
     }
 }

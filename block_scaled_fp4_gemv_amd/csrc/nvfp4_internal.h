@@ -17,4 +17,7 @@ __attribute__((visibility("hidden"))) nvfp4_status_t nvfp4_gemv_two_vectors(
     const void *a, const void *b, const void *sfa, const void *sfb, void *c, int64_t M, int64_t K, int64_t L,
     int sf_layout, float alpha, void *stream);
 
+// What every call with a cache checks of it first (null: NVFP4_ERR_NULL_POINTER).
+__attribute__((visibility("hidden"))) nvfp4_status_t nvfp4_check_cache(const nvfp4_cache_t *cache);
+
 #endif

@@ -1,6 +1,7 @@
 /*
  * nvfp4_gemv.h -- C ABI of the MI355X (gfx950) NVFP4 block-scaled batched GEMV,
- * and of the FP4 linear layers and routed experts around it (last part).
+ * of the FP4 linear layers and routed experts around it, and of attention over a
+ * paged NVFP4 key/value cache (last parts).
  *
  * Operation (kernelbot NVFP4 GEMV, submission 103289, `cute_kernel`: each k
  * contributes a * sfa * b * sfb, the contributions of one output row are
@@ -72,7 +73,9 @@ typedef enum {
     NVFP4_ERR_INVALID_SCALE = 7,    /* the global scale alpha is NaN or infinite   */
     NVFP4_ERR_INVALID_STRIDE = 8,   /* an operand stride is out of range or misaligned */
     NVFP4_ERR_INVALID_TYPE = 9,     /* not an nvfp4_dtype_t                       */
-    NVFP4_ERR_INVALID_ROUTING = 10  /* a router option is out of range            */
+    NVFP4_ERR_INVALID_ROUTING = 10, /* a router option is out of range            */
+    NVFP4_ERR_INVALID_ROTATION = 11, /* a rope layout or scaling is out of range   */
+    NVFP4_ERR_INVALID_CACHE = 12    /* a cache's or attention's option is out of range */
 } nvfp4_status_t;
 
 /* Element types of activations, results and logits. */
@@ -512,6 +515,184 @@ nvfp4_status_t nvfp4_gemm_experts(const void *a, const void *b, const void *sfa,
  */
 nvfp4_status_t nvfp4_moe_combine(const void *y, int dtype, const int32_t *ids, const float *weights,
                                  void *out, int64_t T, int64_t k, int64_t M, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Attention over a paged NVFP4 key/value cache. Conventions as in the part
+ * before (device pointers, nothing synchronised, nothing allocated, no state
+ * between calls, every argument validated before any HIP call; the workspace
+ * of nvfp4_cache_attention is one of that part's, with the same rules and the
+ * same largest size). A layer's step, for the q, k and v of T new tokens:
+ * nvfp4_rope on the heads of q and k, nvfp4_cache_write of k and v,
+ * nvfp4_cache_attention of q.
+ */
+
+/*
+ * Rotary positions. Per token t and head, for the R / 2 pairs of the head's
+ * first R values, with a = positions[t] * frequencies[j]:
+ *
+ *   out[i0] = factor * (x[i0] * cos a - x[i1] * sin a)
+ *   out[i1] = factor * (x[i0] * sin a + x[i1] * cos a)
+ *
+ *   layout     NVFP4_ROPE_HALF: i0 = j, i1 = j + R / 2; NVFP4_ROPE_INTERLEAVED:
+ *              i0 = 2 j, i1 = 2 j + 1. Values from R on are copied as they are.
+ *   transpose  1: with -a for a. That is the gradient: the gradient of x is
+ *              nvfp4_rope with transpose = 1 of the gradient of out.
+ *   x, out     dtype (nvfp4_dtype_t) [T][H][D], strides in elements between
+ *              tokens and between heads (x's may be 0; rows of out must not
+ *              overlap); a row contiguous; aligned to their type. out may be x
+ *              with the same strides; else the two do not overlap. The heads of
+ *              q and k in one packed projection are one call.
+ *   positions  int64 [T], frequencies float64 [R / 2], both 8-byte aligned
+ * The angle is exact to 2^-24 while its size is below 2^40 (so are positions
+ * up to 2^40 with frequencies up to 1), cos and sin to 2^-22, the sum is float32
+ * and rounded once to dtype. Requirements: T, H >= 1; 2 <= R <= D, R even, at most 2048;
+ * H, D <= 2^20; factor finite; at most 2^24 - 1 workgroups (about one per token
+ * or more).
+ */
+typedef enum {
+    NVFP4_ROPE_HALF = 0,
+    NVFP4_ROPE_INTERLEAVED = 1
+} nvfp4_rope_layout_t;
+
+nvfp4_status_t nvfp4_rope(const void *x, int dtype, void *out, const int64_t *positions, const double *frequencies,
+                          int64_t T, int64_t H, int64_t D, int64_t R, int64_t x_token_stride, int64_t x_head_stride,
+                          int64_t out_token_stride, int64_t out_head_stride, int layout, float factor, int transpose,
+                          void *stream);
+
+/*
+ * Frequencies for nvfp4_rope, on the HOST (float64 [R / 2], written): f[j] =
+ * base^(-2 j / R), scaled for contexts longer than `length`, the positions that
+ * a model was trained on (scaling NULL: NVFP4_ROPE_UNSCALED):
+ *
+ *   LINEAR  f / factor
+ *   BASE    base * factor^(R / (R - 2)) in place of base
+ *   BANDS   f * keep + f / factor * (1 - keep), keep rising from 0 to 1 with the
+ *           turns length * f / (2 pi) from `low` to `high`, linear in the turns
+ *   RAMP    the same with keep falling from 1 to 0 linearly in j, from the pair
+ *           that turns `high` times (rounded down, at least 0) to the one that
+ *           turns `low` times (rounded up, at most R - 1)
+ * Requirements: R even, 2..2048 (BASE: not 2); base > 1; factor >= 1; BANDS and
+ * RAMP: 0 < low < high, length > 0; all finite.
+ */
+typedef enum {
+    NVFP4_ROPE_UNSCALED = 0,
+    NVFP4_ROPE_LINEAR = 1,
+    NVFP4_ROPE_BASE = 2,
+    NVFP4_ROPE_BANDS = 3,
+    NVFP4_ROPE_RAMP = 4
+} nvfp4_rope_method_t;
+
+typedef struct {
+    int32_t method;                 /* nvfp4_rope_method_t */
+    double factor, length, low, high;
+} nvfp4_rope_scaling_t;
+
+nvfp4_status_t nvfp4_rope_frequencies(double *frequencies, int64_t R, double base,
+                                      const nvfp4_rope_scaling_t *scaling);
+
+/*
+ * A paged key/value cache in NVFP4 (the struct is read on the host, by each call):
+ *
+ *   k_codes, v_codes    uint8 [pages][heads][page_size][head_size / 2]
+ *   k_scales, v_scales  uint8 [pages][heads][page_size][head_size / 16] (E4M3)
+ * A page is dense; code_page_stride and scale_page_stride are the bytes between
+ * pages (of keys and of values alike), so keys and values may share an
+ * allocation. The value of a code is q * s * g with g = *k_scale (*v_scale),
+ * float32 on the device, NULL: 1. The slot of a token is page * page_size + its
+ * place in the page. Requirements: 1 <= pages < 2^31; page_size a power of two,
+ * 16..4096; 1 <= heads <= 4096; head_size a multiple of 32, 32..256; a page's
+ * codes below 2^31 bytes; codes and scales 16-byte aligned, page strides
+ * multiples of 16, at least a page and below 2^40; k_scale, v_scale 4-byte aligned.
+ */
+typedef struct {
+    void *k_codes, *k_scales, *v_codes, *v_scales;
+    const float *k_scale, *v_scale;
+    int64_t pages, page_size, heads, head_size;
+    int64_t code_page_stride, scale_page_stride;
+} nvfp4_cache_t;
+
+/*
+ * Keys and values of T tokens into the cache, quantised as by nvfp4_quantize
+ * with the cache's global scales (blocks of 16 values along the head; a NaN
+ * makes its block's scale NaN):
+ *   k, v    dtype [T][heads][head_size], strides in elements between tokens and
+ *           between heads (>= 0); a row contiguous; aligned to their type
+ *   slots   int64 [T]; a token whose slot is outside the cache (negative, say)
+ *           is not written. Each slot at most once: of two tokens with one slot
+ *           either's blocks may stay.
+ * Nothing else of the cache changes. Requirements: T >= 1; T * heads *
+ * head_size / 16 <= 256 * (2^23 - 1).
+ */
+nvfp4_status_t nvfp4_cache_write(const nvfp4_cache_t *cache, const void *k, const void *v, int dtype,
+                                 const int64_t *slots, int64_t T, int64_t k_token_stride, int64_t k_head_stride,
+                                 int64_t v_token_stride, int64_t v_head_stride, void *stream);
+
+/*
+ * Rows of the cache as values, rounded as by nvfp4_dequantize: k and v dtype
+ * [T][heads][head_size] dense, written; slots as above, in any order and any
+ * number of times; zeros for a slot outside the cache. Requirements as above.
+ */
+nvfp4_status_t nvfp4_cache_read(const nvfp4_cache_t *cache, void *k, void *v, int dtype, const int64_t *slots, int64_t T,
+                                void *stream);
+
+/*
+ * Attention of the queries of B sequences over their pages of the cache. The
+ * queries of sequence b are rows offsets[b] .. offsets[b + 1] of q, n_b of them:
+ * the last n_b of its lengths[b] positions (decoding: 1; drafted tokens: a few;
+ * prompts and their chunks: many; any mixture). Position t is in page
+ * table[b][t / page_size], at place t % page_size. Query head h reads the
+ * cache's head h / (H / heads). For query i of sequence b, at position
+ * p = lengths[b] - n_b + i:
+ *
+ *   logit[t] = scale * q . K[t]      over the positions t that it sees:
+ *              0 <= t < lengths[b]; causal: t <= p; window > 0: t > p - window;
+ *              and the page of t is a page of the cache
+ *   out      = sum_t softmax(logit)[t] * V[t]
+ *   lse      = ln sum_t exp(logit[t])            (float32 [T][H], optional)
+ *
+ * A query that sees nothing gets zeros, and -inf. What it does not see does not
+ * enter, whatever it holds: positions behind a sequence's length, NaN scales of keys or
+ * values that the mask hides. (A NaN scale of a value makes NaN the block of every
+ * query that sees it, whatever its probability.) A query with an infinite or NaN value gets NaN.
+ *
+ *   q        dtype [T][H][head_size], strides in elements between tokens and
+ *            between heads (>= 0); a row contiguous; aligned to its type
+ *   out      dtype [T][H][head_size] dense; aligned to its type; does not overlap
+ *            q. Rows of no sequence (behind offsets[B], say) are not written.
+ *   offsets  int32 [B + 1], rising from 0 to at most T; lengths int32 [B]; table
+ *            int32 [B][table_width]; on the device, where they may change
+ *            between a captured graph's replays. Offsets are clamped to 0..T, lengths to
+ *            0..max_length, and entries of the table outside the cache hide
+ *            their positions: nothing is read or written out of bounds
+ *            whatever they hold.
+ *   max_q, max_length   bounds of the host on n_b and lengths[b], from which
+ *            the grid is planned. Rows behind a sequence's first max_q are not
+ *            written. max_length <= table_width * page_size.
+ * Keys and values are exact in float16 and go to the matrix cores as that; q is
+ * taken to float16 with a power of two of its row's own (float32: as two float16,
+ * 22 bits), probabilities to float16 (float32: two), sums, maxima and norms are
+ * float32, out is rounded once to dtype. The order of summation is fixed for
+ * given arguments and lengths, so equal calls give equal bits.
+ * Requirements: T, B >= 1; T <= 2^30; B * max_q <= 2^30; heads divides H, H / heads
+ * <= 1024; head_size 64, 96, 128, 192 or 256; 1 <= max_q <= T; 1 <= max_length <=
+ * table_width * page_size <= 2^30; scale finite; window >= 0 and below 2^31; at most 2^23 - 1
+ * workgroups.
+ */
+typedef struct {
+    int64_t q_token_stride, q_head_stride;
+    int64_t max_q, max_length;
+    int64_t window;                 /* 0: none */
+    float scale;
+    int32_t causal;                 /* 0 or 1 */
+} nvfp4_attention_t;
+
+size_t nvfp4_cache_attention_workspace_bytes(const nvfp4_cache_t *cache, int dtype, int64_t T, int64_t H, int64_t B,
+                                             const nvfp4_attention_t *attention);
+nvfp4_status_t nvfp4_cache_attention(const nvfp4_cache_t *cache, const void *q, int dtype, void *out, float *lse,
+                                     const int32_t *offsets, const int32_t *lengths, const int32_t *table, int64_t T,
+                                     int64_t H, int64_t B, int64_t table_width, const nvfp4_attention_t *attention,
+                                     void *workspace, size_t workspace_bytes, void *stream);
 
 /* Static description of a status code (never NULL). */
 const char *nvfp4_status_string(int status);

@@ -14,6 +14,7 @@
 #include "nvfp4_device.h"
 #include "nvfp4_gemv.h"
 #include "nvfp4_internal.h"
+#include "nvfp4_lds.h"
 
 namespace {
 
@@ -30,6 +31,11 @@ struct AttParams {
     int64_t code_page, scale_page;
     int32_t T, H, B, width, pages, shift, heads, G, D;
     int32_t max_q, max_length, window, causal, dtype;
+    int32_t splits, chunk;                      // of a sequence's positions; chunk in tiles of 64
+    int32_t few_rows;                           // sequences of so many rows are the rows kernel's
+    int32_t most_rows;                          // of a partial result
+    uint32_t *tickets;
+    float *sums, *norms;                        // partial results: [tile][split][most_rows][D], [..][2]
     float scale;
 };
 
@@ -66,7 +72,7 @@ __global__ __launch_bounds__(64) void nvfp4_attention_simple_kernel(AttParams p)
     const int h = (int)(blockIdx.x % (uint32_t)p.H), i = (int)(blockIdx.x / (uint32_t)p.H % (uint32_t)p.max_q),
               b = (int)(blockIdx.x / (uint32_t)p.H / (uint32_t)p.max_q);
     const Sequence s = sequence_of(p, b);
-    if (i >= s.n)
+    if (i >= s.n || (int64_t)min(s.n, p.max_q) * p.G <= p.few_rows)
         return;
     const int32_t pos = s.length - s.n + i;
     const int32_t end = p.causal ? min(s.length, pos + 1) : s.length;
@@ -121,7 +127,604 @@ __global__ __launch_bounds__(64) void nvfp4_attention_simple_kernel(AttParams p)
         p.lse[row] = !any ? -__builtin_inff() : finite ? top + logf(sum) : __builtin_nanf("");
 }
 
+// ------------------------------------------------------------------ rows kernel
+
+typedef float float4_t __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+// Probabilities are kept times 2^12, the largest at 4096: float16 then holds them to 2^-26
+// of the largest as normal numbers.
+constexpr float kShift = 12.0f;
+constexpr int kRowsThreads = 256, kRowsWaves = 4;
+constexpr int kMaxSplits = 64, kRowsTarget = 2048;
+
+// The head's D values go through the matrix instruction in steps of 32. A lane (row
+// lane % 16, g = lane / 16) has 8 of a step's; which 8 is free while q and K agree: runs
+// of 128 (64, 32) values are cut into 4 pieces of 16 (8, 4) bytes of codes, piece g the
+// lane's, so it reads its codes in one. Value of K step f and lane group g: base + mult * g + add.
+template <int D>
+struct Steps {
+    static constexpr int N = D / 32, n128 = D / 128, n64 = D % 128 / 64, n32 = D % 64 / 32;
+    static constexpr int base(int f) { return f < 4 * n128 ? f / 4 * 128 : f < 4 * n128 + 2 * n64 ? n128 * 128 : n128 * 128 + n64 * 64; }
+    static constexpr int mult(int f) { return f < 4 * n128 ? 32 : f < 4 * n128 + 2 * n64 ? 16 : 8; }
+    static constexpr int add(int f) { return f < 4 * n128 ? f % 4 * 8 : f < 4 * n128 + 2 * n64 ? (f - 4 * n128) * 8 : 0; }
+};
+
+// A tile of 64 positions in LDS: codes of K and of V, their scales, each of 4 subtiles
+// of 16 positions (a page holds whole subtiles).
+template <int D>
+struct RowsTile {
+    static constexpr int RB = D / 2, SB = D / 16, NB = D / 16;     // bytes of a row's codes, of its scales; blocks
+    static constexpr int kCopies16 = (16 * RB + 1023) / 1024;      // 16-byte copies of a wave per subtile
+    static constexpr int kOffV = 64 * RB, kOffKs = 2 * 64 * RB, kOffVs = kOffKs + 64 * SB, kStage = kOffVs + 64 * SB;
+    static constexpr int kCopies = 4 * (2 * kCopies16 + 2);        // of a wave per tile
+    static constexpr int kScales = NB * 64 * 2;                    // V's scales as float16 [block][64]
+    static constexpr int kStages = 2;
+    static constexpr int kWave = kStages * kStage + kScales;
+    // Places of a row's 16-byte pieces, so that the lanes that read at once meet every bank:
+    // 16 neighbouring rows for K, for V four rows of each subtile.
+    __device__ static constexpr int swizzle_k(int r)
+    {
+        return D == 64 || D == 192 ? r / 8 & 1 : D == 128 ? r / 4 & 3 : D == 256 ? r / 2 & 7 : 0;
+    }
+    __device__ static constexpr int swizzle_v(int r)
+    {
+        return D == 64 || D == 192 ? r / 16 & 1 : D == 128 ? r / 16 & 3 : D == 256 ? (r / 16 * 2 + r % 4 / 2) & 7 : 0;
+    }
+};
+
+// 8 neighbouring values of q as float32
+__device__ __attribute__((always_inline)) inline void load8(const uint8_t *x, int dtype, float (&v)[8])
+{
+    if (dtype == NVFP4_F32) {
+        __builtin_memcpy(v, x, 32);
+        return;
+    }
+    uint32_t w[4];
+    __builtin_memcpy(w, x, 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (dtype == NVFP4_BF16) {
+            v[2 * e] = __builtin_bit_cast(float, w[e] << 16);
+            v[2 * e + 1] = __builtin_bit_cast(float, w[e] & 0xFFFF0000u);
+        } else {
+            v[2 * e] = (float)as_h2(w[e]).x;
+            v[2 * e + 1] = (float)as_h2(w[e]).y;
+        }
+    }
+}
+
+// A row of q as float16 times 2^e, the largest value in [2^14, 2^15): bfloat16 and float16
+// rows are exact so (below 2^-29 of the largest to 2^-40 of it), of float32 ones the second part
+// holds what the first leaves. Returns the logits' factor of the row, NaN if a value is not finite.
+template <int N, int PARTS>
+struct QRow {
+    half8_t part[PARTS][N];
+};
+
+__device__ __attribute__((always_inline)) inline int row_exponent(float top)
+{
+    return top > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
+}
+
+template <int N, int PARTS>
+__device__ __attribute__((always_inline)) inline void to_parts(const float (&v)[8], int e, QRow<N, PARTS> &q, int f)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float x = __builtin_ldexpf(v[j], e);
+        const _Float16 high = (_Float16)x;
+        q.part[0][f][j] = high;
+        if constexpr (PARTS == 2)
+            q.part[1][f][j] = (_Float16)(x - (float)high);
+    }
+}
+
+// Results of one tile of rows, joined over W lots (waves, or splits): weights of
+// the lots by their maxima (log2, -inf where a lot saw nothing), and the norm.
+struct Norm {
+    float top, sum;
+};
+
+__device__ __attribute__((always_inline)) inline float weight_of(float top, float above)
+{
+    return top == -__builtin_inff() ? (above == -__builtin_inff() ? 1.0f : 0.0f) : __builtin_amdgcn_exp2f(top - above);
+}
+
+// Row r of a sequence's (head, queries): its place among the T * H rows of out.
+__device__ __attribute__((always_inline)) inline int64_t out_row(const AttParams &p, const Sequence &s, int hk, int r)
+{
+    return (int64_t)(s.first + r / p.G) * p.H + hk * p.G + r % p.G;
+}
+
+// N (2 or 4) neighbouring values of a row, divided by the norm and scaled; a row that saw nothing is zero.
+template <int N>
+__device__ __attribute__((always_inline)) inline void store_values(const AttParams &p, int64_t at, const float (&x)[N], float sum, float gv)
+{
+    const float f = sum == 0.0f ? 0.0f : gv / sum;
+    float v[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        v[e] = sum == 0.0f ? 0.0f : x[e] * f;
+    if (p.dtype == NVFP4_F32) {
+        __builtin_memcpy((float *)p.out + at, v, 4 * N);
+        return;
+    }
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e)
+        w[e] = p.dtype == NVFP4_BF16 ? bf16_bits(v[2 * e]) | bf16_bits(v[2 * e + 1]) << 16
+                                     : (uint32_t)f16_bits(v[2 * e]) | (uint32_t)f16_bits(v[2 * e + 1]) << 16;
+    __builtin_memcpy((uint16_t *)p.out + at, w, 2 * N);
+}
+
+__device__ __attribute__((always_inline)) inline void store_lse(const AttParams &p, int64_t row, Norm n)
+{
+    if (p.lse)
+        p.lse[row] = n.sum == 0.0f ? -__builtin_inff() : kLn2 * (n.top - kShift + __builtin_amdgcn_logf(n.sum));
+}
+
+// Partial results, two values at a time, past the caches that the XCDs do not share.
+typedef float float2_u __attribute__((ext_vector_type(2)));
+
+__device__ __attribute__((always_inline)) inline void store_partial(float *to, float2_u v)
+{
+    __hip_atomic_store((uint64_t *)to, __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __attribute__((always_inline)) inline float2_u load_partial(const float *from)
+{
+    return __builtin_bit_cast(float2_u, __hip_atomic_load((const uint64_t *)from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+}
+
+// Takes the tile's ticket after this workgroup's partial results; true for the last of
+// its `splits` workgroups, which clears the ticket. All threads call it.
+__device__ __attribute__((always_inline)) inline bool last_of_splits(const AttParams &p, uint32_t tile, int splits, uint32_t *s_ticket)
+{
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");          // this wave's partial results are out
+    __syncthreads();
+    if (threadIdx.x == 0)
+        *s_ticket = __hip_atomic_fetch_add(&p.tickets[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (*s_ticket != (uint32_t)splits - 1)
+        return false;
+    if (threadIdx.x == 0)
+        __hip_atomic_store(&p.tickets[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return true;
+}
+
+// Adds the splits' partial results of a tile's rows in the order of the splits and stores
+// them, 8 splits' loads in flight. `norms`: LDS for [splits][rows] of them.
+template <int D, int THREADS>
+__device__ __attribute__((always_inline)) inline void join_splits(const AttParams &p, const Sequence &s, int hk, uint32_t tile,
+                                                                  int row0, int rows, int splits, float gv, Norm *norms)
+{
+    constexpr int AHEAD = 8;
+    const float *sums = p.sums + (int64_t)tile * p.splits * p.most_rows * D;
+    const float *from = p.norms + (int64_t)tile * p.splits * p.most_rows * 2;
+    for (int i = (int)threadIdx.x; i < splits * rows; i += THREADS) {
+        const float2_u n = load_partial(from + (i / rows * p.most_rows + i % rows) * 2);
+        norms[i] = {n.x, n.y};
+    }
+    __syncthreads();
+    for (int u = (int)threadIdx.x; u < rows * (D / 2); u += THREADS) {
+        const int r = u / (D / 2), d = u % (D / 2) * 2;
+        Norm n{-__builtin_inff(), 0.0f};
+        for (int k = 0; k < splits; ++k)
+            n.top = fmaxf(n.top, norms[k * rows + r].top);
+        float2_u v = {0.0f, 0.0f};
+        for (int k0 = 0; k0 < splits; k0 += AHEAD) {
+            float2_u x[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                x[k] = load_partial(sums + ((int64_t)min(k0 + k, splits - 1) * p.most_rows + r) * D + d);
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                if (k0 + k < splits) {
+                    const Norm one = norms[(k0 + k) * rows + r];
+                    const float w = weight_of(one.top, n.top);
+                    n.sum += one.sum * w;
+                    v.x += x[k].x * w;
+                    v.y += x[k].y * w;
+                }
+        }
+        const int64_t row = out_row(p, s, hk, row0 + r);
+        store_values<2>(p, row * D + d, {v.x, v.y}, n.sum, gv);
+        if (d == 0)
+            store_lse(p, row, n);
+    }
+}
+
+// largest (sum) over the lanes of one row: l, l ^ 16, l ^ 32, l ^ 48
+__device__ __attribute__((always_inline)) inline float max_of_row(float v)
+{
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+
+// Which of a sequence's positions a workgroup takes: tiles of 64 from `lo` on.
+struct Span {
+    int32_t lo, hi;                             // visible to some row of the tile
+    int32_t first, end;                         // tiles of this workgroup, counted from lo / 64
+    int32_t splits;                             // that take part
+};
+
+// Rows of queries tok0 .. tok1 - 1.
+__device__ __attribute__((always_inline)) inline Span span_of(const AttParams &p, const Sequence &s, int tok0, int tok1, int split)
+{
+    Span v;
+    v.hi = p.causal ? max(0, min(s.length, s.length - s.n + tok1)) : s.length;
+    v.lo = p.window ? max(0, s.length - s.n + tok0 - p.window + 1) : 0;
+    const int32_t tiles = v.hi > v.lo ? (v.hi - v.lo / 64 * 64 + 63) / 64 : 0;
+    const int32_t chunk = max(p.chunk, (tiles + p.splits - 1) / p.splits);
+    v.splits = max(1, (tiles + chunk - 1) / chunk);
+    v.first = min(tiles, split * chunk);
+    v.end = min(tiles, v.first + chunk);
+    return v;
+}
+
+// This wave's reads and writes of LDS are done, for all its lanes; its copies are, but the last N.
+__device__ __attribute__((always_inline)) inline void settle()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+template <int N>
+__device__ __attribute__((always_inline)) inline void landed()
+{
+    wait_copies<N>();
+    asm volatile("" : : : "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Few rows: n queries times the heads that share a key head, at most 16 * NQ. Every wave
+// takes tiles of 64 positions in turn, with a ring of its own in LDS that copies fill while
+// it works on the tile before.
+//   S^T = K Q^T by 16 x 16 x 32 products, K the first operand: a lane then has the logits
+//     of one row (lane % 16), positions 16 a + 4 g + b in register b of subtile a.
+//   O^T = V^T P^T: a lane's P registers are its k-range as they stand, if V's operand has the same
+//     order. Its codes come from LDS transposed (16 positions of one value per
+//     lane), so a pair of codes is two positions, and so is a pair of scales.
+template <int D, int NQ, bool F32>
+__global__ __launch_bounds__(kRowsThreads) void nvfp4_attention_rows_kernel(AttParams p)
+{
+    using S = RowsTile<D>;
+    using St = Steps<D>;
+    constexpr int PARTS = F32 ? 2 : 1, NB = S::NB;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    __shared__ uint32_t s_ticket;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64), lane = (int)threadIdx.x % 64;
+    const int i = lane % 16, g = lane / 16;
+    const uint32_t tile = blockIdx.x / (uint32_t)p.splits;
+    const int split = (int)(blockIdx.x % (uint32_t)p.splits);
+    const int b = (int)(tile / (uint32_t)p.heads), hk = (int)(tile % (uint32_t)p.heads);
+    const Sequence s = sequence_of(p, b);
+    const int queries = min(s.n, p.max_q);
+    if (queries == 0 || queries > 16 * NQ || queries * p.G > 16 * NQ)
+        return;
+    const int rows = queries * p.G;
+    const Span span = span_of(p, s, 0, queries, split);
+    if (split >= span.splits)
+        return;
+
+    // --- this lane's rows of q
+    const float factor = p.scale * (p.gk ? *p.gk : 1.0f) * kLog2e;
+    QRow<St::N, PARTS> q[NQ];
+    float rf[NQ];
+    int32_t begin[NQ], end[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        const int r = 16 * n + i, tok = r / p.G, pos = s.length - s.n + tok;
+        const bool real = r < rows;
+        end[n] = p.causal ? min(s.length, pos + 1) : s.length;
+        begin[n] = p.window ? max(0, pos - p.window + 1) : 0;
+        const uint8_t *x = p.q + (int64_t)(s.first + (real ? tok : 0)) * p.q_token +
+                           (int64_t)(hk * p.G + (real ? r % p.G : 0)) * p.q_head;
+        float v[St::N][8], top = 0.0f;
+        bool finite = true;
+#pragma unroll
+        for (int f = 0; f < St::N; ++f) {
+            load8(x + (St::base(f) + St::mult(f) * g + St::add(f)) * (F32 ? 4 : 2), F32 ? NVFP4_F32 : p.dtype, v[f]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool good = __builtin_isfinite(v[f][j]);
+                finite &= good;
+                v[f][j] = good ? v[f][j] : 0.0f;
+                top = fmaxf(top, fabsf(v[f][j]));
+            }
+        }
+        top = max_of_row(top);
+        finite = max_of_row(finite ? 0.0f : 1.0f) == 0.0f;
+        const int e = row_exponent(top);
+#pragma unroll
+        for (int f = 0; f < St::N; ++f)
+            to_parts(v[f], e, q[n], f);
+        rf[n] = !real ? 0.0f : finite ? __builtin_ldexpf(factor, -e) : __builtin_nanf("");
+    }
+    // positions that all rows see: no mask within them
+    const int32_t all_from = p.window ? max(0, s.length - s.n + queries - p.window) : 0;
+    const int32_t all_to = p.causal ? min(s.length, s.length - s.n + 1) : s.length;
+
+    float4_t acc[NQ][NB];
+    float top[NQ], sum[NQ];
+    uint32_t nan_blocks[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        top[n] = -__builtin_inff();
+        sum[n] = 0.0f;
+        nan_blocks[n] = 0u;
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+            acc[n][k] = {0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    // --- copies. Lane offsets of a subtile's codes within its rows.
+    uint8_t *const ring = lds + wave * S::kWave;
+    const uint32_t ring_at = (uint32_t)(uintptr_t)ring;
+    uint32_t at_row[S::kCopies16], at_piece[S::kCopies16];
+#pragma unroll
+    for (int c = 0; c < S::kCopies16; ++c) {
+        const int o = c * 1024 + lane * 16;
+        at_row[c] = (uint32_t)(o / S::RB), at_piece[c] = (uint32_t)(o % S::RB / 16);
+    }
+    const int32_t mask = (1 << p.shift) - 1;
+    const int32_t first_position = span.lo / 64 * 64;
+    auto entries = [&](int32_t n, int32_t (&e)[4]) {
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            const int32_t t = first_position + n * 64 + a * 16;
+            e[a] = n < span.end && t < span.hi ? p.table[(int64_t)b * p.width + (t >> p.shift)] : -1;
+        }
+    };
+    // A subtile that is not there is copied from the cache's first page, so that every
+    // tile has the same number of copies; its bit is 0.
+    auto issue = [&](int32_t n, const int32_t (&e)[4], int stage) -> uint32_t {
+        uint32_t there = 0u;
+        const uint32_t to = ring_at + stage * S::kStage;
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            const bool ok = (uint32_t)e[a] < (uint32_t)p.pages;
+            there |= (uint32_t)ok << a;
+            const int64_t page = ok ? e[a] : 0;
+            const int64_t row = ((int64_t)hk << p.shift) + ((first_position + n * 64 + a * 16) & mask);
+            const int64_t codes = page * p.code_page + row * S::RB, scales = page * p.scale_page + row * S::SB;
+#pragma unroll
+            for (int c = 0; c < S::kCopies16; ++c) {
+                const uint32_t r = at_row[c];
+                if (c * 1024 + lane * 16 < 16 * S::RB) {
+                    copy16_s(p.kc + codes, r * S::RB + (at_piece[c] ^ (uint32_t)S::swizzle_k((int)r)) * 16, to + a * 16 * S::RB + c * 1024);
+                    copy16_s(p.vc + codes, r * S::RB + (at_piece[c] ^ (uint32_t)S::swizzle_v(16 * a + (int)r)) * 16,
+                           to + S::kOffV + a * 16 * S::RB + c * 1024);
+                }
+            }
+            if (lane < 4 * S::SB) {
+                copy4_s(p.ks + scales, (uint32_t)lane * 4, to + S::kOffKs + a * 16 * S::SB);
+                copy4_s(p.vs + scales, (uint32_t)lane * 4, to + S::kOffVs + a * 16 * S::SB);
+            }
+        }
+        return there;
+    };
+
+    auto compute = [&](int32_t n, uint32_t there, const uint8_t *tile_at) {
+        const int32_t t0 = first_position + n * 64;
+        // --- S^T
+        float logit[NQ][4][4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            float4_t c[NQ];
+#pragma unroll
+            for (int m = 0; m < NQ; ++m)
+                c[m] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const uint8_t *row = tile_at + (16 * a + i) * S::RB, *sc = tile_at + S::kOffKs + (16 * a + i) * S::SB;
+            const int sw = S::swizzle_k(i);
+            auto step = [&](int f, uint32_t w, half2_t s2) {
+                const half8_t k8 = decode8(w, s2);
+#pragma unroll
+                for (int m = 0; m < NQ; ++m)
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part)
+                        c[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, q[m].part[part][f], c[m], 0, 0, 0);
+            };
+#pragma unroll
+            for (int x = 0; x < St::n128; ++x) {
+                const uint4_t w = *(const uint4_t *)(row + (((4 * x + g) ^ sw) * 16));
+                const half2_t both = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)*(const uint16_t *)(sc + 8 * x + 2 * g), 1.0f, false);
+                const half2_t s0 = {both.x, both.x}, s1 = {both.y, both.y};
+                step(4 * x, w.x, s0);
+                step(4 * x + 1, w.y, s0);
+                step(4 * x + 2, w.z, s1);
+                step(4 * x + 3, w.w, s1);
+            }
+            if constexpr (St::n64 != 0) {
+                const int u = St::n128 * 8 + g;                                // 8-byte units of the row
+                const uint2_t w = *(const uint2_t *)(row + (((u / 2) ^ sw) * 16 + u % 2 * 8));
+                const half2_t both = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)sc[St::n128 * 8 + g], 1.0f, false);
+                const half2_t s0 = {both.x, both.x};
+                step(4 * St::n128, w.x, s0);
+                step(4 * St::n128 + 1, w.y, s0);
+            }
+            if constexpr (St::n32 != 0) {
+                const int u = St::n128 * 16 + St::n64 * 8 + g;                  // 4-byte units
+                const uint32_t w = *(const uint32_t *)(row + (((u / 4) ^ sw) * 16 + u % 4 * 4));
+                const half2_t both = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)sc[St::n128 * 8 + St::n64 * 4 + g / 2], 1.0f, false);
+                const half2_t s0 = {both.x, both.x};
+                step(St::N - 1, w, s0);
+            }
+#pragma unroll
+            for (int m = 0; m < NQ; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    logit[m][a][e] = c[m][e] * rf[m];
+        }
+        if (there != 15u || t0 < all_from || t0 + 64 > all_to) {
+#pragma unroll
+            for (int m = 0; m < NQ; ++m)
+#pragma unroll
+                for (int a = 0; a < 4; ++a)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int32_t t = t0 + 16 * a + 4 * g + e;
+                        if (!(there >> a & 1u) || t < begin[m] || t >= end[m])
+                            logit[m][a][e] = -__builtin_inff();
+                    }
+        }
+        // --- V's scales as float16 in the order of the k-ranges; a position that no row sees gets 0,
+        // and so does a NaN, which is noted for the rows that see it. A lane has one position.
+        {
+            const int32_t t = t0 + lane;
+            const bool seen = (there >> (lane / 16) & 1u) && t >= span.lo && t < span.hi;
+            const uint8_t *sc = tile_at + S::kOffVs + lane * S::SB;
+            _Float16 *to = (_Float16 *)(ring + S::kStages * S::kStage) + (lane / 4 % 4) * 16 + lane / 16 * 4 + lane % 4;
+            uint32_t nan = 0u;
+#pragma unroll
+            for (int k = 0; k < NB; k += 2) {
+                const uint32_t two = *(const uint16_t *)(sc + k);
+                half2_t h = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(two, 1.0f, false);
+                nan |= (uint32_t)((two & 0x7Fu) == 0x7Fu) << k | (uint32_t)((two & 0x7F00u) == 0x7F00u) << (k + 1);
+                h.x = seen && (two & 0x7Fu) != 0x7Fu ? h.x : (_Float16)0.0f;
+                h.y = seen && (two & 0x7F00u) != 0x7F00u ? h.y : (_Float16)0.0f;
+                to[k * 64] = h.x;
+                to[k * 64 + 64] = h.y;
+            }
+            uint64_t left = __ballot(seen && nan);
+            while (left) {
+                const int k = __builtin_ctzll(left);
+                left &= left - 1;
+                const uint32_t blocks = (uint32_t)__builtin_amdgcn_readlane((int)nan, k);
+#pragma unroll
+                for (int m = 0; m < NQ; ++m)
+                    if (t0 + k >= begin[m] && t0 + k < end[m])
+                        nan_blocks[m] |= blocks;
+            }
+        }
+        settle();                                                       // the scales are in place
+        // --- softmax
+        half8_t prob[PARTS][NQ][2];
+#pragma unroll
+        for (int m = 0; m < NQ; ++m) {
+            float most = logit[m][0][0];
+#pragma unroll
+            for (int k = 1; k < 16; ++k)
+                most = fmaxf(most, logit[m][k / 4][k % 4]);
+            most = fmaxf(top[m], max_of_row(most));
+            if (__ballot(most > top[m])) {
+                const float keep = weight_of(top[m], most);
+                sum[m] *= keep;
+#pragma unroll
+                for (int k = 0; k < NB; ++k)
+                    acc[m][k] *= keep;
+                top[m] = most;
+            }
+            const float from = (most == -__builtin_inff() ? 0.0f : most) - kShift;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float w = __builtin_amdgcn_exp2f(logit[m][k / 4][k % 4] - from);
+                sum[m] += w;
+                const _Float16 high = (_Float16)w;
+                prob[0][m][k / 8][k % 8] = high;
+                if constexpr (PARTS == 2)
+                    prob[PARTS - 1][m][k / 8][k % 8] = (_Float16)(w - (float)high);
+            }
+        }
+        // --- O^T
+        const int vr = 16 * (i / 4) + 4 * g + i % 4;
+        const uint8_t *row = tile_at + S::kOffV + vr * S::RB;
+        const int sw = S::swizzle_v(vr);
+        const uint8_t *sc = ring + S::kStages * S::kStage + g * 32;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            const uint2_t w = read_transposed4(row + ((k / 2) ^ sw) * 16 + k % 2 * 8);
+            const uint4_t a0 = *(const uint4_t *)(sc + k * 128), a1 = *(const uint4_t *)(sc + k * 128 + 16);
+            const half8_t v0 = decode8_by(w.x, a0), v1 = decode8_by(w.y, a1);
+#pragma unroll
+            for (int m = 0; m < NQ; ++m)
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part) {
+                    acc[m][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, prob[part][m][0], acc[m][k], 0, 0, 0);
+                    acc[m][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, prob[part][m][1], acc[m][k], 0, 0, 0);
+                }
+        }
+    };
+
+    // --- the loop: tile n's copies are awaited while those of the next are out
+    int32_t n = span.first + wave;
+    if (n < span.end) {
+        int32_t e[4];
+        entries(n, e);
+        uint32_t there = issue(n, e, 0);
+        entries(n + kRowsWaves, e);
+        int stage = 0;
+        for (; n + kRowsWaves < span.end; n += kRowsWaves) {
+            const uint32_t next = issue(n + kRowsWaves, e, stage ^ 1);
+            entries(n + 2 * kRowsWaves, e);
+            landed<S::kCopies>();
+            compute(n, there, ring + stage * S::kStage);
+            settle();                                                   // this stage is read: the next round refills it
+            there = next;
+            stage ^= 1;
+        }
+        landed<0>();
+        compute(n, there, ring + stage * S::kStage);
+    }
+
+    // --- the waves' results through LDS: sums [wave][16 NQ][D], norms
+    __syncthreads();                                                   // every ring is read
+    float *const w_sums = (float *)lds;
+    Norm *const w_norms = (Norm *)(lds + kRowsWaves * 16 * NQ * D * 4);
+#pragma unroll
+    for (int m = 0; m < NQ; ++m) {
+        sum[m] += __shfl_xor(sum[m], 16);
+        sum[m] += __shfl_xor(sum[m], 32);
+        const int r = wave * 16 * NQ + 16 * m + i;
+        if (g == 0)
+            w_norms[r] = {top[m], sum[m]};
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            float4_t v = acc[m][k];
+            if (nan_blocks[m] >> k & 1u)
+                v = {__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
+            *(float4_t *)(w_sums + r * D + 16 * k + 4 * g) = v;
+        }
+    }
+    __syncthreads();
+    const float gv = p.gv ? *p.gv : 1.0f;
+    float *const sums = p.sums + ((int64_t)tile * p.splits + split) * p.most_rows * D;
+    float *const norms = p.norms + ((int64_t)tile * p.splits + split) * p.most_rows * 2;
+    for (int u = (int)threadIdx.x; u < rows * (D / 4); u += kRowsThreads) {
+        const int r = u / (D / 4), d = u % (D / 4) * 4;
+        Norm all{-__builtin_inff(), 0.0f};
+#pragma unroll
+        for (int w = 0; w < kRowsWaves; ++w)
+            all.top = fmaxf(all.top, w_norms[w * 16 * NQ + r].top);
+        float4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < kRowsWaves; ++w) {
+            const Norm one = w_norms[w * 16 * NQ + r];
+            const float part = weight_of(one.top, all.top);
+            all.sum += one.sum * part;
+            v += *(const float4_t *)(w_sums + (w * 16 * NQ + r) * D + d) * part;
+        }
+        if (span.splits == 1) {
+            const int64_t row = out_row(p, s, hk, r);
+            store_values<4>(p, row * D + d, {v.x, v.y, v.z, v.w}, all.sum, gv);
+            if (d == 0)
+                store_lse(p, row, all);
+            continue;
+        }
+        store_partial(sums + r * D + d, (float2_u){v.x, v.y});
+        store_partial(sums + r * D + d + 2, (float2_u){v.z, v.w});
+        if (d == 0)
+            store_partial(norms + r * 2, (float2_u){all.top, all.sum});
+    }
+    if (span.splits == 1 || !last_of_splits(p, tile, span.splits, &s_ticket))
+        return;
+    join_splits<D, kRowsThreads>(p, s, hk, tile, 0, rows, span.splits, gv, (Norm *)lds);
+}
+
 // ------------------------------------------------------------------ host
+
+constexpr int64_t kTicketBytes = 65536, kMaxPartialBytes = INT64_C(64) << 20;
+constexpr int64_t kMaxTickets = kTicketBytes / 4;
+static_assert(kTicketBytes + kMaxPartialBytes == NVFP4_WORKSPACE_MAX_BYTES);
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
@@ -150,6 +753,71 @@ nvfp4_status_t check(const nvfp4_cache_t *cache, int dtype, int64_t T, int64_t H
     return NVFP4_OK;
 }
 
+// How the positions are shared out: `tiles` workgroups if none were split.
+struct Plan {
+    int64_t tiles;
+    int32_t splits, chunk, most_rows;
+    size_t bytes;                               // of workspace
+};
+
+int64_t partial_bytes(int64_t tiles, int64_t splits, int64_t rows, int64_t D)
+{
+    return tiles * splits * rows * (D + 2) * 4;
+}
+
+Plan rows_plan(const nvfp4_cache_t &c, int64_t H, int64_t B, const nvfp4_attention_t &a)
+{
+    Plan p{};
+    const int64_t G = H / c.heads;
+    p.tiles = B * c.heads;
+    p.most_rows = (int32_t)std::min<int64_t>(32, a.max_q * G);
+    // most tiles of 64 positions that a sequence's rows see
+    const int64_t span = a.window ? std::min<int64_t>(a.max_length, a.window + std::min<int64_t>(a.max_q, 32) + 64) : a.max_length;
+    const int64_t most = (span + 63) / 64 + 1;
+    int64_t splits = std::min<int64_t>((kRowsTarget + p.tiles - 1) / p.tiles, (most + kRowsWaves - 1) / kRowsWaves);
+    splits = std::max<int64_t>(1, std::min<int64_t>(splits, kMaxSplits));
+    if (p.tiles > kMaxTickets)
+        splits = 1;
+    while (splits > 1 && partial_bytes(p.tiles, splits, p.most_rows, c.head_size) > kMaxPartialBytes)
+        --splits;
+    p.chunk = (int32_t)((most + splits - 1) / splits + kRowsWaves - 1) / kRowsWaves * kRowsWaves;
+    p.splits = (int32_t)((most + p.chunk - 1) / p.chunk);
+    p.bytes = p.splits > 1 ? kTicketBytes + (partial_bytes(p.tiles, p.splits, p.most_rows, c.head_size) + 255) / 256 * 256 : 0;
+    return p;
+}
+
+template <int D, int NQ, bool F32>
+hipError_t launch_rows(const AttParams &p, int64_t grid, hipStream_t st)
+{
+    using S = RowsTile<D>;
+    const int lds = std::max({kRowsWaves * S::kWave, kRowsWaves * 16 * NQ * (D * 4 + 8), p.splits * p.most_rows * 8});
+    static_assert(kRowsWaves * S::kWave + 64 <= 160 * 1024 && kRowsWaves * 16 * NQ * (D * 4 + 8) + 64 <= 160 * 1024 && kMaxSplits * 32 * 8 < 64 * 1024);
+    auto kern = nvfp4_attention_rows_kernel<D, NQ, F32>;
+    hipLaunchKernelGGL(kern, dim3((uint32_t)grid), dim3(kRowsThreads), lds, st, p);
+    return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_rows_of(const AttParams &p, int64_t grid, hipStream_t st)
+{
+    const bool f32 = p.dtype == NVFP4_F32;
+    if (p.few_rows == 16)
+        return f32 ? launch_rows<D, 1, true>(p, grid, st) : launch_rows<D, 1, false>(p, grid, st);
+    return f32 ? launch_rows<D, 2, true>(p, grid, st) : launch_rows<D, 2, false>(p, grid, st);
+}
+
+template <typename F>
+hipError_t by_head(int D, F f)
+{
+    switch (D) {
+    case 64: return f(std::integral_constant<int, 64>{});
+    case 96: return f(std::integral_constant<int, 96>{});
+    case 128: return f(std::integral_constant<int, 128>{});
+    case 192: return f(std::integral_constant<int, 192>{});
+    default: return f(std::integral_constant<int, 256>{});
+    }
+}
+
 } // namespace
 
 extern "C" {
@@ -157,7 +825,9 @@ extern "C" {
 size_t nvfp4_cache_attention_workspace_bytes(const nvfp4_cache_t *cache, int dtype, int64_t T, int64_t H, int64_t B,
                                              const nvfp4_attention_t *attention)
 {
-    return 0;
+    if (check(cache, dtype, T, H, B, attention) != NVFP4_OK)
+        return 0;
+    return rows_plan(*cache, H, B, *attention).bytes;
 }
 
 nvfp4_status_t nvfp4_cache_attention(const nvfp4_cache_t *cache, const void *q, int dtype, void *out, float *lse,
@@ -189,12 +859,27 @@ nvfp4_status_t nvfp4_cache_attention(const nvfp4_cache_t *cache, const void *q, 
     p.shift = __builtin_ctzll((uint64_t)cache->page_size);
     p.heads = (int32_t)cache->heads, p.G = (int32_t)(H / cache->heads), p.D = (int32_t)cache->head_size;
     p.max_q = (int32_t)attention->max_q, p.max_length = (int32_t)attention->max_length;
-    p.window = (int32_t)attention->window, p.causal = attention->causal, p.dtype = dtype, p.scale = attention->scale;
-    if (B * attention->max_q > kMaxGrid / H)
+    // a window as long as the longest sequence hides nothing
+    p.window = attention->window >= attention->max_length ? 0 : (int32_t)attention->window, p.causal = attention->causal, p.dtype = dtype, p.scale = attention->scale;
+    const Plan plan = rows_plan(*cache, H, B, *attention);
+    if (plan.tiles > kMaxGrid / plan.splits)
         return NVFP4_ERR_INVALID_SHAPE;
-    hipLaunchKernelGGL(nvfp4_attention_simple_kernel, dim3((uint32_t)(B * attention->max_q * H)), dim3(64), 0,
-                       (hipStream_t)stream, p);
-    const hipError_t e = hipGetLastError();
+    const bool many = attention->max_q * p.G > 32;
+    if (many && B * attention->max_q > kMaxGrid / H)
+        return NVFP4_ERR_INVALID_SHAPE;
+    if (plan.bytes && (!workspace || workspace_bytes < plan.bytes || !aligned(workspace, 256)))
+        return NVFP4_ERR_WORKSPACE;
+    p.few_rows = attention->max_q * p.G <= 16 ? 16 : 32;
+    p.splits = plan.splits, p.chunk = plan.chunk, p.most_rows = plan.most_rows;
+    p.tickets = (uint32_t *)workspace;
+    p.sums = workspace ? (float *)((uint8_t *)workspace + kTicketBytes) : nullptr;
+    p.norms = p.sums ? p.sums + plan.tiles * plan.splits * plan.most_rows * p.D : nullptr;
+    const hipStream_t hs = (hipStream_t)stream;
+    hipError_t e = by_head(p.D, [&](auto d) { return launch_rows_of<d()>(p, plan.tiles * plan.splits, hs); });
+    if (e == hipSuccess && many) {
+        hipLaunchKernelGGL(nvfp4_attention_simple_kernel, dim3((uint32_t)(B * attention->max_q * H)), dim3(64), 0, hs, p);
+        e = hipGetLastError();
+    }
     if (e == hipSuccess)
         return NVFP4_OK;
     nvfp4_record_hip_error((int)e);

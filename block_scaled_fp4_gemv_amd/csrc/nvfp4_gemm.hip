@@ -46,10 +46,10 @@
 #include "nvfp4_device.h"
 #include "nvfp4_gemv.h"
 #include "nvfp4_internal.h"
+#include "nvfp4_lds.h"
 
 namespace {
 
-typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float16_t __attribute__((ext_vector_type(16)));
 
 constexpr int kLdsBytes = 160 * 1024;           // LDS of a CU
@@ -63,44 +63,7 @@ static_assert(kTicketBytes + kMaxPartialBytes == NVFP4_WORKSPACE_MAX_BYTES && NV
 constexpr int kMaxSplits = 16;
 constexpr int64_t kMaxGrid = 0x7FFFFF;          // workgroups of up to 512 threads in 2^32 work items
 
-// ------------------------------------------------------------------ copies to LDS
-
-// A pointer that is the same in every lane, in scalar registers (nothing to do
-// where the compiler has it there).
-__device__ __attribute__((always_inline)) inline const uint8_t *uniform_ptr(const uint8_t *p)
-{
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uintptr_t)p >> 32));
-    return (const uint8_t *)(uintptr_t)((uint64_t)hi << 32 | lo);
-}
-
-// 16, 4 or 2 bytes per lane from base + off into LDS at dst + lane * 16 (lane *
-// 4; 2 bytes land in the low half of a dword). The base is uniform and steps
-// along K in scalar registers, the lane's offset stays. The compiler does not
-// count the copies: the kernels wait for them themselves.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __attribute__((always_inline)) inline void copy16(const uint8_t *base, uint32_t off, uint32_t dst)
-{
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(uniform_ptr(base)), "s"(dst) : "memory", "m0");
-}
-__device__ __attribute__((always_inline)) inline void copy4(const uint8_t *base, uint32_t off, uint32_t dst)
-{
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(uniform_ptr(base)), "s"(dst) : "memory", "m0");
-}
-__device__ __attribute__((always_inline)) inline void copy2(const uint8_t *base, uint32_t off, uint32_t dst)
-{
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_ushort %0, %1" : : "v"(off), "s"(uniform_ptr(base)), "s"(dst) : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-// s_waitcnt vmcnt(N), other counters unconstrained
-template <int N>
-__device__ __attribute__((always_inline)) inline void wait_copies()
-{
-    static_assert(N >= 0 && N < 64, "vmcnt holds 0..63");
-    __builtin_amdgcn_s_waitcnt((0x0F70 & ~0xC00F) | (N & 15) | ((N >> 4) << 14));
-}
+// ------------------------------------------------------------------ barrier
 
 // Past it, what any wave has read from LDS before may be overwritten: each waits
 // for its own reads to return. The compiler waits where it uses a read, which may
@@ -147,13 +110,6 @@ __device__ __attribute__((always_inline)) inline void store_value(uint8_t *c, in
         ((float *)c)[i] = v;
     else
         ((uint16_t *)c)[i] = dtype == NVFP4_BF16 ? (uint16_t)bf16_bits(v) : f16_bits(v);
-}
-
-// 8 codes (a dword) times a scale -> 8 float16
-__device__ __attribute__((always_inline)) inline half8_t decode8(uint32_t w, half2_t s)
-{
-    const half2_t v0 = fp4x2<0>(w) * s, v1 = fp4x2<1>(w) * s, v2 = fp4x2<2>(w) * s, v3 = fp4x2<3>(w) * s;
-    return (half8_t){v0.x, v0.y, v1.x, v1.y, v2.x, v2.y, v3.x, v3.y};
 }
 
 // NW consecutive scale words (1, 2 or 4) from LDS

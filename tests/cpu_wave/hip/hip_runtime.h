@@ -1,5 +1,5 @@
-// The part of HIP that the kernels of nvfp4_moe.hip, nvfp4_quantize.hip and
-// nvfp4_gemm.hip use, on the CPU, so that a test runs the sources themselves,
+// The part of HIP that the kernels of nvfp4_moe.hip, nvfp4_quantize.hip,
+// nvfp4_gemm.hip, nvfp4_rope.hip, nvfp4_cache.hip and nvfp4_attention.hip use, on the CPU, so that a test runs the sources themselves,
 // launches included, on memory whose ends it guards.
 // One workgroup at a time; each thread is a coroutine with a stack of its own.
 // Cross-lane operations and barriers switch to the next thread until all of the
@@ -400,6 +400,61 @@ inline cpu_wave_float16 cpu_wave_mfma(cpu_wave_half8 a, cpu_wave_half8 b, cpu_wa
     return c;
 }
 
+// 16 x 16 x 32: lane l holds row (column) l % 16, k 8 (l / 16) .. + 7 of each operand;
+// register r of its result is row 4 (l / 16) + r of column l % 16
+typedef float cpu_wave_float4 __attribute__((ext_vector_type(4)));
+inline cpu_wave_float4 cpu_wave_mfma16(cpu_wave_half8 a, cpu_wave_half8 b, cpu_wave_float4 c, int, int, int)
+{
+    static float rows[cpu_wave::kMaxThreads / 64][2][64][8], columns[cpu_wave::kMaxThreads / 64][2][64][8];
+    const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    const uint32_t turn = cpu_wave::threads[threadIdx.x].wave_ops % 2;
+    for (int k = 0; k < 8; ++k) {
+        rows[wave][turn][lane][k] = a[k];
+        columns[wave][turn][lane][k] = b[k];
+    }
+    cpu_wave::exchange(0);
+    for (uint32_t r = 0; r < 4; ++r) {
+        double sum = 0.0;
+        for (uint32_t k = 0; k < 32; ++k)
+            sum += (double)rows[wave][turn][4 * (lane / 16) + r + 16 * (k / 8)][k % 8] *
+                   (double)columns[wave][turn][lane % 16 + 16 * (k / 8)][k % 8];
+        c[r] = (float)(c[r] + sum);
+    }
+    return c;
+}
+
+// Transposed reads of 8 bytes per lane among 16 lanes: 16 codes, of which lane i gets the i-th of
+// each lane; 4 float16, of which lane i gets the (i % 4)-th of lanes i / 4 + 0, 4, 8, 12
+typedef int cpu_wave_int2 __attribute__((ext_vector_type(2)));
+typedef short cpu_wave_short4 __attribute__((ext_vector_type(4)));
+template <typename P>
+uint64_t cpu_wave_8_bytes(P p)
+{
+    uint64_t v;
+    memcpy(&v, (const void *)(uintptr_t)p, 8);
+    return v;
+}
+template <typename P>
+cpu_wave_int2 cpu_wave_tr4(P p)
+{
+    const uint64_t *all = cpu_wave::exchange(cpu_wave_8_bytes(p));
+    const uint32_t lane = threadIdx.x % 64, i = lane % 16;
+    uint64_t v = 0;
+    for (uint32_t n = 0; n < 16; ++n)
+        v |= (all[lane - i + n] >> (4 * i) & 15) << (4 * n);
+    return {(int)(uint32_t)v, (int)(uint32_t)(v >> 32)};
+}
+template <typename P>
+cpu_wave_short4 cpu_wave_tr16(P p)
+{
+    const uint64_t *all = cpu_wave::exchange(cpu_wave_8_bytes(p));
+    const uint32_t lane = threadIdx.x % 64, i = lane % 16;
+    cpu_wave_short4 v;
+    for (uint32_t n = 0; n < 4; ++n)
+        v[n] = (short)(all[lane - i + 4 * n + i / 4] >> (16 * (i % 4)));
+    return v;
+}
+
 inline void cpu_wave_s_waitcnt(int imm)
 {
     cpu_wave::exchange(0);
@@ -420,6 +475,11 @@ inline void cpu_wave_s_waitcnt(int imm)
 #define __builtin_amdgcn_frexp_mantf cpu_wave_frexp_mant
 #define __builtin_amdgcn_frexp_expf cpu_wave_frexp_exp
 #define __builtin_amdgcn_mfma_f32_32x32x16_f16 cpu_wave_mfma
+#define __builtin_amdgcn_mfma_f32_16x16x32_f16 cpu_wave_mfma16
+#define __builtin_amdgcn_ds_read_tr4_b64_v2i32 cpu_wave_tr4
+#define __builtin_amdgcn_ds_read_tr16_b64_v4i16 cpu_wave_tr16
+#define __builtin_amdgcn_exp2f(v) exp2f(v)
+#define __builtin_amdgcn_logf(v) log2f(v)
 #define __builtin_amdgcn_s_waitcnt cpu_wave_s_waitcnt
 #define __builtin_amdgcn_s_barrier __syncthreads
 

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 
 import attention_reference as ref
+from cache_cases import poisoned
 from test_gpu_cache import on_device
 
 pytestmark = pytest.mark.gpu
@@ -22,26 +23,6 @@ DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
 @pytest.fixture(scope="module")
 def workspace():
     return torch.zeros(g.NVFP4_WORKSPACE_MAX_BYTES, dtype=torch.uint8, device="cuda")
-
-
-def poisoned(rng, lengths, page_size, heads, D, spare=3, width=None):
-    """A cache whose pages hold rows of the sequences, in any order, and NaN scales everywhere else; its table."""
-    held = [-(-n // page_size) for n in lengths]
-    width = width or max(1, max(held))
-    pages = sum(held) + spare
-    c = ref.Cache(rng, pages, page_size, heads, D)
-    order = rng.permutation(pages)
-    table = np.full((len(lengths), width), -1, np.int32)
-    for name in ("ks", "vs"):
-        scales, keep = getattr(c, name), np.zeros((pages, page_size), bool)
-        at = 0
-        for b, n in enumerate(lengths):
-            table[b, :held[b]] = order[at:at + held[b]]
-            for j in range(held[b]):
-                keep[order[at + j], :min(page_size, n - j * page_size)] = True
-            at += held[b]
-        scales.transpose(0, 2, 1, 3)[~keep] = 0x7F
-    return c, table
 
 
 def run(c, table, lengths, counts, H, dtype, workspace, seed=0, max_q=None, max_length=None, scale=None, causal=True, window=0,
@@ -273,6 +254,25 @@ def test_captured_calls_follow_their_inputs(n, lengths):
         torch.cuda.synchronize()
         assert torch.equal(out.view(torch.int16), eager.view(torch.int16))        # NaN where a rolled table meets other pages
     assert not ws[:65536].any()
+
+
+def test_workspace_rules():
+    rng = np.random.default_rng(15)
+    c, table = poisoned(rng, [4096], 64, 1, 128)
+    handle, _ = on_device(c)
+    q, out = torch.randn(1, 4, 128, device="cuda").half(), torch.empty(1, 4, 128, dtype=torch.float16, device="cuda")
+    args = (handle, q, out, torch.tensor([0, 1], dtype=torch.int32).cuda(), torch.tensor([4096], dtype=torch.int32).cuda(),
+            torch.from_numpy(table).cuda(), 1, 4, 1, 1, 4096)
+    need = g.nvfp4_cache_attention_workspace_bytes(handle, torch.float16, 1, 4, 1, 1, 4096)
+    assert 0 < need <= g.NVFP4_WORKSPACE_MAX_BYTES and need % 256 == 0
+    ws = torch.zeros(need + 256, dtype=torch.uint8, device="cuda")
+    g.nvfp4_cache_attention(*args, workspace=ws[:need])
+    for bad in (dict(workspace=None), dict(workspace=ws[:need - 1]), dict(workspace=ws[16:16 + need])):
+        with pytest.raises(g.Nvfp4Error) as e:
+            g.nvfp4_cache_attention(*args, **bad)
+        assert e.value.status == g.NVFP4_ERR_WORKSPACE
+    with pytest.raises(ValueError, match="workspace holds"):
+        g.nvfp4_cache_attention(*args, workspace=ws, workspace_bytes=need + 4096)
 
 
 def test_binding_refuses_what_does_not_fit(workspace):

@@ -2,8 +2,9 @@
 //
 //   out = sum_t p_t V[t],   p = softmax over the visible t of scale * q . K[t]
 //
-// This form: a wave per query and head, which takes the visible positions one by one
-// with a running maximum and sum.
+// Two kernels: one for sequences of few rows (queries times the heads that share a key
+// head), one for many; a call with both kinds launches both, and each leaves the
+// other's sequences alone.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -33,6 +34,7 @@ struct AttParams {
     int32_t max_q, max_length, window, causal, dtype;
     int32_t splits, chunk;                      // of a sequence's positions; chunk in tiles of 64
     int32_t few_rows;                           // sequences of so many rows are the rows kernel's
+    int32_t row_tiles;                          // of 128 rows, at most, for a sequence and key head
     int32_t most_rows;                          // of a partial result
     uint32_t *tickets;
     float *sums, *norms;                        // partial results: [tile][split][most_rows][D], [..][2]
@@ -50,83 +52,6 @@ __device__ __attribute__((always_inline)) inline Sequence sequence_of(const AttP
     return {first, end - first, min(max(p.lengths[b], 0), p.max_length)};
 }
 
-__device__ __attribute__((always_inline)) inline float load_value(const uint8_t *x, int i, int dtype)
-{
-    if (dtype == NVFP4_F32)
-        return ((const float *)x)[i];
-    const uint16_t v = ((const uint16_t *)x)[i];
-    return dtype == NVFP4_BF16 ? __builtin_bit_cast(float, (uint32_t)v << 16) : (float)__builtin_bit_cast(_Float16, v);
-}
-
-__device__ __attribute__((always_inline)) inline void store_value(uint8_t *c, int64_t i, float v, int dtype)
-{
-    if (dtype == NVFP4_F32)
-        ((float *)c)[i] = v;
-    else
-        ((uint16_t *)c)[i] = dtype == NVFP4_BF16 ? (uint16_t)bf16_bits(v) : f16_bits(v);
-}
-
-__global__ __launch_bounds__(64) void nvfp4_attention_simple_kernel(AttParams p)
-{
-    const int lane = (int)threadIdx.x;
-    const int h = (int)(blockIdx.x % (uint32_t)p.H), i = (int)(blockIdx.x / (uint32_t)p.H % (uint32_t)p.max_q),
-              b = (int)(blockIdx.x / (uint32_t)p.H / (uint32_t)p.max_q);
-    const Sequence s = sequence_of(p, b);
-    if (i >= s.n || (int64_t)min(s.n, p.max_q) * p.G <= p.few_rows)
-        return;
-    const int32_t pos = s.length - s.n + i;
-    const int32_t end = p.causal ? min(s.length, pos + 1) : s.length;
-    const int32_t begin = p.window ? max(0, pos - p.window + 1) : 0;
-    const uint8_t *x = p.q + (int64_t)(s.first + i) * p.q_token + (int64_t)h * p.q_head;
-    float q[4], acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    bool finite = true;
-    for (int e = 0; e < 4; ++e) {
-        const int d = 2 * (lane + e / 2 * 64) + e % 2;
-        q[e] = d < p.D ? load_value(x, d, p.dtype) : 0.0f;
-        finite &= __builtin_isfinite(q[e]);
-    }
-    finite = __ballot(finite) == ~0ull;
-    const float factor = p.scale * (p.gk ? *p.gk : 1.0f), gv = p.gv ? *p.gv : 1.0f;
-    float top = -__builtin_inff(), sum = 0.0f;
-    bool any = false;
-    for (int32_t t = begin; t < end; ++t) {
-        const uint32_t page = (uint32_t)p.table[(int64_t)b * p.width + (t >> p.shift)];
-        if (page >= (uint32_t)p.pages)
-            continue;
-        const int64_t row = ((int64_t)(h / p.G) << p.shift) + (t & ((1 << p.shift) - 1));
-        const uint8_t *kc = p.kc + page * p.code_page + row * (p.D / 2), *ks = p.ks + page * p.scale_page + row * (p.D / 16);
-        const uint8_t *vc = p.vc + page * p.code_page + row * (p.D / 2), *vs = p.vs + page * p.scale_page + row * (p.D / 16);
-        float dot = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int e = 0; e < 2; ++e) {
-            const int at = lane + e * 64;
-            if (2 * at < p.D) {
-                const half2_t k2 = fp4x2<0>(kc[at]), v2 = fp4x2<0>(vc[at]);
-                const float sk = __builtin_amdgcn_cvt_f32_fp8((int)ks[at / 8], 0), sv = __builtin_amdgcn_cvt_f32_fp8((int)vs[at / 8], 0);
-                dot += q[2 * e] * ((float)k2.x * sk) + q[2 * e + 1] * ((float)k2.y * sk);
-                v[2 * e] = (float)v2.x * sv;
-                v[2 * e + 1] = (float)v2.y * sv;
-            }
-        }
-        for (int d = 1; d < 64; d <<= 1)
-            dot += __shfl_xor(dot, d);
-        const float logit = dot * factor, above = fmaxf(top, logit);
-        const float keep = any ? expf(top - above) : 0.0f, w = expf(logit - above);
-        sum = sum * keep + w;
-        for (int e = 0; e < 4; ++e)
-            acc[e] = acc[e] * keep + w * v[e];
-        top = above;
-        any = true;
-    }
-    const int64_t row = (int64_t)(s.first + i) * p.H + h;
-    for (int e = 0; e < 4; ++e) {
-        const int d = 2 * (lane + e / 2 * 64) + e % 2;
-        if (d < p.D)
-            store_value(p.out, row * p.D + d, !any ? 0.0f : finite ? acc[e] / sum * gv : __builtin_nanf(""), p.dtype);
-    }
-    if (p.lse && lane == 0)
-        p.lse[row] = !any ? -__builtin_inff() : finite ? top + logf(sum) : __builtin_nanf("");
-}
-
 // ------------------------------------------------------------------ rows kernel
 
 typedef float float4_t __attribute__((ext_vector_type(4)));
@@ -136,7 +61,7 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 // of the largest as normal numbers.
 constexpr float kShift = 12.0f;
 constexpr int kRowsThreads = 256, kRowsWaves = 4;
-constexpr int kMaxSplits = 64, kRowsTarget = 2048;
+constexpr int kMaxSplits = 64, kRowsTarget = 2048, kTileTarget = 512, kTileLeast = 8;
 
 // The head's D values go through the matrix instruction in steps of 32. A lane (row
 // lane % 16, g = lane / 16) has 8 of a step's; which 8 is free while q and K agree: runs
@@ -720,6 +645,328 @@ __global__ __launch_bounds__(kRowsThreads) void nvfp4_attention_rows_kernel(AttP
     join_splits<D, kRowsThreads>(p, s, hk, tile, 0, rows, span.splits, gv, (Norm *)lds);
 }
 
+// ------------------------------------------------------------------ tile kernel
+
+typedef float float16_t __attribute__((ext_vector_type(16)));
+
+constexpr int kTileThreads = 256, kTileRows = 128;      // 4 waves of 32 rows
+
+// 64 positions in LDS as float16, [position][D] for K and for V. Places of a row's 16-byte
+// pieces: 16 neighbouring rows meet every bank where K is read, where V is read 64 bytes of
+// 4 neighbouring rows do (and rows that are written at once differ too).
+template <int D>
+struct WideTile {
+    static constexpr int kRow = 2 * D, kBytes = 64 * kRow, PR = D / 32;        // pieces of 32 codes in a row
+    static constexpr int kPieces = (2 * 64 * PR + kTileThreads - 1) / kTileThreads;
+    __device__ static constexpr int swizzle_k(int t)
+    {
+        return D == 64 || D == 192 ? t / 2 & 7 : D == 96 ? t / 4 & 3 : t & 15;
+    }
+    __device__ static constexpr int swizzle_v(int t)
+    {
+        return (t / 4 & 3) + (D == 64 || D == 192 ? (t / 2 & 1) * 4 : D == 96 ? 0 : (t & 3) * 4);
+    }
+};
+
+__device__ __attribute__((always_inline)) inline void lds_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" : : : "memory");
+}
+
+// Many rows (prompts): a workgroup has 128 of a sequence's rows for one key head, a wave 32 of
+// them. Codes of 64 positions come in registers while the 64 before are worked on, are
+// decoded once for all rows into LDS, and go through 32 x 32 x 16 products:
+//   S^T = K Q^T: a lane has the logits of one row (lane % 32), positions 32 t + 8 (r / 4) + 4 h
+//     + r % 4 in register r (h = lane / 32).
+//   O^T = V^T P^T: P's registers are the k-range of the second operand as they stand; V's operand is read
+//     transposed in that order, 4 positions of a value at a time.
+template <int D, bool F32>
+__global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attention_tile_kernel(AttParams p)
+{
+    using S = WideTile<D>;
+    constexpr int PARTS = F32 ? 2 : 1, NK = D / 16, ND = D / 32;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    __shared__ uint32_t s_ticket, s_flag[2], s_nan[2][64];
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64), lane = (int)threadIdx.x % 64;
+    const int i = lane % 32, h = lane / 32;
+    // the last rows, which see most under the causal mask, first
+    const uint32_t pairs = (uint32_t)p.B * (uint32_t)p.heads, id = blockIdx.x / (uint32_t)p.splits;
+    const int split = (int)(blockIdx.x % (uint32_t)p.splits), rt = (int)(((uint32_t)p.row_tiles - 1u) - id / pairs);
+    const int b = (int)(id % pairs / (uint32_t)p.heads), hk = (int)(id % pairs % (uint32_t)p.heads);
+    const Sequence s = sequence_of(p, b);
+    const int queries = min(s.n, p.max_q);
+    const int64_t all_rows = (int64_t)queries * p.G;
+    if (all_rows <= p.few_rows || (int64_t)rt * kTileRows >= all_rows)
+        return;
+    const int row0 = rt * kTileRows, rows = (int)min((int64_t)kTileRows, all_rows - row0);
+    const int tok0 = row0 / p.G, tok1 = (row0 + rows - 1) / p.G + 1;
+    const Span span = span_of(p, s, tok0, tok1, split);
+    if (split >= span.splits)
+        return;
+
+    // --- this lane's row of q
+    const int r = 32 * wave + i;
+    const bool real = r < rows;
+    const int tok = (row0 + (real ? r : 0)) / p.G, pos = s.length - s.n + tok;
+    const int32_t end = p.causal ? min(s.length, pos + 1) : s.length;
+    const int32_t begin = p.window ? max(0, pos - p.window + 1) : 0;
+    QRow<NK, PARTS> q;
+    float rf;
+    {
+        const float factor = p.scale * (p.gk ? *p.gk : 1.0f) * kLog2e;
+        const uint8_t *x = p.q + (int64_t)(s.first + tok) * p.q_token + (int64_t)(hk * p.G + (row0 + (real ? r : 0)) % p.G) * p.q_head;
+        float v[NK][8], top = 0.0f;
+        bool finite = true;
+#pragma unroll
+        for (int c = 0; c < NK; ++c) {
+            load8(x + (16 * c + 8 * h) * (F32 ? 4 : 2), F32 ? NVFP4_F32 : p.dtype, v[c]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool good = __builtin_isfinite(v[c][j]);
+                finite &= good;
+                v[c][j] = good ? v[c][j] : 0.0f;
+                top = fmaxf(top, fabsf(v[c][j]));
+            }
+        }
+        top = fmaxf(top, __shfl_xor(top, 32));
+        finite = fmaxf(finite ? 0.0f : 1.0f, __shfl_xor(finite ? 0.0f : 1.0f, 32)) == 0.0f;
+        const int e = row_exponent(top);
+#pragma unroll
+        for (int c = 0; c < NK; ++c)
+            to_parts(v[c], e, q, c);
+        rf = !real ? 0.0f : finite ? __builtin_ldexpf(factor, -e) : __builtin_nanf("");
+    }
+    // positions that some, and that all, of the wave's rows see
+    const int w0 = min(32 * wave, rows - 1), w1 = min(32 * wave + 31, rows - 1);
+    const int32_t pos0 = s.length - s.n + (row0 + w0) / p.G, pos1 = s.length - s.n + (row0 + w1) / p.G;
+    const int32_t some_from = p.window ? max(0, pos0 - p.window + 1) : 0, some_to = p.causal ? min(s.length, pos1 + 1) : s.length;
+    const int32_t all_from = p.window ? max(0, pos1 - p.window + 1) : 0, all_to = p.causal ? min(s.length, pos0 + 1) : s.length;
+    const bool has_rows = 32 * wave < rows;
+
+    float16_t acc[ND];
+#pragma unroll
+    for (int k = 0; k < ND; ++k)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            acc[k][e] = 0.0f;
+    float top = -__builtin_inff(), sum = 0.0f;
+    uint32_t nan_blocks = 0u;
+
+    // --- staging. Entry of the page of position lane of a tile: -1 where there is none.
+    const int32_t mask = (1 << p.shift) - 1, first_position = span.lo / 64 * 64;
+    auto entry = [&](int32_t n) -> int32_t {
+        const int32_t t = first_position + n * 64 + lane;
+        if (n >= span.end || t >= span.hi)
+            return -1;
+        const int32_t e = p.table[(int64_t)b * p.width + (t >> p.shift)];
+        return (uint32_t)e < (uint32_t)p.pages ? e : -1;
+    };
+    uint4_t codes[S::kPieces];
+    uint32_t scales[S::kPieces];
+    auto load = [&](int32_t n, int32_t e) {
+#pragma unroll
+        for (int k = 0; k < S::kPieces; ++k) {
+            const int u = k * kTileThreads + (int)threadIdx.x, v = u % (64 * S::PR), t = v / S::PR, piece = v % S::PR;
+            const int32_t page = __shfl(e, t);
+            codes[k] = (uint4_t){0u, 0u, 0u, 0u};
+            scales[k] = 0u;
+            if (page < 0 || u >= 2 * 64 * S::PR)
+                continue;
+            const bool values = u >= 64 * S::PR;
+            const int64_t row = ((int64_t)hk << p.shift) + ((first_position + n * 64 + t) & mask);
+            codes[k] = *(const uint4_t *)((values ? p.vc : p.kc) + page * p.code_page + row * (D / 2) + piece * 16);
+            scales[k] = *(const uint16_t *)((values ? p.vs : p.ks) + page * p.scale_page + row * (D / 16) + piece * 2);
+        }
+    };
+    auto stage = [&](int parity) {
+#pragma unroll
+        for (int k = 0; k < S::kPieces; ++k) {
+            const int u = k * kTileThreads + (int)threadIdx.x, v = u % (64 * S::PR), t = v / S::PR, piece = v % S::PR;
+            if (2 * 64 * S::PR % kTileThreads != 0 && u >= 2 * 64 * S::PR)
+                continue;
+            const bool values = u >= 64 * S::PR;
+            half2_t both = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(scales[k], 1.0f, false);
+            if (values) {
+                // a NaN scale is noted for the rows that see it and counts as 0 in the products
+                const uint32_t nan = (uint32_t)((scales[k] & 0x7Fu) == 0x7Fu) | (uint32_t)((scales[k] & 0x7F00u) == 0x7F00u) << 1;
+                if (nan) {
+                    atomicOr(&s_nan[parity][t], nan << (2 * piece));
+                    s_flag[parity] = 1u;
+                    both.x = nan & 1u ? (_Float16)0.0f : both.x;
+                    both.y = nan & 2u ? (_Float16)0.0f : both.y;
+                }
+            }
+            const half2_t s0 = {both.x, both.x}, s1 = {both.y, both.y};
+            uint8_t *row = lds + (values ? S::kBytes : 0) + t * S::kRow;
+            const int sw = values ? S::swizzle_v(t) : S::swizzle_k(t);
+            *(half8_t *)(row + ((4 * piece) ^ sw) * 16) = decode8(codes[k].x, s0);
+            *(half8_t *)(row + ((4 * piece + 1) ^ sw) * 16) = decode8(codes[k].y, s0);
+            *(half8_t *)(row + ((4 * piece + 2) ^ sw) * 16) = decode8(codes[k].z, s1);
+            *(half8_t *)(row + ((4 * piece + 3) ^ sw) * 16) = decode8(codes[k].w, s1);
+        }
+        // nobody reads the other tile's notes any more
+        if (threadIdx.x < 64) {
+            s_nan[parity ^ 1][threadIdx.x] = 0u;
+            s_flag[parity ^ 1] = 0u;
+        }
+    };
+
+    auto compute = [&](int32_t n, uint64_t there, int parity) {
+        const int32_t t0 = first_position + n * 64;
+        if (!has_rows || t0 >= some_to || t0 + 64 <= some_from)
+            return;
+        // --- S^T
+        float logit[2][16];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            float16_t c;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                c[e] = 0.0f;
+            const int kr = 32 * t + i;
+            const uint8_t *row = lds + kr * S::kRow;
+            const int sw = S::swizzle_k(kr);
+#pragma unroll
+            for (int k = 0; k < NK; ++k) {
+                const half8_t k8 = *(const half8_t *)(row + ((2 * k + h) ^ sw) * 16);
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part)
+                    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(k8, q.part[part][k], c, 0, 0, 0);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                logit[t][e] = c[e] * rf;
+        }
+        if (there != ~0ull || t0 < all_from || t0 + 64 > all_to) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int at = 32 * t + 8 * (e / 4) + 4 * h + e % 4;
+                    if (!(there >> at & 1u) || t0 + at < begin || t0 + at >= end)
+                        logit[t][e] = -__builtin_inff();
+                }
+        }
+        if (s_flag[parity]) {
+            for (int t = 0; t < 64; ++t) {
+                const uint32_t blocks = s_nan[parity][t];
+                if (t0 + t >= begin && t0 + t < end)
+                    nan_blocks |= blocks;
+            }
+        }
+        // --- softmax
+        float most = logit[0][0];
+#pragma unroll
+        for (int e = 1; e < 32; ++e)
+            most = fmaxf(most, logit[e / 16][e % 16]);
+        most = fmaxf(most, __shfl_xor(most, 32));
+        most = fmaxf(top, most);
+        if (__ballot(most > top)) {
+            const float keep = weight_of(top, most);
+            sum *= keep;
+#pragma unroll
+            for (int k = 0; k < ND; ++k)
+                acc[k] *= keep;
+            top = most;
+        }
+        const float from = (most == -__builtin_inff() ? 0.0f : most) - kShift;
+        half8_t prob[PARTS][4];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            const float w = __builtin_amdgcn_exp2f(logit[e / 16][e % 16] - from);
+            sum += w;
+            const _Float16 high = (_Float16)w;
+            prob[0][e / 8][e % 8] = high;
+            if constexpr (PARTS == 2)
+                prob[PARTS - 1][e / 8][e % 8] = (_Float16)(w - (float)high);
+        }
+        // --- O^T: lanes of 16 give the places of 4 rows, 4 values each
+        const int vi = lane % 16, vd = lane / 16 % 2;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r0 = 16 * k + 4 * h + vi / 4, r1 = r0 + 8;
+            const uint8_t *a0 = lds + S::kBytes + r0 * S::kRow + vi % 2 * 8, *a1 = lds + S::kBytes + r1 * S::kRow + vi % 2 * 8;
+            const int sw0 = S::swizzle_v(r0), sw1 = S::swizzle_v(r1);
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                const int piece = 4 * d + 2 * vd + vi % 4 / 2;
+                const uint2_t x0 = read_transposed16(a0 + (piece ^ sw0) * 16), x1 = read_transposed16(a1 + (piece ^ sw1) * 16);
+                const uint4_t x = {x0.x, x0.y, x1.x, x1.y};
+                const half8_t v8 = __builtin_bit_cast(half8_t, x);
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part)
+                    acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v8, prob[part][k], acc[d], 0, 0, 0);
+            }
+        }
+    };
+
+    if (threadIdx.x < 64) {
+        s_nan[0][threadIdx.x] = s_nan[1][threadIdx.x] = 0u;
+        s_flag[0] = s_flag[1] = 0u;
+    }
+    if (span.first < span.end) {
+        int32_t e = entry(span.first);
+        uint64_t there = __ballot(e >= 0);
+        load(span.first, e);
+        e = entry(span.first + 1);
+        for (int32_t n = span.first; n < span.end; ++n) {
+            const int parity = (n - span.first) & 1;
+            lds_barrier();                                      // the tile before has been read
+            stage(parity);
+            const uint64_t now = there;
+            there = __ballot(e >= 0);
+            load(n + 1, e);                                     // past the end: no position has a page, nothing is read
+            e = entry(n + 2);
+            lds_barrier();
+            compute(n, now, parity);
+        }
+    }
+
+    // --- results
+    sum += __shfl_xor(sum, 32);
+    const float gv = p.gv ? *p.gv : 1.0f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (nan_blocks >> (2 * d + e / 8) & 1u)
+                acc[d][e] = __builtin_nanf("");
+    if (span.splits == 1) {
+        if (!real)
+            return;
+        const int64_t row = out_row(p, s, hk, row0 + r);
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+                store_values<4>(p, row * D + 32 * d + 2 * e + 4 * h, {acc[d][e], acc[d][e + 1], acc[d][e + 2], acc[d][e + 3]}, sum, gv);
+        if (h == 0)
+            store_lse(p, row, {top, sum});
+        return;
+    }
+    const uint32_t tile = id;
+    if (real) {
+        float *const sums = p.sums + (((int64_t)tile * p.splits + split) * kTileRows + r) * D;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const float4_t v = {acc[d][e], acc[d][e + 1], acc[d][e + 2], acc[d][e + 3]};
+                *(float4_t *)(sums + 32 * d + 2 * e + 4 * h) = v;
+            }
+        if (h == 0)
+            *(Norm *)(p.norms + (((int64_t)tile * p.splits + split) * kTileRows + r) * 2) = {top, sum};
+    }
+    // whole lines leave the L2 before the ticket, and the last one reads none that it held before
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+    if (!last_of_splits(p, tile, span.splits, &s_ticket))
+        return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    join_splits<D, kTileThreads>(p, s, hk, tile, row0, rows, span.splits, gv, (Norm *)lds);
+}
+
 // ------------------------------------------------------------------ host
 
 constexpr int64_t kTicketBytes = 65536, kMaxPartialBytes = INT64_C(64) << 20;
@@ -742,7 +989,7 @@ nvfp4_status_t check(const nvfp4_cache_t *cache, int dtype, int64_t T, int64_t H
         return NVFP4_ERR_INVALID_CACHE;
     const int64_t most = INT64_C(1) << 30;
     if (T < 1 || B < 1 || H < 1 || T > most || B > most || H % cache->heads || H / cache->heads > 1024 || a->max_q < 1 ||
-        a->max_q > T || a->max_q > most / B || a->max_length < 1 || a->max_length > most)
+        a->max_q > T || a->max_q > most / B || a->max_q > most / (H / cache->heads) || a->max_length < 1 || a->max_length > most)
         return NVFP4_ERR_INVALID_SHAPE;
     if (a->window < 0 || a->window > INT32_MAX || (a->causal != 0 && a->causal != 1))
         return NVFP4_ERR_INVALID_CACHE;
@@ -786,6 +1033,54 @@ Plan rows_plan(const nvfp4_cache_t &c, int64_t H, int64_t B, const nvfp4_attenti
     return p;
 }
 
+// 2^30 rows of a sequence at most (max_q * G), so row_tiles and rows fit 32 bits.
+Plan tile_plan(const nvfp4_cache_t &c, int64_t H, int64_t B, const nvfp4_attention_t &a)
+{
+    Plan p{};
+    const int64_t G = H / c.heads, row_tiles = (a.max_q * G + kTileRows - 1) / kTileRows;
+    p.tiles = B * c.heads * row_tiles;
+    p.most_rows = kTileRows;
+    const int64_t span = a.window ? std::min<int64_t>(a.max_length, a.window + kTileRows + 64) : a.max_length;
+    const int64_t most = (span + 63) / 64 + 1;
+    int64_t splits = std::min<int64_t>((kTileTarget + p.tiles - 1) / p.tiles, (most + kTileLeast - 1) / kTileLeast);
+    splits = std::max<int64_t>(1, std::min<int64_t>(splits, kMaxSplits));
+    if (p.tiles > kMaxTickets)
+        splits = 1;
+    while (splits > 1 && partial_bytes(p.tiles, splits, kTileRows, c.head_size) > kMaxPartialBytes)
+        --splits;
+    p.chunk = (int32_t)((most + splits - 1) / splits);
+    p.splits = (int32_t)((most + p.chunk - 1) / p.chunk);
+    p.bytes = p.splits > 1 ? kTicketBytes + (partial_bytes(p.tiles, p.splits, kTileRows, c.head_size) + 255) / 256 * 256 : 0;
+    return p;
+}
+
+// Sequences of more rows than the rows kernel takes.
+bool has_many(const nvfp4_cache_t &c, int64_t H, const nvfp4_attention_t &a) { return a.max_q * (H / c.heads) > 32; }
+
+size_t need_of(const nvfp4_cache_t &c, int64_t H, int64_t B, const nvfp4_attention_t &a)
+{
+    const size_t rows = rows_plan(c, H, B, a).bytes;
+    return has_many(c, H, a) ? std::max(rows, tile_plan(c, H, B, a).bytes) : rows;
+}
+
+void set_plan(AttParams &p, const Plan &plan, void *workspace)
+{
+    p.splits = plan.splits, p.chunk = plan.chunk, p.most_rows = plan.most_rows;
+    p.tickets = (uint32_t *)workspace;
+    p.sums = workspace ? (float *)((uint8_t *)workspace + kTicketBytes) : nullptr;
+    p.norms = p.sums ? p.sums + plan.tiles * plan.splits * plan.most_rows * p.D : nullptr;
+}
+
+template <int D>
+hipError_t launch_tile(const AttParams &p, int64_t grid, hipStream_t st)
+{
+    static_assert(2 * WideTile<D>::kBytes + 1024 <= 160 * 1024);
+    const int lds = std::max(2 * WideTile<D>::kBytes, p.splits > 1 ? p.splits * kTileRows * 8 : 0);
+    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((uint32_t)grid), dim3(kTileThreads), lds, st, p); };
+    p.dtype == NVFP4_F32 ? go(nvfp4_attention_tile_kernel<D, true>) : go(nvfp4_attention_tile_kernel<D, false>);
+    return hipGetLastError();
+}
+
 template <int D, int NQ, bool F32>
 hipError_t launch_rows(const AttParams &p, int64_t grid, hipStream_t st)
 {
@@ -827,7 +1122,7 @@ size_t nvfp4_cache_attention_workspace_bytes(const nvfp4_cache_t *cache, int dty
 {
     if (check(cache, dtype, T, H, B, attention) != NVFP4_OK)
         return 0;
-    return rows_plan(*cache, H, B, *attention).bytes;
+    return need_of(*cache, H, B, *attention);
 }
 
 nvfp4_status_t nvfp4_cache_attention(const nvfp4_cache_t *cache, const void *q, int dtype, void *out, float *lse,
@@ -861,24 +1156,22 @@ nvfp4_status_t nvfp4_cache_attention(const nvfp4_cache_t *cache, const void *q, 
     p.max_q = (int32_t)attention->max_q, p.max_length = (int32_t)attention->max_length;
     // a window as long as the longest sequence hides nothing
     p.window = attention->window >= attention->max_length ? 0 : (int32_t)attention->window, p.causal = attention->causal, p.dtype = dtype, p.scale = attention->scale;
-    const Plan plan = rows_plan(*cache, H, B, *attention);
-    if (plan.tiles > kMaxGrid / plan.splits)
+    const Plan few = rows_plan(*cache, H, B, *attention), many = tile_plan(*cache, H, B, *attention);
+    const bool both = has_many(*cache, H, *attention);
+    if (few.tiles > kMaxGrid / few.splits || (both && many.tiles > kMaxGrid / many.splits))
         return NVFP4_ERR_INVALID_SHAPE;
-    const bool many = attention->max_q * p.G > 32;
-    if (many && B * attention->max_q > kMaxGrid / H)
-        return NVFP4_ERR_INVALID_SHAPE;
-    if (plan.bytes && (!workspace || workspace_bytes < plan.bytes || !aligned(workspace, 256)))
+    const size_t need = need_of(*cache, H, B, *attention);
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
         return NVFP4_ERR_WORKSPACE;
     p.few_rows = attention->max_q * p.G <= 16 ? 16 : 32;
-    p.splits = plan.splits, p.chunk = plan.chunk, p.most_rows = plan.most_rows;
-    p.tickets = (uint32_t *)workspace;
-    p.sums = workspace ? (float *)((uint8_t *)workspace + kTicketBytes) : nullptr;
-    p.norms = p.sums ? p.sums + plan.tiles * plan.splits * plan.most_rows * p.D : nullptr;
+    p.row_tiles = (int32_t)((attention->max_q * p.G + kTileRows - 1) / kTileRows);
     const hipStream_t hs = (hipStream_t)stream;
-    hipError_t e = by_head(p.D, [&](auto d) { return launch_rows_of<d()>(p, plan.tiles * plan.splits, hs); });
-    if (e == hipSuccess && many) {
-        hipLaunchKernelGGL(nvfp4_attention_simple_kernel, dim3((uint32_t)(B * attention->max_q * H)), dim3(64), 0, hs, p);
-        e = hipGetLastError();
+    // one after the other on the stream, so one workspace serves both
+    set_plan(p, few, need ? workspace : nullptr);
+    hipError_t e = by_head(p.D, [&](auto d) { return launch_rows_of<d()>(p, few.tiles * few.splits, hs); });
+    if (e == hipSuccess && both) {
+        set_plan(p, many, need ? workspace : nullptr);
+        e = by_head(p.D, [&](auto d) { return launch_tile<d()>(p, many.tiles * many.splits, hs); });
     }
     if (e == hipSuccess)
         return NVFP4_OK;

@@ -671,11 +671,12 @@ nvfp4_status_t nvfp4_cache_read(const nvfp4_cache_t *cache, void *k, void *v, in
  *            written. max_length <= table_width * page_size.
  * Keys and values are exact in float16 and go to the matrix cores as that; q is
  * taken to float16 with a power of two of its row's own (float32: as two float16,
- * 22 bits), probabilities to float16 (float32: two), sums, maxima and norms are
+ * 22 bits), probabilities to float16 (float32: two; all to at least 2^-37 of the
+ * query's largest), sums, maxima and norms are
  * float32, out is rounded once to dtype. The order of summation is fixed for
  * given arguments and lengths, so equal calls give equal bits.
- * Requirements: T, B >= 1; T <= 2^30; B * max_q <= 2^30; heads divides H, H / heads
- * <= 1024; head_size 64, 96, 128, 192 or 256; 1 <= max_q <= T; 1 <= max_length <=
+ * Requirements: T, B >= 1; T <= 2^30; B * max_q and H / heads * max_q <= 2^30; heads
+ * divides H, H / heads <= 1024; head_size 64, 96, 128, 192 or 256; 1 <= max_q <= T; 1 <= max_length <=
  * table_width * page_size <= 2^30; scale finite; window >= 0 and below 2^31; at most 2^23 - 1
  * workgroups.
  */

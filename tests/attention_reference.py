@@ -66,11 +66,11 @@ class Cache:
 
 def attention(cache, q, offsets, lengths, table, max_q, max_length, scale, causal=True, window=0):
     """q float64 [T][H][D] -> dict of float64 arrays: out, lse [T][H], written [T] and, for the
-    tolerance, size = sum p |v| and spread = the largest sum_d |scale q k| of a visible position."""
+    tolerance, size = sum p |v|, all = sum |v| and spread = the largest sum_d |scale q k| of a visible position."""
     T, H, D = q.shape
     G = H // cache.heads
     got = {"out": np.zeros((T, H, D)), "lse": np.full((T, H), -np.inf), "written": np.zeros(T, bool),
-           "size": np.zeros((T, H, D)), "spread": np.zeros((T, H)), "count": np.zeros((T, H))}
+           "size": np.zeros((T, H, D)), "all": np.zeros((T, H, D)), "spread": np.zeros((T, H)), "count": np.zeros((T, H))}
     for b in range(len(lengths)):
         first = min(max(int(offsets[b]), 0), T)
         end = min(max(int(offsets[b + 1]), first), T)
@@ -98,6 +98,7 @@ def attention(cache, q, offsets, lengths, table, max_q, max_length, scale, causa
                 w = e / e.sum(0)
                 got["out"][row] = np.einsum("nh,nhd->hd", w, vv)
                 got["size"][row] = np.einsum("nh,nhd->hd", w, np.abs(vv))
+                got["all"][row] = np.abs(vv).sum(0)
                 got["spread"][row] = np.einsum("hd,nhd->nh", np.abs(q[row]), np.abs(kk)).max(0) * abs(scale)
             bad = ~np.isfinite(q[row]).all(-1)
             got["out"][row][bad], got["lse"][row][bad] = np.nan, np.nan
@@ -111,13 +112,15 @@ def check_attention(out, lse, want, dtype, what=""):
     (256 + 2 + 4) 2^-23 spread, and 2^-22 of the exponential. Weights change by twice that (numerator and norm); the
     sums over the positions add a step for each, in the norm and in the values, and so do
     the rescalings of the running maximum (at most one for each). Weights are
-    rounded to float16, 2^-11 of each (float32: to two, 2^-22). Then the rounding to dtype."""
+    rounded to float16, 2^-11 of each (float32: to two, 2^-22), and as they are held times 2^12,
+    whose least step's half is 2^-25, by at most 2^-37 of the largest where they are smaller
+    still: 2^-37 sum |v|. Then the rounding to dtype."""
     written = want["written"]
     o, ref = out.double().cpu().numpy(), want["out"]
     delta = (262 * 2.0 ** -23 * want["spread"] + 2.0 ** -22)[..., None]
     steps = (3 * want["count"][..., None] + 64) * 2.0 ** -23
     weight = 2.0 ** -22 if dtype == torch.float32 else 2.0 ** -11
-    tol = want["size"] * (2 * delta + steps + weight) + fp4.HALF_STEP[dtype] * (1 + 2.0 ** -7) * np.abs(ref) + fp4.LEAST[dtype]
+    tol = want["size"] * (2 * delta + steps + weight) + 2.0 ** -37 * want["all"] + fp4.HALF_STEP[dtype] * (1 + 2.0 ** -7) * np.abs(ref) + fp4.LEAST[dtype]
     nan = np.isnan(ref)
     assert np.array_equal(np.isnan(o)[written], nan[written]), f"{what}: NaN at other places"
     fine = written[:, None, None] & ~nan

@@ -278,6 +278,12 @@ inline uint64_t __ballot(bool one)
 inline int __ffsll(unsigned long long v) { return __builtin_ffsll((long long)v); }
 inline int __popcll(unsigned long long v) { return __builtin_popcountll(v); }
 inline int atomicAdd(int *p, int v) { return (*p += v) - v; }
+inline uint32_t atomicOr(uint32_t *p, uint32_t v)
+{
+    const uint32_t was = *p;
+    *p |= v;
+    return was;
+}
 inline float __expf(float v) { return expf(v); }
 
 template <typename A, typename B>

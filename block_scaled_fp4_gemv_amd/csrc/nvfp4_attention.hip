@@ -29,7 +29,7 @@ struct AttParams {
     float *lse;
     const int32_t *offsets, *lengths, *table;
     int64_t q_token, q_head;                    // bytes
-    int64_t code_page, scale_page;
+    uint32_t code_page, scale_page;
     int32_t T, H, B, width, pages, shift, heads, G, D;
     int32_t max_q, max_length, window, causal, dtype;
     int32_t splits, chunk;                      // of a sequence's positions; chunk in tiles of 64
@@ -121,23 +121,34 @@ __device__ __attribute__((always_inline)) inline void load8(const uint8_t *x, in
 
 // A row of q as float16 times 2^e, the largest value in [2^14, 2^15): bfloat16 and float16
 // rows are exact so (below 2^-29 of the largest to 2^-40 of it), of float32 ones the second part
-// holds what the first leaves. Returns the logits' factor of the row, NaN if a value is not finite.
+// holds what the first leaves. The logits' factor of the row is NaN if a value is not finite.
 template <int N, int PARTS>
 struct QRow {
     half8_t part[PARTS][N];
 };
 
-__device__ __attribute__((always_inline)) inline int row_exponent(float top)
+struct RowScale {
+    float sign;                                 // of the factor, or 0: it goes into q
+    int e;
+    float factor;                               // what is left: positive, or NaN
+};
+
+// With a positive factor the largest logit is that of the largest product, and a mask's
+// -inf stays -inf through the multiplication.
+__device__ __attribute__((always_inline)) inline RowScale row_scale(float top, float factor, bool real, bool finite)
 {
-    return top > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
+    const int e = top > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
+    const float f = real ? __builtin_ldexpf(factor, -e) : 0.0f;
+    const bool zero = f == 0.0f;
+    return {zero ? 0.0f : f < 0.0f ? -1.0f : 1.0f, e, zero ? 1.0f : finite ? fabsf(f) : __builtin_nanf("")};
 }
 
 template <int N, int PARTS>
-__device__ __attribute__((always_inline)) inline void to_parts(const float (&v)[8], int e, QRow<N, PARTS> &q, int f)
+__device__ __attribute__((always_inline)) inline void to_parts(const float (&v)[8], const RowScale &scale, QRow<N, PARTS> &q, int f)
 {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float x = __builtin_ldexpf(v[j], e);
+        const float x = __builtin_ldexpf(v[j] * scale.sign, scale.e);
         const _Float16 high = (_Float16)x;
         q.part[0][f][j] = high;
         if constexpr (PARTS == 2)
@@ -218,12 +229,12 @@ __device__ __attribute__((always_inline)) inline bool last_of_splits(const AttPa
 }
 
 // Adds the splits' partial results of a tile's rows in the order of the splits and stores
-// them, 8 splits' loads in flight. `norms`: LDS for [splits][rows] of them.
+// them, 16 splits' loads in flight. `norms`: LDS for [splits][rows] of them.
 template <int D, int THREADS>
 __device__ __attribute__((always_inline)) inline void join_splits(const AttParams &p, const Sequence &s, int hk, uint32_t tile,
                                                                   int row0, int rows, int splits, float gv, Norm *norms)
 {
-    constexpr int AHEAD = 8;
+    constexpr int AHEAD = 16;
     const float *sums = p.sums + (int64_t)tile * p.splits * p.most_rows * D;
     const float *from = p.norms + (int64_t)tile * p.splits * p.most_rows * 2;
     for (int i = (int)threadIdx.x; i < splits * rows; i += THREADS) {
@@ -259,11 +270,40 @@ __device__ __attribute__((always_inline)) inline void join_splits(const AttParam
     }
 }
 
-// largest (sum) over the lanes of one row: l, l ^ 16, l ^ 32, l ^ 48
-__device__ __attribute__((always_inline)) inline float max_of_row(float v)
+// Lanes l and l ^ 32 (l ^ 16): both values in both, in one order, without LDS.
+struct Both {
+    float a, b;
+};
+__device__ __attribute__((always_inline)) inline Both across32(float v)
 {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    return {__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1])};
+}
+__device__ __attribute__((always_inline)) inline Both across16(float v)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    return {__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1])};
+}
+// largest (sum) over lanes l and l ^ 32; over l, l ^ 16, l ^ 32, l ^ 48
+__device__ __attribute__((always_inline)) inline float max_of_2(float v)
+{
+    const Both x = across32(v);
+    return fmaxf(x.a, x.b);
+}
+__device__ __attribute__((always_inline)) inline float max_of_4(float v)
+{
+    const Both x = across16(v);
+    return max_of_2(fmaxf(x.a, x.b));
+}
+__device__ __attribute__((always_inline)) inline float sum_of_2(float v)
+{
+    const Both x = across32(v);
+    return x.a + x.b;
+}
+__device__ __attribute__((always_inline)) inline float sum_of_4(float v)
+{
+    const Both x = across16(v);
+    return sum_of_2(x.a + x.b);
 }
 
 // Which of a sequence's positions a workgroup takes: tiles of 64 from `lo` on.
@@ -310,7 +350,7 @@ __device__ __attribute__((always_inline)) inline void landed()
 //     order. Its codes come from LDS transposed (16 positions of one value per
 //     lane), so a pair of codes is two positions, and so is a pair of scales.
 template <int D, int NQ, bool F32>
-__global__ __launch_bounds__(kRowsThreads) void nvfp4_attention_rows_kernel(AttParams p)
+__global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 ? 2 : 1) void nvfp4_attention_rows_kernel(AttParams p)
 {
     using S = RowsTile<D>;
     using St = Steps<D>;
@@ -319,8 +359,11 @@ __global__ __launch_bounds__(kRowsThreads) void nvfp4_attention_rows_kernel(AttP
     __shared__ uint32_t s_ticket;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64), lane = (int)threadIdx.x % 64;
     const int i = lane % 16, g = lane / 16;
-    const uint32_t tile = blockIdx.x / (uint32_t)p.splits;
-    const int split = (int)(blockIdx.x % (uint32_t)p.splits);
+    // Splits outermost: neighbouring workgroups, which run on different XCDs, are different
+    // sequences and heads. (Innermost, every XCD had one of the splits: those whose splits
+    // lie behind most sequences' ends stood idle, 172 us for 64 sequences of 1024 to 8192 positions.)
+    const uint32_t tiles = (uint32_t)p.B * (uint32_t)p.heads, tile = blockIdx.x % tiles;
+    const int split = (int)(blockIdx.x / tiles);
     const int b = (int)(tile / (uint32_t)p.heads), hk = (int)(tile % (uint32_t)p.heads);
     const Sequence s = sequence_of(p, b);
     const int queries = min(s.n, p.max_q);
@@ -330,44 +373,6 @@ __global__ __launch_bounds__(kRowsThreads) void nvfp4_attention_rows_kernel(AttP
     const Span span = span_of(p, s, 0, queries, split);
     if (split >= span.splits)
         return;
-
-    // --- this lane's rows of q
-    const float factor = p.scale * (p.gk ? *p.gk : 1.0f) * kLog2e;
-    QRow<St::N, PARTS> q[NQ];
-    float rf[NQ];
-    int32_t begin[NQ], end[NQ];
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-        const int r = 16 * n + i, tok = r / p.G, pos = s.length - s.n + tok;
-        const bool real = r < rows;
-        end[n] = p.causal ? min(s.length, pos + 1) : s.length;
-        begin[n] = p.window ? max(0, pos - p.window + 1) : 0;
-        const uint8_t *x = p.q + (int64_t)(s.first + (real ? tok : 0)) * p.q_token +
-                           (int64_t)(hk * p.G + (real ? r % p.G : 0)) * p.q_head;
-        float v[St::N][8], top = 0.0f;
-        bool finite = true;
-#pragma unroll
-        for (int f = 0; f < St::N; ++f) {
-            load8(x + (St::base(f) + St::mult(f) * g + St::add(f)) * (F32 ? 4 : 2), F32 ? NVFP4_F32 : p.dtype, v[f]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const bool good = __builtin_isfinite(v[f][j]);
-                finite &= good;
-                v[f][j] = good ? v[f][j] : 0.0f;
-                top = fmaxf(top, fabsf(v[f][j]));
-            }
-        }
-        top = max_of_row(top);
-        finite = max_of_row(finite ? 0.0f : 1.0f) == 0.0f;
-        const int e = row_exponent(top);
-#pragma unroll
-        for (int f = 0; f < St::N; ++f)
-            to_parts(v[f], e, q[n], f);
-        rf[n] = !real ? 0.0f : finite ? __builtin_ldexpf(factor, -e) : __builtin_nanf("");
-    }
-    // positions that all rows see: no mask within them
-    const int32_t all_from = p.window ? max(0, s.length - s.n + queries - p.window) : 0;
-    const int32_t all_to = p.causal ? min(s.length, s.length - s.n + 1) : s.length;
 
     float4_t acc[NQ][NB];
     float top[NQ], sum[NQ];
@@ -409,9 +414,9 @@ __global__ __launch_bounds__(kRowsThreads) void nvfp4_attention_rows_kernel(AttP
         for (int a = 0; a < 4; ++a) {
             const bool ok = (uint32_t)e[a] < (uint32_t)p.pages;
             there |= (uint32_t)ok << a;
-            const int64_t page = ok ? e[a] : 0;
-            const int64_t row = ((int64_t)hk << p.shift) + ((first_position + n * 64 + a * 16) & mask);
-            const int64_t codes = page * p.code_page + row * S::RB, scales = page * p.scale_page + row * S::SB;
+            const uint64_t page = ok ? (uint32_t)e[a] : 0u;
+            const uint32_t row = ((uint32_t)hk << p.shift) + (uint32_t)((first_position + n * 64 + a * 16) & mask);
+            const uint64_t codes = page * p.code_page + row * S::RB, scales = page * p.scale_page + row * S::SB;
 #pragma unroll
             for (int c = 0; c < S::kCopies16; ++c) {
                 const uint32_t r = at_row[c];
@@ -428,6 +433,52 @@ __global__ __launch_bounds__(kRowsThreads) void nvfp4_attention_rows_kernel(AttP
         }
         return there;
     };
+
+    // the first tile's copies are out before q is loaded
+    int32_t n = span.first + wave, e[4];
+    uint32_t there = 0u;
+    entries(n, e);
+    if (n < span.end)
+        there = issue(n, e, 0);
+    entries(n + kRowsWaves, e);
+
+    // --- this lane's rows of q
+    const float factor = p.scale * (p.gk ? *p.gk : 1.0f) * kLog2e;
+    QRow<St::N, PARTS> q[NQ];
+    float rf[NQ];
+    int32_t begin[NQ], end[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        const int r = 16 * n + i, tok = r / p.G, pos = s.length - s.n + tok;
+        const bool real = r < rows;
+        end[n] = p.causal ? min(s.length, pos + 1) : s.length;
+        begin[n] = p.window ? max(0, pos - p.window + 1) : 0;
+        const uint8_t *x = p.q + (int64_t)(s.first + (real ? tok : 0)) * p.q_token +
+                           (int64_t)(hk * p.G + (real ? r % p.G : 0)) * p.q_head;
+        float v[St::N][8], top = 0.0f;
+        bool finite = true;
+#pragma unroll
+        for (int f = 0; f < St::N; ++f) {
+            load8(x + (St::base(f) + St::mult(f) * g + St::add(f)) * (F32 ? 4 : 2), F32 ? NVFP4_F32 : p.dtype, v[f]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool good = __builtin_isfinite(v[f][j]);
+                finite &= good;
+                v[f][j] = good ? v[f][j] : 0.0f;
+                top = fmaxf(top, fabsf(v[f][j]));
+            }
+        }
+        top = max_of_4(top);
+        finite = max_of_4(finite ? 0.0f : 1.0f) == 0.0f;
+        const RowScale scale = row_scale(top, factor, real, finite);
+#pragma unroll
+        for (int f = 0; f < St::N; ++f)
+            to_parts(v[f], scale, q[n], f);
+        rf[n] = scale.factor;
+    }
+    // positions that all rows see: no mask within them
+    const int32_t all_from = p.window ? max(0, s.length - s.n + queries - p.window) : 0;
+    const int32_t all_to = p.causal ? min(s.length, s.length - s.n + 1) : s.length;
 
     auto compute = [&](int32_t n, uint32_t there, const uint8_t *tile_at) {
         const int32_t t0 = first_position + n * 64;
@@ -478,9 +529,10 @@ __global__ __launch_bounds__(kRowsThreads) void nvfp4_attention_rows_kernel(AttP
             for (int m = 0; m < NQ; ++m)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    logit[m][a][e] = c[m][e] * rf[m];
+                    logit[m][a][e] = c[m][e];
         }
         if (there != 15u || t0 < all_from || t0 + 64 > all_to) {
+            asm volatile("" : : : "memory");                            // a branch, not 16 selects in every tile
 #pragma unroll
             for (int m = 0; m < NQ; ++m)
 #pragma unroll
@@ -497,28 +549,45 @@ __global__ __launch_bounds__(kRowsThreads) void nvfp4_attention_rows_kernel(AttP
         {
             const int32_t t = t0 + lane;
             const bool seen = (there >> (lane / 16) & 1u) && t >= span.lo && t < span.hi;
-            const uint8_t *sc = tile_at + S::kOffVs + lane * S::SB;
-            _Float16 *to = (_Float16 *)(ring + S::kStages * S::kStage) + (lane / 4 % 4) * 16 + lane / 16 * 4 + lane % 4;
-            uint32_t nan = 0u;
+            uint32_t w[(NB + 3) / 4], nan = 0u;
+            w[(NB - 1) / 4] = 0u;                                       // 6 blocks end inside a word
+            __builtin_memcpy(w, tile_at + S::kOffVs + lane * S::SB, NB);
 #pragma unroll
-            for (int k = 0; k < NB; k += 2) {
-                const uint32_t two = *(const uint16_t *)(sc + k);
-                half2_t h = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(two, 1.0f, false);
-                nan |= (uint32_t)((two & 0x7Fu) == 0x7Fu) << k | (uint32_t)((two & 0x7F00u) == 0x7F00u) << (k + 1);
-                h.x = seen && (two & 0x7Fu) != 0x7Fu ? h.x : (_Float16)0.0f;
-                h.y = seen && (two & 0x7F00u) != 0x7F00u ? h.y : (_Float16)0.0f;
-                to[k * 64] = h.x;
-                to[k * 64 + 64] = h.y;
+            for (int k = 0; k < (NB + 3) / 4; ++k) {
+                w[k] = seen ? w[k] : 0u;
+                nan |= ((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;      // bytes of 0x7F and 0xFF
             }
-            uint64_t left = __ballot(seen && nan);
-            while (left) {
-                const int k = __builtin_ctzll(left);
-                left &= left - 1;
-                const uint32_t blocks = (uint32_t)__builtin_amdgcn_readlane((int)nan, k);
+            uint64_t left = __ballot(nan != 0u);
+            if (left) {
+                asm volatile("" : : : "memory");
+                uint32_t mine = 0u;
 #pragma unroll
-                for (int m = 0; m < NQ; ++m)
-                    if (t0 + k >= begin[m] && t0 + k < end[m])
-                        nan_blocks[m] |= blocks;
+                for (int k = 0; k < NB; ++k) {
+                    const bool bad = (w[k / 4] >> (8 * (k % 4)) & 0x7Fu) == 0x7Fu;
+                    mine |= (uint32_t)bad << k;
+                    w[k / 4] &= bad ? ~(0xFFu << (8 * (k % 4))) : ~0u;
+                }
+                while (left) {
+                    const int k = __builtin_ctzll(left);
+                    left &= left - 1;
+                    const uint32_t blocks = (uint32_t)__builtin_amdgcn_readlane((int)mine, k);
+#pragma unroll
+                    for (int m = 0; m < NQ; ++m)
+                        if (t0 + k >= begin[m] && t0 + k < end[m])
+                            nan_blocks[m] |= blocks;
+                }
+            }
+            _Float16 *to = (_Float16 *)(ring + S::kStages * S::kStage) + (lane / 4 % 4) * 16 + lane / 16 * 4 + lane % 4;
+#pragma unroll
+            for (int k = 0; k < NB; k += 4) {
+                const half2_t low = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[k / 4], 1.0f, false);
+                to[k * 64] = low.x;
+                to[k * 64 + 64] = low.y;
+                if (k + 2 < NB) {
+                    const half2_t high = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[k / 4], 1.0f, true);
+                    to[k * 64 + 128] = high.x;
+                    to[k * 64 + 192] = high.y;
+                }
             }
         }
         settle();                                                       // the scales are in place
@@ -530,7 +599,7 @@ __global__ __launch_bounds__(kRowsThreads) void nvfp4_attention_rows_kernel(AttP
 #pragma unroll
             for (int k = 1; k < 16; ++k)
                 most = fmaxf(most, logit[m][k / 4][k % 4]);
-            most = fmaxf(top[m], max_of_row(most));
+            most = fmaxf(top[m], max_of_4(most) * rf[m]);
             if (__ballot(most > top[m])) {
                 const float keep = weight_of(top[m], most);
                 sum[m] *= keep;
@@ -539,10 +608,10 @@ __global__ __launch_bounds__(kRowsThreads) void nvfp4_attention_rows_kernel(AttP
                     acc[m][k] *= keep;
                 top[m] = most;
             }
-            const float from = (most == -__builtin_inff() ? 0.0f : most) - kShift;
+            const float less = kShift - (most == -__builtin_inff() ? 0.0f : most);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-                const float w = __builtin_amdgcn_exp2f(logit[m][k / 4][k % 4] - from);
+                const float w = __builtin_amdgcn_exp2f(fmaf(logit[m][k / 4][k % 4], rf[m], less));
                 sum[m] += w;
                 const _Float16 high = (_Float16)w;
                 prob[0][m][k / 8][k % 8] = high;
@@ -571,24 +640,18 @@ __global__ __launch_bounds__(kRowsThreads) void nvfp4_attention_rows_kernel(AttP
     };
 
     // --- the loop: tile n's copies are awaited while those of the next are out
-    int32_t n = span.first + wave;
-    if (n < span.end) {
-        int32_t e[4];
-        entries(n, e);
-        uint32_t there = issue(n, e, 0);
-        entries(n + kRowsWaves, e);
-        int stage = 0;
-        for (; n + kRowsWaves < span.end; n += kRowsWaves) {
-            const uint32_t next = issue(n + kRowsWaves, e, stage ^ 1);
+    for (int stage = 0; n < span.end; n += kRowsWaves, stage ^= 1) {
+        uint32_t next = 0u;
+        if (n + kRowsWaves < span.end) {
+            next = issue(n + kRowsWaves, e, stage ^ 1);
             entries(n + 2 * kRowsWaves, e);
             landed<S::kCopies>();
-            compute(n, there, ring + stage * S::kStage);
-            settle();                                                   // this stage is read: the next round refills it
-            there = next;
-            stage ^= 1;
+        } else {
+            landed<0>();
         }
-        landed<0>();
         compute(n, there, ring + stage * S::kStage);
+        settle();                                                       // this stage is read: the next round refills it
+        there = next;
     }
 
     // --- the waves' results through LDS: sums [wave][16 NQ][D], norms
@@ -597,8 +660,7 @@ __global__ __launch_bounds__(kRowsThreads) void nvfp4_attention_rows_kernel(AttP
     Norm *const w_norms = (Norm *)(lds + kRowsWaves * 16 * NQ * D * 4);
 #pragma unroll
     for (int m = 0; m < NQ; ++m) {
-        sum[m] += __shfl_xor(sum[m], 16);
-        sum[m] += __shfl_xor(sum[m], 32);
+        sum[m] = sum_of_4(sum[m]);
         const int r = wave * 16 * NQ + 16 * m + i;
         if (g == 0)
             w_norms[r] = {top[m], sum[m]};
@@ -692,8 +754,8 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64), lane = (int)threadIdx.x % 64;
     const int i = lane % 32, h = lane / 32;
     // the last rows, which see most under the causal mask, first
-    const uint32_t pairs = (uint32_t)p.B * (uint32_t)p.heads, id = blockIdx.x / (uint32_t)p.splits;
-    const int split = (int)(blockIdx.x % (uint32_t)p.splits), rt = (int)(((uint32_t)p.row_tiles - 1u) - id / pairs);
+    const uint32_t pairs = (uint32_t)p.B * (uint32_t)p.heads, tiles = pairs * (uint32_t)p.row_tiles, id = blockIdx.x % tiles;
+    const int split = (int)(blockIdx.x / tiles), rt = (int)(((uint32_t)p.row_tiles - 1u) - id / pairs);
     const int b = (int)(id % pairs / (uint32_t)p.heads), hk = (int)(id % pairs % (uint32_t)p.heads);
     const Sequence s = sequence_of(p, b);
     const int queries = min(s.n, p.max_q);
@@ -730,13 +792,13 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
                 top = fmaxf(top, fabsf(v[c][j]));
             }
         }
-        top = fmaxf(top, __shfl_xor(top, 32));
-        finite = fmaxf(finite ? 0.0f : 1.0f, __shfl_xor(finite ? 0.0f : 1.0f, 32)) == 0.0f;
-        const int e = row_exponent(top);
+        top = max_of_2(top);
+        finite = max_of_2(finite ? 0.0f : 1.0f) == 0.0f;
+        const RowScale scale = row_scale(top, factor, real, finite);
 #pragma unroll
         for (int c = 0; c < NK; ++c)
-            to_parts(v[c], e, q, c);
-        rf = !real ? 0.0f : finite ? __builtin_ldexpf(factor, -e) : __builtin_nanf("");
+            to_parts(v[c], scale, q, c);
+        rf = scale.factor;
     }
     // positions that some, and that all, of the wave's rows see
     const int w0 = min(32 * wave, rows - 1), w1 = min(32 * wave + 31, rows - 1);
@@ -776,8 +838,8 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
                 continue;
             const bool values = u >= 64 * S::PR;
             const int64_t row = ((int64_t)hk << p.shift) + ((first_position + n * 64 + t) & mask);
-            codes[k] = *(const uint4_t *)((values ? p.vc : p.kc) + page * p.code_page + row * (D / 2) + piece * 16);
-            scales[k] = *(const uint16_t *)((values ? p.vs : p.ks) + page * p.scale_page + row * (D / 16) + piece * 2);
+            codes[k] = *(const uint4_t *)((values ? p.vc : p.kc) + (uint64_t)(uint32_t)page * p.code_page + row * (D / 2) + piece * 16);
+            scales[k] = *(const uint16_t *)((values ? p.vs : p.ks) + (uint64_t)(uint32_t)page * p.scale_page + row * (D / 16) + piece * 2);
         }
     };
     auto stage = [&](int parity) {
@@ -837,9 +899,10 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                logit[t][e] = c[e] * rf;
+                logit[t][e] = c[e];
         }
         if (there != ~0ull || t0 < all_from || t0 + 64 > all_to) {
+            asm volatile("" : : : "memory");                            // a branch, not 32 selects in every tile
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -861,8 +924,7 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
 #pragma unroll
         for (int e = 1; e < 32; ++e)
             most = fmaxf(most, logit[e / 16][e % 16]);
-        most = fmaxf(most, __shfl_xor(most, 32));
-        most = fmaxf(top, most);
+        most = fmaxf(top, max_of_2(most) * rf);
         if (__ballot(most > top)) {
             const float keep = weight_of(top, most);
             sum *= keep;
@@ -871,11 +933,11 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
                 acc[k] *= keep;
             top = most;
         }
-        const float from = (most == -__builtin_inff() ? 0.0f : most) - kShift;
+        const float less = kShift - (most == -__builtin_inff() ? 0.0f : most);
         half8_t prob[PARTS][4];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-            const float w = __builtin_amdgcn_exp2f(logit[e / 16][e % 16] - from);
+            const float w = __builtin_amdgcn_exp2f(fmaf(logit[e / 16][e % 16], rf, less));
             sum += w;
             const _Float16 high = (_Float16)w;
             prob[0][e / 8][e % 8] = high;
@@ -925,7 +987,7 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
     }
 
     // --- results
-    sum += __shfl_xor(sum, 32);
+    sum = sum_of_2(sum);
     const float gv = p.gv ? *p.gv : 1.0f;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
@@ -1149,7 +1211,7 @@ nvfp4_status_t nvfp4_cache_attention(const nvfp4_cache_t *cache, const void *q, 
     p.gk = cache->k_scale, p.gv = cache->v_scale;
     p.offsets = offsets, p.lengths = lengths, p.table = table;
     p.q_token = attention->q_token_stride * (int64_t)size, p.q_head = attention->q_head_stride * (int64_t)size;
-    p.code_page = cache->code_page_stride, p.scale_page = cache->scale_page_stride;
+    p.code_page = (uint32_t)cache->code_page_stride, p.scale_page = (uint32_t)cache->scale_page_stride;
     p.T = (int32_t)T, p.H = (int32_t)H, p.B = (int32_t)B, p.width = (int32_t)table_width, p.pages = (int32_t)cache->pages;
     p.shift = __builtin_ctzll((uint64_t)cache->page_size);
     p.heads = (int32_t)cache->heads, p.G = (int32_t)(H / cache->heads), p.D = (int32_t)cache->head_size;

@@ -21,7 +21,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int64_t kMaxGrid = 0xFFFFFF;          // workgroups of 256 threads in 2^32 work items
-constexpr int64_t kMaxStride = INT64_C(1) << 40;
+constexpr int64_t kMaxStride = INT64_C(1) << 40, kMaxPage = INT64_C(1) << 32;
 
 struct RowParams {
     uint8_t *codes[2], *scales[2];              // keys, values
@@ -181,7 +181,7 @@ nvfp4_status_t nvfp4_check_cache(const nvfp4_cache_t *c)
     if (rows * (D / 2) > INT32_MAX)
         return NVFP4_ERR_INVALID_CACHE;
     if (c->code_page_stride < rows * (D / 2) || c->scale_page_stride < rows * (D / 16) || c->code_page_stride % 16 ||
-        c->scale_page_stride % 16 || c->code_page_stride >= kMaxStride || c->scale_page_stride >= kMaxStride)
+        c->scale_page_stride % 16 || c->code_page_stride >= kMaxPage || c->scale_page_stride >= kMaxPage)
         return NVFP4_ERR_INVALID_STRIDE;
     if (!aligned(c->k_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_codes, 16) || !aligned(c->v_scales, 16) ||
         (c->k_scale && !aligned(c->k_scale, 4)) || (c->v_scale && !aligned(c->v_scale, 4)))

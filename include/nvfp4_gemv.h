@@ -603,7 +603,7 @@ nvfp4_status_t nvfp4_rope_frequencies(double *frequencies, int64_t R, double bas
  * place in the page. Requirements: 1 <= pages < 2^31; page_size a power of two,
  * 16..4096; 1 <= heads <= 4096; head_size a multiple of 32, 32..256; a page's
  * codes below 2^31 bytes; codes and scales 16-byte aligned, page strides
- * multiples of 16, at least a page and below 2^40; k_scale, v_scale 4-byte aligned.
+ * multiples of 16, at least a page and below 2^32; k_scale, v_scale 4-byte aligned.
  */
 typedef struct {
     void *k_codes, *k_scales, *v_codes, *v_scales;

@@ -429,6 +429,16 @@ inline cpu_wave_float4 cpu_wave_mfma16(cpu_wave_half8 a, cpu_wave_half8 b, cpu_w
     return c;
 }
 
+// halves (odd and even rows of 16) of two registers exchanged
+typedef uint32_t cpu_wave_uint2 __attribute__((ext_vector_type(2)));
+inline cpu_wave_uint2 cpu_wave_swap(uint32_t a, uint32_t b, uint32_t step)
+{
+    const uint32_t lane = threadIdx.x % 64;
+    const bool low = !(lane & step);
+    const uint32_t other = (uint32_t)cpu_wave::from(low ? b : a, (int)(lane ^ step));
+    return low ? (cpu_wave_uint2){a, other} : (cpu_wave_uint2){other, b};
+}
+
 // Transposed reads of 8 bytes per lane among 16 lanes: 16 codes, of which lane i gets the i-th of
 // each lane; 4 float16, of which lane i gets the (i % 4)-th of lanes i / 4 + 0, 4, 8, 12
 typedef int cpu_wave_int2 __attribute__((ext_vector_type(2)));
@@ -484,6 +494,8 @@ inline void cpu_wave_s_waitcnt(int imm)
 #define __builtin_amdgcn_mfma_f32_16x16x32_f16 cpu_wave_mfma16
 #define __builtin_amdgcn_ds_read_tr4_b64_v2i32 cpu_wave_tr4
 #define __builtin_amdgcn_ds_read_tr16_b64_v4i16 cpu_wave_tr16
+#define __builtin_amdgcn_permlane32_swap(a, b, f, c) cpu_wave_swap(a, b, 32)
+#define __builtin_amdgcn_permlane16_swap(a, b, f, c) cpu_wave_swap(a, b, 16)
 #define __builtin_amdgcn_exp2f(v) exp2f(v)
 #define __builtin_amdgcn_logf(v) log2f(v)
 #define __builtin_amdgcn_s_waitcnt cpu_wave_s_waitcnt

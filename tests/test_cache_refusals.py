@@ -64,7 +64,7 @@ BAD_CACHES = [(dict(kc=None), NULL), (dict(ks=None), NULL), (dict(vc=None), NULL
               (dict(pages=0), CACHE), (dict(pages=2 ** 31), CACHE), (dict(ps=8), CACHE), (dict(ps=48), CACHE), (dict(ps=8192), CACHE),
               (dict(heads=0), CACHE), (dict(heads=4097), CACHE), (dict(D=16), CACHE), (dict(D=48), CACHE), (dict(D=288), CACHE),
               (dict(heads=4096, ps=4096, D=256), CACHE), (dict(cp=2032), STRIDE), (dict(sp=240), STRIDE), (dict(cp=2056), STRIDE),
-              (dict(sp=264), STRIDE), (dict(cp=2 ** 40), STRIDE), (dict(kc=P + 8), ALIGN), (dict(ks=P + 8), ALIGN),
+              (dict(sp=264), STRIDE), (dict(cp=2 ** 40), STRIDE), (dict(sp=2 ** 32), STRIDE), (dict(kc=P + 8), ALIGN), (dict(ks=P + 8), ALIGN),
               (dict(vc=P + 4), ALIGN), (dict(vs=P + 4), ALIGN), (dict(gk=P + 2), ALIGN), (dict(gv=P + 1), ALIGN)]
 
 

@@ -55,6 +55,7 @@ __device__ __attribute__((always_inline)) inline Sequence sequence_of(const AttP
 // ------------------------------------------------------------------ rows kernel
 
 typedef float float4_t __attribute__((ext_vector_type(4)));
+typedef int32_t int4_t __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 // Probabilities are kept times 2^12, the largest at 4096: float16 then holds them to 2^-26
@@ -75,27 +76,31 @@ struct Steps {
     static constexpr int add(int f) { return f < 4 * n128 ? f % 4 * 8 : f < 4 * n128 + 2 * n64 ? (f - 4 * n128) * 8 : 0; }
 };
 
-// A tile of 64 positions in LDS: codes of K and of V, their scales, each of 4 subtiles
-// of 16 positions (a page holds whole subtiles).
+// A tile of 64 positions: 4 subtiles of 16 (a page holds whole subtiles). Codes and scales
+// of the next tile wait in registers, K's as the products take them; V's codes and scales
+// go through the wave's own LDS to be transposed.
 template <int D>
 struct RowsTile {
     static constexpr int RB = D / 2, SB = D / 16, NB = D / 16;     // bytes of a row's codes, of its scales; blocks
-    static constexpr int kCopies16 = (16 * RB + 1023) / 1024;      // 16-byte copies of a wave per subtile
-    static constexpr int kOffV = 64 * RB, kOffKs = 2 * 64 * RB, kOffVs = kOffKs + 64 * SB, kStage = kOffVs + 64 * SB;
-    static constexpr int kCopies = 4 * (2 * kCopies16 + 2);        // of a wave per tile
+    static constexpr int kRuns = D / 128 + D % 128 / 64 + D % 64 / 32;
+    static constexpr int PB = D == 64 ? 8 : 16;                    // bytes of V's codes that a lane loads at once
+    static constexpr int kLoads = (16 * RB / PB + 63) / 64;        // of them per subtile
     static constexpr int kScales = NB * 64 * 2;                    // V's scales as float16 [block][64]
-    static constexpr int kStages = 2;
-    static constexpr int kWave = kStages * kStage + kScales;
-    // Places of a row's 16-byte pieces, so that the lanes that read at once meet every bank:
-    // 16 neighbouring rows for K, for V four rows of each subtile.
-    __device__ static constexpr int swizzle_k(int r)
-    {
-        return D == 64 || D == 192 ? r / 8 & 1 : D == 128 ? r / 4 & 3 : D == 256 ? r / 2 & 7 : 0;
-    }
+    static constexpr int kWave = 64 * RB + kScales;
+    // Places of a row's pieces of PB bytes, so that the lanes that read at once, four rows of each
+    // subtile, meet more banks: all of them for 64, 128 and 256.
     __device__ static constexpr int swizzle_v(int r)
     {
-        return D == 64 || D == 192 ? r / 16 & 1 : D == 128 ? r / 16 & 3 : D == 256 ? (r / 16 * 2 + r % 4 / 2) & 7 : 0;
+        return D == 64 || D == 128 ? r / 16 & 3 : D == 192 ? r / 16 & 1 : D == 256 ? (r / 16 * 2 + r % 4 / 2) & 7 : 0;
     }
+    using Piece = std::conditional_t<PB == 8, uint2_t, uint4_t>;
+    struct Raw {
+        uint4_t k128[4][D / 128 ? D / 128 : 1];                    // a lane's codes of each run, and its scales
+        uint2_t k64[4];
+        uint32_t k32[4], k_scales[4][kRuns];
+        Piece v[4][kLoads];
+        uint32_t v_scales[(NB + 3) / 4];
+    };
 };
 
 // 8 neighbouring values of q as float32
@@ -229,12 +234,12 @@ __device__ __attribute__((always_inline)) inline bool last_of_splits(const AttPa
 }
 
 // Adds the splits' partial results of a tile's rows in the order of the splits and stores
-// them, 16 splits' loads in flight. `norms`: LDS for [splits][rows] of them.
+// them, 32 splits' loads in flight. `norms`: LDS for [splits][rows] of them.
 template <int D, int THREADS>
 __device__ __attribute__((always_inline)) inline void join_splits(const AttParams &p, const Sequence &s, int hk, uint32_t tile,
                                                                   int row0, int rows, int splits, float gv, Norm *norms)
 {
-    constexpr int AHEAD = 16;
+    constexpr int AHEAD = 32;
     const float *sums = p.sums + (int64_t)tile * p.splits * p.most_rows * D;
     const float *from = p.norms + (int64_t)tile * p.splits * p.most_rows * 2;
     for (int i = (int)threadIdx.x; i < splits * rows; i += THREADS) {
@@ -327,30 +332,23 @@ __device__ __attribute__((always_inline)) inline Span span_of(const AttParams &p
     return v;
 }
 
-// This wave's reads and writes of LDS are done, for all its lanes; its copies are, but the last N.
-__device__ __attribute__((always_inline)) inline void settle()
+// Accesses to LDS of this wave's lanes stay on their side of this point. The hardware
+// carries a wave's out in order; nothing is waited for.
+__device__ __attribute__((always_inline)) inline void settle_order()
 {
-    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
-    __builtin_amdgcn_wave_barrier();
-}
-template <int N>
-__device__ __attribute__((always_inline)) inline void landed()
-{
-    wait_copies<N>();
     asm volatile("" : : : "memory");
     __builtin_amdgcn_wave_barrier();
 }
 
 // Few rows: n queries times the heads that share a key head, at most 16 * NQ. Every wave
-// takes tiles of 64 positions in turn, with a ring of its own in LDS that copies fill while
-// it works on the tile before.
+// takes tiles of 64 positions in turn; the next one's codes and scales come while it works on one.
 //   S^T = K Q^T by 16 x 16 x 32 products, K the first operand: a lane then has the logits
 //     of one row (lane % 16), positions 16 a + 4 g + b in register b of subtile a.
 //   O^T = V^T P^T: a lane's P registers are its k-range as they stand, if V's operand has the same
 //     order. Its codes come from LDS transposed (16 positions of one value per
 //     lane), so a pair of codes is two positions, and so is a pair of scales.
 template <int D, int NQ, bool F32>
-__global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 ? 2 : 1) void nvfp4_attention_rows_kernel(AttParams p)
+__global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 || NQ == 1 ? 2 : 1) void nvfp4_attention_rows_kernel(AttParams p)
 {
     using S = RowsTile<D>;
     using St = Steps<D>;
@@ -387,60 +385,82 @@ __global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 ? 2
             acc[n][k] = {0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    // --- copies. Lane offsets of a subtile's codes within its rows.
-    uint8_t *const ring = lds + wave * S::kWave;
-    const uint32_t ring_at = (uint32_t)(uintptr_t)ring;
-    uint32_t at_row[S::kCopies16], at_piece[S::kCopies16];
-#pragma unroll
-    for (int c = 0; c < S::kCopies16; ++c) {
-        const int o = c * 1024 + lane * 16;
-        at_row[c] = (uint32_t)(o / S::RB), at_piece[c] = (uint32_t)(o % S::RB / 16);
-    }
+    // --- loads
+    uint8_t *const mine = lds + wave * S::kWave;
     const int32_t mask = (1 << p.shift) - 1;
     const int32_t first_position = span.lo / 64 * 64;
-    auto entries = [&](int32_t n, int32_t (&e)[4]) {
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            const int32_t t = first_position + n * 64 + a * 16;
-            e[a] = n < span.end && t < span.hi ? p.table[(int64_t)b * p.width + (t >> p.shift)] : -1;
-        }
+    const int32_t *const table = p.table + (int64_t)b * p.width;
+    auto entry_of = [&](int32_t n, int a) -> int32_t {
+        const int32_t t = first_position + n * 64 + a * 16;
+        return n < span.end && t < span.hi ? table[t >> p.shift] : -1;
     };
-    // A subtile that is not there is copied from the cache's first page, so that every
-    // tile has the same number of copies; its bit is 0.
-    auto issue = [&](int32_t n, const int32_t (&e)[4], int stage) -> uint32_t {
+    auto entries = [&](int32_t n) -> int4_t { return {entry_of(n, 0), entry_of(n, 1), entry_of(n, 2), entry_of(n, 3)}; };
+    // A subtile that is not there is read from the cache's first page; its bit is 0.
+    typename S::Raw raw;
+    auto there_of = [&](int4_t e) -> uint32_t {
         uint32_t there = 0u;
-        const uint32_t to = ring_at + stage * S::kStage;
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            const bool ok = (uint32_t)e[a] < (uint32_t)p.pages;
-            there |= (uint32_t)ok << a;
-            const uint64_t page = ok ? (uint32_t)e[a] : 0u;
-            const uint32_t row = ((uint32_t)hk << p.shift) + (uint32_t)((first_position + n * 64 + a * 16) & mask);
-            const uint64_t codes = page * p.code_page + row * S::RB, scales = page * p.scale_page + row * S::SB;
-#pragma unroll
-            for (int c = 0; c < S::kCopies16; ++c) {
-                const uint32_t r = at_row[c];
-                if (c * 1024 + lane * 16 < 16 * S::RB) {
-                    copy16_s(p.kc + codes, r * S::RB + (at_piece[c] ^ (uint32_t)S::swizzle_k((int)r)) * 16, to + a * 16 * S::RB + c * 1024);
-                    copy16_s(p.vc + codes, r * S::RB + (at_piece[c] ^ (uint32_t)S::swizzle_v(16 * a + (int)r)) * 16,
-                           to + S::kOffV + a * 16 * S::RB + c * 1024);
-                }
-            }
-            if (lane < 4 * S::SB) {
-                copy4_s(p.ks + scales, (uint32_t)lane * 4, to + S::kOffKs + a * 16 * S::SB);
-                copy4_s(p.vs + scales, (uint32_t)lane * 4, to + S::kOffVs + a * 16 * S::SB);
-            }
-        }
+        for (int a = 0; a < 4; ++a)
+            there |= (uint32_t)((uint32_t)e[a] < (uint32_t)p.pages) << a;
         return there;
     };
+    auto page_of = [&](int32_t e) -> uint64_t { return (uint32_t)e < (uint32_t)p.pages ? (uint32_t)e : 0u; };
+    auto row_of = [&](int32_t n, int a) -> uint32_t {
+        return ((uint32_t)hk << p.shift) + (uint32_t)((first_position + n * 64 + a * 16) & mask);
+    };
+    auto load_k = [&](int32_t n, int4_t e, int a) {
+        const uint64_t page = page_of(e[a]);
+        const uint32_t row = row_of(n, a);
+        const uint8_t *codes = p.kc + (page * p.code_page + row * S::RB), *scales = p.ks + (page * p.scale_page + row * S::SB);
+#pragma unroll
+        for (int x = 0; x < St::n128; ++x) {
+            raw.k128[a][x] = *(const uint4_t *)(codes + (uint32_t)(i * S::RB + 64 * x + 16 * g));
+            raw.k_scales[a][x] = *(const uint16_t *)(scales + (uint32_t)(i * S::SB + 8 * x + 2 * g));
+        }
+        if constexpr (St::n64 != 0) {
+            raw.k64[a] = *(const uint2_t *)(codes + (uint32_t)(i * S::RB + 64 * St::n128 + 8 * g));
+            raw.k_scales[a][St::n128] = scales[(uint32_t)(i * S::SB + 8 * St::n128 + g)];
+        }
+        if constexpr (St::n32 != 0) {
+            raw.k32[a] = *(const uint32_t *)(codes + (uint32_t)(i * S::RB + 64 * St::n128 + 32 * St::n64 + 4 * g));
+            raw.k_scales[a][S::kRuns - 1] = scales[(uint32_t)(i * S::SB + 8 * St::n128 + 4 * St::n64 + g / 2)];
+        }
+    };
+    // V's codes as they lie; lanes behind a subtile's end read its start again
+    auto load_v = [&](int32_t n, int4_t e) {
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            const uint8_t *codes = p.vc + (page_of(e[a]) * p.code_page + row_of(n, a) * S::RB);
+#pragma unroll
+            for (int c = 0; c < S::kLoads; ++c) {
+                const uint32_t o = (uint32_t)(c * 64 + lane) * S::PB;
+                raw.v[a][c] = *(const typename S::Piece *)(codes + (o < 16 * S::RB ? o : 0u));
+            }
+        }
+        // a lane has the scales of one position
+        const int32_t mine_e = lane < 32 ? (lane < 16 ? e[0] : e[1]) : (lane < 48 ? e[2] : e[3]);
+        const uint32_t row = ((uint32_t)hk << p.shift) + (uint32_t)((first_position + n * 64 + lane) & mask);
+        const uint8_t *scales = p.vs + (page_of(mine_e) * p.scale_page + row * S::SB);
+        if constexpr (S::SB % 4 == 0) {
+#pragma unroll
+            for (int k = 0; k < S::SB / 4; ++k)
+                raw.v_scales[k] = ((const uint32_t *)scales)[k];
+        } else {
+            const uint16_t *two = (const uint16_t *)scales;
+            raw.v_scales[0] = (uint32_t)two[0] | (uint32_t)two[1] << 16;
+            raw.v_scales[1] = two[2];
+        }
+    };
 
-    // the first tile's copies are out before q is loaded
-    int32_t n = span.first + wave, e[4];
-    uint32_t there = 0u;
-    entries(n, e);
-    if (n < span.end)
-        there = issue(n, e, 0);
-    entries(n + kRowsWaves, e);
+    // the first tile's loads are out before q's
+    int32_t n = span.first + wave;
+    int4_t e = entries(n);
+    uint32_t there = there_of(e);
+    load_v(n, e);
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+        load_k(n, e, a);
+    e = entries(n + kRowsWaves);
 
     // --- this lane's rows of q
     const float factor = p.scale * (p.gk ? *p.gk : 1.0f) * kLog2e;
@@ -480,104 +500,50 @@ __global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 ? 2
     const int32_t all_from = p.window ? max(0, s.length - s.n + queries - p.window) : 0;
     const int32_t all_to = p.causal ? min(s.length, s.length - s.n + 1) : s.length;
 
-    auto compute = [&](int32_t n, uint32_t there, const uint8_t *tile_at) {
+    // --- the loop: what the next tile needs is loaded as soon as its registers are free
+    for (; n < span.end; n += kRowsWaves) {
         const int32_t t0 = first_position + n * 64;
-        // --- S^T
-        float logit[NQ][4][4];
+        // --- V's codes and, as float16 in the order of the k-ranges, its scales to LDS; a position that no
+        // row sees has 0 there, and so has a NaN, which is noted for the rows that see it
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            float4_t c[NQ];
+        for (int a = 0; a < 4; ++a)
 #pragma unroll
-            for (int m = 0; m < NQ; ++m)
-                c[m] = {0.0f, 0.0f, 0.0f, 0.0f};
-            const uint8_t *row = tile_at + (16 * a + i) * S::RB, *sc = tile_at + S::kOffKs + (16 * a + i) * S::SB;
-            const int sw = S::swizzle_k(i);
-            auto step = [&](int f, uint32_t w, half2_t s2) {
-                const half8_t k8 = decode8(w, s2);
-#pragma unroll
-                for (int m = 0; m < NQ; ++m)
-#pragma unroll
-                    for (int part = 0; part < PARTS; ++part)
-                        c[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, q[m].part[part][f], c[m], 0, 0, 0);
-            };
-#pragma unroll
-            for (int x = 0; x < St::n128; ++x) {
-                const uint4_t w = *(const uint4_t *)(row + (((4 * x + g) ^ sw) * 16));
-                const half2_t both = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)*(const uint16_t *)(sc + 8 * x + 2 * g), 1.0f, false);
-                const half2_t s0 = {both.x, both.x}, s1 = {both.y, both.y};
-                step(4 * x, w.x, s0);
-                step(4 * x + 1, w.y, s0);
-                step(4 * x + 2, w.z, s1);
-                step(4 * x + 3, w.w, s1);
+            for (int c = 0; c < S::kLoads; ++c) {
+                const int o = c * 64 + lane, r = 16 * a + o / (S::RB / S::PB), piece = o % (S::RB / S::PB);
+                if (16 * S::RB % (64 * S::PB) == 0 || o < 16 * S::RB / S::PB)
+                    *(typename S::Piece *)(mine + r * S::RB + (piece ^ S::swizzle_v(r)) * S::PB) = raw.v[a][c];
             }
-            if constexpr (St::n64 != 0) {
-                const int u = St::n128 * 8 + g;                                // 8-byte units of the row
-                const uint2_t w = *(const uint2_t *)(row + (((u / 2) ^ sw) * 16 + u % 2 * 8));
-                const half2_t both = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)sc[St::n128 * 8 + g], 1.0f, false);
-                const half2_t s0 = {both.x, both.x};
-                step(4 * St::n128, w.x, s0);
-                step(4 * St::n128 + 1, w.y, s0);
-            }
-            if constexpr (St::n32 != 0) {
-                const int u = St::n128 * 16 + St::n64 * 8 + g;                  // 4-byte units
-                const uint32_t w = *(const uint32_t *)(row + (((u / 4) ^ sw) * 16 + u % 4 * 4));
-                const half2_t both = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)sc[St::n128 * 8 + St::n64 * 4 + g / 2], 1.0f, false);
-                const half2_t s0 = {both.x, both.x};
-                step(St::N - 1, w, s0);
-            }
-#pragma unroll
-            for (int m = 0; m < NQ; ++m)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    logit[m][a][e] = c[m][e];
-        }
-        if (there != 15u || t0 < all_from || t0 + 64 > all_to) {
-            asm volatile("" : : : "memory");                            // a branch, not 16 selects in every tile
-#pragma unroll
-            for (int m = 0; m < NQ; ++m)
-#pragma unroll
-                for (int a = 0; a < 4; ++a)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int32_t t = t0 + 16 * a + 4 * g + e;
-                        if (!(there >> a & 1u) || t < begin[m] || t >= end[m])
-                            logit[m][a][e] = -__builtin_inff();
-                    }
-        }
-        // --- V's scales as float16 in the order of the k-ranges; a position that no row sees gets 0,
-        // and so does a NaN, which is noted for the rows that see it. A lane has one position.
         {
             const int32_t t = t0 + lane;
             const bool seen = (there >> (lane / 16) & 1u) && t >= span.lo && t < span.hi;
-            uint32_t w[(NB + 3) / 4], nan = 0u;
-            w[(NB - 1) / 4] = 0u;                                       // 6 blocks end inside a word
-            __builtin_memcpy(w, tile_at + S::kOffVs + lane * S::SB, NB);
+            uint32_t nan = 0u;
+            uint32_t w[(NB + 3) / 4];
 #pragma unroll
             for (int k = 0; k < (NB + 3) / 4; ++k) {
-                w[k] = seen ? w[k] : 0u;
+                w[k] = seen ? raw.v_scales[k] : 0u;
                 nan |= ((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;      // bytes of 0x7F and 0xFF
             }
             uint64_t left = __ballot(nan != 0u);
             if (left) {
                 asm volatile("" : : : "memory");
-                uint32_t mine = 0u;
+                uint32_t bad_blocks = 0u;
 #pragma unroll
                 for (int k = 0; k < NB; ++k) {
                     const bool bad = (w[k / 4] >> (8 * (k % 4)) & 0x7Fu) == 0x7Fu;
-                    mine |= (uint32_t)bad << k;
+                    bad_blocks |= (uint32_t)bad << k;
                     w[k / 4] &= bad ? ~(0xFFu << (8 * (k % 4))) : ~0u;
                 }
                 while (left) {
                     const int k = __builtin_ctzll(left);
                     left &= left - 1;
-                    const uint32_t blocks = (uint32_t)__builtin_amdgcn_readlane((int)mine, k);
+                    const uint32_t blocks = (uint32_t)__builtin_amdgcn_readlane((int)bad_blocks, k);
 #pragma unroll
                     for (int m = 0; m < NQ; ++m)
                         if (t0 + k >= begin[m] && t0 + k < end[m])
                             nan_blocks[m] |= blocks;
                 }
             }
-            _Float16 *to = (_Float16 *)(ring + S::kStages * S::kStage) + (lane / 4 % 4) * 16 + lane / 16 * 4 + lane % 4;
+            _Float16 *to = (_Float16 *)(mine + 64 * S::RB) + (lane / 4 % 4) * 16 + lane / 16 * 4 + lane % 4;
 #pragma unroll
             for (int k = 0; k < NB; k += 4) {
                 const half2_t low = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[k / 4], 1.0f, false);
@@ -590,7 +556,67 @@ __global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 ? 2
                 }
             }
         }
-        settle();                                                       // the scales are in place
+        load_v(n + kRowsWaves, e);
+        // --- S^T
+        float logit[NQ][4][4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            float4_t c[NQ];
+#pragma unroll
+            for (int m = 0; m < NQ; ++m)
+                c[m] = {0.0f, 0.0f, 0.0f, 0.0f};
+            auto step = [&](int f, uint32_t w, half2_t s2) {
+                const half8_t k8 = decode8(w, s2);
+#pragma unroll
+                for (int m = 0; m < NQ; ++m)
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part)
+                        c[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, q[m].part[part][f], c[m], 0, 0, 0);
+            };
+#pragma unroll
+            for (int x = 0; x < S::kRuns; ++x) {
+                const half2_t both = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(raw.k_scales[a][x], 1.0f, false);
+                const half2_t s0 = {both.x, both.x}, s1 = {both.y, both.y};
+                if (x < St::n128) {
+                    const uint4_t w = raw.k128[a][x < St::n128 ? x : 0];
+                    step(4 * x, w.x, s0);
+                    step(4 * x + 1, w.y, s0);
+                    step(4 * x + 2, w.z, s1);
+                    step(4 * x + 3, w.w, s1);
+                } else if (x < St::n128 + St::n64) {
+                    step(4 * St::n128, raw.k64[a].x, s0);
+                    step(4 * St::n128 + 1, raw.k64[a].y, s0);
+                } else {
+                    step(St::N - 1, raw.k32[a], s0);
+                }
+            }
+            load_k(n + kRowsWaves, e, a);
+#pragma unroll
+            for (int m = 0; m < NQ; ++m)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    logit[m][a][x] = c[m][x];
+        }
+        if (there != 15u || t0 < all_from || t0 + 64 > all_to) {
+#pragma unroll
+            for (int m = 0; m < NQ; ++m) {
+                // what this lane's row sees of its positions, bit 16 a + x for register x of subtile a
+                int32_t from = begin[m] - t0, to = end[m] - t0;
+                asm volatile("" : "+v"(from), "+v"(to));                // a branch, not 16 selects in every tile
+                uint64_t seen = ((there & 1u ? 0xFFFFull : 0ull) | (there & 2u ? 0xFFFFull << 16 : 0ull)) |
+                                ((there & 4u ? 0xFFFFull << 32 : 0ull) | (there & 8u ? 0xFFFFull << 48 : 0ull));
+                seen = from <= 0 ? seen : from < 64 ? seen & ~0ull << from : 0ull;
+                seen = to >= 64 ? seen : to > 0 ? seen & ~(~0ull << to) : 0ull;
+                seen >>= 4 * g;
+#pragma unroll
+                for (int a = 0; a < 4; ++a)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        logit[m][a][x] = (uint32_t)(seen >> (32 * (a / 2))) >> (16 * (a % 2) + x) & 1u ? logit[m][a][x] : -__builtin_inff();
+            }
+        }
+        there = there_of(e);
+        e = entries(n + 2 * kRowsWaves);
         // --- softmax
         half8_t prob[PARTS][NQ][2];
 #pragma unroll
@@ -619,14 +645,16 @@ __global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 ? 2
                     prob[PARTS - 1][m][k / 8][k % 8] = (_Float16)(w - (float)high);
             }
         }
-        // --- O^T
+        // --- O^T. A wave's accesses to LDS are carried out in order: V is there when it is read.
+        settle_order();
         const int vr = 16 * (i / 4) + 4 * g + i % 4;
-        const uint8_t *row = tile_at + S::kOffV + vr * S::RB;
+        const uint8_t *row = mine + vr * S::RB;
         const int sw = S::swizzle_v(vr);
-        const uint8_t *sc = ring + S::kStages * S::kStage + g * 32;
+        const uint8_t *sc = mine + 64 * S::RB + g * 32;
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const uint2_t w = read_transposed4(row + ((k / 2) ^ sw) * 16 + k % 2 * 8);
+            const int at = S::PB == 8 ? (k ^ sw) * 8 : ((k / 2) ^ sw) * 16 + k % 2 * 8;
+            const uint2_t w = read_transposed4(row + at);
             const uint4_t a0 = *(const uint4_t *)(sc + k * 128), a1 = *(const uint4_t *)(sc + k * 128 + 16);
             const half8_t v0 = decode8_by(w.x, a0), v1 = decode8_by(w.y, a1);
 #pragma unroll
@@ -637,25 +665,11 @@ __global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 ? 2
                     acc[m][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, prob[part][m][1], acc[m][k], 0, 0, 0);
                 }
         }
-    };
-
-    // --- the loop: tile n's copies are awaited while those of the next are out
-    for (int stage = 0; n < span.end; n += kRowsWaves, stage ^= 1) {
-        uint32_t next = 0u;
-        if (n + kRowsWaves < span.end) {
-            next = issue(n + kRowsWaves, e, stage ^ 1);
-            entries(n + 2 * kRowsWaves, e);
-            landed<S::kCopies>();
-        } else {
-            landed<0>();
-        }
-        compute(n, there, ring + stage * S::kStage);
-        settle();                                                       // this stage is read: the next round refills it
-        there = next;
+        settle_order();
     }
 
     // --- the waves' results through LDS: sums [wave][16 NQ][D], norms
-    __syncthreads();                                                   // every ring is read
+    __syncthreads();                                                   // every wave's V is read
     float *const w_sums = (float *)lds;
     Norm *const w_norms = (Norm *)(lds + kRowsWaves * 16 * NQ * D * 4);
 #pragma unroll
@@ -714,11 +728,11 @@ typedef float float16_t __attribute__((ext_vector_type(16)));
 constexpr int kTileThreads = 256, kTileRows = 128;      // 4 waves of 32 rows
 
 // 64 positions in LDS as float16, [position][D] for K and for V. Places of a row's 16-byte
-// pieces: 16 neighbouring rows meet every bank where K is read, where V is read 64 bytes of
-// 4 neighbouring rows do (and rows that are written at once differ too).
+// pieces: 16 neighbouring rows meet every bank where K is read, 64 bytes of 4 neighbouring rows
+// do where V is read, and 4 pieces of 4 neighbouring rows where either is written (less well for 96).
 template <int D>
 struct WideTile {
-    static constexpr int kRow = 2 * D, kBytes = 64 * kRow, PR = D / 32;        // pieces of 32 codes in a row
+    static constexpr int kRow = 2 * D, kBytes = 64 * kRow, kBuffer = 2 * kBytes, PR = D / 32;  // pieces of 32 codes in a row
     static constexpr int kPieces = (2 * 64 * PR + kTileThreads - 1) / kTileThreads;
     __device__ static constexpr int swizzle_k(int t)
     {
@@ -726,7 +740,7 @@ struct WideTile {
     }
     __device__ static constexpr int swizzle_v(int t)
     {
-        return (t / 4 & 3) + (D == 64 || D == 192 ? (t / 2 & 1) * 4 : D == 96 ? 0 : (t & 3) * 4);
+        return D == 64 || D == 192 ? (t / 2 & 1) * 4 + (t / 2 & 3) : D == 96 ? t / 4 & 3 : (t & 3) * 5;
     }
 };
 
@@ -750,7 +764,7 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
     using S = WideTile<D>;
     constexpr int PARTS = F32 ? 2 : 1, NK = D / 16, ND = D / 32;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    __shared__ uint32_t s_ticket, s_flag[2], s_nan[2][64];
+    __shared__ uint32_t s_ticket, s_flag[3], s_nan[3][64];
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64), lane = (int)threadIdx.x % 64;
     const int i = lane % 32, h = lane / 32;
     // the last rows, which see most under the causal mask, first
@@ -842,7 +856,7 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
             scales[k] = *(const uint16_t *)((values ? p.vs : p.ks) + (uint64_t)(uint32_t)page * p.scale_page + row * (D / 16) + piece * 2);
         }
     };
-    auto stage = [&](int parity) {
+    auto stage = [&](uint8_t *buffer, int slot) {
 #pragma unroll
         for (int k = 0; k < S::kPieces; ++k) {
             const int u = k * kTileThreads + (int)threadIdx.x, v = u % (64 * S::PR), t = v / S::PR, piece = v % S::PR;
@@ -854,67 +868,105 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
                 // a NaN scale is noted for the rows that see it and counts as 0 in the products
                 const uint32_t nan = (uint32_t)((scales[k] & 0x7Fu) == 0x7Fu) | (uint32_t)((scales[k] & 0x7F00u) == 0x7F00u) << 1;
                 if (nan) {
-                    atomicOr(&s_nan[parity][t], nan << (2 * piece));
-                    s_flag[parity] = 1u;
+                    atomicOr(&s_nan[slot][t], nan << (2 * piece));
+                    s_flag[slot] = 1u;
                     both.x = nan & 1u ? (_Float16)0.0f : both.x;
                     both.y = nan & 2u ? (_Float16)0.0f : both.y;
                 }
             }
             const half2_t s0 = {both.x, both.x}, s1 = {both.y, both.y};
-            uint8_t *row = lds + (values ? S::kBytes : 0) + t * S::kRow;
+            uint8_t *row = buffer + (values ? S::kBytes : 0) + t * S::kRow;
             const int sw = values ? S::swizzle_v(t) : S::swizzle_k(t);
             *(half8_t *)(row + ((4 * piece) ^ sw) * 16) = decode8(codes[k].x, s0);
             *(half8_t *)(row + ((4 * piece + 1) ^ sw) * 16) = decode8(codes[k].y, s0);
             *(half8_t *)(row + ((4 * piece + 2) ^ sw) * 16) = decode8(codes[k].z, s1);
             *(half8_t *)(row + ((4 * piece + 3) ^ sw) * 16) = decode8(codes[k].w, s1);
         }
-        // nobody reads the other tile's notes any more
-        if (threadIdx.x < 64) {
-            s_nan[parity ^ 1][threadIdx.x] = 0u;
-            s_flag[parity ^ 1] = 0u;
-        }
     };
 
-    auto compute = [&](int32_t n, uint64_t there, int parity) {
+    if (threadIdx.x < 64) {
+        s_nan[0][threadIdx.x] = s_nan[1][threadIdx.x] = s_nan[2][threadIdx.x] = 0u;
+        s_flag[0] = s_flag[1] = s_flag[2] = 0u;
+    }
+    // One barrier a tile: behind it this tile's buffer is filled and the other one read. While the
+    // products of K are under way the next tile is decoded, and the one after it loaded.
+    int32_t e = -1;
+    uint64_t there = 0ull, next = 0ull;
+    if (span.first < span.end) {
+        e = entry(span.first);
+        there = __ballot(e >= 0);
+        load(span.first, e);
+        e = entry(span.first + 1);
+        lds_barrier();                                          // the notes are clear
+        stage(lds, 0);
+        next = __ballot(e >= 0);
+        load(span.first + 1, e);                                // past the end no position has a page: nothing is read
+        e = entry(span.first + 2);
+    }
+    int slot = 0;
+    for (int32_t n = span.first; n < span.end; ++n) {
+        uint8_t *const buffer = lds + ((n - span.first) & 1) * S::kBuffer, *const other = lds + ((n - span.first + 1) & 1) * S::kBuffer;
+        const int slot1 = slot == 2 ? 0 : slot + 1, slot2 = slot1 == 2 ? 0 : slot1 + 1;
+        lds_barrier();
+        // nobody reads the notes of the tile before any more
+        if (threadIdx.x < 64) {
+            s_nan[slot2][threadIdx.x] = 0u;
+            s_flag[slot2] = 0u;
+        }
         const int32_t t0 = first_position + n * 64;
-        if (!has_rows || t0 >= some_to || t0 + 64 <= some_from)
-            return;
+        const bool busy = has_rows && t0 < some_to && t0 + 64 > some_from;
         // --- S^T
         float logit[2][16];
+        if (busy) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            float16_t c;
+            for (int t = 0; t < 2; ++t) {
+                float16_t c;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                c[e] = 0.0f;
-            const int kr = 32 * t + i;
-            const uint8_t *row = lds + kr * S::kRow;
-            const int sw = S::swizzle_k(kr);
+                for (int x = 0; x < 16; ++x)
+                    c[x] = 0.0f;
+                const int kr = 32 * t + i;
+                const uint8_t *row = buffer + kr * S::kRow;
+                const int sw = S::swizzle_k(kr);
 #pragma unroll
-            for (int k = 0; k < NK; ++k) {
-                const half8_t k8 = *(const half8_t *)(row + ((2 * k + h) ^ sw) * 16);
+                for (int k = 0; k < NK; ++k) {
+                    const half8_t k8 = *(const half8_t *)(row + ((2 * k + h) ^ sw) * 16);
 #pragma unroll
-                for (int part = 0; part < PARTS; ++part)
-                    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(k8, q.part[part][k], c, 0, 0, 0);
+                    for (int part = 0; part < PARTS; ++part)
+                        c = __builtin_amdgcn_mfma_f32_32x32x16_f16(k8, q.part[part][k], c, 0, 0, 0);
+                }
+#pragma unroll
+                for (int x = 0; x < 16; ++x)
+                    logit[t][x] = c[x];
             }
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                logit[t][e] = c[e];
         }
-        if (there != ~0ull || t0 < all_from || t0 + 64 > all_to) {
-            asm volatile("" : : : "memory");                            // a branch, not 32 selects in every tile
+        if (n + 1 < span.end) {
+            stage(other, slot1);
+            load(n + 2, e);
+        }
+        const uint64_t now = there;
+        there = next;
+        next = __ballot(e >= 0);
+        e = entry(n + 3);
+        const int noted = slot;
+        slot = slot1;
+        if (!busy)
+            continue;
+        if (now != ~0ull || t0 < all_from || t0 + 64 > all_to) {
+            // what this lane's row sees of the tile, bit 32 t + 8 (r / 4) + r % 4 for register r
+            int32_t from = begin - t0, to = end - t0;
+            asm volatile("" : "+v"(from), "+v"(to));            // a branch, not 32 selects in every tile
+            uint64_t seen = from <= 0 ? now : from < 64 ? now & ~0ull << from : 0ull;
+            seen = to >= 64 ? seen : to > 0 ? seen & ~(~0ull << to) : 0ull;
+            seen >>= 4 * h;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int at = 32 * t + 8 * (e / 4) + 4 * h + e % 4;
-                    if (!(there >> at & 1u) || t0 + at < begin || t0 + at >= end)
-                        logit[t][e] = -__builtin_inff();
-                }
+                for (int x = 0; x < 16; ++x)
+                    logit[t][x] = (uint32_t)(seen >> (32 * t)) >> (8 * (x / 4) + x % 4) & 1u ? logit[t][x] : -__builtin_inff();
         }
-        if (s_flag[parity]) {
+        if (s_flag[noted]) {
             for (int t = 0; t < 64; ++t) {
-                const uint32_t blocks = s_nan[parity][t];
+                const uint32_t blocks = s_nan[noted][t];
                 if (t0 + t >= begin && t0 + t < end)
                     nan_blocks |= blocks;
             }
@@ -949,7 +1001,7 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int r0 = 16 * k + 4 * h + vi / 4, r1 = r0 + 8;
-            const uint8_t *a0 = lds + S::kBytes + r0 * S::kRow + vi % 2 * 8, *a1 = lds + S::kBytes + r1 * S::kRow + vi % 2 * 8;
+            const uint8_t *a0 = buffer + S::kBytes + r0 * S::kRow + vi % 2 * 8, *a1 = buffer + S::kBytes + r1 * S::kRow + vi % 2 * 8;
             const int sw0 = S::swizzle_v(r0), sw1 = S::swizzle_v(r1);
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
@@ -961,28 +1013,6 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
                 for (int part = 0; part < PARTS; ++part)
                     acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v8, prob[part][k], acc[d], 0, 0, 0);
             }
-        }
-    };
-
-    if (threadIdx.x < 64) {
-        s_nan[0][threadIdx.x] = s_nan[1][threadIdx.x] = 0u;
-        s_flag[0] = s_flag[1] = 0u;
-    }
-    if (span.first < span.end) {
-        int32_t e = entry(span.first);
-        uint64_t there = __ballot(e >= 0);
-        load(span.first, e);
-        e = entry(span.first + 1);
-        for (int32_t n = span.first; n < span.end; ++n) {
-            const int parity = (n - span.first) & 1;
-            lds_barrier();                                      // the tile before has been read
-            stage(parity);
-            const uint64_t now = there;
-            there = __ballot(e >= 0);
-            load(n + 1, e);                                     // past the end: no position has a page, nothing is read
-            e = entry(n + 2);
-            lds_barrier();
-            compute(n, now, parity);
         }
     }
 
@@ -1136,8 +1166,8 @@ void set_plan(AttParams &p, const Plan &plan, void *workspace)
 template <int D>
 hipError_t launch_tile(const AttParams &p, int64_t grid, hipStream_t st)
 {
-    static_assert(2 * WideTile<D>::kBytes + 1024 <= 160 * 1024);
-    const int lds = std::max(2 * WideTile<D>::kBytes, p.splits > 1 ? p.splits * kTileRows * 8 : 0);
+    static_assert(2 * WideTile<D>::kBuffer + 1024 <= 160 * 1024 && kMaxSplits * kTileRows * 8 <= 64 * 1024);
+    const int lds = std::max(2 * WideTile<D>::kBuffer, p.splits > 1 ? p.splits * kTileRows * 8 : 0);
     auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((uint32_t)grid), dim3(kTileThreads), lds, st, p); };
     p.dtype == NVFP4_F32 ? go(nvfp4_attention_tile_kernel<D, true>) : go(nvfp4_attention_tile_kernel<D, false>);
     return hipGetLastError();

@@ -58,11 +58,14 @@ typedef float float4_t __attribute__((ext_vector_type(4)));
 typedef int32_t int4_t __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-// Probabilities are kept times 2^12, the largest at 4096: float16 then holds them to 2^-26
-// of the largest as normal numbers.
-constexpr float kShift = 12.0f;
+// Weights are 2^(logit - top + 8), where `top` is the row's largest logit when it was last
+// looked at: sums are only rescaled when a logit exceeds it by 7, so weights stay below 2^15
+// and in float16 are normal numbers from 2^-22 of the largest on (their error is at most 2^-33
+// of it below). A row rarely needs that behind its first tile; before, a wave's 32 rows
+// rescaled nearly every one (128 values a row: 66 of 400 instructions of a tile).
+constexpr float kShift = 8.0f, kSlack = 7.0f;
 constexpr int kRowsThreads = 256, kRowsWaves = 4;
-constexpr int kMaxSplits = 64, kRowsTarget = 2048, kTileTarget = 512, kTileLeast = 8;
+constexpr int kMaxSplits = 64, kRowsTarget = 2048, kTileLeast = 4;
 
 // The head's D values go through the matrix instruction in steps of 32. A lane (row
 // lane % 16, g = lane / 16) has 8 of a step's; which 8 is free while q and K agree: runs
@@ -233,48 +236,6 @@ __device__ __attribute__((always_inline)) inline bool last_of_splits(const AttPa
     return true;
 }
 
-// Adds the splits' partial results of a tile's rows in the order of the splits and stores
-// them, 32 splits' loads in flight. `norms`: LDS for [splits][rows] of them.
-template <int D, int THREADS>
-__device__ __attribute__((always_inline)) inline void join_splits(const AttParams &p, const Sequence &s, int hk, uint32_t tile,
-                                                                  int row0, int rows, int splits, float gv, Norm *norms)
-{
-    constexpr int AHEAD = 32;
-    const float *sums = p.sums + (int64_t)tile * p.splits * p.most_rows * D;
-    const float *from = p.norms + (int64_t)tile * p.splits * p.most_rows * 2;
-    for (int i = (int)threadIdx.x; i < splits * rows; i += THREADS) {
-        const float2_u n = load_partial(from + (i / rows * p.most_rows + i % rows) * 2);
-        norms[i] = {n.x, n.y};
-    }
-    __syncthreads();
-    for (int u = (int)threadIdx.x; u < rows * (D / 2); u += THREADS) {
-        const int r = u / (D / 2), d = u % (D / 2) * 2;
-        Norm n{-__builtin_inff(), 0.0f};
-        for (int k = 0; k < splits; ++k)
-            n.top = fmaxf(n.top, norms[k * rows + r].top);
-        float2_u v = {0.0f, 0.0f};
-        for (int k0 = 0; k0 < splits; k0 += AHEAD) {
-            float2_u x[AHEAD];
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k)
-                x[k] = load_partial(sums + ((int64_t)min(k0 + k, splits - 1) * p.most_rows + r) * D + d);
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k)
-                if (k0 + k < splits) {
-                    const Norm one = norms[(k0 + k) * rows + r];
-                    const float w = weight_of(one.top, n.top);
-                    n.sum += one.sum * w;
-                    v.x += x[k].x * w;
-                    v.y += x[k].y * w;
-                }
-        }
-        const int64_t row = out_row(p, s, hk, row0 + r);
-        store_values<2>(p, row * D + d, {v.x, v.y}, n.sum, gv);
-        if (d == 0)
-            store_lse(p, row, n);
-    }
-}
-
 // Lanes l and l ^ 32 (l ^ 16): both values in both, in one order, without LDS.
 struct Both {
     float a, b;
@@ -309,6 +270,99 @@ __device__ __attribute__((always_inline)) inline float sum_of_4(float v)
 {
     const Both x = across16(v);
     return sum_of_2(x.a + x.b);
+}
+
+// Adds the splits' partial results of rows first .. first + rows - 1 of a tile in the order of the
+// splits and stores them; row0 is the tile's first row among the sequence's. `weights`: LDS for
+// [splits][rows] of them, and behind them for [rows] sums. V values of a row at a time, U such at once,
+// AHEAD splits' loads in flight (where fewer are left the last one's again). FENCED: a kernel
+// before this one wrote the partial results; else other workgroups of this one, past the
+// caches that the XCDs do not share, two values at a time.
+template <int D, int THREADS, int V, int U, int AHEAD, bool FENCED>
+__device__ __attribute__((always_inline)) inline void join_splits(const AttParams &p, const Sequence &s, int hk, uint32_t tile,
+                                                                  int row0, int first, int rows, int splits, float gv, float *weights)
+{
+    static_assert(kMaxSplits <= 64);
+    static_assert(V == 2 || (V == 4 && FENCED));
+    const float *sums = p.sums + ((int64_t)tile * p.splits * p.most_rows + first) * D;
+    const float *from = p.norms + ((int64_t)tile * p.splits * p.most_rows + first) * 2;
+    row0 += first;
+    float *const total = weights + splits * rows;
+    // each row's weights of the splits, a lane each: R rows of a wave at once
+    constexpr int R = 4, WAVES = THREADS / 64;
+    const int lane = (int)threadIdx.x % 64, wave = (int)threadIdx.x / 64;
+    for (int r0 = wave; r0 < rows; r0 += R * WAVES) {
+        float2_u one[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+            one[j] = load_partial(from + (min(lane, splits - 1) * p.most_rows + min(r0 + j * WAVES, rows - 1)) * 2);
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            const int r = r0 + j * WAVES;
+            float top = lane < splits ? one[j].x : -__builtin_inff();
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1)
+                top = fmaxf(top, __shfl_xor(top, d));
+            top = max_of_4(top);
+            const float w = lane < splits ? weight_of(one[j].x, top) : 0.0f;
+            float sum = lane < splits ? one[j].y * w : 0.0f;
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1)
+                sum += __shfl_xor(sum, d);
+            sum = sum_of_4(sum);
+            if (r < rows && lane < splits)
+                weights[lane * rows + r] = w;
+            if (r < rows && lane == 0) {
+                total[r] = sum;
+                store_lse(p, out_row(p, s, hk, row0 + r), {top, sum});
+            }
+        }
+    }
+    __syncthreads();
+    const int units = rows * (D / V);
+    for (int u0 = (int)threadIdx.x; u0 < units; u0 += U * THREADS) {
+        float v[U][V];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                v[u][e] = 0.0f;
+        for (int k0 = 0; k0 < splits; k0 += AHEAD) {
+            float x[U][AHEAD][V];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int at = min(u0 + u * THREADS, units - 1);
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) {
+                    const float *one = sums + ((int64_t)min(k0 + k, splits - 1) * p.most_rows + at / (D / V)) * D + at % (D / V) * V;
+                    if constexpr (FENCED) {
+                        __builtin_memcpy(x[u][k], __builtin_assume_aligned(one, 4 * V), 4 * V);
+                    } else {
+                        const float2_u y = load_partial(one);
+                        x[u][k][0] = y.x, x[u][k][1] = y.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = min(u0 + u * THREADS, units - 1) / (D / V);
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k)
+                    if (k0 + k < splits) {
+                        const float w = weights[(k0 + k) * rows + r];
+#pragma unroll
+                        for (int e = 0; e < V; ++e)
+                            v[u][e] += x[u][k][e] * w;
+                    }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int at = u0 + u * THREADS;
+            if (at < units)
+                store_values<V>(p, out_row(p, s, hk, row0 + at / (D / V)) * D + at % (D / V) * V, v[u], total[at / (D / V)], gv);
+        }
+    }
 }
 
 // Which of a sequence's positions a workgroup takes: tiles of 64 from `lo` on.
@@ -626,7 +680,7 @@ __global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 || 
             for (int k = 1; k < 16; ++k)
                 most = fmaxf(most, logit[m][k / 4][k % 4]);
             most = fmaxf(top[m], max_of_4(most) * rf[m]);
-            if (__ballot(most > top[m])) {
+            if (__ballot(most > top[m] + kSlack)) {
                 const float keep = weight_of(top[m], most);
                 sum[m] *= keep;
 #pragma unroll
@@ -634,7 +688,7 @@ __global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 || 
                     acc[m][k] *= keep;
                 top[m] = most;
             }
-            const float less = kShift - (most == -__builtin_inff() ? 0.0f : most);
+            const float less = kShift - (top[m] == -__builtin_inff() ? 0.0f : top[m]);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
                 const float w = __builtin_amdgcn_exp2f(fmaf(logit[m][k / 4][k % 4], rf[m], less));
@@ -718,29 +772,37 @@ __global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 || 
     }
     if (span.splits == 1 || !last_of_splits(p, tile, span.splits, &s_ticket))
         return;
-    join_splits<D, kRowsThreads>(p, s, hk, tile, 0, rows, span.splits, gv, (Norm *)lds);
+    if (span.splits <= 8)
+        join_splits<D, kRowsThreads, 2, 1, 8, false>(p, s, hk, tile, 0, 0, rows, span.splits, gv, (float *)lds);
+    else
+        join_splits<D, kRowsThreads, 2, 1, 32, false>(p, s, hk, tile, 0, 0, rows, span.splits, gv, (float *)lds);
 }
 
 // ------------------------------------------------------------------ tile kernel
 
 typedef float float16_t __attribute__((ext_vector_type(16)));
 
-constexpr int kTileThreads = 256, kTileRows = 128;      // 4 waves of 32 rows
+// Rows of a wave: 32, or 16 where the sums and queries of 32 do not fit into 256 registers
+// (D = 256 with 32 rows, one wave on a SIMD: 772 us for 2 x 2048 queries at 2048 to 4096
+// positions, 8 heads of 32). Waves of a workgroup.
+constexpr int wave_rows(int D, bool f32) { return D == 256 || (D == 192 && f32) ? 16 : 32; }
+constexpr int tile_waves(int D, bool f32) { return D >= 192 ? 8 : 4; }
+constexpr int tile_rows(int D, bool f32) { return wave_rows(D, f32) * tile_waves(D, f32); }
 
 // 64 positions in LDS as float16, [position][D] for K and for V. Places of a row's 16-byte
 // pieces: 16 neighbouring rows meet every bank where K is read, 64 bytes of 4 neighbouring rows
 // do where V is read, and 4 pieces of 4 neighbouring rows where either is written (less well for 96).
-template <int D>
+template <int D, int THREADS>
 struct WideTile {
     static constexpr int kRow = 2 * D, kBytes = 64 * kRow, kBuffer = 2 * kBytes, PR = D / 32;  // pieces of 32 codes in a row
-    static constexpr int kPieces = (2 * 64 * PR + kTileThreads - 1) / kTileThreads;
+    static constexpr int kPieces = (2 * 64 * PR + THREADS - 1) / THREADS;
     __device__ static constexpr int swizzle_k(int t)
     {
         return D == 64 || D == 192 ? t / 2 & 7 : D == 96 ? t / 4 & 3 : t & 15;
     }
     __device__ static constexpr int swizzle_v(int t)
     {
-        return D == 64 || D == 192 ? (t / 2 & 1) * 4 + (t / 2 & 3) : D == 96 ? t / 4 & 3 : (t & 3) * 5;
+        return D == 64 || D == 192 ? (t / 2 & 1) * 4 + (t / 2 & 3) : D == 96 ? t / 4 & 3 : (t & 3) * 4 + ((t & 3) ^ (t / 4 & 1) * 2);
     }
 };
 
@@ -751,22 +813,53 @@ __device__ __attribute__((always_inline)) inline void lds_barrier()
     asm volatile("" : : : "memory");
 }
 
-// Many rows (prompts): a workgroup has 128 of a sequence's rows for one key head, a wave 32 of
-// them. Codes of 64 positions come in registers while the 64 before are worked on, are
-// decoded once for all rows into LDS, and go through 32 x 32 x 16 products:
-//   S^T = K Q^T: a lane has the logits of one row (lane % 32), positions 32 t + 8 (r / 4) + 4 h
-//     + r % 4 in register r (h = lane / 32).
+// Many rows (prompts): a workgroup has 128 or 256 of a sequence's rows for one key head, a wave RW = 32 or
+// 16 of them. Codes of 64 positions come in registers while the 64 before are worked on, are
+// decoded once for all rows into LDS, and go through 32 x 32 x 16 (16 x 16 x 32) products:
+//   S^T = K Q^T: a lane has the logits of one row (lane % RW), positions RW t + 8 (r / 4) + 4 h
+//     + r % 4 in register r (h = lane / RW).
 //   O^T = V^T P^T: P's registers are the k-range of the second operand as they stand; V's operand is read
 //     transposed in that order, 4 positions of a value at a time.
+template <int RW>
+struct Product;
+template <>
+struct Product<32> {
+    using Sum = float16_t;
+    static constexpr int kValues = 16, kStep = 16;
+    __device__ static __attribute__((always_inline)) inline Sum of(half8_t a, half8_t b, Sum c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+    __device__ static __attribute__((always_inline)) inline float max_of(float v) { return max_of_2(v); }
+    __device__ static __attribute__((always_inline)) inline float sum_of(float v) { return sum_of_2(v); }
+};
+template <>
+struct Product<16> {
+    using Sum = float4_t;
+    static constexpr int kValues = 4, kStep = 32;
+    __device__ static __attribute__((always_inline)) inline Sum of(half8_t a, half8_t b, Sum c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+    __device__ static __attribute__((always_inline)) inline float max_of(float v) { return max_of_4(v); }
+    __device__ static __attribute__((always_inline)) inline float sum_of(float v) { return sum_of_4(v); }
+};
+
 template <int D, bool F32>
-__global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attention_tile_kernel(AttParams p)
+__global__ __launch_bounds__(64 * tile_waves(D, F32), 2) void nvfp4_attention_tile_kernel(AttParams p)
 {
-    using S = WideTile<D>;
-    constexpr int PARTS = F32 ? 2 : 1, NK = D / 16, ND = D / 32;
+    constexpr int kTileThreads = 64 * tile_waves(D, F32), kTileRows = tile_rows(D, F32);
+    using S = WideTile<D, kTileThreads>;
+    constexpr int RW = wave_rows(D, F32);
+    using M = Product<RW>;
+    // All 64 positions at once, or 32 after the other, where the logits of 64 do not fit into 256 registers
+    // beside sums and queries.
+    constexpr int GROUPS = RW == 32 && (D > 128 || F32) ? 2 : 1, TT = 64 / RW / GROUPS, NV = M::kValues;
+    constexpr int PARTS = F32 ? 2 : 1, NK = D / M::kStep, ND = D / RW;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    __shared__ uint32_t s_ticket, s_flag[3], s_nan[3][64];
+    __shared__ uint32_t s_flag[3], s_nan[3][64];
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64), lane = (int)threadIdx.x % 64;
-    const int i = lane % 32, h = lane / 32;
+    const int i = lane % RW, h = lane / RW;
     // the last rows, which see most under the causal mask, first
     const uint32_t pairs = (uint32_t)p.B * (uint32_t)p.heads, tiles = pairs * (uint32_t)p.row_tiles, id = blockIdx.x % tiles;
     const int split = (int)(blockIdx.x / tiles), rt = (int)(((uint32_t)p.row_tiles - 1u) - id / pairs);
@@ -783,7 +876,7 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
         return;
 
     // --- this lane's row of q
-    const int r = 32 * wave + i;
+    const int r = RW * wave + i;
     const bool real = r < rows;
     const int tok = (row0 + (real ? r : 0)) / p.G, pos = s.length - s.n + tok;
     const int32_t end = p.causal ? min(s.length, pos + 1) : s.length;
@@ -793,58 +886,68 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
     {
         const float factor = p.scale * (p.gk ? *p.gk : 1.0f) * kLog2e;
         const uint8_t *x = p.q + (int64_t)(s.first + tok) * p.q_token + (int64_t)(hk * p.G + (row0 + (real ? r : 0)) % p.G) * p.q_head;
-        float v[NK][8], top = 0.0f;
+        // twice from memory, so that the row is not held as float32
+        float top = 0.0f;
         bool finite = true;
+        auto piece = [&](int c, float (&v)[8]) { load8(x + (M::kStep * c + 8 * h) * (F32 ? 4 : 2), F32 ? NVFP4_F32 : p.dtype, v); };
 #pragma unroll
         for (int c = 0; c < NK; ++c) {
-            load8(x + (16 * c + 8 * h) * (F32 ? 4 : 2), F32 ? NVFP4_F32 : p.dtype, v[c]);
+            float v[8];
+            piece(c, v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const bool good = __builtin_isfinite(v[c][j]);
+                const bool good = __builtin_isfinite(v[j]);
                 finite &= good;
-                v[c][j] = good ? v[c][j] : 0.0f;
-                top = fmaxf(top, fabsf(v[c][j]));
+                top = fmaxf(top, good ? fabsf(v[j]) : 0.0f);
             }
         }
-        top = max_of_2(top);
-        finite = max_of_2(finite ? 0.0f : 1.0f) == 0.0f;
+        top = M::max_of(top);
+        finite = M::max_of(finite ? 0.0f : 1.0f) == 0.0f;
         const RowScale scale = row_scale(top, factor, real, finite);
+        asm volatile("" : : : "memory");
 #pragma unroll
-        for (int c = 0; c < NK; ++c)
-            to_parts(v[c], scale, q, c);
+        for (int c = 0; c < NK; ++c) {
+            float v[8];
+            piece(c, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = __builtin_isfinite(v[j]) ? v[j] : 0.0f;
+            to_parts(v, scale, q, c);
+        }
         rf = scale.factor;
     }
     // positions that some, and that all, of the wave's rows see
-    const int w0 = min(32 * wave, rows - 1), w1 = min(32 * wave + 31, rows - 1);
+    const int w0 = min(RW * wave, rows - 1), w1 = min(RW * wave + RW - 1, rows - 1);
     const int32_t pos0 = s.length - s.n + (row0 + w0) / p.G, pos1 = s.length - s.n + (row0 + w1) / p.G;
     const int32_t some_from = p.window ? max(0, pos0 - p.window + 1) : 0, some_to = p.causal ? min(s.length, pos1 + 1) : s.length;
     const int32_t all_from = p.window ? max(0, pos1 - p.window + 1) : 0, all_to = p.causal ? min(s.length, pos0 + 1) : s.length;
-    const bool has_rows = 32 * wave < rows;
+    const bool has_rows = RW * wave < rows;
 
-    float16_t acc[ND];
+    typename M::Sum acc[ND];
 #pragma unroll
     for (int k = 0; k < ND; ++k)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            acc[k][e] = 0.0f;
+        for (int x = 0; x < NV; ++x)
+            acc[k][x] = 0.0f;
     float top = -__builtin_inff(), sum = 0.0f;
     uint32_t nan_blocks = 0u;
 
-    // --- staging. Entry of the page of position lane of a tile: -1 where there is none.
+    // --- staging. The table's entry of position lane of a tile, -1 past the end. It is not looked
+    // at before the next round: a wait for it would wait for the loads before it too.
     const int32_t mask = (1 << p.shift) - 1, first_position = span.lo / 64 * 64;
+    const int32_t *const table = p.table + (int64_t)b * p.width;
+    const uint32_t tid = threadIdx.x % kTileThreads;            // known to be below kTileThreads
     auto entry = [&](int32_t n) -> int32_t {
         const int32_t t = first_position + n * 64 + lane;
-        if (n >= span.end || t >= span.hi)
-            return -1;
-        const int32_t e = p.table[(int64_t)b * p.width + (t >> p.shift)];
-        return (uint32_t)e < (uint32_t)p.pages ? e : -1;
+        return n < span.end && t < span.hi ? table[t >> p.shift] : -1;
     };
+    auto page_of = [&](int32_t e) -> int32_t { return (uint32_t)e < (uint32_t)p.pages ? e : -1; };
     uint4_t codes[S::kPieces];
     uint32_t scales[S::kPieces];
     auto load = [&](int32_t n, int32_t e) {
 #pragma unroll
         for (int k = 0; k < S::kPieces; ++k) {
-            const int u = k * kTileThreads + (int)threadIdx.x, v = u % (64 * S::PR), t = v / S::PR, piece = v % S::PR;
+            const int u = k * kTileThreads + (int)tid, v = u % (64 * S::PR), t = v / S::PR, piece = v % S::PR;
             const int32_t page = __shfl(e, t);
             codes[k] = (uint4_t){0u, 0u, 0u, 0u};
             scales[k] = 0u;
@@ -859,7 +962,7 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
     auto stage = [&](uint8_t *buffer, int slot) {
 #pragma unroll
         for (int k = 0; k < S::kPieces; ++k) {
-            const int u = k * kTileThreads + (int)threadIdx.x, v = u % (64 * S::PR), t = v / S::PR, piece = v % S::PR;
+            const int u = k * kTileThreads + (int)tid, v = u % (64 * S::PR), t = v / S::PR, piece = v % S::PR;
             if (2 * 64 * S::PR % kTileThreads != 0 && u >= 2 * 64 * S::PR)
                 continue;
             const bool values = u >= 64 * S::PR;
@@ -893,10 +996,10 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
     int32_t e = -1;
     uint64_t there = 0ull, next = 0ull;
     if (span.first < span.end) {
-        e = entry(span.first);
+        e = page_of(entry(span.first));
         there = __ballot(e >= 0);
         load(span.first, e);
-        e = entry(span.first + 1);
+        e = page_of(entry(span.first + 1));
         lds_barrier();                                          // the notes are clear
         stage(lds, 0);
         next = __ballot(e >= 0);
@@ -915,116 +1018,131 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
         }
         const int32_t t0 = first_position + n * 64;
         const bool busy = has_rows && t0 < some_to && t0 + 64 > some_from;
-        // --- S^T
-        float logit[2][16];
-        if (busy) {
+        uint64_t now = 0ull;
+        int noted = 0;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                float16_t c;
+        for (int group = 0; group < GROUPS; ++group) {
+            // --- S^T
+            float logit[TT][NV];
+            if (busy) {
 #pragma unroll
-                for (int x = 0; x < 16; ++x)
-                    c[x] = 0.0f;
-                const int kr = 32 * t + i;
-                const uint8_t *row = buffer + kr * S::kRow;
-                const int sw = S::swizzle_k(kr);
+                for (int t = 0; t < TT; ++t) {
+                    typename M::Sum c;
 #pragma unroll
-                for (int k = 0; k < NK; ++k) {
-                    const half8_t k8 = *(const half8_t *)(row + ((2 * k + h) ^ sw) * 16);
+                    for (int x = 0; x < NV; ++x)
+                        c[x] = 0.0f;
+                    const int kr = RW * (group * TT + t) + i;
+                    const uint8_t *row = buffer + kr * S::kRow;
+                    int sw = S::swizzle_k(kr);
+                    if constexpr (D == 192 && RW == 32)
+                        asm volatile("" : "+v"(sw));                // places computed anew, not kept in 12 registers
+#pragma unroll
+                    for (int k = 0; k < NK; ++k) {
+                        const half8_t k8 = *(const half8_t *)(row + ((M::kStep / 8 * k + h) ^ sw) * 16);
+#pragma unroll
+                        for (int part = 0; part < PARTS; ++part)
+                            c = M::of(k8, q.part[part][k], c);
+                    }
+#pragma unroll
+                    for (int x = 0; x < NV; ++x)
+                        logit[t][x] = c[x];
+                }
+            }
+            if (group == 0) {
+                now = there;
+                there = next;
+                if (n + 1 < span.end) {
+                    stage(other, slot1);
+                    const int32_t page = page_of(e);
+                    next = __ballot(page >= 0);
+                    load(n + 2, page);
+                    e = entry(n + 3);
+                }
+                noted = slot;
+                slot = slot1;
+            }
+            if (!busy)
+                break;
+            if (now != ~0ull || t0 < all_from || t0 + 64 > all_to) {
+                // what this lane's row sees of the tile, bit RW t + 8 (r / 4) + r % 4 for register r
+                int32_t from = begin - t0, to = end - t0;
+                asm volatile("" : "+v"(from), "+v"(to));            // a branch, not 32 selects in every tile
+                uint64_t seen = from <= 0 ? now : from < 64 ? now & ~0ull << from : 0ull;
+                seen = to >= 64 ? seen : to > 0 ? seen & ~(~0ull << to) : 0ull;
+                seen >>= 4 * h;
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int x = 0; x < NV; ++x) {
+                        const int at = RW * (group * TT + t) + 8 * (x / 4) + x % 4;
+                        logit[t][x] = (uint32_t)(seen >> (at / 32 * 32)) >> (at % 32) & 1u ? logit[t][x] : -__builtin_inff();
+                    }
+            }
+            if (group == 0 && s_flag[noted]) {
+                for (int t = 0; t < 64; ++t) {
+                    const uint32_t blocks = s_nan[noted][t];
+                    if (t0 + t >= begin && t0 + t < end)
+                        nan_blocks |= blocks;
+                }
+            }
+            // --- softmax
+            float most = logit[0][0];
+#pragma unroll
+            for (int x = 1; x < NV * TT; ++x)
+                most = fmaxf(most, logit[x / NV][x % NV]);
+            most = fmaxf(top, M::max_of(most) * rf);
+            if (__ballot(most > top + kSlack)) {
+                const float keep = weight_of(top, most);
+                sum *= keep;
+#pragma unroll
+                for (int k = 0; k < ND; ++k)
+                    acc[k] *= keep;
+                top = most;
+            }
+            const float less = kShift - (top == -__builtin_inff() ? 0.0f : top);
+            constexpr int NP = NV * TT / 8;                             // k-ranges of 8 positions a lane
+            half8_t prob[PARTS][NP];
+#pragma unroll
+            for (int x = 0; x < NV * TT; ++x) {
+                const float w = __builtin_amdgcn_exp2f(fmaf(logit[x / NV][x % NV], rf, less));
+                sum += w;
+                const _Float16 high = (_Float16)w;
+                prob[0][x / 8][x % 8] = high;
+                if constexpr (PARTS == 2)
+                    prob[PARTS - 1][x / 8][x % 8] = (_Float16)(w - (float)high);
+            }
+            // --- O^T: lanes of 16 give the places of 4 rows, 4 values each
+            const int vi = lane % 16, vd = RW == 32 ? lane / 16 % 2 : 0;
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                const int r0 = M::kStep * (NP * group + k) + 4 * h + vi / 4, r1 = r0 + M::kStep / 2;
+                const uint8_t *a0 = buffer + S::kBytes + r0 * S::kRow + vi % 2 * 8, *a1 = buffer + S::kBytes + r1 * S::kRow + vi % 2 * 8;
+                int sw0 = S::swizzle_v(r0), sw1 = S::swizzle_v(r1);
+                if constexpr (D == 192 && RW == 32)
+                    asm volatile("" : "+v"(sw0), "+v"(sw1));
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    const int piece = RW / 8 * d + 2 * vd + vi % 4 / 2;
+                    const uint2_t x0 = read_transposed16(a0 + (piece ^ sw0) * 16), x1 = read_transposed16(a1 + (piece ^ sw1) * 16);
+                    const uint4_t x = {x0.x, x0.y, x1.x, x1.y};
+                    const half8_t v8 = __builtin_bit_cast(half8_t, x);
 #pragma unroll
                     for (int part = 0; part < PARTS; ++part)
-                        c = __builtin_amdgcn_mfma_f32_32x32x16_f16(k8, q.part[part][k], c, 0, 0, 0);
+                        acc[d] = M::of(v8, prob[part][k], acc[d]);
                 }
-#pragma unroll
-                for (int x = 0; x < 16; ++x)
-                    logit[t][x] = c[x];
-            }
-        }
-        if (n + 1 < span.end) {
-            stage(other, slot1);
-            load(n + 2, e);
-        }
-        const uint64_t now = there;
-        there = next;
-        next = __ballot(e >= 0);
-        e = entry(n + 3);
-        const int noted = slot;
-        slot = slot1;
-        if (!busy)
-            continue;
-        if (now != ~0ull || t0 < all_from || t0 + 64 > all_to) {
-            // what this lane's row sees of the tile, bit 32 t + 8 (r / 4) + r % 4 for register r
-            int32_t from = begin - t0, to = end - t0;
-            asm volatile("" : "+v"(from), "+v"(to));            // a branch, not 32 selects in every tile
-            uint64_t seen = from <= 0 ? now : from < 64 ? now & ~0ull << from : 0ull;
-            seen = to >= 64 ? seen : to > 0 ? seen & ~(~0ull << to) : 0ull;
-            seen >>= 4 * h;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int x = 0; x < 16; ++x)
-                    logit[t][x] = (uint32_t)(seen >> (32 * t)) >> (8 * (x / 4) + x % 4) & 1u ? logit[t][x] : -__builtin_inff();
-        }
-        if (s_flag[noted]) {
-            for (int t = 0; t < 64; ++t) {
-                const uint32_t blocks = s_nan[noted][t];
-                if (t0 + t >= begin && t0 + t < end)
-                    nan_blocks |= blocks;
-            }
-        }
-        // --- softmax
-        float most = logit[0][0];
-#pragma unroll
-        for (int e = 1; e < 32; ++e)
-            most = fmaxf(most, logit[e / 16][e % 16]);
-        most = fmaxf(top, max_of_2(most) * rf);
-        if (__ballot(most > top)) {
-            const float keep = weight_of(top, most);
-            sum *= keep;
-#pragma unroll
-            for (int k = 0; k < ND; ++k)
-                acc[k] *= keep;
-            top = most;
-        }
-        const float less = kShift - (most == -__builtin_inff() ? 0.0f : most);
-        half8_t prob[PARTS][4];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            const float w = __builtin_amdgcn_exp2f(fmaf(logit[e / 16][e % 16], rf, less));
-            sum += w;
-            const _Float16 high = (_Float16)w;
-            prob[0][e / 8][e % 8] = high;
-            if constexpr (PARTS == 2)
-                prob[PARTS - 1][e / 8][e % 8] = (_Float16)(w - (float)high);
-        }
-        // --- O^T: lanes of 16 give the places of 4 rows, 4 values each
-        const int vi = lane % 16, vd = lane / 16 % 2;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int r0 = 16 * k + 4 * h + vi / 4, r1 = r0 + 8;
-            const uint8_t *a0 = buffer + S::kBytes + r0 * S::kRow + vi % 2 * 8, *a1 = buffer + S::kBytes + r1 * S::kRow + vi % 2 * 8;
-            const int sw0 = S::swizzle_v(r0), sw1 = S::swizzle_v(r1);
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                const int piece = 4 * d + 2 * vd + vi % 4 / 2;
-                const uint2_t x0 = read_transposed16(a0 + (piece ^ sw0) * 16), x1 = read_transposed16(a1 + (piece ^ sw1) * 16);
-                const uint4_t x = {x0.x, x0.y, x1.x, x1.y};
-                const half8_t v8 = __builtin_bit_cast(half8_t, x);
-#pragma unroll
-                for (int part = 0; part < PARTS; ++part)
-                    acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v8, prob[part][k], acc[d], 0, 0, 0);
             }
         }
     }
 
     // --- results
-    sum = sum_of_2(sum);
+    sum = M::sum_of(sum);
     const float gv = p.gv ? *p.gv : 1.0f;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            if (nan_blocks >> (2 * d + e / 8) & 1u)
-                acc[d][e] = __builtin_nanf("");
+        for (int x = 0; x < NV; ++x)
+            if (nan_blocks >> ((RW * d + 8 * (x / 4)) / 16) & 1u)
+                acc[d][x] = __builtin_nanf("");
     if (span.splits == 1) {
         if (!real)
             return;
@@ -1032,8 +1150,8 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-                store_values<4>(p, row * D + 32 * d + 2 * e + 4 * h, {acc[d][e], acc[d][e + 1], acc[d][e + 2], acc[d][e + 3]}, sum, gv);
+            for (int x = 0; x < NV; x += 4)
+                store_values<4>(p, row * D + RW * d + 2 * x + 4 * h, {acc[d][x], acc[d][x + 1], acc[d][x + 2], acc[d][x + 3]}, sum, gv);
         if (h == 0)
             store_lse(p, row, {top, sum});
         return;
@@ -1044,19 +1162,38 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void nvfp4_attentio
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                const float4_t v = {acc[d][e], acc[d][e + 1], acc[d][e + 2], acc[d][e + 3]};
-                *(float4_t *)(sums + 32 * d + 2 * e + 4 * h) = v;
+            for (int x = 0; x < NV; x += 4) {
+                const float4_t v = {acc[d][x], acc[d][x + 1], acc[d][x + 2], acc[d][x + 3]};
+                *(float4_t *)(sums + RW * d + 2 * x + 4 * h) = v;
             }
         if (h == 0)
             *(Norm *)(p.norms + (((int64_t)tile * p.splits + split) * kTileRows + r) * 2) = {top, sum};
     }
-    // whole lines leave the L2 before the ticket, and the last one reads none that it held before
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-    if (!last_of_splits(p, tile, span.splits, &s_ticket))
+}
+
+// The rows of the tile kernel's split tiles, kJoinRows a workgroup, over the whole card. (Joined by
+// the last workgroup of each tile instead: 80 us more for 515 queries at 20011 positions, where
+// few tiles have many splits and one workgroup moved 2.8 MB.)
+constexpr int kJoinThreads = 256, kJoinRows = 16;
+
+template <int D>
+__global__ __launch_bounds__(kJoinThreads) void nvfp4_attention_join_kernel(AttParams p, int32_t tile_rows)
+{
+    __shared__ float s_weights[(kMaxSplits + 1) * kJoinRows];
+    const uint32_t parts = (uint32_t)(tile_rows / kJoinRows), id = blockIdx.x / parts;
+    const int first = (int)(blockIdx.x % parts) * kJoinRows;
+    const uint32_t pairs = (uint32_t)p.B * (uint32_t)p.heads;
+    const int rt = (int)(((uint32_t)p.row_tiles - 1u) - id / pairs);
+    const int b = (int)(id % pairs / (uint32_t)p.heads), hk = (int)(id % pairs % (uint32_t)p.heads);
+    const Sequence s = sequence_of(p, b);
+    const int64_t all_rows = (int64_t)min(s.n, p.max_q) * p.G;
+    if (all_rows <= p.few_rows || (int64_t)rt * tile_rows + first >= all_rows)
         return;
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-    join_splits<D, kTileThreads>(p, s, hk, tile, row0, rows, span.splits, gv, (Norm *)lds);
+    const int row0 = rt * tile_rows, rows = (int)min((int64_t)tile_rows, all_rows - row0);
+    const Span span = span_of(p, s, row0 / p.G, (row0 + rows - 1) / p.G + 1, 0);
+    if (span.splits > 1)
+        join_splits<D, kJoinThreads, 4, 2, 8, true>(p, s, hk, id, row0, first, min(kJoinRows, rows - first), span.splits,
+                                                    p.gv ? *p.gv : 1.0f, s_weights);
 }
 
 // ------------------------------------------------------------------ host
@@ -1126,33 +1263,35 @@ Plan rows_plan(const nvfp4_cache_t &c, int64_t H, int64_t B, const nvfp4_attenti
 }
 
 // 2^30 rows of a sequence at most (max_q * G), so row_tiles and rows fit 32 bits.
-Plan tile_plan(const nvfp4_cache_t &c, int64_t H, int64_t B, const nvfp4_attention_t &a)
+Plan tile_plan(const nvfp4_cache_t &c, int dtype, int64_t H, int64_t B, const nvfp4_attention_t &a)
 {
     Plan p{};
-    const int64_t G = H / c.heads, row_tiles = (a.max_q * G + kTileRows - 1) / kTileRows;
+    const int rows = tile_rows((int)c.head_size, dtype == NVFP4_F32);
+    const int64_t G = H / c.heads, row_tiles = (a.max_q * G + rows - 1) / rows;
     p.tiles = B * c.heads * row_tiles;
-    p.most_rows = kTileRows;
-    const int64_t span = a.window ? std::min<int64_t>(a.max_length, a.window + kTileRows + 64) : a.max_length;
+    p.most_rows = rows;
+    const int64_t span = a.window ? std::min<int64_t>(a.max_length, a.window + rows + 64) : a.max_length;
     const int64_t most = (span + 63) / 64 + 1;
-    int64_t splits = std::min<int64_t>((kTileTarget + p.tiles - 1) / p.tiles, (most + kTileLeast - 1) / kTileLeast);
-    splits = std::max<int64_t>(1, std::min<int64_t>(splits, kMaxSplits));
-    if (p.tiles > kMaxTickets)
-        splits = 1;
-    while (splits > 1 && partial_bytes(p.tiles, splits, kTileRows, c.head_size) > kMaxPartialBytes)
+    // As many as fill the places for workgroups once (two on a CU up to 128 values, one beyond), or
+    // twice where that leaves fewer of them idle
+    const int64_t places = c.head_size <= 128 ? 512 : 256, once = places / p.tiles, twice = 2 * places / p.tiles;
+    int64_t splits = twice * p.tiles * 10 > once * p.tiles * 22 ? twice : once;
+    splits = std::max<int64_t>(1, std::min<int64_t>({splits, kMaxSplits, (most + kTileLeast - 1) / kTileLeast}));
+    while (splits > 1 && partial_bytes(p.tiles, splits, rows, c.head_size) > kMaxPartialBytes)
         --splits;
     p.chunk = (int32_t)((most + splits - 1) / splits);
     p.splits = (int32_t)((most + p.chunk - 1) / p.chunk);
-    p.bytes = p.splits > 1 ? kTicketBytes + (partial_bytes(p.tiles, p.splits, kTileRows, c.head_size) + 255) / 256 * 256 : 0;
+    p.bytes = p.splits > 1 ? kTicketBytes + (partial_bytes(p.tiles, p.splits, rows, c.head_size) + 255) / 256 * 256 : 0;
     return p;
 }
 
 // Sequences of more rows than the rows kernel takes.
 bool has_many(const nvfp4_cache_t &c, int64_t H, const nvfp4_attention_t &a) { return a.max_q * (H / c.heads) > 32; }
 
-size_t need_of(const nvfp4_cache_t &c, int64_t H, int64_t B, const nvfp4_attention_t &a)
+size_t need_of(const nvfp4_cache_t &c, int dtype, int64_t H, int64_t B, const nvfp4_attention_t &a)
 {
     const size_t rows = rows_plan(c, H, B, a).bytes;
-    return has_many(c, H, a) ? std::max(rows, tile_plan(c, H, B, a).bytes) : rows;
+    return has_many(c, H, a) ? std::max(rows, tile_plan(c, dtype, H, B, a).bytes) : rows;
 }
 
 void set_plan(AttParams &p, const Plan &plan, void *workspace)
@@ -1163,13 +1302,17 @@ void set_plan(AttParams &p, const Plan &plan, void *workspace)
     p.norms = p.sums ? p.sums + plan.tiles * plan.splits * plan.most_rows * p.D : nullptr;
 }
 
-template <int D>
+template <int D, bool F32>
 hipError_t launch_tile(const AttParams &p, int64_t grid, hipStream_t st)
 {
-    static_assert(2 * WideTile<D>::kBuffer + 1024 <= 160 * 1024 && kMaxSplits * kTileRows * 8 <= 64 * 1024);
-    const int lds = std::max(2 * WideTile<D>::kBuffer, p.splits > 1 ? p.splits * kTileRows * 8 : 0);
-    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((uint32_t)grid), dim3(kTileThreads), lds, st, p); };
-    p.dtype == NVFP4_F32 ? go(nvfp4_attention_tile_kernel<D, true>) : go(nvfp4_attention_tile_kernel<D, false>);
+    constexpr int threads = 64 * tile_waves(D, F32), rows = tile_rows(D, F32), buffers = 2 * WideTile<D, threads>::kBuffer;
+    static_assert(buffers + 1024 <= 160 * 1024 && rows % kJoinRows == 0);
+    hipLaunchKernelGGL((nvfp4_attention_tile_kernel<D, F32>), dim3((uint32_t)grid), dim3(threads), buffers, st, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.splits == 1)
+        return e;
+    hipLaunchKernelGGL((nvfp4_attention_join_kernel<D>), dim3((uint32_t)(grid / p.splits * (rows / kJoinRows))), dim3(kJoinThreads), 0, st,
+                       p, rows);
     return hipGetLastError();
 }
 
@@ -1177,8 +1320,8 @@ template <int D, int NQ, bool F32>
 hipError_t launch_rows(const AttParams &p, int64_t grid, hipStream_t st)
 {
     using S = RowsTile<D>;
-    const int lds = std::max({kRowsWaves * S::kWave, kRowsWaves * 16 * NQ * (D * 4 + 8), p.splits * p.most_rows * 8});
-    static_assert(kRowsWaves * S::kWave + 64 <= 160 * 1024 && kRowsWaves * 16 * NQ * (D * 4 + 8) + 64 <= 160 * 1024 && kMaxSplits * 32 * 8 < 64 * 1024);
+    const int lds = std::max({kRowsWaves * S::kWave, kRowsWaves * 16 * NQ * (D * 4 + 8), (p.splits + 1) * 4 * p.most_rows});
+    static_assert(kRowsWaves * S::kWave + 64 <= 160 * 1024 && kRowsWaves * 16 * NQ * (D * 4 + 8) + 64 <= 160 * 1024 && (kMaxSplits + 1) * 4 * 64 < 64 * 1024);
     auto kern = nvfp4_attention_rows_kernel<D, NQ, F32>;
     hipLaunchKernelGGL(kern, dim3((uint32_t)grid), dim3(kRowsThreads), lds, st, p);
     return hipGetLastError();
@@ -1214,7 +1357,7 @@ size_t nvfp4_cache_attention_workspace_bytes(const nvfp4_cache_t *cache, int dty
 {
     if (check(cache, dtype, T, H, B, attention) != NVFP4_OK)
         return 0;
-    return need_of(*cache, H, B, *attention);
+    return need_of(*cache, dtype, H, B, *attention);
 }
 
 nvfp4_status_t nvfp4_cache_attention(const nvfp4_cache_t *cache, const void *q, int dtype, void *out, float *lse,
@@ -1248,22 +1391,26 @@ nvfp4_status_t nvfp4_cache_attention(const nvfp4_cache_t *cache, const void *q, 
     p.max_q = (int32_t)attention->max_q, p.max_length = (int32_t)attention->max_length;
     // a window as long as the longest sequence hides nothing
     p.window = attention->window >= attention->max_length ? 0 : (int32_t)attention->window, p.causal = attention->causal, p.dtype = dtype, p.scale = attention->scale;
-    const Plan few = rows_plan(*cache, H, B, *attention), many = tile_plan(*cache, H, B, *attention);
+    const Plan few = rows_plan(*cache, H, B, *attention), many = tile_plan(*cache, dtype, H, B, *attention);
     const bool both = has_many(*cache, H, *attention);
     if (few.tiles > kMaxGrid / few.splits || (both && many.tiles > kMaxGrid / many.splits))
         return NVFP4_ERR_INVALID_SHAPE;
-    const size_t need = need_of(*cache, H, B, *attention);
+    const size_t need = need_of(*cache, dtype, H, B, *attention);
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
         return NVFP4_ERR_WORKSPACE;
     p.few_rows = attention->max_q * p.G <= 16 ? 16 : 32;
-    p.row_tiles = (int32_t)((attention->max_q * p.G + kTileRows - 1) / kTileRows);
+    const int tile = tile_rows(p.D, dtype == NVFP4_F32);
+    p.row_tiles = (int32_t)((attention->max_q * p.G + tile - 1) / tile);
     const hipStream_t hs = (hipStream_t)stream;
     // one after the other on the stream, so one workspace serves both
     set_plan(p, few, need ? workspace : nullptr);
     hipError_t e = by_head(p.D, [&](auto d) { return launch_rows_of<d()>(p, few.tiles * few.splits, hs); });
     if (e == hipSuccess && both) {
         set_plan(p, many, need ? workspace : nullptr);
-        e = by_head(p.D, [&](auto d) { return launch_tile<d()>(p, many.tiles * many.splits, hs); });
+        e = by_head(p.D, [&](auto d) {
+            const int64_t grid = many.tiles * many.splits;
+            return dtype == NVFP4_F32 ? launch_tile<d(), true>(p, grid, hs) : launch_tile<d(), false>(p, grid, hs);
+        });
     }
     if (e == hipSuccess)
         return NVFP4_OK;

@@ -671,7 +671,7 @@ nvfp4_status_t nvfp4_cache_read(const nvfp4_cache_t *cache, void *k, void *v, in
  *            written. max_length <= table_width * page_size.
  * Keys and values are exact in float16 and go to the matrix cores as that; q is
  * taken to float16 with a power of two of its row's own (float32: as two float16,
- * 22 bits), probabilities to float16 (float32: two; all to at least 2^-37 of the
+ * 22 bits), probabilities to float16 (float32: two; all to at least 2^-33 of the
  * query's largest), sums, maxima and norms are
  * float32, out is rounded once to dtype. The order of summation is fixed for
  * given arguments and lengths, so equal calls give equal bits.

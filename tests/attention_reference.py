@@ -112,15 +112,15 @@ def check_attention(out, lse, want, dtype, what=""):
     (256 + 2 + 4) 2^-23 spread, and 2^-22 of the exponential. Weights change by twice that (numerator and norm); the
     sums over the positions add a step for each, in the norm and in the values, and so do
     the rescalings of the running maximum (at most one for each). Weights are
-    rounded to float16, 2^-11 of each (float32: to two, 2^-22), and as they are held times 2^12,
-    whose least step's half is 2^-25, by at most 2^-37 of the largest where they are smaller
-    still: 2^-37 sum |v|. Then the rounding to dtype."""
+    rounded to float16, 2^-11 of each (float32: to two, 2^-22), and as they are held times 2^8,
+    whose least step's half is 2^-25, by at most 2^-33 of the largest where they are smaller
+    still: 2^-33 sum |v|. Then the rounding to dtype."""
     written = want["written"]
     o, ref = out.double().cpu().numpy(), want["out"]
     delta = (262 * 2.0 ** -23 * want["spread"] + 2.0 ** -22)[..., None]
     steps = (3 * want["count"][..., None] + 64) * 2.0 ** -23
     weight = 2.0 ** -22 if dtype == torch.float32 else 2.0 ** -11
-    tol = want["size"] * (2 * delta + steps + weight) + 2.0 ** -37 * want["all"] + fp4.HALF_STEP[dtype] * (1 + 2.0 ** -7) * np.abs(ref) + fp4.LEAST[dtype]
+    tol = want["size"] * (2 * delta + steps + weight) + 2.0 ** -33 * want["all"] + fp4.HALF_STEP[dtype] * (1 + 2.0 ** -7) * np.abs(ref) + fp4.LEAST[dtype]
     nan = np.isnan(ref)
     assert np.array_equal(np.isnan(o)[written], nan[written]), f"{what}: NaN at other places"
     fine = written[:, None, None] & ~nan

@@ -72,7 +72,7 @@ def test_drafts(program, tmp_path, window, causal, dt):
 
 
 @pytest.mark.parametrize("dt", [1, 2])
-@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
 def test_prompts(program, tmp_path, D, dt):
     rng = np.random.default_rng(4)
     lengths, counts = [140, 45, 30, 90], [70, 45, 1, 9]

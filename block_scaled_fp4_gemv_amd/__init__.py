@@ -725,25 +725,63 @@ def nvfp4_moe_combine(y, ids, weights, out, T: int, k: int, M: int, dtype=None, 
 _LAYOUTS = {"half": NVFP4_ROPE_HALF, "interleaved": NVFP4_ROPE_INTERLEAVED}
 _METHODS = {"unscaled": NVFP4_ROPE_UNSCALED, "linear": NVFP4_ROPE_LINEAR, "base": NVFP4_ROPE_BASE,
             "bands": NVFP4_ROPE_BANDS, "ramp": NVFP4_ROPE_RAMP}
-_I64, _F64, _U8 = "torch.int64", "torch.float64", "torch.uint8"
+# What a call costs on the host is as long as a small kernel: types are compared as
+# objects here, not as text (0.4 us each), and each tensor is asked once for what is needed.
+_torch = None
 
 
-_current_device = None
+class _Torch:
+    """torch's types and device query, looked up once (torch is imported with the first call)."""
 
-
-def _check_device(x, name):
-    """Kernels are launched on the current device: a tensor of another is refused."""
-    global _current_device
-    if not x.is_cuda:
-        raise ValueError("operands must be device tensors")
-    if _current_device is None:
+    def __init__(self):
         import torch
-        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-    if x.get_device() != _current_device():
+        self.kinds = {torch.float16: NVFP4_F16, torch.bfloat16: NVFP4_BF16, torch.float32: NVFP4_F32}
+        self.f32, self.f64, self.i32, self.i64, self.u8 = (torch.float32, torch.float64, torch.int32, torch.int64,
+                                                           torch.uint8)
+        self.current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _types() -> _Torch:
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
+
+
+def _kind(x, dtype, t):
+    """nvfp4_dtype_t of a tensor (or of ``dtype``, needed for raw pointers)."""
+    if dtype is None and x is not None and not isinstance(x, int):
+        kind = t.kinds.get(x.dtype)
+        if kind is not None:
+            return kind
+    return _dtype_id(x, dtype)
+
+
+def _here(x, name, t):
+    """Kernels are launched on the current device: a tensor of another is refused."""
+    device = x.get_device()
+    if device < 0:
+        raise ValueError("operands must be device tensors")
+    if device != t.current_device():
         raise ValueError(f"{name} is on {x.device}, not on the current device")
 
 
-def _rows(x, name, dt, T, H, D, token_stride, head_stride):
+def _at(x, need, name, dtype, t):
+    """Device pointer of a dense tensor of type ``dtype`` that holds at least ``need`` bytes;
+    raw pointers and None pass."""
+    if x is None or isinstance(x, int):
+        return x
+    _here(x, name, t)
+    if not x.is_contiguous():
+        raise ValueError("operands must be contiguous")
+    if x.dtype is not dtype and dtype is not None:
+        raise ValueError(f"{name} is {x.dtype}, not {str(dtype).replace('torch.', '')}")
+    if x.nbytes < need:
+        raise ValueError(f"{name} holds {x.nbytes} bytes, the shape needs {need}")
+    return x.data_ptr()
+
+
+def _rows(x, name, dt, T, H, D, token_stride, head_stride, t):
     """Pointer of a [T][H][D] tensor of type ``dt`` and its strides in elements (dense
     by default), checked against what its memory holds behind its first element."""
     given = token_stride is not None or head_stride is not None
@@ -753,17 +791,19 @@ def _rows(x, name, dt, T, H, D, token_stride, head_stride):
         token_stride = H * head_stride
     if x is None or isinstance(x, int):
         return x, token_stride, head_stride
-    _check_device(x, name)
-    if _dtype_id(x, None) != dt:
+    _here(x, name, t)
+    if t.kinds.get(x.dtype) != dt:
         raise ValueError(f"{name} is {x.dtype}, not of the call's type")
-    if not given and not x.is_contiguous():
-        raise ValueError(f"{name} is not contiguous: give its strides")
-    if given and x.dim() and x.stride(-1) != 1 and x.shape[-1] > 1:
-        raise ValueError(f"rows of {name} are not contiguous")
-    if min(T, H, D) >= 1 and min(token_stride, head_stride) >= 0:
-        size = x.element_size()
+    if not given:
+        if not x.is_contiguous():
+            raise ValueError(f"{name} is not contiguous: give its strides")
+        held = x.numel()
+    else:
+        if x.dim() and x.stride(-1) != 1 and x.shape[-1] > 1:
+            raise ValueError(f"rows of {name} are not contiguous")
+        held = x.untyped_storage().nbytes() // x.element_size() - x.storage_offset()
+    if T >= 1 and H >= 1 and D >= 1 and token_stride >= 0 and head_stride >= 0:
         need = (T - 1) * token_stride + (H - 1) * head_stride + D
-        held = x.untyped_storage().nbytes() // size - x.storage_offset() if given else x.numel()
         if held < need:
             raise ValueError(f"{name} holds {held} elements, the shape needs {need}")
     return x.data_ptr(), token_stride, head_stride
@@ -784,14 +824,15 @@ def nvfp4_rope(x, out, positions, frequencies, T: int, H: int, D: int, R: int, l
     """Enqueue out = x [T][H][D] with the pairs of each head's first R values turned by
     positions[t] * frequencies[j] (``transpose``: back, the gradient). Strides in
     elements, dense by default; out may be x (with x's strides then)."""
-    dt = _dtype_id(x, dtype)
-    px, ts, hs = _rows(x, "x", dt, T, H, D, token_stride, head_stride)
-    if out_token_stride is None and out_head_stride is None and out is x:
+    t = _torch or _types()
+    dt = _kind(x, dtype, t)
+    px, ts, hs = _rows(x, "x", dt, T, H, D, token_stride, head_stride, t)
+    if out is x and out_token_stride is None and out_head_stride is None:
         out_token_stride, out_head_stride = ts, hs
-    po, ots, ohs = _rows(out, "out", dt, T, H, D, out_token_stride, out_head_stride)
-    on = 1 if min(T, R) >= 1 else 0                          # the library reports shape errors itself
-    _done(lib().nvfp4_rope(px, dt, po, _op(positions, on * 8 * T, "positions", _I64),
-                           _op(frequencies, on * 4 * R, "frequencies", _F64), T, H, D, R, ts, hs, ots, ohs,
+    po, ots, ohs = _rows(out, "out", dt, T, H, D, out_token_stride, out_head_stride, t)
+    # (the library reports shape errors itself: a negative size needs nothing here)
+    _done(lib().nvfp4_rope(px, dt, po, _at(positions, 8 * T, "positions", t.i64, t),
+                           _at(frequencies, 4 * R, "frequencies", t.f64, t), T, H, D, R, ts, hs, ots, ohs,
                            _LAYOUTS.get(layout, layout), factor, int(transpose), _stream_handle(stream)), "nvfp4_rope")
 
 
@@ -809,56 +850,56 @@ class Nvfp4Cache:
         strides, pointers = [], []
         for given, each in ((code_page_stride, row * head_size // 2), (scale_page_stride, row * head_size // 16)):
             strides.append(each if given is None else given)
+        t = _types()
         for name, x, stride, given, each in (
                 ("k_codes", k_codes, strides[0], code_page_stride, row * head_size // 2),
                 ("k_scales", k_scales, strides[1], scale_page_stride, row * head_size // 16),
                 ("v_codes", v_codes, strides[0], code_page_stride, row * head_size // 2),
                 ("v_scales", v_scales, strides[1], scale_page_stride, row * head_size // 16)):
             if given is None or x is None or isinstance(x, int):
-                pointers.append(_op(x, max(0, pages * each), name, _U8))
+                pointers.append(_at(x, max(0, pages * each), name, t.u8, t))
                 continue
-            if not x.is_cuda:
-                raise ValueError("operands must be device tensors")
-            if str(x.dtype) != _U8:
+            _here(x, name, t)
+            if x.dtype is not t.u8:
                 raise ValueError(f"{name} is {x.dtype}, not uint8")
             need, held = (pages - 1) * stride + each, x.untyped_storage().nbytes() - x.storage_offset()
             if min(pages, stride) >= 1 and held < need:
                 raise ValueError(f"{name} holds {held} bytes, the shape needs {need}")
             pointers.append(x.data_ptr())
-        self.struct = CacheStruct(*pointers, _op(k_scale, 4, "k_scale", _F32), _op(v_scale, 4, "v_scale", _F32), pages,
-                                  page_size, heads, head_size, *strides)
+        self.struct = CacheStruct(*pointers, _at(k_scale, 4, "k_scale", t.f32, t), _at(v_scale, 4, "v_scale", t.f32, t),
+                                  pages, page_size, heads, head_size, *strides)
         self._ref = ctypes.byref(self.struct)
+
+
+_DENSE = (None, None)
 
 
 def nvfp4_cache_write(cache, k, v, slots, T: int, k_strides=None, v_strides=None, dtype=None, stream=None) -> None:
     """Enqueue the quantisation of k, v [T][heads][head_size] (strides: (token, head) in elements,
     dense by default) into the cache's rows ``slots`` (int64 [T]; outside the cache: not written)."""
-    dt = _dtype_id(k, dtype)
-    pk, kt, kh = _rows(k, "k", dt, T, cache.heads, cache.head_size, *(k_strides or (None, None)))
-    pv, vt, vh = _rows(v, "v", dt, T, cache.heads, cache.head_size, *(v_strides or (None, None)))
-    _done(lib().nvfp4_cache_write(cache._ref, pk, pv, dt, _op(slots, 8 * max(T, 0), "slots", _I64), T, kt, kh, vt, vh,
+    t = _torch or _types()
+    dt, H, D = _kind(k, dtype, t), cache.heads, cache.head_size
+    pk, kt, kh = _rows(k, "k", dt, T, H, D, *(k_strides or _DENSE), t)
+    pv, vt, vh = _rows(v, "v", dt, T, H, D, *(v_strides or _DENSE), t)
+    _done(lib().nvfp4_cache_write(cache._ref, pk, pv, dt, _at(slots, 8 * T, "slots", t.i64, t), T, kt, kh, vt, vh,
                                   _stream_handle(stream)), "nvfp4_cache_write")
 
 
 def nvfp4_cache_read(cache, k, v, slots, T: int, dtype=None, stream=None) -> None:
     """Enqueue k, v [T][heads][head_size] = the values of the cache's rows ``slots`` (int64 [T];
     outside the cache: zeros)."""
-    dt = _dtype_id(k, dtype)
-    pk, _, _ = _rows(k, "k", dt, T, cache.heads, cache.head_size, None, None)
-    pv, _, _ = _rows(v, "v", dt, T, cache.heads, cache.head_size, None, None)
-    _done(lib().nvfp4_cache_read(cache._ref, pk, pv, dt, _op(slots, 8 * max(T, 0), "slots", _I64), T,
+    t = _torch or _types()
+    dt, H, D = _kind(k, dtype, t), cache.heads, cache.head_size
+    pk, _, _ = _rows(k, "k", dt, T, H, D, None, None, t)
+    pv, _, _ = _rows(v, "v", dt, T, H, D, None, None, t)
+    _done(lib().nvfp4_cache_read(cache._ref, pk, pv, dt, _at(slots, 8 * T, "slots", t.i64, t), T,
                                  _stream_handle(stream)), "nvfp4_cache_read")
 
 
-def _attention(cache, H, max_q, max_length, scale, causal, window, token_stride, head_stride):
-    if scale is None:
-        scale = max(cache.head_size, 1) ** -0.5
-    return Attention(token_stride, head_stride, max_q, max_length, window, scale, int(causal))
-
-
-def nvfp4_cache_attention_workspace_bytes(cache, dtype, T: int, H: int, B: int, max_q: int, max_length: int) -> int:
+def nvfp4_cache_attention_workspace_bytes(cache, dtype, T: int, H: int, B: int, max_q: int, max_length: int,
+                                          window: int = 0) -> int:
     """Bytes of a workspace for such a call (0: none needed, or a call that is refused); ``dtype`` as q's."""
-    opts = _attention(cache, H, max_q, max_length, None, True, 0, 0, 0)
+    opts = Attention(0, 0, max_q, max_length, window, 1.0, 1)
     return int(lib().nvfp4_cache_attention_workspace_bytes(cache._ref, _dtype_id(None, dtype), T, H, B,
                                                            ctypes.byref(opts)))
 
@@ -873,21 +914,25 @@ def nvfp4_cache_attention(cache, q, out, offsets, lengths, table, T: int, H: int
     the pages table[b] (int32 [B][table_width]; its last dimension by default). scale None:
     head_size ** -0.5; lse: float32 [T][H]; a (zero-initialised) workspace of
     nvfp4_cache_attention_workspace_bytes or of NVFP4_WORKSPACE_MAX_BYTES."""
-    D, dt = cache.head_size, _dtype_id(q, dtype)
-    pq, ts, hs = _rows(q, "q", dt, T, H, D, token_stride, head_stride)
-    po, _, _ = _rows(out, "out", dt, T, H, D, None, None)
+    t = _torch or _types()
+    D, dt = cache.head_size, _kind(q, dtype, t)
+    pq, ts, hs = _rows(q, "q", dt, T, H, D, token_stride, head_stride, t)
+    po, _, _ = _rows(out, "out", dt, T, H, D, None, None, t)
     if table_width is None:
         if isinstance(table, int) or table is None:
             raise ValueError("raw pointers need table_width=")
         table_width = table.shape[-1]
-    pw, nw = _workspace(workspace, workspace_bytes)
-    opts = _attention(cache, H, max_q, max_length, scale, causal, window, ts, hs)
-    on = 1 if min(T, H, B, table_width) >= 1 else 0
-    _done(lib().nvfp4_cache_attention(cache._ref, pq, dt, po, _op(lse, on * 4 * T * H, "lse", _F32),
-                                      _op(offsets, on * 4 * (B + 1), "offsets", _I32),
-                                      _op(lengths, on * 4 * B, "lengths", _I32),
-                                      _op(table, on * 4 * B * table_width, "table", _I32), T, H, B, table_width,
-                                      ctypes.byref(opts), pw, nw, _stream_handle(stream)), "nvfp4_cache_attention")
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else workspace.nbytes
+    elif workspace_bytes < 0:
+        raise ValueError(f"workspace_bytes is {workspace_bytes}")
+    opts = Attention(ts, hs, max_q, max_length, window, max(D, 1) ** -0.5 if scale is None else scale, causal)
+    # (the library reports shape errors itself: a negative size needs nothing here)
+    _done(lib().nvfp4_cache_attention(cache._ref, pq, dt, po, _at(lse, 4 * T * H, "lse", t.f32, t),
+                                      _at(offsets, 4 * (B + 1), "offsets", t.i32, t), _at(lengths, 4 * B, "lengths", t.i32, t),
+                                      _at(table, 4 * B * table_width, "table", t.i32, t), T, H, B, table_width,
+                                      ctypes.byref(opts), _at(workspace, workspace_bytes, "workspace", None, t),
+                                      workspace_bytes, _stream_handle(stream)), "nvfp4_cache_attention")
 
 
 def nvfp4_status_string(status: int) -> str:

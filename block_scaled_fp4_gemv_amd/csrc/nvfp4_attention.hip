@@ -34,8 +34,9 @@ struct AttParams {
     int32_t max_q, max_length, window, causal, dtype;
     int32_t splits, chunk;                      // of a sequence's positions; chunk in tiles of 64
     int32_t few_rows;                           // sequences of so many rows are the rows kernel's
-    int32_t row_tiles;                          // of 128 rows, at most, for a sequence and key head
+    int32_t row_tiles;                          // at most, for a sequence and key head
     int32_t most_rows;                          // of a partial result
+    int32_t join_here;                          // rows kernel: the last workgroup of a tile joins its splits
     uint32_t *tickets;
     float *sums, *norms;                        // partial results: [tile][split][most_rows][D], [..][2]
     float scale;
@@ -64,8 +65,10 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 // of it below). A row rarely needs that behind its first tile; before, a wave's 32 rows
 // rescaled nearly every one (128 values a row: 66 of 400 instructions of a tile).
 constexpr float kShift = 8.0f, kSlack = 7.0f;
-constexpr int kRowsThreads = 256, kRowsWaves = 4;
-constexpr int kMaxSplits = 64, kRowsTarget = 2048, kTileLeast = 4;
+constexpr int kCus = 256;
+// Sequences of up to 64 rows are the rows kernel's, 16 or 32 at a time: 33 sequences' 40 rows at 1000
+// visible positions took 24 us in the tile kernel.
+constexpr int kFewRows = 64, kJoinHere = 8, kMaxSplits = 64, kTileLeast = 4;
 
 // The head's D values go through the matrix instruction in steps of 32. A lane (row
 // lane % 16, g = lane / 16) has 8 of a step's; which 8 is free while q and K agree: runs
@@ -272,6 +275,27 @@ __device__ __attribute__((always_inline)) inline float sum_of_4(float v)
     return sum_of_2(x.a + x.b);
 }
 
+// Over all 64 lanes, in every lane: within rows of 16 by rotations.
+template <int N>
+__device__ __attribute__((always_inline)) inline float rotated(float v)
+{
+    return as_f32(__builtin_amdgcn_update_dpp(0, as_i32(v), 0x120 + N, 0xF, 0xF, true));
+}
+__device__ __attribute__((always_inline)) inline float max_of_64(float v)
+{
+    v = fmaxf(v, rotated<1>(v));
+    v = fmaxf(v, rotated<2>(v));
+    v = fmaxf(v, rotated<4>(v));
+    return max_of_4(fmaxf(v, rotated<8>(v)));
+}
+__device__ __attribute__((always_inline)) inline float sum_of_64(float v)
+{
+    v += rotated<1>(v);
+    v += rotated<2>(v);
+    v += rotated<4>(v);
+    return sum_of_4(v + rotated<8>(v));
+}
+
 // Adds the splits' partial results of rows first .. first + rows - 1 of a tile in the order of the
 // splits and stores them; row0 is the tile's first row among the sequence's. `weights`: LDS for
 // [splits][rows] of them, and behind them for [rows] sums. V values of a row at a time, U such at once,
@@ -288,6 +312,25 @@ __device__ __attribute__((always_inline)) inline void join_splits(const AttParam
     const float *from = p.norms + ((int64_t)tile * p.splits * p.most_rows + first) * 2;
     row0 += first;
     float *const total = weights + splits * rows;
+    const int units = rows * (D / V);
+    float x[U][AHEAD][V];
+    auto load = [&](int u0, int k0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int at = min(u0 + u * THREADS, units - 1);
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const float *one = sums + ((int64_t)min(k0 + k, splits - 1) * p.most_rows + at / (D / V)) * D + at % (D / V) * V;
+                if constexpr (FENCED) {
+                    __builtin_memcpy(x[u][k], __builtin_assume_aligned(one, 4 * V), 4 * V);
+                } else {
+                    const float2_u y = load_partial(one);
+                    x[u][k][0] = y.x, x[u][k][1] = y.y;
+                }
+            }
+        }
+    };
+    load((int)threadIdx.x, 0);                                  // under way while the weights are found
     // each row's weights of the splits, a lane each: R rows of a wave at once
     constexpr int R = 4, WAVES = THREADS / 64;
     const int lane = (int)threadIdx.x % 64, wave = (int)threadIdx.x / 64;
@@ -299,17 +342,9 @@ __device__ __attribute__((always_inline)) inline void join_splits(const AttParam
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             const int r = r0 + j * WAVES;
-            float top = lane < splits ? one[j].x : -__builtin_inff();
-#pragma unroll
-            for (int d = 1; d < 16; d <<= 1)
-                top = fmaxf(top, __shfl_xor(top, d));
-            top = max_of_4(top);
+            const float top = max_of_64(lane < splits ? one[j].x : -__builtin_inff());
             const float w = lane < splits ? weight_of(one[j].x, top) : 0.0f;
-            float sum = lane < splits ? one[j].y * w : 0.0f;
-#pragma unroll
-            for (int d = 1; d < 16; d <<= 1)
-                sum += __shfl_xor(sum, d);
-            sum = sum_of_4(sum);
+            const float sum = sum_of_64(lane < splits ? one[j].y * w : 0.0f);
             if (r < rows && lane < splits)
                 weights[lane * rows + r] = w;
             if (r < rows && lane == 0) {
@@ -319,7 +354,6 @@ __device__ __attribute__((always_inline)) inline void join_splits(const AttParam
         }
     }
     __syncthreads();
-    const int units = rows * (D / V);
     for (int u0 = (int)threadIdx.x; u0 < units; u0 += U * THREADS) {
         float v[U][V];
 #pragma unroll
@@ -328,21 +362,8 @@ __device__ __attribute__((always_inline)) inline void join_splits(const AttParam
             for (int e = 0; e < V; ++e)
                 v[u][e] = 0.0f;
         for (int k0 = 0; k0 < splits; k0 += AHEAD) {
-            float x[U][AHEAD][V];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int at = min(u0 + u * THREADS, units - 1);
-#pragma unroll
-                for (int k = 0; k < AHEAD; ++k) {
-                    const float *one = sums + ((int64_t)min(k0 + k, splits - 1) * p.most_rows + at / (D / V)) * D + at % (D / V) * V;
-                    if constexpr (FENCED) {
-                        __builtin_memcpy(x[u][k], __builtin_assume_aligned(one, 4 * V), 4 * V);
-                    } else {
-                        const float2_u y = load_partial(one);
-                        x[u][k][0] = y.x, x[u][k][1] = y.y;
-                    }
-                }
-            }
+            if (u0 != (int)threadIdx.x || k0 != 0)
+                load(u0, k0);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int r = min(u0 + u * THREADS, units - 1) / (D / V);
@@ -401,8 +422,8 @@ __device__ __attribute__((always_inline)) inline void settle_order()
 //   O^T = V^T P^T: a lane's P registers are its k-range as they stand, if V's operand has the same
 //     order. Its codes come from LDS transposed (16 positions of one value per
 //     lane), so a pair of codes is two positions, and so is a pair of scales.
-template <int D, int NQ, bool F32>
-__global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 || NQ == 1 ? 2 : 1) void nvfp4_attention_rows_kernel(AttParams p)
+template <int D, int NQ, bool F32, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : D <= 64 && NQ == 1 ? 4 : D <= 128 || NQ == 1 ? 2 : 1) void nvfp4_attention_rows_kernel(AttParams p)
 {
     using S = RowsTile<D>;
     using St = Steps<D>;
@@ -414,15 +435,16 @@ __global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 || 
     // Splits outermost: neighbouring workgroups, which run on different XCDs, are different
     // sequences and heads. (Innermost, every XCD had one of the splits: those whose splits
     // lie behind most sequences' ends stood idle, 172 us for 64 sequences of 1024 to 8192 positions.)
-    const uint32_t tiles = (uint32_t)p.B * (uint32_t)p.heads, tile = blockIdx.x % tiles;
-    const int split = (int)(blockIdx.x / tiles);
-    const int b = (int)(tile / (uint32_t)p.heads), hk = (int)(tile % (uint32_t)p.heads);
+    const uint32_t pairs = (uint32_t)p.B * (uint32_t)p.heads, tiles = pairs * (uint32_t)p.row_tiles, tile = blockIdx.x % tiles;
+    const int split = (int)(blockIdx.x / tiles), row0 = (int)(tile / pairs) * 16 * NQ;
+    const int b = (int)(tile % pairs / (uint32_t)p.heads), hk = (int)(tile % pairs % (uint32_t)p.heads);
     const Sequence s = sequence_of(p, b);
     const int queries = min(s.n, p.max_q);
-    if (queries == 0 || queries > 16 * NQ || queries * p.G > 16 * NQ)
+    if (queries > kFewRows || queries * p.G > p.few_rows || row0 >= queries * p.G)
         return;
-    const int rows = queries * p.G;
-    const Span span = span_of(p, s, 0, queries, split);
+    const int rows = min(16 * NQ, queries * p.G - row0);
+    const int tok0 = row0 / p.G, tok1 = (row0 + rows - 1) / p.G + 1;
+    const Span span = span_of(p, s, tok0, tok1, split);
     if (split >= span.splits)
         return;
 
@@ -514,7 +536,7 @@ __global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 || 
 #pragma unroll
     for (int a = 0; a < 4; ++a)
         load_k(n, e, a);
-    e = entries(n + kRowsWaves);
+    e = entries(n + WAVES);
 
     // --- this lane's rows of q
     const float factor = p.scale * (p.gk ? *p.gk : 1.0f) * kLog2e;
@@ -523,8 +545,8 @@ __global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 || 
     int32_t begin[NQ], end[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-        const int r = 16 * n + i, tok = r / p.G, pos = s.length - s.n + tok;
-        const bool real = r < rows;
+        const int r = row0 + 16 * n + i, tok = r / p.G, pos = s.length - s.n + tok;
+        const bool real = r < row0 + rows;
         end[n] = p.causal ? min(s.length, pos + 1) : s.length;
         begin[n] = p.window ? max(0, pos - p.window + 1) : 0;
         const uint8_t *x = p.q + (int64_t)(s.first + (real ? tok : 0)) * p.q_token +
@@ -551,11 +573,11 @@ __global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 || 
         rf[n] = scale.factor;
     }
     // positions that all rows see: no mask within them
-    const int32_t all_from = p.window ? max(0, s.length - s.n + queries - p.window) : 0;
-    const int32_t all_to = p.causal ? min(s.length, s.length - s.n + 1) : s.length;
+    const int32_t all_from = p.window ? max(0, s.length - s.n + tok1 - p.window) : 0;
+    const int32_t all_to = p.causal ? min(s.length, s.length - s.n + tok0 + 1) : s.length;
 
     // --- the loop: what the next tile needs is loaded as soon as its registers are free
-    for (; n < span.end; n += kRowsWaves) {
+    for (; n < span.end; n += WAVES) {
         const int32_t t0 = first_position + n * 64;
         // --- V's codes and, as float16 in the order of the k-ranges, its scales to LDS; a position that no
         // row sees has 0 there, and so has a NaN, which is noted for the rows that see it
@@ -610,7 +632,7 @@ __global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 || 
                 }
             }
         }
-        load_v(n + kRowsWaves, e);
+        load_v(n + WAVES, e);
         // --- S^T
         float logit[NQ][4][4];
 #pragma unroll
@@ -644,7 +666,7 @@ __global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 || 
                     step(St::N - 1, raw.k32[a], s0);
                 }
             }
-            load_k(n + kRowsWaves, e, a);
+            load_k(n + WAVES, e, a);
 #pragma unroll
             for (int m = 0; m < NQ; ++m)
 #pragma unroll
@@ -670,7 +692,7 @@ __global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 || 
             }
         }
         there = there_of(e);
-        e = entries(n + 2 * kRowsWaves);
+        e = entries(n + 2 * WAVES);
         // --- softmax
         half8_t prob[PARTS][NQ][2];
 #pragma unroll
@@ -725,7 +747,7 @@ __global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 || 
     // --- the waves' results through LDS: sums [wave][16 NQ][D], norms
     __syncthreads();                                                   // every wave's V is read
     float *const w_sums = (float *)lds;
-    Norm *const w_norms = (Norm *)(lds + kRowsWaves * 16 * NQ * D * 4);
+    Norm *const w_norms = (Norm *)(lds + WAVES * 16 * NQ * D * 4);
 #pragma unroll
     for (int m = 0; m < NQ; ++m) {
         sum[m] = sum_of_4(sum[m]);
@@ -744,38 +766,41 @@ __global__ __launch_bounds__(kRowsThreads, D <= 64 && NQ == 1 ? 4 : D <= 128 || 
     const float gv = p.gv ? *p.gv : 1.0f;
     float *const sums = p.sums + ((int64_t)tile * p.splits + split) * p.most_rows * D;
     float *const norms = p.norms + ((int64_t)tile * p.splits + split) * p.most_rows * 2;
-    for (int u = (int)threadIdx.x; u < rows * (D / 4); u += kRowsThreads) {
+    for (int u = (int)threadIdx.x; u < rows * (D / 4); u += (64 * WAVES)) {
         const int r = u / (D / 4), d = u % (D / 4) * 4;
         Norm all{-__builtin_inff(), 0.0f};
 #pragma unroll
-        for (int w = 0; w < kRowsWaves; ++w)
+        for (int w = 0; w < WAVES; ++w)
             all.top = fmaxf(all.top, w_norms[w * 16 * NQ + r].top);
         float4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int w = 0; w < kRowsWaves; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
             const Norm one = w_norms[w * 16 * NQ + r];
             const float part = weight_of(one.top, all.top);
             all.sum += one.sum * part;
             v += *(const float4_t *)(w_sums + (w * 16 * NQ + r) * D + d) * part;
         }
         if (span.splits == 1) {
-            const int64_t row = out_row(p, s, hk, r);
+            const int64_t row = out_row(p, s, hk, row0 + r);
             store_values<4>(p, row * D + d, {v.x, v.y, v.z, v.w}, all.sum, gv);
             if (d == 0)
                 store_lse(p, row, all);
             continue;
         }
-        store_partial(sums + r * D + d, (float2_u){v.x, v.y});
-        store_partial(sums + r * D + d + 2, (float2_u){v.z, v.w});
-        if (d == 0)
-            store_partial(norms + r * 2, (float2_u){all.top, all.sum});
+        if (p.join_here) {
+            store_partial(sums + r * D + d, (float2_u){v.x, v.y});
+            store_partial(sums + r * D + d + 2, (float2_u){v.z, v.w});
+            if (d == 0)
+                store_partial(norms + r * 2, (float2_u){all.top, all.sum});
+        } else {
+            *(float4_t *)(sums + r * D + d) = v;
+            if (d == 0)
+                *(Norm *)(norms + r * 2) = all;
+        }
     }
-    if (span.splits == 1 || !last_of_splits(p, tile, span.splits, &s_ticket))
+    if (span.splits == 1 || !p.join_here || !last_of_splits(p, tile, span.splits, &s_ticket))
         return;
-    if (span.splits <= 8)
-        join_splits<D, kRowsThreads, 2, 1, 8, false>(p, s, hk, tile, 0, 0, rows, span.splits, gv, (float *)lds);
-    else
-        join_splits<D, kRowsThreads, 2, 1, 32, false>(p, s, hk, tile, 0, 0, rows, span.splits, gv, (float *)lds);
+    join_splits<D, 64 * WAVES, 2, 1, 8, false>(p, s, hk, tile, row0, 0, rows, span.splits, gv, (float *)lds);
 }
 
 // ------------------------------------------------------------------ tile kernel
@@ -1171,29 +1196,30 @@ __global__ __launch_bounds__(64 * tile_waves(D, F32), 2) void nvfp4_attention_ti
     }
 }
 
-// The rows of the tile kernel's split tiles, kJoinRows a workgroup, over the whole card. (Joined by
-// the last workgroup of each tile instead: 80 us more for 515 queries at 20011 positions, where
-// few tiles have many splits and one workgroup moved 2.8 MB.)
-constexpr int kJoinThreads = 256, kJoinRows = 16;
+// The rows of split tiles, kJoinRows a workgroup, over the whole card: all of the tile
+// kernel's, and of the rows kernel's where a tile has many rows. (Joined by the last workgroup of each
+// tile instead: 80 us more for 515 queries at 20011 positions, where few tiles have
+// many splits and one workgroup moved 2.8 MB.) FEW: the rows kernel's tiles.
+constexpr int kJoinThreads = 256, kJoinRows = 8;
 
-template <int D>
+template <int D, bool FEW>
 __global__ __launch_bounds__(kJoinThreads) void nvfp4_attention_join_kernel(AttParams p, int32_t tile_rows)
 {
     __shared__ float s_weights[(kMaxSplits + 1) * kJoinRows];
-    const uint32_t parts = (uint32_t)(tile_rows / kJoinRows), id = blockIdx.x / parts;
+    const uint32_t parts = (uint32_t)((p.most_rows + kJoinRows - 1) / kJoinRows), id = blockIdx.x / parts;
     const int first = (int)(blockIdx.x % parts) * kJoinRows;
     const uint32_t pairs = (uint32_t)p.B * (uint32_t)p.heads;
-    const int rt = (int)(((uint32_t)p.row_tiles - 1u) - id / pairs);
+    const int rt = FEW ? (int)(id / pairs) : (int)(((uint32_t)p.row_tiles - 1u) - id / pairs);
     const int b = (int)(id % pairs / (uint32_t)p.heads), hk = (int)(id % pairs % (uint32_t)p.heads);
     const Sequence s = sequence_of(p, b);
     const int64_t all_rows = (int64_t)min(s.n, p.max_q) * p.G;
-    if (all_rows <= p.few_rows || (int64_t)rt * tile_rows + first >= all_rows)
+    if ((all_rows <= p.few_rows) != FEW || (int64_t)rt * tile_rows + first >= all_rows)
         return;
     const int row0 = rt * tile_rows, rows = (int)min((int64_t)tile_rows, all_rows - row0);
     const Span span = span_of(p, s, row0 / p.G, (row0 + rows - 1) / p.G + 1, 0);
-    if (span.splits > 1)
-        join_splits<D, kJoinThreads, 4, 2, 8, true>(p, s, hk, id, row0, first, min(kJoinRows, rows - first), span.splits,
-                                                    p.gv ? *p.gv : 1.0f, s_weights);
+    if (span.splits > 1 && first < rows)
+        join_splits<D, kJoinThreads, 4, 1, 16, true>(p, s, hk, id, row0, first, min(kJoinRows, rows - first), span.splits,
+                                                     p.gv ? *p.gv : 1.0f, s_weights);
 }
 
 // ------------------------------------------------------------------ host
@@ -1232,7 +1258,7 @@ nvfp4_status_t check(const nvfp4_cache_t *cache, int dtype, int64_t T, int64_t H
 // How the positions are shared out: `tiles` workgroups if none were split.
 struct Plan {
     int64_t tiles;
-    int32_t splits, chunk, most_rows;
+    int32_t splits, chunk, most_rows, row_tiles, waves;
     size_t bytes;                               // of workspace
 };
 
@@ -1241,22 +1267,35 @@ int64_t partial_bytes(int64_t tiles, int64_t splits, int64_t rows, int64_t D)
     return tiles * splits * rows * (D + 2) * 4;
 }
 
+// Rows of a workgroup of the rows kernel, and how many such a sequence's have at most.
+int rows_at_once(int64_t most) { return most <= 16 ? 16 : 32; }
+
 Plan rows_plan(const nvfp4_cache_t &c, int64_t H, int64_t B, const nvfp4_attention_t &a)
 {
     Plan p{};
-    const int64_t G = H / c.heads;
-    p.tiles = B * c.heads;
-    p.most_rows = (int32_t)std::min<int64_t>(32, a.max_q * G);
+    const int64_t most_rows = std::min<int64_t>(kFewRows, a.max_q * (H / c.heads));
+    const int rows = rows_at_once(most_rows);
+    p.row_tiles = (int32_t)((most_rows + rows - 1) / rows);
+    p.tiles = B * c.heads * p.row_tiles;
+    p.most_rows = (int32_t)std::min<int64_t>(rows, most_rows);
     // most tiles of 64 positions that a sequence's rows see
-    const int64_t span = a.window ? std::min<int64_t>(a.max_length, a.window + std::min<int64_t>(a.max_q, 32) + 64) : a.max_length;
-    const int64_t most = (span + 63) / 64 + 1;
-    int64_t splits = std::min<int64_t>((kRowsTarget + p.tiles - 1) / p.tiles, (most + kRowsWaves - 1) / kRowsWaves);
+    const int64_t span = a.window ? std::min<int64_t>(a.max_length, a.window + std::min<int64_t>(a.max_q, rows) + 64) : a.max_length;
+    const int64_t most = (span + 63) / 64 + (a.window ? 1 : 0);       // a window starts inside a tile
+    // Waves of a workgroup: 8, so that half the partial results have to be joined, where 4 with a tile each
+    // would be more than 16 splits and 8 fill the CUs once at most (one sequence, 8 key heads: 16384
+    // positions 17.5 us, with 4 waves 21.5; 4096 positions 13.0 and 12.5)
+    p.waves = rows == 16 && most > 64 && p.tiles * ((most + 7) / 8) <= kCus ? 8 : 4;
+    // workgroups: 1024 keep the card loading (64 sequences of 1024 to 8192 positions, 4 rows: 93 us, 114 with
+    // 512, 99 with 2048); more rows mean larger partial results (16 sequences of up to 4000, 32 rows: 34 us
+    // with 512, 42 with 1024)
+    const int64_t target = most_rows <= 4 ? 1024 : 512;
+    int64_t splits = std::min<int64_t>((target + p.tiles - 1) / p.tiles, (most + p.waves - 1) / p.waves);
     splits = std::max<int64_t>(1, std::min<int64_t>(splits, kMaxSplits));
     if (p.tiles > kMaxTickets)
         splits = 1;
     while (splits > 1 && partial_bytes(p.tiles, splits, p.most_rows, c.head_size) > kMaxPartialBytes)
         --splits;
-    p.chunk = (int32_t)((most + splits - 1) / splits + kRowsWaves - 1) / kRowsWaves * kRowsWaves;
+    p.chunk = (int32_t)((most + splits - 1) / splits + p.waves - 1) / p.waves * p.waves;
     p.splits = (int32_t)((most + p.chunk - 1) / p.chunk);
     p.bytes = p.splits > 1 ? kTicketBytes + (partial_bytes(p.tiles, p.splits, p.most_rows, c.head_size) + 255) / 256 * 256 : 0;
     return p;
@@ -1268,10 +1307,11 @@ Plan tile_plan(const nvfp4_cache_t &c, int dtype, int64_t H, int64_t B, const nv
     Plan p{};
     const int rows = tile_rows((int)c.head_size, dtype == NVFP4_F32);
     const int64_t G = H / c.heads, row_tiles = (a.max_q * G + rows - 1) / rows;
+    p.row_tiles = (int32_t)row_tiles;
     p.tiles = B * c.heads * row_tiles;
     p.most_rows = rows;
     const int64_t span = a.window ? std::min<int64_t>(a.max_length, a.window + rows + 64) : a.max_length;
-    const int64_t most = (span + 63) / 64 + 1;
+    const int64_t most = (span + 63) / 64 + (a.window ? 1 : 0);       // a window starts inside a tile
     // As many as fill the places for workgroups once (two on a CU up to 128 values, one beyond), or
     // twice where that leaves fewer of them idle
     const int64_t places = c.head_size <= 128 ? 512 : 256, once = places / p.tiles, twice = 2 * places / p.tiles;
@@ -1286,7 +1326,7 @@ Plan tile_plan(const nvfp4_cache_t &c, int dtype, int64_t H, int64_t B, const nv
 }
 
 // Sequences of more rows than the rows kernel takes.
-bool has_many(const nvfp4_cache_t &c, int64_t H, const nvfp4_attention_t &a) { return a.max_q * (H / c.heads) > 32; }
+bool has_many(const nvfp4_cache_t &c, int64_t H, const nvfp4_attention_t &a) { return a.max_q * (H / c.heads) > kFewRows; }
 
 size_t need_of(const nvfp4_cache_t &c, int dtype, int64_t H, int64_t B, const nvfp4_attention_t &a)
 {
@@ -1296,44 +1336,49 @@ size_t need_of(const nvfp4_cache_t &c, int dtype, int64_t H, int64_t B, const nv
 
 void set_plan(AttParams &p, const Plan &plan, void *workspace)
 {
-    p.splits = plan.splits, p.chunk = plan.chunk, p.most_rows = plan.most_rows;
+    p.splits = plan.splits, p.chunk = plan.chunk, p.most_rows = plan.most_rows, p.row_tiles = plan.row_tiles;
     p.tickets = (uint32_t *)workspace;
     p.sums = workspace ? (float *)((uint8_t *)workspace + kTicketBytes) : nullptr;
     p.norms = p.sums ? p.sums + plan.tiles * plan.splits * plan.most_rows * p.D : nullptr;
+}
+
+template <int D, bool FEW>
+hipError_t launch_join(const AttParams &p, int64_t tiles, int rows, hipStream_t st)
+{
+    const int64_t parts = (p.most_rows + kJoinRows - 1) / kJoinRows;
+    hipLaunchKernelGGL((nvfp4_attention_join_kernel<D, FEW>), dim3((uint32_t)(tiles * parts)), dim3(kJoinThreads), 0, st, p, rows);
+    return hipGetLastError();
 }
 
 template <int D, bool F32>
 hipError_t launch_tile(const AttParams &p, int64_t grid, hipStream_t st)
 {
     constexpr int threads = 64 * tile_waves(D, F32), rows = tile_rows(D, F32), buffers = 2 * WideTile<D, threads>::kBuffer;
-    static_assert(buffers + 1024 <= 160 * 1024 && rows % kJoinRows == 0);
+    static_assert(buffers + 1024 <= 160 * 1024);
     hipLaunchKernelGGL((nvfp4_attention_tile_kernel<D, F32>), dim3((uint32_t)grid), dim3(threads), buffers, st, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1)
         return e;
-    hipLaunchKernelGGL((nvfp4_attention_join_kernel<D>), dim3((uint32_t)(grid / p.splits * (rows / kJoinRows))), dim3(kJoinThreads), 0, st,
-                       p, rows);
-    return hipGetLastError();
+    return launch_join<D, false>(p, grid / p.splits, rows, st);
 }
 
-template <int D, int NQ, bool F32>
+template <int D, int NQ, bool F32, int WAVES>
 hipError_t launch_rows(const AttParams &p, int64_t grid, hipStream_t st)
 {
     using S = RowsTile<D>;
-    const int lds = std::max({kRowsWaves * S::kWave, kRowsWaves * 16 * NQ * (D * 4 + 8), (p.splits + 1) * 4 * p.most_rows});
-    static_assert(kRowsWaves * S::kWave + 64 <= 160 * 1024 && kRowsWaves * 16 * NQ * (D * 4 + 8) + 64 <= 160 * 1024 && (kMaxSplits + 1) * 4 * 64 < 64 * 1024);
-    auto kern = nvfp4_attention_rows_kernel<D, NQ, F32>;
-    hipLaunchKernelGGL(kern, dim3((uint32_t)grid), dim3(kRowsThreads), lds, st, p);
-    return hipGetLastError();
+    const int lds = std::max({WAVES * S::kWave, WAVES * 16 * NQ * (D * 4 + 8), (p.splits + 1) * 4 * p.most_rows});
+    static_assert(WAVES * S::kWave + 64 <= 160 * 1024 && WAVES * 16 * NQ * (D * 4 + 8) + 64 <= 160 * 1024 && (kMaxSplits + 1) * 4 * 64 < 64 * 1024);
+    hipLaunchKernelGGL((nvfp4_attention_rows_kernel<D, NQ, F32, WAVES>), dim3((uint32_t)grid), dim3(64 * WAVES), lds, st, p);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || p.splits == 1 || p.join_here ? e : launch_join<D, true>(p, grid / p.splits, 16 * NQ, st);
 }
 
-template <int D>
-hipError_t launch_rows_of(const AttParams &p, int64_t grid, hipStream_t st)
+template <int D, bool F32>
+hipError_t launch_rows_of(const AttParams &p, int waves, int64_t grid, hipStream_t st)
 {
-    const bool f32 = p.dtype == NVFP4_F32;
-    if (p.few_rows == 16)
-        return f32 ? launch_rows<D, 1, true>(p, grid, st) : launch_rows<D, 1, false>(p, grid, st);
-    return f32 ? launch_rows<D, 2, true>(p, grid, st) : launch_rows<D, 2, false>(p, grid, st);
+    if (waves == 8)
+        return launch_rows<D, 1, F32, 8>(p, grid, st);
+    return rows_at_once(p.most_rows) == 16 ? launch_rows<D, 1, F32, 4>(p, grid, st) : launch_rows<D, 2, F32, 4>(p, grid, st);
 }
 
 template <typename F>
@@ -1398,13 +1443,15 @@ nvfp4_status_t nvfp4_cache_attention(const nvfp4_cache_t *cache, const void *q, 
     const size_t need = need_of(*cache, dtype, H, B, *attention);
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
         return NVFP4_ERR_WORKSPACE;
-    p.few_rows = attention->max_q * p.G <= 16 ? 16 : 32;
-    const int tile = tile_rows(p.D, dtype == NVFP4_F32);
-    p.row_tiles = (int32_t)((attention->max_q * p.G + tile - 1) / tile);
+    p.few_rows = kFewRows;
+    p.join_here = few.most_rows <= kJoinHere;
     const hipStream_t hs = (hipStream_t)stream;
     // one after the other on the stream, so one workspace serves both
     set_plan(p, few, need ? workspace : nullptr);
-    hipError_t e = by_head(p.D, [&](auto d) { return launch_rows_of<d()>(p, few.tiles * few.splits, hs); });
+    hipError_t e = by_head(p.D, [&](auto d) {
+        const int64_t grid = few.tiles * few.splits;
+        return dtype == NVFP4_F32 ? launch_rows_of<d(), true>(p, few.waves, grid, hs) : launch_rows_of<d(), false>(p, few.waves, grid, hs);
+    });
     if (e == hipSuccess && both) {
         set_plan(p, many, need ? workspace : nullptr);
         e = by_head(p.D, [&](auto d) {

@@ -19,7 +19,8 @@
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kBlocks = 4;
+constexpr int64_t kManyBlocks = 1 << 20;         // of keys (of values): 16 waves of single blocks on every CU
 constexpr int64_t kMaxGrid = 0xFFFFFF;          // workgroups of 256 threads in 2^32 work items
 constexpr int64_t kMaxStride = INT64_C(1) << 40, kMaxPage = INT64_C(1) << 32;
 
@@ -31,25 +32,31 @@ struct RowParams {
     const int64_t *slots;
     int64_t in_token[2], in_head[2];            // bytes
     int64_t code_page, scale_page, all_slots;
-    int32_t shift, H, nkb;                      // page_size = 1 << shift; blocks of a row
+    Divisor heads, blocks;                      // blocks of a row
+    int32_t shift, nkb;                         // page_size = 1 << shift
     uint32_t rows, wgs;                         // T * H; workgroups for the keys
 };
 
-// A thread's block: 0 keys, 1 values; row, block of the row. False past the end.
+// A block: 0 keys, 1 values; token, head, block of the row. False past the end.
 struct Place {
     uint32_t which, t, h, kb;
+    bool real;
 };
 
-__device__ __attribute__((always_inline)) inline bool place_of(const RowParams &p, Place &at)
+// The k-th block of a thread of U.
+template <int U>
+__device__ __attribute__((always_inline)) inline Place place_of(const RowParams &p, int k)
 {
+    Place at;
     at.which = blockIdx.x >= p.wgs;
-    // the grid keeps every index of a block below 2^32
-    const uint32_t i = (blockIdx.x - (at.which ? p.wgs : 0u)) * kThreads + threadIdx.x;
-    const uint32_t row = i / (uint32_t)p.nkb;
-    at.kb = i % (uint32_t)p.nkb;
-    at.t = row / (uint32_t)p.H;
-    at.h = row % (uint32_t)p.H;
-    return row < p.rows;
+    // the grid keeps every index of a block below 2^31
+    const uint32_t i = ((blockIdx.x - (at.which ? p.wgs : 0u)) * U + k) * kThreads + threadIdx.x;
+    const uint32_t row = divided(i, p.blocks);
+    at.kb = i - row * p.blocks.d;
+    at.t = divided(row, p.heads);
+    at.h = row - at.t * p.heads.d;
+    at.real = row < p.rows;
+    return at;
 }
 
 // Byte offsets of a slot's block in codes and scales; the slot is inside the cache.
@@ -62,57 +69,80 @@ __device__ __attribute__((always_inline)) inline void offsets_of(const RowParams
     scale = page * p.scale_page + row * p.nkb + at.kb;
 }
 
-template <int DT>
+// U blocks a thread: their slots are all loaded before the first is used.
+template <int DT, int U>
 __global__ __launch_bounds__(kThreads) void nvfp4_cache_write_kernel(RowParams p)
 {
-    Place at;
-    if (!place_of(p, at))
-        return;
-    const int64_t slot = p.slots[at.t];
-    if ((uint64_t)slot >= (uint64_t)p.all_slots)
-        return;
-    const uint8_t *x = (at.which ? p.in[1] + at.t * p.in_token[1] + at.h * p.in_head[1]
-                                 : p.in[0] + at.t * p.in_token[0] + at.h * p.in_head[0]) + at.kb * 16 * kSize<DT>;
-    const Global gl = global_of(p.global[at.which]);
-    uint32_t s;
-    const uint2_t q = quantize_block<DT>(x, gl, s);
-    int64_t code, scale;
-    offsets_of(p, slot, at, code, scale);
-    *(uint2_t *)(p.codes[at.which] + code) = q;
-    p.scales[at.which][scale] = (uint8_t)s;
+    Place at[U];
+    int64_t slot[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        at[k] = place_of<U>(p, k);
+        slot[k] = at[k].real ? p.slots[at[k].t] : -1;
+    }
+    const uint32_t which = at[0].which;
+    const Global gl = global_of(p.global[which]);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        if ((uint64_t)slot[k] >= (uint64_t)p.all_slots)
+            continue;
+        const uint8_t *x = (which ? p.in[1] + at[k].t * p.in_token[1] + at[k].h * p.in_head[1]
+                                  : p.in[0] + at[k].t * p.in_token[0] + at[k].h * p.in_head[0]) + at[k].kb * 16 * kSize<DT>;
+        uint32_t s;
+        const uint2_t q = quantize_block<DT>(x, gl, s);
+        int64_t code, scale;
+        offsets_of(p, slot[k], at[k], code, scale);
+        *(uint2_t *)(p.codes[which] + code) = q;
+        p.scales[which][scale] = (uint8_t)s;
+    }
 }
 
-// Rows of slots outside the cache are zeros.
-template <int DT>
+// Rows of slots outside the cache are zeros. U blocks a thread, loaded together.
+template <int DT, int U>
 __global__ __launch_bounds__(kThreads) void nvfp4_cache_read_kernel(RowParams p)
 {
-    Place at;
-    if (!place_of(p, at))
-        return;
-    const int64_t slot = p.slots[at.t];
-    float v[16];
+    Place at[U];
+    int64_t slot[U];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        v[i] = 0.0f;
-    if ((uint64_t)slot < (uint64_t)p.all_slots) {
-        int64_t code, scale;
-        offsets_of(p, slot, at, code, scale);
-        const uint2_t q = *(const uint2_t *)(p.codes[at.which] + code);
-        const float s = e4m3_value(p.scales[at.which][scale]);
-        const float *gp = p.global[at.which];
-        const float g = gp ? *gp : 1.0f;
-        const uint32_t w[2] = {q.x, q.y};
+    for (int k = 0; k < U; ++k) {
+        at[k] = place_of<U>(p, k);
+        slot[k] = at[k].real ? p.slots[at[k].t] : -1;
+    }
+    const uint32_t which = at[0].which;
+    const float *gp = p.global[which];
+    const float g = gp ? *gp : 1.0f;
+    uint2_t q[U];
+    uint32_t scale[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        q[k] = (uint2_t){0u, 0u};
+        scale[k] = 0u;
+        if ((uint64_t)slot[k] < (uint64_t)p.all_slots) {
+            int64_t code, sc;
+            offsets_of(p, slot[k], at[k], code, sc);
+            q[k] = *(const uint2_t *)(p.codes[which] + code);
+            scale[k] = p.scales[which][sc];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        // a slot outside: zeros whatever the global scale
+        const bool there = (uint64_t)slot[k] < (uint64_t)p.all_slots;
+        const float s = e4m3_value(scale[k]), by = there ? g : 0.0f;
+        float v[16];
+        const uint32_t w[2] = {q[k].x, q[k].y};
 #pragma unroll
         for (int d = 0; d < 2; ++d) {
             const half2_t h[4] = {fp4x2<0>(w[d]), fp4x2<1>(w[d]), fp4x2<2>(w[d]), fp4x2<3>(w[d])};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                v[8 * d + 2 * j] = (float)h[j].x * s * g;
-                v[8 * d + 2 * j + 1] = (float)h[j].y * s * g;
+                v[8 * d + 2 * j] = (float)h[j].x * s * by;
+                v[8 * d + 2 * j + 1] = (float)h[j].y * s * by;
             }
         }
+        if (at[k].real)
+            store16<DT>(p.out[which] + (((int64_t)at[k].t * p.heads.d + at[k].h) * p.nkb + at[k].kb) * 16 * kSize<DT>, v);
     }
-    store16<DT>(p.out[at.which] + (((int64_t)at.t * p.H + at.h) * p.nkb + at.kb) * 16 * kSize<DT>, v);
 }
 
 // ------------------------------------------------------------------ host
@@ -127,10 +157,7 @@ nvfp4_status_t rows_of(const nvfp4_cache_t *cache, const int64_t *slots, int64_t
     if (st != NVFP4_OK)
         return st;
     const int64_t H = cache->heads, nkb = cache->head_size / 16;
-    if (T < 1 || T > (INT64_C(1) << 32) / H / nkb)
-        return NVFP4_ERR_INVALID_SHAPE;
-    const int64_t wgs = (T * H * nkb + kThreads - 1) / kThreads;
-    if (wgs > kMaxGrid / 2)
+    if (T < 1 || T > kMaxGrid / 2 * kThreads / H / nkb)
         return NVFP4_ERR_INVALID_SHAPE;
     if (!aligned(slots, 8))
         return NVFP4_ERR_MISALIGNED;
@@ -142,8 +169,9 @@ nvfp4_status_t rows_of(const nvfp4_cache_t *cache, const int64_t *slots, int64_t
     p.code_page = cache->code_page_stride, p.scale_page = cache->scale_page_stride;
     p.all_slots = cache->pages * cache->page_size;
     p.shift = __builtin_ctzll((uint64_t)cache->page_size);
-    p.H = (int32_t)H, p.nkb = (int32_t)nkb;
-    p.rows = (uint32_t)(T * H), p.wgs = (uint32_t)wgs;
+    p.nkb = (int32_t)nkb;
+    p.heads = divisor_of((uint32_t)H), p.blocks = divisor_of((uint32_t)nkb);
+    p.rows = (uint32_t)(T * H);
     return NVFP4_OK;
 }
 
@@ -154,6 +182,16 @@ nvfp4_status_t finish()
         return NVFP4_OK;
     nvfp4_record_hip_error((int)e);
     return NVFP4_ERR_HIP;
+}
+
+// One block a thread where that does not fill the card, else kBlocks.
+template <typename K>
+void launch(K one, K several, RowParams &p, hipStream_t st)
+{
+    const int64_t blocks = (int64_t)p.rows * p.nkb;
+    const int each = blocks >= kManyBlocks ? kBlocks : 1;
+    p.wgs = (uint32_t)((blocks + each * kThreads - 1) / (each * kThreads));
+    hipLaunchKernelGGL((each == 1 ? one : several), dim3(2 * p.wgs), dim3(kThreads), 0, st, p);
 }
 
 template <typename F>
@@ -213,7 +251,7 @@ nvfp4_status_t nvfp4_cache_write(const nvfp4_cache_t *cache, const void *k, cons
     p.in_token[0] = k_token_stride * size, p.in_token[1] = v_token_stride * size;
     p.in_head[0] = k_head_stride * size, p.in_head[1] = v_head_stride * size;
     by_type(dtype, [&](auto dt) {
-        hipLaunchKernelGGL(nvfp4_cache_write_kernel<dt()>, dim3(2 * p.wgs), dim3(kThreads), 0, (hipStream_t)stream, p);
+        launch(nvfp4_cache_write_kernel<dt(), 1>, nvfp4_cache_write_kernel<dt(), kBlocks>, p, (hipStream_t)stream);
     });
     return finish();
 }
@@ -234,7 +272,7 @@ nvfp4_status_t nvfp4_cache_read(const nvfp4_cache_t *cache, void *k, void *v, in
         return NVFP4_ERR_MISALIGNED;
     p.out[0] = (uint8_t *)k, p.out[1] = (uint8_t *)v;
     by_type(dtype, [&](auto dt) {
-        hipLaunchKernelGGL(nvfp4_cache_read_kernel<dt()>, dim3(2 * p.wgs), dim3(kThreads), 0, (hipStream_t)stream, p);
+        launch(nvfp4_cache_read_kernel<dt(), 1>, nvfp4_cache_read_kernel<dt(), kBlocks>, p, (hipStream_t)stream);
     });
     return finish();
 }

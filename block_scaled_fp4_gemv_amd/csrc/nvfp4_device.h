@@ -25,6 +25,24 @@ __device__ inline uint32_t xcd_remap(uint32_t i, uint32_t n)
     return x * q + min(x, r) + j;
 }
 
+// Division of n < 2^31 by a number that the host knows: with 2^(s-1) < d <= 2^s and m = floor(2^32
+// (2^s - d) / d) + 1 the quotient is (n m / 2^32 + n) / 2^s, rounded down twice (the error m
+// leaves is below n / 2^32 < 1 / d of a step). 3 instructions for about 25.
+struct Divisor {
+    uint32_t d, m, s;
+};
+inline Divisor divisor_of(uint32_t d)
+{
+    uint32_t s = 0;
+    while ((uint64_t(1) << s) < d)
+        ++s;
+    return {d, (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << s) - d)) / d + 1), s};
+}
+__device__ __attribute__((always_inline)) inline uint32_t divided(uint32_t n, const Divisor &by)
+{
+    return ((uint32_t)(((uint64_t)n * by.m) >> 32) + n) >> by.s;
+}
+
 // Reinterpretation helpers. They take their operand by value on purpose:
 // applying __builtin_bit_cast to an ext-vector element such as `v.y` directly
 // read the vector's first element with this compiler.

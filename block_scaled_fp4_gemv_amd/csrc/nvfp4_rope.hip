@@ -27,7 +27,7 @@
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, U = 4;             // units that a thread loads together
 constexpr int kMaxAngles = 1024;                // of a workgroup, 8 KiB of LDS
 constexpr int kMaxR = 2 * kMaxAngles;
 constexpr int64_t kMaxGrid = 0xFFFFFF;          // workgroups of 256 threads in 2^32 work items
@@ -41,7 +41,8 @@ struct RopeParams {
     int64_t T, x_token, x_head, out_token, out_head;    // strides in bytes
     int32_t H, D, half;                                 // half: R / 2
     int32_t tokens_per_wg, heads_per_wg, head_runs;
-    int32_t units, turned;                              // units of a row; the first `turned` are pairs
+    Divisor units, pairs;                               // units of a row, R / 2
+    int32_t turned;                                     // the first `turned` units are pairs
     float factor, sign;
 };
 
@@ -111,7 +112,7 @@ __global__ __launch_bounds__(kThreads) void nvfp4_rope_kernel(RopeParams p)
     const int h0 = (int)(blockIdx.x % (uint32_t)p.head_runs) * p.heads_per_wg;
     const int tokens = (int)min((int64_t)p.tokens_per_wg, p.T - t0), heads = min(p.heads_per_wg, p.H - h0);
     for (uint32_t i = threadIdx.x; i < (uint32_t)(tokens * p.half); i += kThreads) {
-        const uint32_t t = i / (uint32_t)p.half, j = i % (uint32_t)p.half;
+        const uint32_t t = divided(i, p.pairs), j = i - t * p.pairs.d;
         float c, s;
         cos_sin((double)p.positions[t0 + t], p.frequencies[j], c, s);
         s_cos[i] = c * p.factor;
@@ -119,47 +120,62 @@ __global__ __launch_bounds__(kThreads) void nvfp4_rope_kernel(RopeParams p)
     }
     __syncthreads();
     constexpr int S = sizeof(Raw<DT>);
-    const uint32_t n = (uint32_t)tokens * (uint32_t)heads * (uint32_t)p.units;
-    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-        const uint32_t row = i / (uint32_t)p.units, u = i % (uint32_t)p.units;
-        const uint32_t t = row / (uint32_t)heads, h = row % (uint32_t)heads;
-        const uint8_t *x = p.x + (t0 + t) * p.x_token + (int64_t)(h0 + h) * p.x_head;
-        uint8_t *y = p.out + (t0 + t) * p.out_token + (int64_t)(h0 + h) * p.out_head;
-        using P = Piece<DT, V>;
-        if ((int)u >= p.turned) {
-            const uint32_t at = ((u - p.turned) * V + 2 * p.half) * S;
-            *(P *)(y + at) = *(const P *)(x + at);
-            continue;
+    using P = Piece<DT, V>;
+    // A unit's two parts: pairs' first and second values (halves, and pairs one by one), or none.
+    constexpr bool TWO = HALVES || V == 1;
+    const uint32_t n = (uint32_t)tokens * (uint32_t)heads * p.units.d;
+    for (uint32_t i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
+        P a[U], b[U];
+        uint8_t *y[U];
+        uint32_t t[U], u[U];
+        // all loads, then all stores: a unit's values are no other's, also in place
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const uint32_t i = min(i0 + k * kThreads, n - 1);
+            const uint32_t row = divided(i, p.units);
+            u[k] = i - row * p.units.d;
+            t[k] = heads == 1 ? row : row / (uint32_t)heads;
+            const uint32_t h = row - t[k] * (uint32_t)heads;
+            const uint8_t *x = p.x + (t0 + t[k]) * p.x_token + (int64_t)(h0 + h) * p.x_head;
+            y[k] = p.out + (t0 + t[k]) * p.out_token + (int64_t)(h0 + h) * p.out_head;
+            if ((int)u[k] >= p.turned) {
+                a[k] = *(const P *)(x + ((u[k] - p.turned) * V + 2 * p.half) * S);
+            } else {
+                const uint32_t at = u[k] * (HALVES || V > 1 ? V : 2);
+                a[k] = *(const P *)(x + at * S);
+                if constexpr (TWO)
+                    b[k] = *(const P *)(x + (at + (HALVES ? p.half : 1)) * S);
+            }
         }
-        const float *cs = s_cos + t * p.half, *sn = s_sin + t * p.half;
-        if constexpr (HALVES) {
-            const uint32_t j = u * V;
-            P a = *(const P *)(x + j * S), b = *(const P *)(x + (j + p.half) * S);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float x0 = to_float<DT>(a.v[e]), x1 = to_float<DT>(b.v[e]), c = cs[j + e], s = sn[j + e];
-                a.v[e] = from_float<DT>(fmaf(-x1, s, x0 * c));
-                b.v[e] = from_float<DT>(fmaf(x1, c, x0 * s));
+        for (int k = 0; k < U; ++k) {
+            if (i0 + k * kThreads >= n)
+                continue;
+            if ((int)u[k] >= p.turned) {
+                *(P *)(y[k] + ((u[k] - p.turned) * V + 2 * p.half) * S) = a[k];
+                continue;
             }
-            *(P *)(y + j * S) = a;
-            *(P *)(y + (j + p.half) * S) = b;
-        } else {
-            constexpr int N = V == 1 ? 2 : V;
-            const uint32_t at = u * N * S;
-            Piece<DT, V == 1 ? 1 : V> one[V == 1 ? 2 : 1];
-            for (int k = 0; k < (V == 1 ? 2 : 1); ++k)
-                one[k] = *(const P *)(x + at + k * S);
+            const float *cs = s_cos + t[k] * p.half, *sn = s_sin + t[k] * p.half;
+            const uint32_t at = u[k] * (HALVES || V > 1 ? V : 2);
+            if constexpr (TWO) {
+                const uint32_t j = HALVES ? at : u[k];
 #pragma unroll
-            for (int e = 0; e < N; e += 2) {
-                auto &v0 = V == 1 ? one[0].v[0] : one[0].v[e % V];
-                auto &v1 = V == 1 ? one[V == 1].v[0] : one[0].v[(e + 1) % V];
-                const uint32_t j = (u * N + e) / 2;
-                const float x0 = to_float<DT>(v0), x1 = to_float<DT>(v1), c = cs[j], s = sn[j];
-                v0 = from_float<DT>(fmaf(-x1, s, x0 * c));
-                v1 = from_float<DT>(fmaf(x1, c, x0 * s));
+                for (int e = 0; e < V; ++e) {
+                    const float x0 = to_float<DT>(a[k].v[e]), x1 = to_float<DT>(b[k].v[e]), c = cs[j + e], s = sn[j + e];
+                    a[k].v[e] = from_float<DT>(fmaf(-x1, s, x0 * c));
+                    b[k].v[e] = from_float<DT>(fmaf(x1, c, x0 * s));
+                }
+                *(P *)(y[k] + at * S) = a[k];
+                *(P *)(y[k] + (at + (HALVES ? p.half : 1)) * S) = b[k];
+            } else {
+#pragma unroll
+                for (int e = 0; e + 1 < V; e += 2) {
+                    const float x0 = to_float<DT>(a[k].v[e]), x1 = to_float<DT>(a[k].v[e + 1]), c = cs[(at + e) / 2], s = sn[(at + e) / 2];
+                    a[k].v[e] = from_float<DT>(fmaf(-x1, s, x0 * c));
+                    a[k].v[e + 1] = from_float<DT>(fmaf(x1, c, x0 * s));
+                }
+                *(P *)(y[k] + at * S) = a[k];
             }
-            for (int k = 0; k < (V == 1 ? 2 : 1); ++k)
-                *(P *)(y + at + k * S) = one[k];
         }
     }
 }
@@ -281,15 +297,16 @@ nvfp4_status_t nvfp4_rope(const void *x, int dtype, void *out, const int64_t *po
     p.out_token = out_token_stride * size, p.out_head = out_head_stride * size;
     p.factor = factor, p.sign = transpose ? -1.0f : 1.0f;
     p.turned = (int32_t)(wide ? (halves ? half : R) / V : half);
-    p.units = p.turned + (int32_t)(x == out ? 0 : wide ? (D - R) / V : D - R);     // in place the rest stays
+    const int64_t units = p.turned + (x == out ? 0 : wide ? (D - R) / V : D - R);      // in place the rest stays
+    p.units = divisor_of((uint32_t)units), p.pairs = divisor_of((uint32_t)half);
     // tokens whose angles fill two rounds of the threads; fewer, then heads apart, while there is not a
     // workgroup for every place (1024 of them are four on each CU)
     int64_t tokens = std::max<int64_t>(1, std::min<int64_t>(T, 2 * kThreads / half)), heads = H;
     while (tokens > 1 && (T + tokens - 1) / tokens < 1024)
         tokens = (tokens + 1) / 2;
-    while (heads > 1 && (T + tokens - 1) / tokens * ((H + heads - 1) / heads) < 1024 && tokens * heads * p.units > kThreads)
+    while (heads > 1 && (T + tokens - 1) / tokens * ((H + heads - 1) / heads) < 1024 && tokens * heads * units > kThreads)
         heads = (heads + 1) / 2;
-    while (heads > 1 && tokens * heads * p.units > (1 << 20))        // units of a workgroup are counted in 32 bits
+    while (heads > 1 && tokens * heads * units > (1 << 20))        // units of a workgroup are counted in 32 bits
         heads = (heads + 1) / 2;
     p.tokens_per_wg = (int32_t)tokens, p.heads_per_wg = (int32_t)heads;
     p.head_runs = (int32_t)((H + heads - 1) / heads);

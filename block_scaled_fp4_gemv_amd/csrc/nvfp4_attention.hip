@@ -151,7 +151,7 @@ __device__ __attribute__((always_inline)) inline RowScale row_scale(float top, f
     const int e = top > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
     const float f = real ? __builtin_ldexpf(factor, -e) : 0.0f;
     const bool zero = f == 0.0f;
-    return {zero ? 0.0f : f < 0.0f ? -1.0f : 1.0f, e, zero ? 1.0f : finite ? fabsf(f) : __builtin_nanf("")};
+    return {zero ? 0.0f : f < 0.0f ? -1.0f : 1.0f, e, !finite ? __builtin_nanf("") : zero ? 1.0f : fabsf(f)};
 }
 
 template <int N, int PARTS>

@@ -621,8 +621,8 @@ typedef struct {
  *   slots   int64 [T]; a token whose slot is outside the cache (negative, say)
  *           is not written. Each slot at most once: of two tokens with one slot
  *           either's blocks may stay.
- * Nothing else of the cache changes. Requirements: T >= 1; T * heads *
- * head_size / 16 <= 256 * (2^23 - 1).
+ * Nothing else of the cache changes. Requirements: T >= 1; (T + 64) * heads *
+ * head_size / 16 <= 2^31 - 2048.
  */
 nvfp4_status_t nvfp4_cache_write(const nvfp4_cache_t *cache, const void *k, const void *v, int dtype,
                                  const int64_t *slots, int64_t T, int64_t k_token_stride, int64_t k_head_stride,

@@ -62,6 +62,18 @@ def test_long_ones_are_split(program, tmp_path, dt):
 
 
 @pytest.mark.parametrize("dt", [0, 2])
+@pytest.mark.parametrize("D,H,n", [(64, 2, 1), (128, 3, 2), (256, 4, 1), (96, 20, 1), (64, 10, 4), (192, 16, 3)])
+def test_a_long_bound_on_short_lengths(program, tmp_path, D, H, n, dt):
+    """A table for 5000 positions: eight waves a workgroup, more splits than there are tiles, rows
+    joined by the last workgroup and by a kernel of its own."""
+    rng = np.random.default_rng(7)
+    lengths = [500, 40]
+    c, table = poisoned(rng, lengths, 16, 1, D, spare=0, width=313)
+    names = run(program, tmp_path, c, table, lengths, [0, n, 2 * n], H, 2 * n, dt, n)
+    assert ("join" in names) == (min(H * n, 32) > 8) and "rows" in names
+
+
+@pytest.mark.parametrize("dt", [0, 2])
 @pytest.mark.parametrize("window", [0, 20])
 @pytest.mark.parametrize("causal", [True, False])
 def test_drafts(program, tmp_path, window, causal, dt):

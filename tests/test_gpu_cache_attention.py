@@ -83,7 +83,9 @@ def test_without_the_causal_mask(dtype, window, workspace):
 
 
 @pytest.mark.parametrize("dtype", sorted(DTYPES))
-@pytest.mark.parametrize("D,H,heads,B,n", [(128, 8, 2, 1, 1), (64, 4, 1, 3, 2), (192, 2, 1, 2, 40), (256, 8, 1, 1, 20), (96, 3, 3, 2, 1)])
+@pytest.mark.parametrize("D,H,heads,B,n", [(128, 8, 2, 1, 1), (64, 4, 1, 3, 2), (192, 2, 1, 2, 40), (256, 8, 1, 1, 20), (96, 3, 3, 2, 1),
+                                           (256, 2, 1, 1, 1), (192, 3, 1, 1, 2), (128, 16, 1, 1, 2), (64, 8, 1, 2, 6), (96, 16, 1, 1, 3),
+                                           (64, 40, 1, 1, 7), (96, 4, 1, 1, 50), (128, 4, 1, 1, 130), (256, 20, 1, 1, 1)])
 def test_long_lengths_are_split_and_joined(D, H, heads, B, n, dtype, workspace):
     rng = np.random.default_rng([D, B, n])
     lengths = [int(v) for v in rng.integers(5000, 9000, B)]
@@ -93,6 +95,39 @@ def test_long_lengths_are_split_and_joined(D, H, heads, B, n, dtype, workspace):
     # bounds far above the lengths plan another grid
     wide = np.concatenate([table, np.full((B, 500), -1, np.int32)], 1)
     run(c, wide, lengths, [n] * B, H, DTYPES[dtype], workspace)
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("D,H,heads,n,window", [(128, 8, 2, 1, 2500), (64, 16, 1, 3, 1000), (192, 4, 1, 40, 1500), (256, 4, 2, 60, 3000),
+                                                (128, 4, 4, 200, 700), (96, 8, 1, 9, 4000)])
+def test_windows_of_long_lengths(D, H, heads, n, window, dtype, workspace):
+    rng = np.random.default_rng([D, n, window])
+    lengths = [6007, 300, 4096]
+    c, table = poisoned(rng, lengths, 32, heads, D)
+    run(c, table, lengths, [n] * 3, H, DTYPES[dtype], workspace, window=window)
+
+
+def test_two_streams_at_once_with_workspaces_of_their_own():
+    rng = np.random.default_rng(21)
+    lengths, D, H, heads = [4000, 5000], 128, 8, 2
+    c, table = poisoned(rng, lengths, 64, heads, D)
+    handle, _ = on_device(c)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    calls = []
+    for n in (1, 30):
+        q = torch.from_numpy(rng.standard_normal((2 * n, H, D)) * 2).bfloat16().cuda()
+        off, ln, tb = (torch.arange(3, dtype=torch.int32) * n).cuda(), torch.tensor(lengths, dtype=torch.int32).cuda(), torch.from_numpy(table).cuda()
+        ws = torch.zeros(g.NVFP4_WORKSPACE_MAX_BYTES, dtype=torch.uint8, device="cuda")
+        calls.append((q, off, ln, tb, n, ws, [torch.zeros_like(q) for _ in range(20)]))
+    torch.cuda.synchronize()
+    for k in range(20):
+        for stream, (q, off, ln, tb, n, ws, outs) in zip(streams, calls):
+            g.nvfp4_cache_attention(handle, q, outs[k], off, ln, tb, 2 * n, H, 2, n, 5056, workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    for q, off, ln, tb, n, ws, outs in calls:
+        want = ref.attention(c, q.double().cpu().numpy(), off.tolist(), lengths, table, n, 5056, np.float64(np.float32(D ** -0.5)))
+        ref.check_attention(outs[0], None, want, torch.bfloat16)
+        assert all(torch.equal(o, outs[0]) for o in outs)
 
 
 def test_tables_with_pages_that_are_not_there(workspace):

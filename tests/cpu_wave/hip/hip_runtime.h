@@ -482,6 +482,7 @@ inline void cpu_wave_s_waitcnt(int imm)
 #define __builtin_amdgcn_readfirstlane(v) cpu_wave_first((int)(v))
 #define __builtin_amdgcn_fence(...) ((void)0)
 #define __builtin_amdgcn_wave_barrier() ((void)cpu_wave::exchange(0))
+#define __builtin_amdgcn_s_setprio(priority) ((void)0)
 #define __builtin_amdgcn_rcpf(v) (1.0f / (v))
 #define __builtin_amdgcn_cvt_scalef32_pk_f16_fp4 cpu_wave_h2_of_fp4
 #define __builtin_amdgcn_cvt_scalef32_pk_f16_fp8 cpu_wave_h2_of_fp8

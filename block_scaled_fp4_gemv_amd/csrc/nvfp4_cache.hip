@@ -8,7 +8,8 @@
 // page, for a run of 16 tokens, then the next head: whole lines on both sides, and the rows that
 // are at work at once lie together (head by head over all tokens they were 2 KiB apart: 43 us for 38).
 // Keys and values in one launch.
-// What bounds it: HBM, every byte read and written once; small calls the launch.
+// What bounds it: HBM, every byte read and written once; small calls the launch. 8 heads of 128: 16384 tokens
+// written from bfloat16 and read back 38 to 43 us (36 at a copy's 4.8 TB/s), 32768 read as float16 46 us, 3.8 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

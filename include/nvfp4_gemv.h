@@ -619,8 +619,8 @@ typedef struct {
  *   k, v    dtype [T][heads][head_size], strides in elements between tokens and
  *           between heads (>= 0); a row contiguous; aligned to their type
  *   slots   int64 [T]; a token whose slot is outside the cache (negative, say)
- *           is not written. Each slot at most once: of two tokens with one slot
- *           either's blocks may stay.
+ *           is not written. Each slot at most once: where two tokens have one slot,
+ *           its blocks' codes and scales may stay from either, each by itself.
  * Nothing else of the cache changes. Requirements: T >= 1; (T + 64) * heads *
  * head_size / 16 <= 2^31 - 2048.
  */
@@ -654,7 +654,8 @@ nvfp4_status_t nvfp4_cache_read(const nvfp4_cache_t *cache, void *k, void *v, in
  * A query that sees nothing gets zeros, and -inf. What it does not see does not
  * enter, whatever it holds: positions behind a sequence's length, NaN scales of keys or
  * values that the mask hides. (A NaN scale of a value makes NaN the block of every
- * query that sees it, whatever its probability.) A query with an infinite or NaN value gets NaN.
+ * query that sees it, whatever its probability.) A query with an infinite or
+ * NaN value that sees something gets NaN.
  *
  *   q        dtype [T][H][head_size], strides in elements between tokens and
  *            between heads (>= 0); a row contiguous; aligned to its type
@@ -673,7 +674,7 @@ nvfp4_status_t nvfp4_cache_read(const nvfp4_cache_t *cache, void *k, void *v, in
  * taken to float16 with a power of two of its row's own (float32: as two float16,
  * 22 bits), probabilities to float16 (float32: two; all to at least 2^-33 of the
  * query's largest), sums, maxima and norms are
- * float32, out is rounded once to dtype. The order of summation is fixed for
+ * float32 (logits past its range give NaN), out is rounded once to dtype. The order of summation is fixed for
  * given arguments and lengths, so equal calls give equal bits.
  * Requirements: T, B >= 1; T <= 2^30; B * max_q and H / heads * max_q <= 2^30; heads
  * divides H, H / heads <= 1024; head_size 64, 96, 128, 192 or 256; 1 <= max_q <= T; 1 <= max_length <=

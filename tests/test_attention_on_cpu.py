@@ -111,3 +111,13 @@ def test_nan_scales_reach_only_who_sees_them(program, tmp_path, n):
     c.vs[table[0, late // 16], 0, late % 16, 1] = 0x7F
     c.ks[table[1, late // 16], 0, late % 16, 3] = 0xFF
     run(program, tmp_path, c, table, [100, 100], [0, n, 2 * n], 2, 2 * n, 0, n)
+
+
+@pytest.mark.parametrize("n", [0, 1, 20, 63])
+@pytest.mark.parametrize("D,dt", [(64, 0), (192, 2)])
+def test_a_lone_sequence_below_its_bound(program, tmp_path, D, dt, n):
+    """Room for 63 queries of 2 shared heads, for fewer of them: the many rows' kernel alone."""
+    rng = np.random.default_rng(8)
+    c, table = poisoned(rng, [300], 16, 1, D, spare=0)
+    names = run(program, tmp_path, c, table, [300], [0, n], 2, 63, dt, 63, window=100 if n == 20 else 0)
+    assert "tile" in names and "rows" not in names

@@ -363,3 +363,12 @@ def test_rows_of_a_layer_step_by_step_and_at_once(workspace):
         want = ref.attention(c, q.double().cpu().numpy(), off.tolist(), lengths, table.cpu().numpy(), max(counts), width * page_size,
                              np.float64(np.float32(D ** -0.5)))
         ref.check_attention(out, None, want, torch.bfloat16, str(counts))
+
+
+@pytest.mark.parametrize("n", [0, 1, 7, 64, 130])
+@pytest.mark.parametrize("D,G,dtype", [(64, 1, torch.float16), (128, 4, torch.bfloat16), (192, 4, torch.float32), (256, 8, torch.bfloat16)])
+def test_a_lone_sequence_below_its_bound(workspace, D, G, dtype, n):
+    """Room for 130 queries, for fewer of them; the rows behind stay as they were."""
+    rng = np.random.default_rng(D + n)
+    c, table = poisoned(rng, [2111], 32, 2, D)
+    run(c, table, [2111], [n], 2 * G, dtype, workspace, max_q=130, tail=130 - n)
